@@ -379,6 +379,180 @@ int moe_device_supported(int cc_major, int cc_minor, size_t smem_per_block_optin
  */
 int moe_small_batch_build(int experts, int hidden, int inter, int batch, int grid);
 
+/* ------------------------------------------------------------------------
+ * The decode step around the layer: routing, and attention over a paged
+ * 8-bit cache. These calls need no handle: every buffer is the caller's, and
+ * each call is asynchronous on `stream`, an ordinary launch that starts when
+ * the work before it on the stream has ended. They allocate nothing and may
+ * be captured into a CUDA graph (lengths, tables and slots are read on the
+ * device). Refusals are found before the launch (MOE_ERR_ARG, with
+ * moe_last_error_detail); zero tokens is no work and MOE_OK.
+ * ------------------------------------------------------------------------ */
+
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
+enum moe_scoring { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+#define MOE_ROUTE_MAX_TOPK 32
+#define MOE_ROUTE_MAX_GROUPS 32
+
+/*
+ * moe_route - router logits to the routing ids and weights that moe_run and
+ * moe_run_combined take (with topk = MOE_TOPK).
+ *   score[t, e] = softmax over e, or 1 / (1 + exp(-logit)), in FP32
+ *   key[t, e]   = score + bias[e]; without a bias the score, or the logit
+ *                 itself where keys are only compared (every case but
+ *                 group_score 2 over several groups)
+ *   groups > 1: consecutive runs of experts / groups experts. A group's rank
+ *   is its largest key (group_score 1) or the sum of its two largest
+ *   (group_score 2); only the group_topk groups of highest rank take part.
+ *   ids[t, :]     = the topk experts of largest key, in descending order
+ *   weights[t, :] = their scores (not the biased keys), divided by their sum
+ *                   when renormalize is set, times scale
+ * Equal keys and equal ranks go to the lowest index. A logit of -inf or NaN
+ * masks its expert, and a NaN key counts as masked: masked experts and those of
+ * other groups are taken only when nothing else is left, lowest index first,
+ * with weight 0, so a row's ids are always distinct and in range. A +inf
+ * logit counts as the largest FP32 number. A row whose weights sum to zero
+ * keeps weights of 0. The softmax's sum is taken by halving (element i plus
+ * element i + n/2, over 1024 places), so a row's results do not depend on the
+ * other rows or the launch.
+ *   logits   device, [tokens, experts] of `dtype`, rows `row_stride` elements
+ *            apart (>= experts)
+ *   bias     device, FP32 [experts], or null
+ *   ids      device, int32 [tokens, topk]; weights device, FP32 [tokens, topk]
+ * 1 <= experts <= MOE_MAX_EXPERTS, 1 <= topk <= min(experts,
+ * MOE_ROUTE_MAX_TOPK), groups <= MOE_ROUTE_MAX_GROUPS divides experts,
+ * 1 <= group_topk <= groups, group_score 2 needs two experts to a group.
+ */
+typedef struct moe_route_t {
+  const void* logits;
+  int64_t row_stride;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int dtype, tokens, experts, topk;
+  int scoring, groups, group_topk, group_score, renormalize;
+  float scale;
+} moe_route_t;
+
+int moe_route(const moe_route_t* route, void* stream);
+
+/*
+ * The cache: keys and values as e4m3 codes in pages of page_tokens tokens,
+ *   k, v             uint8 [pages, kv_heads, page_tokens, head_dim]
+ *   k_scale, v_scale uint8 [pages, kv_heads], E8M0: byte b stands for
+ *                    2^(b - 127); an element is code * 2^(b - 127)
+ * page_tokens 16, 32, 64 or 128; head_dim 64, 128 or 256; k and v 16-byte
+ * aligned. Token `pos` of request r lies in page block_table[r][pos /
+ * page_tokens], row pos % page_tokens; slot = page * page_tokens + row.
+ */
+#define MOE_KV_MAX_REQUESTS 1024
+#define MOE_KV_WORKSPACE_BYTES (32 << 20)
+
+typedef struct moe_kv_cache_t {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int pages, page_tokens, kv_heads, head_dim;
+} moe_kv_cache_t;
+
+/*
+ * moe_kv_plan - block-table entries, lengths and slots of a step's new tokens.
+ * Request r holds context_lens[r] tokens and adds query_lens[r] (zero or
+ * more). With P = page_tokens it needs pages ceil(context / P) ..
+ * ceil((context + query) / P) - 1; the requests' needs, in order, take
+ * free_pages[*free_head], free_pages[*free_head + 1], ...
+ *   block_table  int32 [requests, table_width], rows table_stride apart: the
+ *                entries of the pages taken are written, the others kept
+ *   query_start  int32 [requests + 1]: prefix sums of query_lens
+ *   seq_lens     int32 [requests]: context + query
+ *   positions    int32 [tokens]: each new token's position in its request
+ *   slots        int64 [tokens]: its slot, -1 where it has no page
+ *   counts       int32 [4]: new tokens, the free list's head after this call
+ *                (pass its address as the next call's free_head; the two
+ *                calls' counts must be different buffers), the longest
+ *                seq_len, and error bits: 1 a negative or too large length
+ *                (counted as 0 tokens), 2 more new tokens than `tokens` (the
+ *                rest is left out), 4 a request longer than its table row,
+ *                8 free pages exhausted (4 and 8: the tokens concerned get
+ *                slot -1, and the entries -1 where the row has them)
+ * Rows of positions and slots past the last new token get 0 and -1.
+ * requests <= MOE_KV_MAX_REQUESTS. The same inputs give the same outputs:
+ * nothing but block_table is both read and written, and no entry both.
+ */
+typedef struct moe_kv_plan_t {
+  const int32_t* context_lens;
+  const int32_t* query_lens;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t* query_start;
+  int32_t* seq_lens;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* counts;
+  int requests, page_tokens, table_width, free_count, tokens;
+} moe_kv_plan_t;
+
+int moe_kv_plan(const moe_kv_plan_t* plan, void* stream);
+
+/*
+ * moe_kv_append - quantize the new tokens' keys and values into the cache.
+ * The scale of a page and head is the smallest power of two 2^E with
+ * max|x| <= 448 * 2^E over the rows written to it (E = -127 when they are all
+ * zero); a page that already holds earlier tokens (its first new row is not
+ * row 0) keeps the larger of that and its own, and where its scale grows, its
+ * earlier codes are rounded once more to the new one. Codes round to nearest
+ * even. Infinities take no part in max|x| and are stored as +-448 * 2^E, a
+ * NaN as NaN.
+ *   k, v   device, BF16 [tokens, kv_heads, head_dim] with token and head
+ *          strides in elements (multiples of 8; rows 16-byte aligned)
+ *   slots  device, int64 [tokens] (moe_kv_plan). The tokens of one page
+ *          follow one another in slots, in order; a slot outside the cache
+ *          (-1) writes nothing.
+ */
+int moe_kv_append(const moe_kv_cache_t* cache, const void* k, int64_t k_token_stride,
+                  int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                  int64_t v_head_stride, const int64_t* slots, int tokens, void* stream);
+
+/* The step's requests, as moe_kv_plan left them (all device memory but the sizes). */
+typedef struct moe_kv_batch_t {
+  const int32_t* block_table; /* [requests, table_width], rows table_stride apart */
+  int64_t table_stride;
+  const int32_t* query_start; /* [requests + 1] */
+  const int32_t* seq_lens;    /* [requests] */
+  int table_width, requests, tokens;
+} moe_kv_batch_t;
+
+/*
+ * moe_kv_attend - causal attention of the new tokens over the cache, their
+ * own keys and values included (moe_kv_append before it).
+ * Token i of request r stands at position p = seq_lens[r] - n + i, n its
+ * number of query rows, and sees keys max(0, p - window + 1) .. p (window 0:
+ * all up to p). Query head h reads cache head h / (q_heads / kv_heads).
+ *   out = sum_j w_j v_j,  w_j = exp(scale q.k_j - lse),
+ *   lse = log sum_j exp(scale q.k_j)
+ * in FP32; out is rounded to BF16 once. A query that sees nothing (p < 0) gets a
+ * zero row and lse -inf. Cache rows that no query sees are never used,
+ * whatever they hold; a table entry outside the cache is seen by no query. A
+ * query row that holds a NaN or an infinity gives a NaN row.
+ *   q    device, BF16 [tokens, q_heads, head_dim], strides in elements
+ *        (multiples of 8; rows 16-byte aligned)
+ *   out  device, BF16 [tokens, q_heads, head_dim] contiguous, 16-byte aligned
+ *   lse  device, FP32 [tokens, q_heads], or null
+ *   workspace  device, MOE_KV_WORKSPACE_BYTES, 16-byte aligned, zeroed once
+ *        by the caller; each call leaves it ready for the next. Calls that
+ *        overlap on the GPU need workspaces of their own.
+ * Rows of q past query_start[requests] are left out and their outputs kept.
+ * requests <= MOE_KV_MAX_REQUESTS; q_heads a multiple of kv_heads, at most
+ * 1024. Results do not depend on the other calls or on timing.
+ */
+int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
+                  int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
+                  int window, void* out, float* lse, void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,12 +24,17 @@ __all__ = [
     "MOE_ERR_STATE", "TOPK", "UNIT_ROWS", "MOE_NOALLOC_SCRATCH_BYTES", "moe_last_error_detail",
     "MAX_BATCH", "moe_device_supported", "moe_small_batch_build", "SMALL_NONE", "SMALL_PACKED", "SMALL_WIDE", "moe_debug_kernel_span", "moe_read_kernel_span",
     "moe_kernel_path", "PATH_GRID", "PATH_SMALL", "PATH_CLUSTER", "PATH_SMALL_WIDE",
+    "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "MOE_KV_WORKSPACE_BYTES", "MOE_KV_MAX_REQUESTS",
 ]
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_IDS, MOE_ERR_STATE = 4, 5, 6
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20  # static scratch of moe_run_noalloc
 TOPK, UNIT_ROWS, MAX_BATCH = 16, 8, 256
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MOE_KV_WORKSPACE_BYTES = 32 << 20  # workspace of moe_kv_attend
+MOE_KV_MAX_REQUESTS = 1024
 
 
 class MoeInfo(ctypes.Structure):
@@ -42,6 +47,31 @@ class MoeInfo(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class _Route(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("row_stride", _i64), ("bias", _vp), ("ids", _vp), ("weights", _vp)] + [
+        (n, _i32) for n in ("dtype", "tokens", "experts", "topk", "scoring", "groups", "group_topk", "group_score",
+                            "renormalize")] + [("scale", ctypes.c_float)]
+
+
+class _KvPlan(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("context_lens", "query_lens", "free_pages", "free_head", "block_table")] + [
+        ("table_stride", _i64)] + [(n, _vp) for n in ("query_start", "seq_lens", "positions", "slots", "counts")] + [
+        (n, _i32) for n in ("requests", "page_tokens", "table_width", "free_count", "tokens")]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, _i32) for n in ("pages", "page_tokens", "kv_heads", "head_dim")]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("block_table", _vp), ("table_stride", _i64), ("query_start", _vp), ("seq_lens", _vp)] + [
+        (n, _i32) for n in ("table_width", "requests", "tokens")]
 
 
 def _load():
@@ -77,6 +107,11 @@ def _load():
         "moe_small_batch_build": ([i32, i32, i32, i32, i32], i32),
         "moe_debug_kernel_span": ([vp, i32], i32),
         "moe_read_kernel_span": ([vp, ctypes.POINTER(u64)], i32),
+        "moe_route": ([ctypes.POINTER(_Route), vp], i32),
+        "moe_kv_plan": ([ctypes.POINTER(_KvPlan), vp], i32),
+        "moe_kv_append": ([ctypes.POINTER(_KvCache), vp, _i64, _i64, vp, _i64, _i64, vp, i32, vp], i32),
+        "moe_kv_attend": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), vp, _i64, _i64, i32, ctypes.c_float,
+                           i32, vp, vp, vp, vp], i32),
     }
     for name, (args, res) in signatures.items():
         fn = getattr(lib, name)
@@ -93,8 +128,9 @@ def library():
 
 
 class MoeError(RuntimeError):
-    def __init__(self, code: int, call: str):
-        detail = _lib.moe_last_error_detail().decode()
+    def __init__(self, code: int, call: str, detail: str | None = None):
+        if detail is None:
+            detail = _lib.moe_last_error_detail().decode()
         text = _lib.moe_error_string(code).decode()
         super().__init__(f"{call}: {text} (status {code}){': ' + detail if detail else ''}")
         self.code = code
@@ -274,6 +310,178 @@ def moe_device_supported(cc_major: int, cc_minor: int, smem_per_block_optin: int
 
 def moe_error_string(code: int) -> str:
     return _lib.moe_error_string(code).decode()
+
+
+# --- the decode step around the layer ---------------------------------------
+def _want(call: str, ok: bool, what: str):
+    if not ok:
+        raise MoeError(MOE_ERR_ARG, call, what)
+
+
+def _tensor(call: str, name: str, t, dtypes, shape=None, dense=True):
+    """Check one device tensor (None in `shape`: any size) and give its address."""
+    _want(call, t.is_cuda and t.dtype in dtypes, f"{name} must be a CUDA tensor of {dtypes}")
+    if shape is not None:
+        got = t.shape
+        _want(call, len(got) == len(shape) and all(w is None or w == g for w, g in zip(shape, got)),
+              f"{name} must have shape {shape}, not {tuple(got)}")
+    _want(call, not dense or t.is_contiguous(), f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _one_device(call: str, tensors, stream):
+    """The stream to launch on: every tensor must lie on the current device."""
+    import torch
+
+    device = torch.cuda.current_device()
+    for t in tensors:
+        _want(call, t is None or t.device.index == device, f"every tensor must lie on the current device ({device})")
+    return _stream(stream)
+
+
+_TYPES: dict = {}
+
+
+def _types():
+    if not _TYPES:
+        import torch
+
+        _TYPES.update(logits={torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, f32=(torch.float32,),
+                      i32=(torch.int32,), i64=(torch.int64,), bf16=(torch.bfloat16,),
+                      u8=(torch.uint8, torch.float8_e4m3fn), scale=(torch.uint8,))
+    return _TYPES
+
+
+def moe_route(logits, ids, weights, scoring: int = SCORE_SOFTMAX, bias=None, groups: int = 1, group_topk: int = 1,
+              group_score: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Routing ids (int32 [T, k]) and weights (float32 [T, k]) of logits [T, E]; see include/moe.h."""
+    call, ty = "moe_route", _types()
+    kind = ty["logits"].get(logits.dtype)
+    _want(call, kind is not None and logits.is_cuda, "logits must be a float32, bfloat16 or float16 CUDA tensor")
+    _want(call, logits.dim() == 2 and ids.dim() == 2, "logits and ids must have two dimensions")
+    tokens, experts = logits.shape
+    topk = ids.shape[1]
+    _want(call, logits.stride(1) == 1 or experts <= 1, "logits must have unit stride along the experts")
+    r = _Route(logits.data_ptr(), max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0),
+               None if bias is None else _tensor(call, "bias", bias, ty["f32"], (experts,)),
+               _tensor(call, "ids", ids, ty["i32"], (tokens, topk)),
+               _tensor(call, "weights", weights, ty["f32"], (tokens, topk)), kind, tokens, experts, topk, scoring,
+               groups, group_topk, group_score, int(bool(renormalize)), scale)
+    return _check(_lib.moe_route(r, _one_device(call, (logits, ids, weights, bias), stream)), call)
+
+
+def moe_kv_plan(context_lens, query_lens, page_tokens: int, block_table, free_pages, free_head, query_start, seq_lens,
+                positions, slots, counts, stream=None):
+    """Pages, lengths, positions and slots of a step's new tokens; see include/moe.h."""
+    call, ty = "moe_kv_plan", _types()
+    i32, requests, tokens = ty["i32"], context_lens.shape[0], positions.shape[0]
+    _want(call, block_table.dim() == 2 and block_table.stride(1) == 1, "block_table must be rows of unit stride")
+    width = block_table.shape[1]
+    p = _KvPlan(_tensor(call, "context_lens", context_lens, i32, (requests,)),
+                _tensor(call, "query_lens", query_lens, i32, (requests,)),
+                _tensor(call, "free_pages", free_pages, i32, (None,)), _tensor(call, "free_head", free_head, i32, (1,)),
+                _tensor(call, "block_table", block_table, i32, (requests, width), dense=False),
+                max(block_table.stride(0), width) if requests <= 1 else block_table.stride(0),
+                _tensor(call, "query_start", query_start, i32, (requests + 1,)),
+                _tensor(call, "seq_lens", seq_lens, i32, (requests,)),
+                _tensor(call, "positions", positions, i32, (tokens,)), _tensor(call, "slots", slots, ty["i64"], (tokens,)),
+                _tensor(call, "counts", counts, i32, (4,)), requests, page_tokens, width, free_pages.shape[0], tokens)
+    tensors = (context_lens, query_lens, free_pages, free_head, block_table, query_start, seq_lens, positions, slots,
+               counts)
+    return _check(_lib.moe_kv_plan(p, _one_device(call, tensors, stream)), call)
+
+
+def _cache(call: str, cache):
+    """The C description of a cache given as its tensors (k, v, k_scale, v_scale)."""
+    ty = _types()
+    k, v, ks, vs = cache
+    _want(call, k.dim() == 4, "the cache's keys must be [pages, kv_heads, page_tokens, head_dim]")
+    pages, heads, page, dim = k.shape
+    return _KvCache(_tensor(call, "k cache", k, ty["u8"]), _tensor(call, "v cache", v, ty["u8"], tuple(k.shape)),
+                    _tensor(call, "k_scale", ks, ty["scale"], (pages, heads)),
+                    _tensor(call, "v_scale", vs, ty["scale"], (pages, heads)), pages, page, heads, dim)
+
+
+def moe_kv_append(cache, k, v, slots, stream=None):
+    """Quantize keys and values (bfloat16 [T, kv_heads, head_dim], any token and head strides) into a cache given as
+    its tensors (k, v, k_scale, v_scale), at `slots`; see include/moe.h."""
+    call, ty = "moe_kv_append", _types()
+    c = _cache(call, cache)
+    tokens = slots.shape[0]
+    shape = (tokens, c.kv_heads, c.head_dim)
+    kp, vp = (_tensor(call, n, x, ty["bf16"], shape, dense=False) for n, x in (("k", k), ("v", v)))
+    _want(call, k.stride(2) == 1 and v.stride(2) == 1, "k and v must have unit stride along head_dim")
+    return _check(_lib.moe_kv_append(c, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
+                                     _tensor(call, "slots", slots, ty["i64"], (tokens,)), tokens,
+                                     _one_device(call, (*cache, k, v, slots), stream)), call)
+
+
+def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, lse=None, scale=None, window: int = 0,
+                  stream=None):
+    """Causal attention of q (bfloat16 [T, q_heads, head_dim]) over the cache, into out and lse (float32 [T, q_heads]);
+    scale None: head_dim ** -0.5. `workspace`: MOE_KV_WORKSPACE_BYTES of zeroed uint8; see include/moe.h."""
+    call, ty = "moe_kv_attend", _types()
+    i32, c = ty["i32"], _cache(call, cache)
+    _want(call, q.dim() == 3, "q must be [tokens, q_heads, head_dim]")
+    tokens, heads, dim = q.shape
+    requests = seq_lens.shape[0]
+    _want(call, block_table.dim() == 2 and block_table.stride(1) == 1, "block_table must be rows of unit stride")
+    width = block_table.shape[1]
+    b = _KvBatch(_tensor(call, "block_table", block_table, i32, (requests, width), dense=False),
+                 max(block_table.stride(0), width) if requests <= 1 else block_table.stride(0),
+                 _tensor(call, "query_start", query_start, i32, (requests + 1,)),
+                 _tensor(call, "seq_lens", seq_lens, i32, (requests,)), width, requests, tokens)
+    qp = _tensor(call, "q", q, ty["bf16"], (tokens, heads, c.head_dim), dense=False)
+    _want(call, q.stride(2) == 1, "q must have unit stride along head_dim")
+    _want(call, workspace.numel() * workspace.element_size() >= MOE_KV_WORKSPACE_BYTES,
+          f"workspace must have {MOE_KV_WORKSPACE_BYTES} bytes")
+    op = _tensor(call, "out", out, ty["bf16"], (tokens, heads, dim))
+    lp = None if lse is None else _tensor(call, "lse", lse, ty["f32"], (tokens, heads))
+    stream = _one_device(call, (*cache, q, block_table, query_start, seq_lens, out, workspace, lse), stream)
+    return _check(_lib.moe_kv_attend(c, b, qp, q.stride(0), q.stride(1), heads, dim ** -0.5 if scale is None else scale,
+                                     window, op, lp, workspace.data_ptr(), stream), call)
+
+
+class KvCache:
+    """A layer's paged cache: its tensors (e4m3 codes, E8M0 scales) and an attention workspace.
+
+    ``append(k, v, slots)`` writes a step's keys and values, ``attend(q,
+    block_table, query_start, seq_lens)`` returns the BF16 [T, q_heads,
+    head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``), both
+    on the current torch stream. Layers that run one after the other on one
+    stream can share a workspace.
+    """
+
+    def __init__(self, pages: int, kv_heads: int, page_tokens: int = 64, head_dim: int = 128, device="cuda",
+                 workspace=None):
+        import torch
+
+        codes = (pages, kv_heads, page_tokens, head_dim)
+        self.k = torch.zeros(codes, dtype=torch.uint8, device=device)
+        self.v = torch.zeros(codes, dtype=torch.uint8, device=device)
+        self.k_scale = torch.zeros(codes[:2], dtype=torch.uint8, device=device)
+        self.v_scale = torch.zeros(codes[:2], dtype=torch.uint8, device=device)
+        if workspace is None:
+            workspace = torch.zeros(MOE_KV_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        self.workspace = workspace
+
+    @property
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+    def append(self, k, v, slots, stream=None):
+        moe_kv_append(self.tensors, k, v, slots, stream)
+
+    def attend(self, q, block_table, query_start, seq_lens, out=None, scale=None, window: int = 0,
+               return_lse: bool = False, stream=None):
+        import torch
+
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+        moe_kv_attend(self.tensors, q, block_table, query_start, seq_lens, out, self.workspace, lse, scale, window,
+                      stream)
+        return (out, lse) if return_lse else out
 
 
 class MoeLayer:

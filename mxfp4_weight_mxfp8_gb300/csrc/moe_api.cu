@@ -1,6 +1,7 @@
 // The C ABI (include/moe.h): handle, weight repack, buffers, launches.
 #include <cudaTypedefs.h>
 
+#include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -471,6 +472,14 @@ int capture_host_run(moe_ctx* h, const void* x_host, const int32_t* ids_host, vo
 }
 
 }  // namespace
+
+int moe::fail(int status, const char* format, ...) {
+  va_list args;
+  va_start(args, format);
+  std::vsnprintf(g_detail, sizeof g_detail, format, args);
+  va_end(args);
+  return status;
+}
 
 extern "C" {
 
