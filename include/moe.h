@@ -448,6 +448,7 @@ int moe_route(const moe_route_t* route, void* stream);
  */
 #define MOE_KV_MAX_REQUESTS 1024
 #define MOE_KV_WORKSPACE_BYTES (32 << 20)
+#define MOE_KV_WORKSPACE_HEADER 4096 /* status and counters: the bytes that must start as zero */
 
 typedef struct moe_kv_cache_t {
   uint8_t* k;
@@ -542,8 +543,8 @@ typedef struct moe_kv_batch_t {
  *        (multiples of 8; rows 16-byte aligned)
  *   out  device, BF16 [tokens, q_heads, head_dim] contiguous, 16-byte aligned
  *   lse  device, FP32 [tokens, q_heads], or null
- *   workspace  device, MOE_KV_WORKSPACE_BYTES, 16-byte aligned, zeroed once
- *        by the caller; each call leaves it ready for the next. Calls that
+ *   workspace  device, MOE_KV_WORKSPACE_BYTES, 16-byte aligned, its first
+ *        MOE_KV_WORKSPACE_HEADER bytes zeroed once by the caller; each call leaves it ready for the next. Calls that
  *        overlap on the GPU need workspaces of their own.
  * Rows of q past query_start[requests] are left out and their outputs kept.
  * requests <= MOE_KV_MAX_REQUESTS; q_heads a multiple of kv_heads, at most
@@ -552,6 +553,15 @@ typedef struct moe_kv_batch_t {
 int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
                   int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
                   int window, void* out, float* lse, void* workspace, void* stream);
+
+/*
+ * moe_kv_sync_status - synchronize `stream` and return (and clear) the status
+ * word that moe_kv_attend's kernels write into the workspace: MOE_OK, or
+ * MOE_ERR_DEVICE_TIMEOUT (a bounded wait for a copy ran out; the kernel still
+ * finished, its outputs are not to be used). MOE_ERR_CUDA if the
+ * synchronization itself fails.
+ */
+int moe_kv_sync_status(void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

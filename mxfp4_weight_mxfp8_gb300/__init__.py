@@ -24,7 +24,7 @@ __all__ = [
     "MOE_ERR_STATE", "TOPK", "UNIT_ROWS", "MOE_NOALLOC_SCRATCH_BYTES", "moe_last_error_detail",
     "MAX_BATCH", "moe_device_supported", "moe_small_batch_build", "SMALL_NONE", "SMALL_PACKED", "SMALL_WIDE", "moe_debug_kernel_span", "moe_read_kernel_span",
     "moe_kernel_path", "PATH_GRID", "PATH_SMALL", "PATH_CLUSTER", "PATH_SMALL_WIDE",
-    "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
     "MOE_KV_WORKSPACE_BYTES", "MOE_KV_MAX_REQUESTS",
 ]
 
@@ -110,6 +110,7 @@ def _load():
         "moe_route": ([ctypes.POINTER(_Route), vp], i32),
         "moe_kv_plan": ([ctypes.POINTER(_KvPlan), vp], i32),
         "moe_kv_append": ([ctypes.POINTER(_KvCache), vp, _i64, _i64, vp, _i64, _i64, vp, i32, vp], i32),
+        "moe_kv_sync_status": ([vp, vp], i32),
         "moe_kv_attend": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), vp, _i64, _i64, i32, ctypes.c_float,
                            i32, vp, vp, vp, vp], i32),
     }
@@ -440,6 +441,11 @@ def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, 
     stream = _one_device(call, (*cache, q, block_table, query_start, seq_lens, out, workspace, lse), stream)
     return _check(_lib.moe_kv_attend(c, b, qp, q.stride(0), q.stride(1), heads, dim ** -0.5 if scale is None else scale,
                                      window, op, lp, workspace.data_ptr(), stream), call)
+
+
+def moe_kv_sync_status(workspace, stream=None) -> int:
+    """Device status of the finished moe_kv_attend calls on this workspace (not raised)."""
+    return _lib.moe_kv_sync_status(_ptr(workspace), _stream(stream))
 
 
 class KvCache:

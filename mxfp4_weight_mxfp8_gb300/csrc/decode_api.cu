@@ -20,6 +20,7 @@ const char* cache_fault(const moe_kv_cache_t* c) {
   if (c == nullptr || !c->k || !c->v || !c->k_scale || !c->v_scale) return "null cache pointer";
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return "cache not 16-byte aligned";
   if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024) return "cache pages or heads out of range";
+  if (static_cast<int64_t>(c->pages) * c->kv_heads > 0x7FFFFFFF) return "pages * kv_heads past 2^31";
   if (!page_size_ok(c->page_tokens)) return "page_tokens must be 16, 32, 64 or 128";
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
     return "head_dim must be 64, 128 or 256";
@@ -139,6 +140,19 @@ int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, cons
   a.lse = lse;
   a.workspace = static_cast<uint8_t*>(workspace);
   return launched(moe::launch_kv_attend(a, static_cast<cudaStream_t>(stream)), "moe_kv_attend");
+}
+
+int moe_kv_sync_status(void* workspace, void* stream) {
+  if (workspace == nullptr || !aligned(workspace, 16)) return refuse("null or misaligned workspace");
+  int32_t status = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&status, workspace, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && status != MOE_OK) {
+    e = cudaMemsetAsync(workspace, 0, MOE_KV_WORKSPACE_HEADER, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e == cudaSuccess ? status : launched(e, "moe_kv_sync_status");
 }
 
 }  // extern "C"
