@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from .build import LIBRARY
 
@@ -314,133 +315,172 @@ def moe_error_string(code: int) -> str:
 
 
 # --- the decode step around the layer ---------------------------------------
-def _want(call: str, ok: bool, what: str):
-    if not ok:
-        raise MoeError(MOE_ERR_ARG, call, what)
+# These calls take torch tensors and are made for every layer of every step, so
+# their host cost counts: each tensor is checked once, by the fewest calls, and
+# the argument blocks are packed in one go (native alignment, as the C structs).
+_ROUTE = struct.Struct("PqPPP9if")
+_PLAN = struct.Struct("5Pq5P5i")
+_CACHE = struct.Struct("4P4i")
+_BATCH = struct.Struct("PqPP3i")
 
 
-def _tensor(call: str, name: str, t, dtypes, shape=None, dense=True):
-    """Check one device tensor (None in `shape`: any size) and give its address."""
-    _want(call, t.is_cuda and t.dtype in dtypes, f"{name} must be a CUDA tensor of {dtypes}")
-    if shape is not None:
-        got = t.shape
-        _want(call, len(got) == len(shape) and all(w is None or w == g for w, g in zip(shape, got)),
-              f"{name} must have shape {shape}, not {tuple(got)}")
-    _want(call, not dense or t.is_contiguous(), f"{name} must be contiguous")
-    return t.data_ptr()
+def _packed(name: str):
+    """The C entry `name`, its argument blocks given as packed bytes."""
+    fn, ref = _lib[name], getattr(_lib, name)
+    fn.argtypes = [_vp if issubclass(t, ctypes._Pointer) else t for t in ref.argtypes]
+    fn.restype = ref.restype
+    return fn
 
 
-def _one_device(call: str, tensors, stream):
-    """The stream to launch on: every tensor must lie on the current device."""
+_route, _plan, _append, _attend = (_packed(n) for n in ("moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend"))
+_torch = None
+_LOGITS: dict = {}
+
+
+def _use_torch():
+    """torch and the lookups that need it, on the first call."""
+    global _torch, _i32t, _i64t, _f32t, _bf16t, _u8t, _raw_stream
     import torch
 
-    device = torch.cuda.current_device()
-    for t in tensors:
-        _want(call, t is None or t.device.index == device, f"every tensor must lie on the current device ({device})")
-    return _stream(stream)
+    _i32t, _i64t, _f32t, _bf16t, _u8t = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+    _LOGITS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    # The current stream's handle without building a stream object, where torch has it.
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
 
 
-_TYPES: dict = {}
+def _refuse(call: str, what: str):
+    raise MoeError(MOE_ERR_ARG, call, what)
 
 
-def _types():
-    if not _TYPES:
-        import torch
+def _dense(call: str, name: str, t, dtype, shape, device: int):
+    """Address of a contiguous tensor of this type and shape on `device`."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(call, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, "
+                  f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
-        _TYPES.update(logits={torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, f32=(torch.float32,),
-                      i32=(torch.int32,), i64=(torch.int64,), bf16=(torch.bfloat16,),
-                      u8=(torch.uint8, torch.float8_e4m3fn), scale=(torch.uint8,))
-    return _TYPES
+
+def _rows(call: str, name: str, t, dtype, shape, device: int):
+    """(address, token stride, head stride) of a [tokens, heads, dim] tensor with unit stride along dim."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape:
+        token, head, unit = t.stride()
+        if unit == 1:
+            return t.data_ptr(), token, head
+    _refuse(call, f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{device} with unit stride along its "
+                  f"last dimension, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _table(call: str, t, requests: int, device: int):
+    """(address, row stride, width) of a block table."""
+    if t.dtype is _i32t and t.get_device() == device and t.dim() == 2:
+        rows, width = t.shape
+        stride, unit = t.stride()
+        if rows == requests and unit == 1:
+            return t.data_ptr(), stride if requests > 1 else max(stride, width), width
+    _refuse(call, f"block_table must be an int32 tensor of {requests} rows with unit stride on cuda:{device}")
+
+
+def _on(call: str, t, stream) -> tuple:
+    """(device, stream) of a call whose tensors lie where `t` does: the current device."""
+    if _torch is None:
+        _use_torch()
+    device = t.get_device()
+    if device < 0 or device != _torch.cuda.current_device():
+        _refuse(call, f"tensors must lie on the current CUDA device, not on {t.device}")
+    return device, _raw_stream(device) if stream is None else _stream(stream)
 
 
 def moe_route(logits, ids, weights, scoring: int = SCORE_SOFTMAX, bias=None, groups: int = 1, group_topk: int = 1,
               group_score: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
     """Routing ids (int32 [T, k]) and weights (float32 [T, k]) of logits [T, E]; see include/moe.h."""
-    call, ty = "moe_route", _types()
-    kind = ty["logits"].get(logits.dtype)
-    _want(call, kind is not None and logits.is_cuda, "logits must be a float32, bfloat16 or float16 CUDA tensor")
-    _want(call, logits.dim() == 2 and ids.dim() == 2, "logits and ids must have two dimensions")
+    call = "moe_route"
+    device, stream = _on(call, logits, stream)
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None or logits.dim() != 2 or ids.dim() != 2:
+        _refuse(call, "logits must be float32, bfloat16 or float16, logits and ids two-dimensional")
     tokens, experts = logits.shape
-    topk = ids.shape[1]
-    _want(call, logits.stride(1) == 1 or experts <= 1, "logits must have unit stride along the experts")
-    r = _Route(logits.data_ptr(), max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0),
-               None if bias is None else _tensor(call, "bias", bias, ty["f32"], (experts,)),
-               _tensor(call, "ids", ids, ty["i32"], (tokens, topk)),
-               _tensor(call, "weights", weights, ty["f32"], (tokens, topk)), kind, tokens, experts, topk, scoring,
-               groups, group_topk, group_score, int(bool(renormalize)), scale)
-    return _check(_lib.moe_route(r, _one_device(call, (logits, ids, weights, bias), stream)), call)
+    row, unit = logits.stride()
+    if unit != 1 and experts > 1:
+        _refuse(call, "logits must have unit stride along the experts")
+    shape = (tokens, ids.shape[1])
+    block = _ROUTE.pack(
+        logits.data_ptr(), row if tokens > 1 else max(row, experts),
+        0 if bias is None else _dense(call, "bias", bias, _f32t, (experts,), device),
+        _dense(call, "ids", ids, _i32t, shape, device), _dense(call, "weights", weights, _f32t, shape, device), kind,
+        tokens, experts, shape[1], scoring, groups, group_topk, group_score, 1 if renormalize else 0, scale)
+    return _check(_route(block, stream), call)
 
 
 def moe_kv_plan(context_lens, query_lens, page_tokens: int, block_table, free_pages, free_head, query_start, seq_lens,
                 positions, slots, counts, stream=None):
     """Pages, lengths, positions and slots of a step's new tokens; see include/moe.h."""
-    call, ty = "moe_kv_plan", _types()
-    i32, requests, tokens = ty["i32"], context_lens.shape[0], positions.shape[0]
-    _want(call, block_table.dim() == 2 and block_table.stride(1) == 1, "block_table must be rows of unit stride")
-    width = block_table.shape[1]
-    p = _KvPlan(_tensor(call, "context_lens", context_lens, i32, (requests,)),
-                _tensor(call, "query_lens", query_lens, i32, (requests,)),
-                _tensor(call, "free_pages", free_pages, i32, (None,)), _tensor(call, "free_head", free_head, i32, (1,)),
-                _tensor(call, "block_table", block_table, i32, (requests, width), dense=False),
-                max(block_table.stride(0), width) if requests <= 1 else block_table.stride(0),
-                _tensor(call, "query_start", query_start, i32, (requests + 1,)),
-                _tensor(call, "seq_lens", seq_lens, i32, (requests,)),
-                _tensor(call, "positions", positions, i32, (tokens,)), _tensor(call, "slots", slots, ty["i64"], (tokens,)),
-                _tensor(call, "counts", counts, i32, (4,)), requests, page_tokens, width, free_pages.shape[0], tokens)
-    tensors = (context_lens, query_lens, free_pages, free_head, block_table, query_start, seq_lens, positions, slots,
-               counts)
-    return _check(_lib.moe_kv_plan(p, _one_device(call, tensors, stream)), call)
+    call = "moe_kv_plan"
+    device, stream = _on(call, context_lens, stream)
+    requests, tokens, free = context_lens.shape[0], positions.shape[0], free_pages.shape[0]
+    table, table_stride, width = _table(call, block_table, requests, device)
+    per = (requests,)
+    block = _PLAN.pack(
+        _dense(call, "context_lens", context_lens, _i32t, per, device),
+        _dense(call, "query_lens", query_lens, _i32t, per, device),
+        _dense(call, "free_pages", free_pages, _i32t, (free,), device),
+        _dense(call, "free_head", free_head, _i32t, (1,), device), table, table_stride,
+        _dense(call, "query_start", query_start, _i32t, (requests + 1,), device),
+        _dense(call, "seq_lens", seq_lens, _i32t, per, device),
+        _dense(call, "positions", positions, _i32t, (tokens,), device),
+        _dense(call, "slots", slots, _i64t, (tokens,), device),
+        _dense(call, "counts", counts, _i32t, (4,), device), requests, page_tokens, width, free, tokens)
+    return _check(_plan(block, stream), call)
 
 
-def _cache(call: str, cache):
-    """The C description of a cache given as its tensors (k, v, k_scale, v_scale)."""
-    ty = _types()
-    k, v, ks, vs = cache
-    _want(call, k.dim() == 4, "the cache's keys must be [pages, kv_heads, page_tokens, head_dim]")
-    pages, heads, page, dim = k.shape
-    return _KvCache(_tensor(call, "k cache", k, ty["u8"]), _tensor(call, "v cache", v, ty["u8"], tuple(k.shape)),
-                    _tensor(call, "k_scale", ks, ty["scale"], (pages, heads)),
-                    _tensor(call, "v_scale", vs, ty["scale"], (pages, heads)), pages, page, heads, dim)
+def _cache_block(call: str, cache, device: int):
+    """(packed description, kv_heads, head_dim) of a cache given as its tensors (k, v, k_scale, v_scale)."""
+    k, v, k_scale, v_scale = cache
+    shape = k.shape
+    if len(shape) != 4:
+        _refuse(call, "the cache's keys must be [pages, kv_heads, page_tokens, head_dim]")
+    pages, heads, page, dim = shape
+    scales = (pages, heads)
+    return _CACHE.pack(_dense(call, "k cache", k, _u8t, shape, device), _dense(call, "v cache", v, _u8t, shape, device),
+                       _dense(call, "k_scale", k_scale, _u8t, scales, device),
+                       _dense(call, "v_scale", v_scale, _u8t, scales, device), pages, page, heads, dim), heads, dim
 
 
 def moe_kv_append(cache, k, v, slots, stream=None):
     """Quantize keys and values (bfloat16 [T, kv_heads, head_dim], any token and head strides) into a cache given as
-    its tensors (k, v, k_scale, v_scale), at `slots`; see include/moe.h."""
-    call, ty = "moe_kv_append", _types()
-    c = _cache(call, cache)
+    its uint8 tensors (k, v, k_scale, v_scale), at `slots`; see include/moe.h."""
+    call = "moe_kv_append"
+    device, stream = _on(call, k, stream)
+    block, heads, dim = _cache_block(call, cache, device)
     tokens = slots.shape[0]
-    shape = (tokens, c.kv_heads, c.head_dim)
-    kp, vp = (_tensor(call, n, x, ty["bf16"], shape, dense=False) for n, x in (("k", k), ("v", v)))
-    _want(call, k.stride(2) == 1 and v.stride(2) == 1, "k and v must have unit stride along head_dim")
-    return _check(_lib.moe_kv_append(c, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
-                                     _tensor(call, "slots", slots, ty["i64"], (tokens,)), tokens,
-                                     _one_device(call, (*cache, k, v, slots), stream)), call)
+    shape = (tokens, heads, dim)
+    return _check(_append(block, *_rows(call, "k", k, _bf16t, shape, device), *_rows(call, "v", v, _bf16t, shape, device),
+                          _dense(call, "slots", slots, _i64t, (tokens,), device), tokens, stream), call)
 
 
 def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, lse=None, scale=None, window: int = 0,
                   stream=None):
     """Causal attention of q (bfloat16 [T, q_heads, head_dim]) over the cache, into out and lse (float32 [T, q_heads]);
     scale None: head_dim ** -0.5. `workspace`: MOE_KV_WORKSPACE_BYTES of zeroed uint8; see include/moe.h."""
-    call, ty = "moe_kv_attend", _types()
-    i32, c = ty["i32"], _cache(call, cache)
-    _want(call, q.dim() == 3, "q must be [tokens, q_heads, head_dim]")
-    tokens, heads, dim = q.shape
+    call = "moe_kv_attend"
+    device, stream = _on(call, q, stream)
+    block, _, dim = _cache_block(call, cache, device)
     requests = seq_lens.shape[0]
-    _want(call, block_table.dim() == 2 and block_table.stride(1) == 1, "block_table must be rows of unit stride")
-    width = block_table.shape[1]
-    b = _KvBatch(_tensor(call, "block_table", block_table, i32, (requests, width), dense=False),
-                 max(block_table.stride(0), width) if requests <= 1 else block_table.stride(0),
-                 _tensor(call, "query_start", query_start, i32, (requests + 1,)),
-                 _tensor(call, "seq_lens", seq_lens, i32, (requests,)), width, requests, tokens)
-    qp = _tensor(call, "q", q, ty["bf16"], (tokens, heads, c.head_dim), dense=False)
-    _want(call, q.stride(2) == 1, "q must have unit stride along head_dim")
-    _want(call, workspace.numel() * workspace.element_size() >= MOE_KV_WORKSPACE_BYTES,
-          f"workspace must have {MOE_KV_WORKSPACE_BYTES} bytes")
-    op = _tensor(call, "out", out, ty["bf16"], (tokens, heads, dim))
-    lp = None if lse is None else _tensor(call, "lse", lse, ty["f32"], (tokens, heads))
-    stream = _one_device(call, (*cache, q, block_table, query_start, seq_lens, out, workspace, lse), stream)
-    return _check(_lib.moe_kv_attend(c, b, qp, q.stride(0), q.stride(1), heads, dim ** -0.5 if scale is None else scale,
-                                     window, op, lp, workspace.data_ptr(), stream), call)
+    table, table_stride, width = _table(call, block_table, requests, device)
+    if q.dim() != 3:
+        _refuse(call, "q must be [tokens, q_heads, head_dim]")
+    tokens, heads, _ = q.shape
+    shape = (tokens, heads, dim)
+    batch = _BATCH.pack(table, table_stride, _dense(call, "query_start", query_start, _i32t, (requests + 1,), device),
+                        _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device), width, requests, tokens)
+    room = workspace.shape
+    if len(room) != 1 or room[0] < MOE_KV_WORKSPACE_BYTES:
+        _refuse(call, f"workspace must be {MOE_KV_WORKSPACE_BYTES} bytes of uint8")
+    return _check(_attend(block, batch, *_rows(call, "q", q, _bf16t, shape, device), heads,
+                          dim ** -0.5 if scale is None else scale, window, _dense(call, "out", out, _bf16t, shape, device),
+                          None if lse is None else _dense(call, "lse", lse, _f32t, (tokens, heads), device),
+                          _dense(call, "workspace", workspace, _u8t, room, device), stream), call)
 
 
 def moe_kv_sync_status(workspace, stream=None) -> int:
