@@ -39,6 +39,7 @@ constexpr int kTile = 32;        // cache tokens of a tile
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 2;       // tiles of a warp's ring
+constexpr int kItemTiles = 6;    // what starting and joining an item costs, in tiles
 constexpr int kMaxCtas = 512;
 constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,6 +81,25 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_e4m3_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// 2^x; what underflows FP32's normal range is zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^(b - 127) of an E8M0 byte.
+__device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
@@ -131,14 +151,16 @@ struct Request {
     tiles = max(1, (end + kTile - 1) / kTile - tile0);
     row_tiles = (static_cast<int>(min(static_cast<long long>(n) * a.group, 0x7FFFFF00ll)) + rows - 1) / rows;
   }
-  __device__ long long work(int heads) const { return static_cast<long long>(heads) * row_tiles * tiles; }
+  __device__ long long work(int heads) const { return static_cast<long long>(heads) * row_tiles * (tiles + kItemTiles); }
 };
 
-// A run of one item's tiles in this CTA.
+// A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
 struct Segment {
   int r, head, row_tile;
   int begin, end;          // tiles of the request, from tile0 on
-  long long item;          // the item's first tile among all
+  int length;              // in the units that the work is dealt in: kItemTiles for the item, then its tiles
+  bool first, whole;       // the item starts here; and ends here too
+  long long item;          // the item's first unit among all
   __device__ void find(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
     int lo = 0, hi = a.b.requests;
     while (hi - lo > 1) {
@@ -148,10 +170,16 @@ struct Segment {
     }
     r = lo;
     const Request q(a, shift, r, rows);
-    const long long local = x - prefix[lo], index = local / q.tiles;
-    begin = static_cast<int>(local - index * q.tiles);
-    end = static_cast<int>(min(static_cast<long long>(q.tiles), begin + (stop - x)));
-    item = x - begin;
+    const int units = q.tiles + kItemTiles;
+    const long long local = x - prefix[lo], index = local / units;
+    const int from = static_cast<int>(local - index * units);
+    const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
+    item = x - from;
+    length = to - from;
+    whole = length == units;
+    first = from == 0;
+    begin = max(0, from - kItemTiles);
+    end = max(0, to - kItemTiles);
     row_tile = static_cast<int>(index / a.c.kv_heads);
     head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
   }
@@ -176,7 +204,7 @@ struct Producer {
   __device__ void segment(const AttendArgs& a, const long long* prefix, int shift, int warp) {
     while (x < stop) {
       s.find(a, prefix, shift, X::kRows, x, stop);
-      x += s.end - s.begin;
+      x += s.length;
       tile = s.begin + warp;
       batch = 0;
       if (tile < s.end) {
@@ -214,33 +242,40 @@ struct Producer {
     if (batch == 0) look_up(a, shift, lane);
     const int p0 = __shfl_sync(kAll, pages[0], batch), p1 = __shfl_sync(kAll, pages[1], batch);
     const uint32_t sc = __shfl_sync(kAll, scales, batch);
+    // Lane 0 announces the bytes; then one lane for each box: keys and values, page halves, 128-byte spans.
+    constexpr int kBoxes = 4 * X::kHalves;
+    uint8_t* dst = ring + slot * X::kStageBytes;
+    uint64_t* bar = bars + slot;
     if (lane == 0) {
-      uint8_t* dst = ring + slot * X::kStageBytes;
-      uint64_t* bar = bars + slot;
-      const int row = ((tile0 + tile) * kTile) & (a.c.page_tokens - 1);
-      const int boxes = (p0 >= 0) + (p1 >= 0);  // of 16 tokens each, or one of 32
       meta[slot] = make_uint2(sc, shift == 4 ? (p0 >= 0) | (p1 >= 0) << 1 : (p0 >= 0 ? 3u : 0u));
       const uint32_t bytes = shift == 4 ? X::kStageBytes / 2 : X::kStageBytes;
-      if (boxes) mbar_arrive_expect_tx(bar, boxes * bytes);
+      if (p0 >= 0 || p1 >= 0) mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * bytes);
       else mbar_arrive(bar);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int p = i ? p1 : p0;
-        if (p < 0) continue;
-#pragma unroll
-        for (int h = 0; h < X::kHalves; ++h) {
-          uint8_t* to = dst + h * (kTile * X::kSpan) + i * (16 * X::kSpan);
-          tma_load_3d(to, &maps.k, h * X::kSpan, row, p * a.c.kv_heads + s.head, bar, policy);
-          tma_load_3d(to + X::kTileBytes, &maps.v, h * X::kSpan, row, p * a.c.kv_heads + s.head, bar, policy);
-        }
-      }
     }
+    __syncwarp();
+    const int second = (lane >> 1) & 1, half = lane >> 2, p = second ? p1 : p0;
+    if (lane < kBoxes && p >= 0)
+      tma_load_3d(dst + (lane & 1) * X::kTileBytes + half * (kTile * X::kSpan) + second * (16 * X::kSpan),
+                  lane & 1 ? &maps.v : &maps.k, half * X::kSpan, ((tile0 + tile) * kTile) & (a.c.page_tokens - 1),
+                  p * a.c.kv_heads + s.head, bar, policy);
     slot = slot + 1 == kStages ? 0 : slot + 1;
     batch = (batch + 1) & 31;
     tile += kWarps;
     if (tile >= s.end) segment(a, prefix, shift, warp);
   }
 };
+
+// Bounded wait for a tile's copies. Once one has run out the call's outputs are void, and later waits, which
+// see the status word set, give up at once.
+__device__ __noinline__ void wait_slot(uint64_t* bar, uint32_t parity, int32_t* status) {
+  const uint64_t began = global_timer_ns();
+  while (!mbar_wait_hint(bar, parity, 20000)) {
+    if (global_timer_ns() - began > kWaitNs || *reinterpret_cast<volatile int32_t*>(status) != 0) {
+      report(status, MOE_ERR_DEVICE_TIMEOUT);
+      return;
+    }
+  }
+}
 
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(const AttendArgs a, const __grid_constant__ Maps maps,
@@ -266,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
     for (int i = 0; i < kStages; ++i) mbar_init(bars + i, 1);
     fence_mbar_init();
   }
-  // Prefix sums of the requests' tiles.
+  // Prefix sums of the requests' work.
   {
     const int per = (a.b.requests + kThreads - 1) / kThreads;
     long long sum = 0;
@@ -295,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
     __syncthreads();
   }
   const long long total = prefix[a.b.requests];
-  // Each CTA gets at least a tile for each of its warps.
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kWarps - 1) / kWarps);
+  // Each CTA gets at least an item's start and a tile for each of its warps.
+  constexpr int kLeast = kItemTiles + kWarps;
+  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kLeast - 1) / kLeast);
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
 
@@ -311,7 +347,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
 
   int slot = 0;
   uint32_t phase = 0;
-  bool dead = false;  // a wait ran out: no more waiting
   for (long long x = start; x < stop;) {
     Segment s;
     s.find(a, prefix, shift, X::kRows, x, stop);
@@ -384,44 +419,34 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
     }
 
     for (int tile = s.begin + warp; tile < s.end; tile += kWarps) {
-      if (!dead && !mbar_test(bars + slot, phase)) {
-        const uint64_t began = global_timer_ns();
-        while (!mbar_wait_hint(bars + slot, phase, 20000))
-          if (global_timer_ns() - began > kWaitNs) {
-            dead = true;
-            report(status, MOE_ERR_DEVICE_TIMEOUT);
-            break;
-          }
-      }
-      dead = __any_sync(kAll, dead);
+      if (!mbar_test(bars + slot, phase)) wait_slot(bars + slot, phase, status);
+      __syncwarp();
       const uint2 info = meta[slot];
       const uint8_t* keys = ring + slot * X::kStageBytes;
       const uint8_t* vals = keys + X::kTileBytes;
       const int base = (rq.tile0 + tile) * kTile;
       const bool edge = info.y != 3u || base < all_lo || base + kTile - 1 > all_hi;
 
+      const float ks0 = scale_of(info.x & 0xFFu), ks1 = shift == 4 ? scale_of((info.x >> 16) & 0xFFu) : ks0;
       // Scores of 32 tokens: lane (g, t4) holds row g's of tokens 8 q + 2 t4 + {0, 1}.
       float sc[RT][4][2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float c[RT][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) c[rt][0] = c[rt][1] = c[rt][2] = c[rt][3] = 0.0f;
-#pragma unroll
         for (int j = 0; j < X::kSteps / 2; ++j) {  // 16 bytes of a key: two steps
           const int half = D >= 128 ? j / 2 : 0, c16 = D >= 128 ? t4 * 2 + j % 2 : t4;
           const uint4 k = *reinterpret_cast<const uint4*>(keys + chunk_at<D>(8 * q + g, half, c16));
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            mma_e4m3(c[rt], qa[rt][2 * j], k.x, k.y);
+            if (j == 0) mma_e4m3_first(c[rt], qa[rt][0], k.x, k.y);
+            else mma_e4m3(c[rt], qa[rt][2 * j], k.x, k.y);
             mma_e4m3(c[rt], qa[rt][2 * j + 1], k.z, k.w);
           }
         }
-        const uint32_t kb = (q < 2 || shift != 4 ? info.x : info.x >> 16) & 0xFFu;
-        const float ks = pow2f(static_cast<int>(kb) - 127);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const float f = factor[rt] * ks;
+          const float f = factor[rt] * (q < 2 ? ks0 : ks1);
           sc[rt][q][0] = fmaf(c[rt][2], kLo, c[rt][0]) * f;
           sc[rt][q][1] = fmaf(c[rt][3], kLo, c[rt][1]) * f;
         }
@@ -438,9 +463,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
             }
       }
       // Weights against the tile's own maximum, split for the second product.
-      const int vb0 = (info.x >> 8) & 0xFF, vb1 = shift == 4 ? info.x >> 24 : vb0;
-      const int vb = max(vb0, vb1);
-      const float up0 = 256.0f * pow2f(max(vb0 - vb, -126)), up1 = 256.0f * pow2f(max(vb1 - vb, -126));
+      const int vb0 = (info.x >> 8) & 0xFF;
+      float up0 = 256.0f, up1 = 256.0f, vs = scale_of(vb0) * (1.0f / 256.0f);
+      if (shift == 4) {  // two pages: to the larger of their scales
+        const int vb1 = info.x >> 24, vb = max(vb0, vb1);
+        up0 *= pow2f(max(vb0 - vb, -126));
+        up1 *= pow2f(max(vb1 - vb, -126));
+        vs = scale_of(vb) * (1.0f / 256.0f);
+      }
       uint32_t pa[RT][4];
       float into[RT];
 #pragma unroll
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            w[q][e] = exp2f(sc[rt][q][e] - ref);
+            w[q][e] = exp2_fast(sc[rt][q][e] - ref);
             sum += w[q][e];
             w[q][e] *= q < 2 ? up0 : up1;
           }
@@ -464,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
         split4(w[2][0], w[2][1], w[3][0], w[3][1], pa[rt][2], pa[rt][3]);
         const float mn = fmaxf(m[rt], top);
         const float safe = mn == -INFINITY ? 0.0f : mn;
-        const float keep = exp2f(m[rt] - safe), add = exp2f(top - safe);
+        const float keep = exp2_fast(m[rt] - safe), add = exp2_fast(top - safe);
         l[rt] = l[rt] * keep + sum * add;
-        into[rt] = add * (1.0f / 256.0f);
+        into[rt] = add * vs;
         m[rt] = mn;
         if (__any_sync(kAll, keep != 1.0f)) {
 #pragma unroll
@@ -476,7 +506,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
           }
         }
       }
-      const float vs = pow2f(vb - 127);
       // Output += weights x values. Values that no row sees are dropped; where rows see different
       // tokens and one of them holds a NaN, each row takes a pass of its own.
       int passes = 1;
@@ -535,13 +564,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
             for (int b = 0; b < 4; ++b)
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_e4m3(c, pa[rt], b0[b], b1[b]);
-                const float f = into[rt] * vs;
+                float c[4];
+                mma_e4m3_first(c, pa[rt], b0[b], b1[b]);
                 const int i = half * 16 + 4 * k + b;
                 if (passes == 1 || (pass & 7) == g && rt == pass >> 3) {
-                  acc[rt][i][0] += fmaf(c[2], kLo, c[0]) * f;
-                  acc[rt][i][1] += fmaf(c[3], kLo, c[1]) * f;
+                  acc[rt][i][0] += fmaf(c[2], kLo, c[0]) * into[rt];
+                  acc[rt][i][1] += fmaf(c[3], kLo, c[1]) * into[rt];
                 }
               }
           }
@@ -579,8 +607,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
       }
     }
     __syncthreads();
-    const bool whole = s.begin == 0 && s.end == rq.tiles;
-    const int part = s.begin > 0 ? 0 : 1;  // an item that began before this CTA's run, or goes on after it
+    const int part = s.first ? 1 : 0;  // an item that began before this CTA's run, or goes on after it
     float* mine = partials + static_cast<int64_t>(blockIdx.x * 2 + part) * X::kPartialFloats;
     for (int i = tid; i < X::kRows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), c = (i % (D / 4)) * 4;
@@ -600,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
         o.z += u.z * f;
         o.w += u.w * f;
       }
-      if (!whole) {
+      if (!s.whole) {
         *reinterpret_cast<float4*>(mine + row * D + c) = o;
         if (c == 0) {
           mine[X::kRows * D + row] = top;
@@ -615,9 +642,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
         if (a.lse != nullptr && c == 0) a.lse[dst] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
     }
-    if (!whole) {
+    if (!s.whole) {
       // The CTAs of this item: first .. last, by their runs' bounds.
-      const long long item_end = s.item + rq.tiles - 1;
+      const long long item_end = s.item + rq.tiles + kItemTiles - 1;
       const int c0 = static_cast<int>(((s.item + 1) * ctas - 1) / total);
       const int c1 = static_cast<int>(((item_end + 1) * ctas - 1) / total);
       __threadfence();
@@ -658,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_attend_kernel(c
       }
     }
     __syncthreads();  // the join buffers are free again
-    x += s.end - s.begin;
+    x += s.length;
   }
 }
 
