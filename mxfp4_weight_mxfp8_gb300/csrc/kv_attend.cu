@@ -80,7 +80,7 @@ struct Shape {
   static constexpr int kNan = kRowHi + kRows * 4;         // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;      // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kPrefix = kBars + (2 * kStages + 6) * 8;
+  static constexpr int kPrefix = kBars + (2 * kStages + 6) * 8;  // full, empty, s_full[2], o_full, p_ready, q_ready, drained
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
   static_assert(kPartialOffset + 2ll * kMaxCtas * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand images on swizzle boundaries");
@@ -219,20 +219,34 @@ struct Maps {
   CUtensorMap k, v;  // [pages * heads][page_tokens][head_dim]
 };
 
-// Bounded wait for a barrier's phase. Once one has run out the call's outputs are void, and later waits, which
-// see the status word set, give up at their first pause.
-__device__ __noinline__ void wait_more(uint64_t* bar, uint32_t parity, int32_t* status) {
+// Bounded wait for a barrier's phase: false, and the error reported, when it runs out. A role that sees that issues
+// nothing more, waits (bounded again) for what it has in flight, and goes to the CTA's end.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, int32_t* status) {
   const uint64_t began = global_timer_ns();
   while (!mbar_wait_hint(bar, parity, 20000)) {
-    if (global_timer_ns() - began > kWaitNs || *reinterpret_cast<volatile int32_t*>(status) != 0) {
+    if (global_timer_ns() - began > kWaitNs) {
       report(status, MOE_ERR_DEVICE_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (!mbar_test(bar, parity)) wait_more(bar, parity, status);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return mbar_test(bar, parity) || wait_more(bar, parity, status);
+}
+
+// Barrier of the compute warps; true everywhere if any thread brings true.
+__device__ __forceinline__ bool compute_any(bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "selp.u32 %0, 1, 0, q; }"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
 }
 
 template <int D, int RT>
@@ -249,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   uint64_t* o_full = s_full + 2;          // a tile's output in TMEM
   uint64_t* p_ready = o_full + 1;         // a tile's weights in shared memory
   uint64_t* q_ready = p_ready + 1;        // a segment's queries in shared memory
+  uint64_t* drained = q_ready + 1;        // every MMA issued has completed
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
   __shared__ long long s_sum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -267,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     mbar_init(o_full, 1);
     mbar_init(p_ready, kCompute);
     mbar_init(q_ready, kCompute);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   // Prefix sums of the requests' work.
@@ -303,7 +319,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   const long long ctas = min(static_cast<long long>(gridDim.x), (total + kLeast - 1) / kLeast);
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
-  if (warp == kIssueWarp) tmem_alloc(&s_tmem, X::kTmem);
+  if (warp == kIssueWarp) {
+    tmem_alloc(&s_tmem, X::kTmem);
+    tmem_relinquish();  // the SM's other CTA allocates its own
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -314,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     const int per_tile = kTile >> shift, in_tile = lane & (per_tile - 1);  // pages of a tile; this lane's
     const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
     int k = 0;
-    for (long long x = start; x < stop;) {
+    bool alive = true;
+    for (long long x = start; x < stop && alive;) {
       Segment s;
       s.find(a, prefix, shift, X::kRows, x, stop);
       x += s.length;
@@ -337,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
         }
         const int stage = k % X::kStages;
-        if (k >= X::kStages) wait(empty + stage, (k / X::kStages - 1) & 1, status);
-        __syncwarp();
+        if (k >= X::kStages) alive = __all_sync(kAll, wait(empty + stage, (k / X::kStages - 1) & 1, status));
+        if (!alive) break;
         const bool mine = lane / per_tile == batch;
         uint32_t* m = meta + stage * (kMaxPages + 1);
         if (mine) {
@@ -364,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         __syncwarp();
       }
     }
+    // The copies in flight land before the CTA ends (at once, unless another role gave up).
+    for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
@@ -371,8 +393,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     constexpr uint32_t kScoreDesc = idesc_f8(X::kCols, false), kOutDesc = idesc_f8(X::kCols, true);
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
     int k = 0, segments = 0;
+    bool alive = true;
     auto scores = [&](int i) {
-      wait(full + i % X::kStages, (i / X::kStages) & 1, status);
+      alive = __all_sync(kAll, wait(full + i % X::kStages, (i / X::kStages) & 1, status));
+      if (!alive) return;
       tc_fence_after_sync();
       if (lane == 0) {
         const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes, d = tmem + (i & 1) * X::kCols;
@@ -386,16 +410,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       }
       __syncwarp();
     };
-    for (long long x = start; x < stop;) {
+    for (long long x = start; x < stop && alive;) {
       Segment s;
       s.find(a, prefix, shift, X::kRows, x, stop);
       x += s.length;
       if (s.begin == s.end) continue;
-      wait(q_ready, segments++ & 1, status);
-      scores(k);
-      for (int tile = s.begin; tile < s.end; ++tile, ++k) {
+      alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
+      if (alive) scores(k);
+      for (int tile = s.begin; tile < s.end && alive; ++tile, ++k) {
         if (tile + 1 < s.end) scores(k + 1);
-        wait(p_ready, k & 1, status);
+        alive = alive && __all_sync(kAll, wait(p_ready, k & 1, status));
+        if (!alive) break;
         tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t vals = ring + (k % X::kStages) * X::kStageBytes + X::kTileBytes;
@@ -411,6 +436,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         __syncwarp();
       }
     }
+    if (lane == 0) {
+      tc_commit(drained);
+      wait(drained, 0, status);
+    }
+    __syncwarp();
   } else {
     float* red = reinterpret_cast<float*>(sm + X::kRed);
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
@@ -419,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21), lanes_o = tmem_o + (static_cast<uint32_t>(warp) << 21);
     int k = 0;
+    bool failed = false;  // a wait of this thread's ran out; agreed on at the barriers
     for (long long x = start; x < stop;) {
       Segment s;
       s.find(a, prefix, shift, X::kRows, x, stop);
@@ -487,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       float pend[X::kRows], pend_vs = 0.0f;  // factors of the output still in TMEM
       bool pend_f = false;
       auto take_output = [&](int i) {  // tile i's product joins the running output
-        wait(o_full, i & 1, status);
+        failed |= !wait(o_full, i & 1, status);
+        __syncwarp();
         tc_fence_after_sync();
 #pragma unroll
         for (int h = 0; h < X::kHalves; ++h)
@@ -516,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       };
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
         const int stage = k % X::kStages;
-        wait(full + stage, (k / X::kStages) & 1, status);
+        failed |= !wait(full + stage, (k / X::kStages) & 1, status);
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const uint32_t entry = mt[tid >> shift];
         const int base = (rq.tile0 + tile) * kTile, token = base + tid;
@@ -524,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         bool edge = base < all_lo || base + kTile - 1 > all_hi;
         edge = __any_sync(kAll, edge || !(entry >> 16));
         const float ks = scale_of(entry & 0xFFu);
-        wait(s_full + (k & 1), (k >> 1) & 1, status);
+        failed |= !wait(s_full + (k & 1), (k >> 1) & 1, status);
+        __syncwarp();
         tc_fence_after_sync();
         float sc[X::kRows];
 #pragma unroll
@@ -556,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           if (lane == i) top = v;
         }
         if (lane < X::kRows) red[lane * 4 + warp] = top;
-        compute_sync();
+        failed = compute_any(failed);
+        if (failed) break;
         float ref = 0.0f, keep = 1.0f, add = 1.0f;
         if (lane < X::kRows) {
           const float4 v = *reinterpret_cast<const float4*>(red + lane * 4);
@@ -645,10 +679,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         tc_fence_before_sync();
         mbar_arrive(p_ready);
       }
-      if (s.begin < s.end) take_output(k - 1);
+      if (s.begin < s.end && !failed) take_output(k - 1);
 
       // The segment's sums over the tokens, and its rows.
-      compute_sync();
+      failed = compute_any(failed);
+      if (failed) break;
 #pragma unroll
       for (int i = 0; i < X::kRows; ++i) {
         float v = l[i];
@@ -758,7 +793,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   __syncthreads();
   if (warp == kIssueWarp) {
     tc_fence_after_sync();
-    tmem_relinquish();
     tmem_dealloc(tmem, X::kTmem);
   }
 }
