@@ -67,7 +67,7 @@ struct Shape {
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
-  static constexpr int kStages = D == 64 ? 5 : (D == 128 && RT == 4 ? 2 : 3);
+  static constexpr int kStages = D == 64 ? 5 : (D == 128 && RT >= 3 ? 2 : 3);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
@@ -103,21 +103,19 @@ __host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed) {
          | ((128u >> 4) << 24);                   // M / 16
 }
 
-__device__ __forceinline__ void tmem_load_16_async(uint32_t taddr, float (&r)[16]) {
+// Eight consecutive TMEM columns of this thread's lane as floats, without the wait.
+__device__ __forceinline__ void tmem_load_8_async(uint32_t taddr, float (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
       : "r"(taddr)
       : "memory");
 }
 
 // The wait for tcgen05.ld, tied to the registers that it completes.
-__device__ __forceinline__ void tmem_wait_16(float (&r)[16]) {
+__device__ __forceinline__ void tmem_wait_8(float (&r)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
                :
                : "memory");
 }
@@ -156,6 +154,15 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_
   lo = pack2((v0 - f.x) * 16.0f, (v1 - f.y) * 16.0f);
 }
 
+// The same in half precision, for values of which 11 bits are enough: a weight is held to fewer by its codes.
+__device__ __forceinline__ void split2_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  const __half2 v = __floats2half2_rn(v0, v1);
+  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
+  const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
+  const __half2 rest = __hmul2(__hsub2(v, f), __float2half2_rn(16.0f));
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+}
+
 __device__ __forceinline__ uint32_t nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
 
 // Byte offset of 16-byte chunk c of row n in an image of kSpan-byte rows, as the swizzle of that width places it.
@@ -165,6 +172,12 @@ __device__ __forceinline__ uint32_t chunk_at(int n, int c) {
 }
 
 // ----------------------------------------------------------------------- work
+// a / b of numbers that mostly fit 32 bits, where the division is far shorter.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // A request's share of the work.
 struct Request {
   int first, n, seq;       // first query row's token, query tokens, visible length
@@ -201,7 +214,7 @@ struct Segment {
     r = lo;
     const Request q(a, shift, r, rows);
     const int units = q.tiles + kItemTiles;
-    const long long local = x - prefix[lo], index = local / units;
+    const long long local = x - prefix[lo], index = divide(local, units);
     const int from = static_cast<int>(local - index * units);
     const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
     item = x - from;
@@ -210,7 +223,7 @@ struct Segment {
     first = from == 0;
     begin = max(0, from - kItemTiles);
     end = max(0, to - kItemTiles);
-    row_tile = static_cast<int>(index / a.c.kv_heads);
+    row_tile = static_cast<int>(divide(index, a.c.kv_heads));
     head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
   }
 };
@@ -341,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       const Request q(a, shift, s.r, X::kRows);
       int page = -1;
       uint32_t entry = 0, top = 0;
+      bool fresh = false;  // a batch whose scales are not read yet
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
         const int batch = (tile - s.begin) & (batch_tiles - 1);
         if (batch == 0) {
@@ -348,30 +362,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           page = -1;
           if (token < q.end && tile + lane / per_tile < s.end) page = a.b.block_table[s.r * a.b.table_stride + (token >> shift)];
           if (page >= a.c.pages) page = -1;
-          entry = 0;
-          if (page >= 0) {
-            const long long at = static_cast<long long>(page) * a.c.kv_heads + s.head;
-            entry = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8 | 1u << 16;
-          }
-          top = (entry >> 8) & 0xFFu;  // the tile's largest value scale
-          for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
+          fresh = true;
         }
         const int stage = k % X::kStages;
         if (k >= X::kStages) alive = __all_sync(kAll, wait(empty + stage, (k / X::kStages - 1) & 1, status));
         if (!alive) break;
+        // The copies first; the barrier's phase stays open until lane 0 arrives.
         const bool mine = lane / per_tile == batch;
-        uint32_t* m = meta + stage * (kMaxPages + 1);
-        if (mine) {
-          m[in_tile] = entry;
-          if (in_tile == 0) m[kMaxPages] = top;
-        }
         const int boxes = __popc(__ballot_sync(kAll, mine && page >= 0));
-        __syncwarp();  // the entries are written before lane 0 arrives
-        if (lane == 0) {
-          if (boxes) mbar_arrive_expect_tx(full + stage, boxes * (2 * D << shift));
-          else mbar_arrive(full + stage);
-        }
-        __syncwarp();
         if (mine && page >= 0) {
           uint8_t* dst = sm + X::kRing + stage * X::kStageBytes + (in_tile << shift) * X::kSpan;
 #pragma unroll
@@ -381,7 +379,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
                         full + stage, policy);
           }
         }
-        __syncwarp();
+        if (fresh) {
+          fresh = false;
+          entry = 0;
+          if (page >= 0) {
+            const long long at = static_cast<long long>(page) * a.c.kv_heads + s.head;
+            entry = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8 | 1u << 16;
+          }
+          top = (entry >> 8) & 0xFFu;  // the tile's largest value scale
+          for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
+        }
+        uint32_t* m = meta + stage * (kMaxPages + 1);
+        if (mine) {
+          m[in_tile] = entry;
+          if (in_tile == 0) m[kMaxPages] = top;
+        }
+        __syncwarp();  // the entries are written before lane 0 arrives
+        if (lane == 0) {
+          if (boxes) mbar_arrive_expect_tx(full + stage, boxes * (2 * D << shift));
+          else mbar_arrive(full + stage);
+        }
       }
     }
     // The copies in flight land before the CTA ends (at once, unless another role gave up).
@@ -489,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             split2(__uint_as_float(v[j] << 16) * down, __uint_as_float(v[j] & 0xFFFF0000u) * down, hi[j], lo[j]);
+          if (row >= X::kRows) continue;  // whole warps, past the loop's shuffles
           const int span = c * 8 / X::kSpan, in = c * 8 % X::kSpan;
           uint8_t* dst = sm + X::kQ + span * (X::kCols * X::kSpan) + in % 16;
           *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(row, in / 16)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -525,25 +543,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
           for (int part = 0; part < X::kRows; part += 8) {
-            float o[16];  // hi columns part .. + 7, lo columns
-            float lo8[16];
-            if (RT == 1) {
-              tmem_load_16_async(lanes_o + h * X::kCols, o);
-              tmem_wait_16(o);
-            } else if (part % 16 == 0) {
-              tmem_load_16_async(lanes_o + h * X::kCols + part, o);
-              tmem_load_16_async(lanes_o + h * X::kCols + X::kRows + part, lo8);
-              tmem_wait_16(o);
-              tmem_wait_16(lo8);
-            }
-            constexpr int kStep = RT == 1 ? 8 : 16;
-            if (part % kStep == 0) {
+            float o[8], u[8];  // hi columns, lo columns
+            tmem_load_8_async(lanes_o + h * X::kCols + part, o);
+            tmem_load_8_async(lanes_o + h * X::kCols + X::kRows + part, u);
+            tmem_wait_8(o);
+            tmem_wait_8(u);
 #pragma unroll
-              for (int j = 0; j < kStep; ++j) {
-                const float v = fmaf(RT == 1 ? o[(8 + j) % 16] : lo8[j], kLo, o[j]);
-                acc[h][part + j] = fmaf(v, pend_f ? pend[part + j] * pend_vs : pend_vs, acc[h][part + j]);
-              }
-            }
+            for (int j = 0; j < 8; ++j)
+              acc[h][part + j] = fmaf(fmaf(u[j], kLo, o[j]), pend_f ? pend[part + j] * pend_vs : pend_vs, acc[h][part + j]);
           }
       };
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
@@ -561,19 +568,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         tc_fence_after_sync();
         float sc[X::kRows];
 #pragma unroll
-        for (int part = 0; part < X::kRows; part += (RT == 1 ? 8 : 16)) {
-          float u[16], w[16];
-          tmem_load_16_async(lanes + (k & 1) * X::kCols + part, u);
-          if (RT > 1) tmem_load_16_async(lanes + (k & 1) * X::kCols + X::kRows + part, w);
-          tmem_wait_16(u);
-          if (RT > 1) tmem_wait_16(w);
+        for (int part = 0; part < X::kRows; part += 8) {
+          float u[8], w[8];  // hi columns, lo columns
+          tmem_load_8_async(lanes + (k & 1) * X::kCols + part, u);
+          tmem_load_8_async(lanes + (k & 1) * X::kCols + X::kRows + part, w);
+          tmem_wait_8(u);
+          tmem_wait_8(w);
 #pragma unroll
-          for (int j = 0; j < (RT == 1 ? 8 : 16); j += 4) {
+          for (int j = 0; j < 8; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(row_f + part + j);
             const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[part + j + e] = fmaf(RT == 1 ? u[(8 + j + e) % 16] : w[j + e], kLo, u[j + e]) * (fs[e] * ks);
+            for (int e = 0; e < 4; ++e) sc[part + j + e] = fmaf(w[j + e], kLo, u[j + e]) * (fs[e] * ks);
           }
         }
         if (edge) {
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
             }
           }
           uint32_t hi, lo;
-          split2(p[0] * up, p[1] * up, hi, lo);
+          split2_half(p[0] * up, p[1] * up, hi, lo);
           prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
           prow[chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(hi >> 8);
           prow[chunk_at<128>(X::kRows + i, tid / 16)] = static_cast<uint8_t>(lo);
@@ -738,51 +744,60 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           mine[X::kRows * D + X::kRows + tid] = sum;
         }
         // The CTAs of this item: c0 .. c1, by the bounds of their runs.
-        const int c0 = static_cast<int>(((s.item + 1) * ctas - 1) / total);
-        const int c1 = static_cast<int>(((s.item + rq.tiles + kItemTiles) * ctas - 1) / total);
-        __threadfence();
+        const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
+        const int c1 = static_cast<int>(divide((s.item + rq.tiles + kItemTiles) * ctas - 1, total));
         compute_sync();
         if (tid == 0) {
+          // Releases the CTA's stores (ordered before it by the barrier), acquires the other pieces'.
           const uint32_t before = atom_add_acq_rel_gpu(counters + c0, 1);
           s_last = before == static_cast<uint32_t>(c1 - c0);
           if (s_last) counters[c0] = 0;
         }
         compute_sync();
         if (s_last) {
-          __threadfence();
-          // Maxima and sums over the pieces first (lane = row), then the rows.
-          float all_m = -INFINITY, all_l = 0.0f;
-          if (lane < X::kRows) {
-            for (int c = c0; c <= c1; ++c)
-              all_m = fmaxf(all_m, __ldcg(partials + static_cast<int64_t>(c * 2 + (c == c0)) * X::kPartialFloats + X::kRows * D + lane));
-          }
-          const float base = all_m == -INFINITY ? 0.0f : all_m;
+          // Maxima and sums over the pieces, a row to a warp at a time; then the rows, the pieces' loads in flight together.
+          const float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * X::kPartialFloats;  // the first piece
+          const float* piece0 = partials + static_cast<int64_t>(c0 * 2) * X::kPartialFloats;      // piece i: 2 i slots on
+          auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * X::kPartialFloats; };
+          const int pieces = c1 - c0 + 1;
+          for (int i = warp; i < X::kRows; i += 4) {
+            float top = -INFINITY, total_l = 0.0f;
+            for (int c = lane; c < pieces; c += 32) top = fmaxf(top, __ldcg(piece(c) + X::kRows * D + i));
+            top = warp_max(top);
+            const float ref = top > -INFINITY ? top : 0.0f;
+            for (int c = lane; c < pieces; c += 32)
+              total_l += __ldcg(piece(c) + X::kRows * D + X::kRows + i) * exp2_fast(__ldcg(piece(c) + X::kRows * D + i) - ref);
 #pragma unroll
-          for (int i = 0; i < X::kRows; ++i)
-#pragma unroll
-            for (int h = 0; h < X::kHalves; ++h) acc[h][i] = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* from = partials + static_cast<int64_t>(c * 2 + (c == c0)) * X::kPartialFloats;
-            float f = 0.0f;
-            if (lane < X::kRows) {
-              f = exp2_fast(__ldcg(from + X::kRows * D + lane) - base);
-              all_l = fmaf(__ldcg(from + X::kRows * D + X::kRows + lane), f, all_l);
-            }
-#pragma unroll
-            for (int i = 0; i < X::kRows; ++i) {
-              const float g = __shfl_sync(kAll, f, i);
-              if (holds) {
-#pragma unroll
-                for (int h = 0; h < X::kHalves; ++h) acc[h][i] = fmaf(__ldcg(from + i * D + h * 128 + tid), g, acc[h][i]);
-              }
+            for (int d = 16; d >= 1; d >>= 1) total_l += __shfl_xor_sync(kAll, total_l, d);
+            if (lane == 0) {
+              red[i * 4] = ref;
+              red[i * 4 + 1] = total_l == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l);
+              red[i * 4 + 2] = total_l == 0.0f ? -INFINITY : (top + log2f(total_l)) * kLn2;
             }
           }
-          const float inv = all_l == 0.0f ? 0.0f : __fdiv_rn(1.0f, all_l);
-          const float lse = all_l == 0.0f ? -INFINITY : (all_m + log2f(all_l)) * kLn2;
-#pragma unroll
-          for (int i = 0; i < X::kRows; ++i) {
-            const float f = __shfl_sync(kAll, inv, i), e = __shfl_sync(kAll, lse, i);
-            if (i < rows) store_row(i, acc[0][i], acc[X::kHalves - 1][i], f, e);
+          compute_sync();
+          constexpr int kQuads = D / 4;
+          for (int u = tid; u < X::kRows * kQuads; u += kCompute) {
+            const int i = u / kQuads, c4 = (u % kQuads) * 4;
+            if (i >= rows) break;
+            const float ref = red[i * 4];
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = 0; c < pieces; ++c) {
+              const float* from = piece(c);
+              const float f = exp2_fast(__ldcg(from + X::kRows * D + i) - ref);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + i * D + c4));
+              o.x = fmaf(v.x, f, o.x);
+              o.y = fmaf(v.y, f, o.y);
+              o.z = fmaf(v.z, f, o.z);
+              o.w = fmaf(v.w, f, o.w);
+            }
+            const float inv = red[i * 4 + 1];
+            const int at = row0 + i, tok = at / a.group;
+            const int64_t dst = static_cast<int64_t>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
+            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+            *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
+            if (a.lse != nullptr && c4 == 0) a.lse[dst] = red[i * 4 + 2];
           }
         }
       }
@@ -836,10 +851,11 @@ cudaError_t launch_shape(const AttendArgs& a, const Maps& maps, int shift, cudaS
 
 template <int D>
 cudaError_t launch_dim(const AttendArgs& a, const Maps& maps, int shift, cudaStream_t stream) {
-  // Row tiles of 8, 16 or 32, by the rows that a request has on average.
+  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average.
   const long long rows = static_cast<long long>(a.b.tokens) * a.group;
   if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, stream);
   if (rows <= 16ll * a.b.requests || D == 256) return launch_shape<D, 2>(a, maps, shift, stream);
+  if (rows <= 24ll * a.b.requests) return launch_shape<D, D == 256 ? 2 : 3>(a, maps, shift, stream);
   return launch_shape<D, D == 256 ? 2 : 4>(a, maps, shift, stream);
 }
 
