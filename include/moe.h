@@ -448,7 +448,7 @@ int moe_route(const moe_route_t* route, void* stream);
  */
 #define MOE_KV_MAX_REQUESTS 1024
 #define MOE_KV_WORKSPACE_BYTES (32 << 20)
-#define MOE_KV_WORKSPACE_HEADER 4096 /* status and counters: the bytes that must start as zero */
+#define MOE_KV_WORKSPACE_HEADER 8192 /* status and counters: the bytes that must start as zero */
 
 typedef struct moe_kv_cache_t {
   uint8_t* k;

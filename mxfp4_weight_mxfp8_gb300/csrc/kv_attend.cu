@@ -45,18 +45,19 @@ constexpr int kIssueWarp = 5;
 constexpr int kThreads = 192;
 constexpr int kItemTiles = 2;     // what starting and joining an item costs, in tiles
 constexpr int kMaxPages = 8;      // pages of a tile
-constexpr int kMaxCtas = 384;
+constexpr int kMaxCtas = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
 constexpr float kNear = 8.0f;        // log2 distance of a tile's maximum from the running one
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Workspace: the status word, one arrival counter for each CTA (zero between
-// calls), two partial results for each CTA.
+// Workspace: the status word, arrival counters (zero between calls: for the
+// runs of pieces that start with an item, for its other runs, for the item;
+// each under the CTA of the first piece), two partial results for each CTA.
 constexpr int kCounterOffset = 256;
 constexpr int kPartialOffset = MOE_KV_WORKSPACE_HEADER;
-static_assert(kCounterOffset + kMaxCtas * 4 <= kPartialOffset, "counters fit");
+static_assert(kCounterOffset + 3 * kMaxCtas * 4 <= kPartialOffset, "counters fit");
 
 template <int D, int RT>
 struct Shape {
@@ -66,8 +67,8 @@ struct Shape {
   static constexpr int kSpan = D >= 128 ? 128 : 64;       // bytes of a row in one box: the swizzle's width
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
-  static constexpr int kStages = D == 64 ? 5 : (D == 128 && RT >= 3 ? 2 : 3);
+  static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : 5) : (D == 128 && RT != 2 ? 2 : 3);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
@@ -184,6 +185,7 @@ struct Request {
   int end;                 // tokens that the table has room for
   int tile0, tiles;        // first tile that some query sees, their number (one at least)
   int row_tiles;
+  Request() = default;
   __device__ Request(const AttendArgs& a, int shift, int r, int rows) {
     first = min(max(a.b.query_start[r], 0), a.b.tokens);
     n = min(max(a.b.query_start[r + 1], first), a.b.tokens) - first;
@@ -199,11 +201,25 @@ struct Request {
 
 // A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
 struct Segment {
+  Request q;
   int r, head, row_tile;
-  int begin, end;          // tiles of the request, from tile0 on
+  int begin, end;          // tiles of the request, from q.tile0 on
   int length;              // in the units that the work is dealt in: kItemTiles for the item, then its tiles
   bool first, whole;       // the item starts here; and ends here too
   long long item;          // the item's first unit among all
+
+  __device__ __forceinline__ void cut(long long x, long long stop, int from) {
+    const int units = q.tiles + kItemTiles;
+    const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
+    item = x - from;
+    length = to - from;
+    whole = length == units;
+    first = from == 0;
+    begin = max(0, from - kItemTiles);
+    end = max(0, to - kItemTiles);
+  }
+
+  // The segment at unit x of a run that ends at `stop`.
   __device__ void find(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
     int lo = 0, hi = a.b.requests;
     while (hi - lo > 1) {
@@ -212,19 +228,26 @@ struct Segment {
       else hi = mid;
     }
     r = lo;
-    const Request q(a, shift, r, rows);
+    q = Request(a, shift, r, rows);
     const int units = q.tiles + kItemTiles;
     const long long local = x - prefix[lo], index = divide(local, units);
-    const int from = static_cast<int>(local - index * units);
-    const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
-    item = x - from;
-    length = to - from;
-    whole = length == units;
-    first = from == 0;
-    begin = max(0, from - kItemTiles);
-    end = max(0, to - kItemTiles);
     row_tile = static_cast<int>(divide(index, a.c.kv_heads));
     head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
+    cut(x, stop, static_cast<int>(local - index * units));
+  }
+
+  // The one after it, at unit x < stop: an item's start.
+  __device__ __forceinline__ void next(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
+    if (++head == a.c.kv_heads) {
+      head = 0;
+      if (++row_tile == q.row_tiles) {
+        row_tile = 0;
+        do ++r;
+        while (prefix[r + 1] == x);  // requests without rows
+        q = Request(a, shift, r, rows);
+      }
+    }
+    cut(x, stop, 0);
   }
 };
 
@@ -260,6 +283,37 @@ __device__ __forceinline__ bool compute_any(bool mine) {
       : "r"(static_cast<uint32_t>(mine))
       : "memory");
   return any != 0;
+}
+
+// Sums of each row's values over the warp into red[row][warp]: lanes trade halves of their rows until one (three) is
+// left, so 8 rows take 9 exchanges, not 40.
+template <int kRows>
+__device__ __forceinline__ void row_sums(float (&v)[kRows], float* red, int lane, int warp) {
+  int row = 0, d = 16;
+  constexpr int kLeft = kRows == 24 ? 3 : 1;
+#pragma unroll
+  for (int n = kRows / 2; n >= kLeft; n /= 2, d /= 2) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float give = upper ? v[j] : v[j + n], mine = upper ? v[j + n] : v[j];
+      v[j] = mine + __shfl_xor_sync(kAll, give, d);
+    }
+    row += upper ? n : 0;
+    if (n == kLeft) {
+      d /= 2;
+      break;
+    }
+  }
+#pragma unroll
+  for (; d >= 1; d /= 2)
+#pragma unroll
+    for (int j = 0; j < kLeft; ++j) v[j] += __shfl_xor_sync(kAll, v[j], d);
+  constexpr int kSame = kRows == 8 ? 4 : kRows == 16 ? 2 : kRows == 24 ? 4 : 1;  // lanes that hold the same rows
+  if (lane % kSame == 0) {
+#pragma unroll
+    for (int j = 0; j < kLeft; ++j) red[(row + j) * 4 + warp] = v[j];
+  }
 }
 
 template <int D, int RT>
@@ -327,8 +381,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     __syncthreads();
   }
   const long long total = prefix[a.b.requests];
-  // Each CTA gets at least an item's start and a tile.
-  constexpr int kLeast = kItemTiles + 1;
+  constexpr int kLeast = 2;
   const long long ctas = min(static_cast<long long>(gridDim.x), (total + kLeast - 1) / kLeast);
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
@@ -347,11 +400,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
     int k = 0;
     bool alive = true;
-    for (long long x = start; x < stop && alive;) {
-      Segment s;
-      s.find(a, prefix, shift, X::kRows, x, stop);
-      x += s.length;
-      const Request q(a, shift, s.r, X::kRows);
+    Segment s;
+    s.find(a, prefix, shift, X::kRows, start, stop);
+    for (long long x = start; alive;) {
+      const Request& q = s.q;
       int page = -1;
       uint32_t entry = 0, top = 0;
       bool fresh = false;  // a batch whose scales are not read yet
@@ -400,6 +452,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           else mbar_arrive(full + stage);
         }
       }
+      x += s.length;
+      if (x >= stop) break;
+      s.next(a, prefix, shift, X::kRows, x, stop);
     }
     // The copies in flight land before the CTA ends (at once, unless another role gave up).
     for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
@@ -427,15 +482,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       }
       __syncwarp();
     };
-    for (long long x = start; x < stop && alive;) {
-      Segment s;
-      s.find(a, prefix, shift, X::kRows, x, stop);
-      x += s.length;
-      if (s.begin == s.end) continue;
-      alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
-      if (alive) scores(k);
+    Segment s;
+    s.find(a, prefix, shift, X::kRows, start, stop);
+    for (long long x = start; alive;) {
+      if (s.begin < s.end) {
+        alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
+        if (alive) scores(k);
+      }
       for (int tile = s.begin; tile < s.end && alive; ++tile, ++k) {
-        if (tile + 1 < s.end) scores(k + 1);
+        // The next tile's scores ahead of this one's output, unless its keys are still on their way.
+        const bool more = tile + 1 < s.end;
+        const bool early = more && __all_sync(kAll, mbar_test(full + (k + 1) % X::kStages, ((k + 1) / X::kStages) & 1));
+        if (early) scores(k + 1);
         alive = alive && __all_sync(kAll, wait(p_ready, k & 1, status));
         if (!alive) break;
         tc_fence_after_sync();
@@ -451,7 +509,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           tc_commit(o_full);
         }
         __syncwarp();
+        if (more && !early) scores(k + 1);
       }
+      x += s.length;
+      if (x >= stop) break;
+      s.next(a, prefix, shift, X::kRows, x, stop);
     }
     if (lane == 0) {
       tc_commit(drained);
@@ -467,11 +529,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21), lanes_o = tmem_o + (static_cast<uint32_t>(warp) << 21);
     int k = 0;
     bool failed = false;  // a wait of this thread's ran out; agreed on at the barriers
-    for (long long x = start; x < stop;) {
-      Segment s;
-      s.find(a, prefix, shift, X::kRows, x, stop);
-      x += s.length;
-      const Request rq(a, shift, s.r, X::kRows);
+    Segment s;
+    s.find(a, prefix, shift, X::kRows, start, stop);
+    for (long long x = start;;) {
+      const Request rq = s.q;
       const int row0 = s.row_tile * X::kRows;
       const int rows = min(X::kRows, static_cast<int>(min(static_cast<long long>(rq.n) * a.group - row0, 1ll << 30)));
       float acc[X::kHalves][X::kRows], l[X::kRows], m = -INFINITY;  // m: of row `lane`
@@ -555,7 +616,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       };
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
         const int stage = k % X::kStages;
-        failed |= !wait(full + stage, (k / X::kStages) & 1, status);
+        failed |= !wait(s_full + (k & 1), (k >> 1) & 1, status);
+        failed |= !wait(full + stage, (k / X::kStages) & 1, status);  // complete before the scores: for what it makes visible
+        __syncwarp();
+        tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const uint32_t entry = mt[tid >> shift];
         const int base = (rq.tile0 + tile) * kTile, token = base + tid;
@@ -563,9 +627,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         bool edge = base < all_lo || base + kTile - 1 > all_hi;
         edge = __any_sync(kAll, edge || !(entry >> 16));
         const float ks = scale_of(entry & 0xFFu);
-        failed |= !wait(s_full + (k & 1), (k >> 1) & 1, status);
-        __syncwarp();
-        tc_fence_after_sync();
         float sc[X::kRows];
 #pragma unroll
         for (int part = 0; part < X::kRows; part += 8) {
@@ -690,13 +751,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       // The segment's sums over the tokens, and its rows.
       failed = compute_any(failed);
       if (failed) break;
-#pragma unroll
-      for (int i = 0; i < X::kRows; ++i) {
-        float v = l[i];
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-        if (lane == i) red[i * 4 + warp] = v;
-      }
+      row_sums<X::kRows>(l, red, lane, warp);
       compute_sync();
       float sum = 0.0f;  // of row `lane`
       if (lane < X::kRows) {
@@ -746,61 +801,108 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         // The CTAs of this item: c0 .. c1, by the bounds of their runs.
         const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
         const int c1 = static_cast<int>(divide((s.item + rq.tiles + kItemTiles) * ctas - 1, total));
-        compute_sync();
-        if (tid == 0) {
-          // Releases the CTA's stores (ordered before it by the barrier), acquires the other pieces'.
-          const uint32_t before = atom_add_acq_rel_gpu(counters + c0, 1);
-          s_last = before == static_cast<uint32_t>(c1 - c0);
-          if (s_last) counters[c0] = 0;
-        }
-        compute_sync();
-        if (s_last) {
-          // Maxima and sums over the pieces, a row to a warp at a time; then the rows, the pieces' loads in flight together.
-          const float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * X::kPartialFloats;  // the first piece
-          const float* piece0 = partials + static_cast<int64_t>(c0 * 2) * X::kPartialFloats;      // piece i: 2 i slots on
-          auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * X::kPartialFloats; };
-          const int pieces = c1 - c0 + 1;
-          for (int i = warp; i < X::kRows; i += 4) {
-            float top = -INFINITY, total_l = 0.0f;
-            for (int c = lane; c < pieces; c += 32) top = fmaxf(top, __ldcg(piece(c) + X::kRows * D + i));
-            top = warp_max(top);
-            const float ref = top > -INFINITY ? top : 0.0f;
-            for (int c = lane; c < pieces; c += 32)
-              total_l += __ldcg(piece(c) + X::kRows * D + X::kRows + i) * exp2_fast(__ldcg(piece(c) + X::kRows * D + i) - ref);
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) total_l += __shfl_xor_sync(kAll, total_l, d);
-            if (lane == 0) {
-              red[i * 4] = ref;
-              red[i * 4 + 1] = total_l == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l);
-              red[i * 4 + 2] = total_l == 0.0f ? -INFINITY : (top + log2f(total_l)) * kLn2;
-            }
+        // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
+        // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces.
+        float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * X::kPartialFloats;  // the first piece
+        float* piece0 = partials + static_cast<int64_t>(c0 * 2) * X::kPartialFloats;      // piece i: 2 i slots on
+        auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * X::kPartialFloats; };
+        const int pieces = c1 - c0 + 1;
+        int width = 8;
+        while (width * width < pieces) ++width;
+        int from = (static_cast<int>(blockIdx.x) - c0) / width * width, stride = 1, count = min(width, pieces - from);
+        uint32_t* counter = from == 0 ? counters + c0 : counters + kMaxCtas + c0 + from;
+        for (;;) {
+          compute_sync();
+          if (tid == 0) {
+            // Releases the CTA's stores (ordered before it by the barrier), acquires the other pieces'.
+            const uint32_t before = atom_add_acq_rel_gpu(counter, 1);
+            s_last = before == static_cast<uint32_t>(count - 1);
+            if (s_last) *counter = 0;
           }
           compute_sync();
-          constexpr int kQuads = D / 4;
-          for (int u = tid; u < X::kRows * kQuads; u += kCompute) {
-            const int i = u / kQuads, c4 = (u % kQuads) * 4;
-            if (i >= rows) break;
-            const float ref = red[i * 4];
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = 0; c < pieces; ++c) {
-              const float* from = piece(c);
-              const float f = exp2_fast(__ldcg(from + X::kRows * D + i) - ref);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + i * D + c4));
-              o.x = fmaf(v.x, f, o.x);
-              o.y = fmaf(v.y, f, o.y);
-              o.z = fmaf(v.z, f, o.z);
-              o.w = fmaf(v.w, f, o.w);
+          if (!s_last) break;
+          // A thread joins four dimensions of some rows, several pieces' loads in flight together.
+          constexpr int kQuads = D / 4, kUnits = X::kRows * kQuads / kCompute, kBatch = kUnits >= 4 ? 2 : 8 / kUnits;
+          float4 o[kUnits];
+          float top[kUnits], total_l[kUnits];
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            top[u] = -INFINITY;
+            total_l[u] = 0.0f;
+          }
+          for (int c = 0; c < count; c += kBatch) {
+            float pm[kBatch][kUnits], pl[kBatch][kUnits];
+            float4 pv[kBatch][kUnits];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+              const bool in = c + e < count;
+              const float* src = piece(from + (in ? c + e : c) * stride);
+#pragma unroll
+              for (int u = 0; u < kUnits; ++u) {
+                const int i = (u * kCompute + tid) / kQuads, c4 = (u * kCompute + tid) % kQuads * 4;
+                pm[e][u] = __ldcg(src + X::kRows * D + i);
+                pl[e][u] = __ldcg(src + X::kRows * D + X::kRows + i);
+                pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + i * D + c4));
+                if (!in) pm[e][u] = -INFINITY;
+              }
             }
-            const float inv = red[i * 4 + 1];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+              float mn = top[u];
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) mn = fmaxf(mn, pm[e][u]);
+              const float ref = mn > -INFINITY ? mn : 0.0f, f = exp2_fast(top[u] - ref);
+              total_l[u] *= f;
+              o[u].x *= f;
+              o[u].y *= f;
+              o[u].z *= f;
+              o[u].w *= f;
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                if (e > 0 && c + e >= count) continue;
+                const float g = exp2_fast(pm[e][u] - ref);
+                total_l[u] = fmaf(pl[e][u], g, total_l[u]);
+                o[u].x = fmaf(pv[e][u].x, g, o[u].x);
+                o[u].y = fmaf(pv[e][u].y, g, o[u].y);
+                o[u].z = fmaf(pv[e][u].z, g, o[u].z);
+                o[u].w = fmaf(pv[e][u].w, g, o[u].w);
+              }
+              top[u] = mn;
+            }
+          }
+          const bool last = stride > 1 || count == pieces;
+          if (!last) compute_sync();  // the first piece of the run has been read everywhere: the run's result takes its place
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            const int i = (u * kCompute + tid) / kQuads, c4 = (u * kCompute + tid) % kQuads * 4;
+            if (!last) {
+              float* dst = piece(from);
+              *reinterpret_cast<float4*>(dst + i * D + c4) = o[u];
+              if (c4 == 0) {
+                dst[X::kRows * D + i] = top[u];
+                dst[X::kRows * D + X::kRows + i] = total_l[u];
+              }
+              continue;
+            }
+            if (i >= rows) continue;
+            const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
             const int at = row0 + i, tok = at / a.group;
             const int64_t dst = static_cast<int64_t>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
-            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv), __floats2bfloat162_rn(o[u].z * inv, o[u].w * inv)};
             *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
-            if (a.lse != nullptr && c4 == 0) a.lse[dst] = red[i * 4 + 2];
+            if (a.lse != nullptr && c4 == 0) a.lse[dst] = total_l[u] == 0.0f ? -INFINITY : (top[u] + log2f(total_l[u])) * kLn2;
           }
+          if (last) break;
+          from = 0;
+          stride = width;
+          count = (pieces + width - 1) / width;
+          counter = counters + 2 * kMaxCtas + c0;
         }
       }
+      x += s.length;
+      if (x >= stop) break;
+      s.next(a, prefix, shift, X::kRows, x, stop);
       compute_sync();  // red, the rows' limits and the join word are free again
     }
   }
