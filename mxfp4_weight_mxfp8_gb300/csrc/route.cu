@@ -15,7 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kRouteWarps = 4;
-constexpr int kRouteCtas = 152 * 6;
+constexpr int kRouteSms = 152;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 // Ordered forms: a larger key is a larger integer. Absent elements (past the
 // last expert, or taken already) are 0, below the masked ones.
@@ -23,7 +23,7 @@ constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // -inf
 
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __float_as_uint(f + 0.0f);  // -0 and +0 are equal keys
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float unordered(uint32_t o) {
@@ -60,11 +60,6 @@ __device__ __forceinline__ float tree_sum(float (&v)[N]) {
   return s;
 }
 
-// Order of two candidates: the larger key, then the lower index.
-__device__ __forceinline__ bool ahead(uint32_t k0, int e0, uint32_t k1, int e1) {
-  return k0 > k1 || (k0 == k1 && e0 < e1);
-}
-
 // The k-th largest of the 32 lanes' values (1 <= k <= 32), by a bitonic sort.
 __device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int lane) {
 #pragma unroll
@@ -78,75 +73,87 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int lane) {
   return __shfl_sync(kAll, v, k - 1);
 }
 
+// 1 / (1 + exp(-x)); the reciprocal is the division's value, correctly rounded.
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
 template <typename T, int N>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const moe_route_t a) {
-  __shared__ __align__(16) uint32_t s_keys[kRouteWarps][32 * N];  // a warp's keys, then its candidates' scores
+__global__ void __launch_bounds__(32 * kRouteWarps, N <= 12 ? 6 : N <= 16 ? 4 : 3) route_kernel(const moe_route_t a) {
+  // A warp's keys by expert (groups), then its candidates (key, expert) as they come and in order.
+  constexpr int kOrdered = 72, kKeys = 32 * N > kOrdered + 64 ? 32 * N : kOrdered + 64;
+  __shared__ __align__(16) uint32_t s_keys[kRouteWarps][kKeys];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.experts;
   uint32_t* keys = s_keys[warp];
+  const bool sigmoids = a.scoring == MOE_SCORE_SIGMOID;
   const bool by_sum = a.groups > 1 && a.group_score == 2;
+  const bool scored = a.bias != nullptr || by_sum;  // the keys need every score; else the logits order them
   float bias[N];
-  if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) bias[i] = lane + 32 * i < E ? __ldg(a.bias + lane + 32 * i) : 0.0f;
+  for (int i = 0; i < N; ++i) {
+    bias[i] = a.bias != nullptr && lane + 32 * i < E ? __ldg(a.bias + lane + 32 * i) : 0.0f;
+    if (bias[i] != bias[i]) bias[i] = -INFINITY;  // a NaN key counts as masked
   }
+  // A group to a run of lanes.
+  const int size = E / a.groups;
+  const int each = a.groups <= 2 ? 16 : a.groups <= 4 ? 8 : a.groups <= 8 ? 4 : a.groups <= 16 ? 2 : 1;
+  const int group = lane / each;
 
   for (int t = blockIdx.x * kRouteWarps + warp; t < a.tokens; t += gridDim.x * kRouteWarps) {
     const T* row = static_cast<const T*>(a.logits) + t * a.row_stride;
-    float x[N], score[N];
-    uint32_t masked = 0;
+    float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = lane + 32 * i;
       x[i] = e < E ? load_logit<T>(row + e) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!(x[i] > -INFINITY)) masked |= 1u << i;  // -inf or NaN
-    if (a.scoring == MOE_SCORE_SIGMOID) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) score[i] = __fdiv_rn(1.0f, 1.0f + expf(-x[i]));
-    } else {
-      float top = -INFINITY;
+    for (int i = 0; i < N; ++i) x[i] = fmaxf(x[i], -INFINITY);  // NaN: masked
+    // A logit's score is exp(x - top) / sum, or its sigmoid.
+    float top = 0.0f, sum = 1.0f;
+    uint32_t key[N];
+    if (!sigmoids) {
+      top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         x[i] = fminf(x[i], 3.402823466e38f);
-        if (!(masked >> i & 1)) top = fmaxf(top, x[i]);
+        top = fmaxf(top, x[i]);
       }
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+      if (top == -INFINITY) top = 0.0f;
+      float score[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) score[i] = expf(x[i] - top);
       float part[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        score[i] = (masked >> i & 1) ? 0.0f : expf(x[i] - top);
-        part[i] = score[i];
+      for (int i = 0; i < N; ++i) part[i] = score[i];
+      sum = tree_sum<N>(part);
+      if (scored) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = ordered(x[i] > -INFINITY ? __fdiv_rn(score[i], sum) + bias[i] : -INFINITY);
       }
-      const float sum = tree_sum<N>(part);
+    } else if (scored) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) score[i] = __fdiv_rn(score[i], sum);
+      for (int i = 0; i < N; ++i) key[i] = ordered(x[i] > -INFINITY ? sigmoid(x[i]) + bias[i] : -INFINITY);
     }
-
-    uint32_t key[N];
+    if (!scored) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float f = x[i];
-      if (a.bias != nullptr) f = score[i] + bias[i];
-      else if (by_sum) f = score[i];
-      key[i] = (masked >> i & 1) || f != f ? kMaskedKey : ordered(f);
-      if (lane + 32 * i >= E) key[i] = 0;
+      for (int i = 0; i < N; ++i) key[i] = ordered(x[i]);
+    }
+    if (E < 32 * N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (lane + 32 * i >= E) key[i] = 0;
     }
 
     if (a.groups > 1) {
-      // A group to a run of lanes: its two largest keys, from shared memory.
-      const int size = E / a.groups;
-      const int each = a.groups <= 1 ? 32 : a.groups <= 2 ? 16 : a.groups <= 4 ? 8 : a.groups <= 8 ? 4 : a.groups <= 16 ? 2 : 1;
-      const int group = lane / each;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < N; ++i) keys[lane + 32 * i] = key[i];
       __syncwarp();
-      uint32_t b1 = 0, b2 = 0;
+      uint32_t b1 = 0, b2 = 0;  // the group's two largest
       if (group < a.groups) {
+#pragma unroll 4
         for (int j = lane % each; j < size; j += each) {
           const uint32_t v = keys[group * size + j];
           b2 = max(b2, min(b1, v));
@@ -165,12 +172,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const moe_route
         const uint32_t other = __shfl_sync(kAll, mine, g * each);
         before += other > mine || (other == mine && g < group);
       }
-      const uint32_t kept = __ballot_sync(kAll, group < a.groups && before < a.group_topk);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E && !(kept >> (e / size * each) & 1)) key[i] = kMaskedKey;
+      if (group < a.groups && before >= a.group_topk) {
+#pragma unroll 4
+        for (int j = lane % each; j < size; j += each) keys[group * size + j] = kMaskedKey;
       }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = keys[lane + 32 * i];
     }
 
     // Candidates: the keys from the topk-th largest of the lanes' maxima on. At least topk keys are that large, and
@@ -191,41 +199,35 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const moe_route
     const int count = __shfl_sync(kAll, at, 31);
     at -= mine;
     int id = 0;
-    float w = 0.0f;
+    uint32_t won = kMaskedKey;
+    __syncwarp();
     if (count <= 32) {
-      // One to a lane, sorted.
-      float* scores = reinterpret_cast<float*>(keys) + 64;
-      __syncwarp();
+      // One to a lane; its place is the number of those ahead of it: the larger key, then the lower index.
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (key[i] >= cut) {
-          keys[at] = key[i];
-          keys[32 + at] = lane + 32 * i;
-          scores[at] = score[i];
+          *reinterpret_cast<uint2*>(keys + 2 * at) = make_uint2(key[i], lane + 32 * i);
           ++at;
         }
       __syncwarp();
-      uint32_t k = lane < count ? keys[lane] : 0;
-      int e = lane < count ? static_cast<int>(keys[32 + lane]) : 0x7FFFFFFF;
-      int from = lane;  // where its score lies
-#pragma unroll
-      for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-        for (int d = size / 2; d >= 1; d /= 2) {
-          const uint32_t ok = __shfl_xor_sync(kAll, k, d);
-          const uint32_t oe = __shfl_xor_sync(kAll, static_cast<uint32_t>(e) | static_cast<uint32_t>(from) << 16, d);
-          const int other = static_cast<int>(oe & 0xFFFFu);
-          const bool descending = !(lane & size) || size == 32, lower = !(lane & d);
-          const bool first = ahead(k, e & 0xFFFF, ok, other);
-          if ((descending == lower) != first) {
-            k = ok;
-            e = other;
-            from = static_cast<int>(oe >> 16);
-          }
-        }
+      const uint2 own = *reinterpret_cast<const uint2*>(keys + 2 * lane);
+      if (lane < 4) *reinterpret_cast<uint2*>(keys + 2 * (count + lane)) = make_uint2(0, 0);  // the last four read together
+      __syncwarp();
+      int place = 0;
+      for (int j = 0; j < count; j += 4) {
+        const uint4 o0 = *reinterpret_cast<const uint4*>(keys + 2 * j), o1 = *reinterpret_cast<const uint4*>(keys + 2 * j + 4);
+        place += o0.x > own.x || (o0.x == own.x && o0.y < own.y);
+        place += o0.z > own.x || (o0.z == own.x && o0.w < own.y);
+        place += o1.x > own.x || (o1.x == own.x && o1.y < own.y);
+        place += o1.z > own.x || (o1.z == own.x && o1.w < own.y);
+      }
+      __syncwarp();
+      if (lane < count) *reinterpret_cast<uint2*>(keys + kOrdered + 2 * place) = own;
+      __syncwarp();
+      const uint2 mine2 = *reinterpret_cast<const uint2*>(keys + kOrdered + 2 * lane);
       if (lane < a.topk) {
-        id = e & 0xFFFF;
-        w = k == kMaskedKey ? 0.0f : scores[from];
+        won = mine2.x;
+        id = static_cast<int>(mine2.y);
       }
     } else {
       // Too many equal keys or too large a topk: one by one, a warp maximum, then the lowest index that has it.
@@ -233,31 +235,33 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const moe_route
         best = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) best = max(best, key[i]);
-        const uint32_t top = __reduce_max_sync(kAll, best);
+        const uint32_t largest = __reduce_max_sync(kAll, best);
         int own = 0x7FFFFFFF;
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
-          if (key[i] == top) own = lane + 32 * i;
+          if (key[i] == largest) own = lane + 32 * i;
         const int e = __reduce_min_sync(kAll, own);
-        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (e == lane + 32 * i) {
-            key[i] = 0;
-            s = score[i];
-          }
-        s = __shfl_sync(kAll, s, e & 31);
+          if (e == lane + 32 * i) key[i] = 0;
         if (lane == k) {
           id = e;
-          w = top == kMaskedKey ? 0.0f : s;
+          won = largest;
         }
       }
     }
+    // The winners' scores again, from their logits.
+    float w = 0.0f;
+    if (lane < a.topk && won != kMaskedKey) {
+      float v = load_logit<T>(row + id);
+      if (sigmoids) w = sigmoid(v);
+      else w = __fdiv_rn(expf(fminf(v, 3.402823466e38f) - top), sum);
+    }
     if (a.renormalize) {
-      float sum = w;
+      float all = w;
 #pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-      w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+      for (int d = 16; d >= 1; d >>= 1) all += __shfl_xor_sync(kAll, all, d);
+      w = all > 0.0f ? __fdiv_rn(w, all) : 0.0f;
     }
     if (lane < a.topk) {
       a.ids[static_cast<int64_t>(t) * a.topk + lane] = id;
@@ -266,22 +270,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const moe_route
   }
 }
 
+template <typename T, int N>
+cudaError_t launch_size(const moe_route_t& a, cudaStream_t stream) {
+  // Warps that stay over their tokens, so the bias is read once; no more than are resident together.
+  const int ctas = (a.tokens + kRouteWarps - 1) / kRouteWarps, resident = kRouteSms * (N <= 12 ? 6 : N <= 16 ? 4 : 3);
+  route_kernel<T, N><<<ctas < resident ? ctas : resident, 32 * kRouteWarps, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_type(const moe_route_t& a, cudaStream_t stream) {
-  // Warps that stay over their tokens, so the bias is read once; more than the SMs hold at a time, to even out the end.
-  const int ctas = (a.tokens + kRouteWarps - 1) / kRouteWarps, grid = ctas < kRouteCtas ? ctas : kRouteCtas;
-  const int block = 32 * kRouteWarps;
-  if (a.experts <= 128)
-    route_kernel<T, 4><<<grid, block, 0, stream>>>(a);
-  else if (a.experts <= 256)
-    route_kernel<T, 8><<<grid, block, 0, stream>>>(a);
-  else if (a.experts <= 384)
-    route_kernel<T, 12><<<grid, block, 0, stream>>>(a);
-  else if (a.experts <= 512)
-    route_kernel<T, 16><<<grid, block, 0, stream>>>(a);
-  else
-    route_kernel<T, 32><<<grid, block, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.experts <= 128) return launch_size<T, 4>(a, stream);
+  if (a.experts <= 256) return launch_size<T, 8>(a, stream);
+  if (a.experts <= 384) return launch_size<T, 12>(a, stream);
+  if (a.experts <= 512) return launch_size<T, 16>(a, stream);
+  return launch_size<T, 32>(a, stream);
 }
 
 }  // namespace
