@@ -2,9 +2,10 @@
 // include/moe.h).
 //
 // The tokens of one page follow one another in `slots`; the first of them (its
-// row is 0, or the slot before is not its predecessor) stands for the page and
-// its warps take the whole run: one pass for max|x|, the page's scale (grown
-// if need be, with the earlier codes rounded again), one pass that encodes.
+// row is 0, or the slot before is not its predecessor) stands for the page, and
+// a warp for each head's keys and values takes the whole run: one pass for
+// max|x|, the page's scale (grown if need be, with the earlier codes rounded
+// again), one pass that encodes.
 // Scales are powers of two, so growing one loses only what the smaller codes'
 // last places hold.
 #include "kernels.h"
@@ -12,7 +13,8 @@
 namespace moe {
 namespace {
 
-constexpr int kAppendWarps = 4;
+constexpr int kAppendWarps = 8;
+constexpr int kAppendCtas = 152 * 8;  // as many as are resident together, about
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {
@@ -38,65 +40,106 @@ __device__ __forceinline__ uint32_t rescale2(uint32_t codes, float shift) {
   return (moved & ~nan) | (codes & nan);
 }
 
+// Largest finite magnitude of a lane's share of `run` rows, kUnroll loads in flight.
 template <int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendArgs a, int shift) {
-  constexpr int kChunks = D / 8;  // 8 values: 16 bytes of BF16, 8 of codes
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x, P = a.c.page_tokens;
-  const int64_t slot = a.slots[t], limit = static_cast<int64_t>(a.c.pages) << shift;
-  if (slot < 0 || slot >= limit) return;
-  const int first = static_cast<int>(slot & (P - 1));
-  if (first != 0 && t > 0 && a.slots[t - 1] == slot - 1) return;
-  int run = 0;  // rows of this page, this one included
-  for (int base = 0; base < P - first; base += 32) {
-    const int i = base + lane;
-    const bool in = i < P - first && t + i < a.tokens && a.slots[t + i] == slot + i;
-    const uint32_t votes = __ballot_sync(kAll, in);
-    const int n = votes == kAll ? 32 : __ffs(~votes) - 1;
-    run += n;
-    if (n < 32) break;
-  }
-  const int64_t page = slot >> shift;
-  for (int item = warp; item < 2 * a.c.kv_heads; item += kAppendWarps) {
-    const int which = item & 1, head = item >> 1;
-    const uint16_t* x = a.x[which] + t * a.token_stride[which] + head * a.head_stride[which];
-    uint8_t* scales = which ? a.c.v_scale : a.c.k_scale;
-    uint8_t* codes = (which ? a.c.v : a.c.k) + ((page * a.c.kv_heads + head) << shift) * D;
-    float amax = 0.0f;
-    for (int i = lane; i < run * kChunks; i += 32) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x + (i / kChunks) * a.token_stride[which] + (i % kChunks) * 8);
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float rows_amax(const uint16_t* x, int64_t stride, int run, int lane) {
+  constexpr int kChunks = D / 8, kUnroll = 8;  // a chunk: 8 values, 16 bytes
+  float amax = 0.0f;
+  for (int base = lane; base < run * kChunks; base += 32 * kUnroll) {
+    uint4 w[kUnroll];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(finite_abs(words[j]), finite_abs(words[j] >> 16)));
+    for (int j = 0; j < kUnroll; ++j) {
+      const int i = base + 32 * j;
+      w[j] = i < run * kChunks ? *reinterpret_cast<const uint4*>(x + (i / kChunks) * stride + (i % kChunks) * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
-    int E = mx_exponent(amax, false);
+    for (int j = 0; j < kUnroll; ++j) {
+      const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) amax = fmaxf(amax, fmaxf(finite_abs(words[q]), finite_abs(words[q] >> 16)));
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
+  return amax;
+}
+
+// A warp for each (keys or values, head); a CTA's warps go over the pages that start in its window of tokens.
+template <int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendArgs a, int shift, int window) {
+  constexpr int kChunks = D / 8, kUnroll = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = a.c.page_tokens, item = blockIdx.y * kAppendWarps + warp;
+  if (item >= 2 * a.c.kv_heads) return;
+  const int which = item & 1, head = item >> 1, w0 = blockIdx.x * window;
+  const int64_t limit = static_cast<int64_t>(a.c.pages) << shift, stride = a.token_stride[which];
+  uint8_t* scales = which ? a.c.v_scale : a.c.k_scale;
+
+  bool leads = false;  // the lane's token of the window is the first of its page
+  if (lane < window && w0 + lane < a.tokens) {
+    const int64_t slot = a.slots[w0 + lane], before = w0 + lane > 0 ? a.slots[w0 + lane - 1] : -1;
+    leads = slot >= 0 && slot < limit && ((slot & (P - 1)) == 0 || before != slot - 1);
+  }
+  for (uint32_t leaders = __ballot_sync(kAll, leads); leaders; leaders &= leaders - 1) {
+    const int t = w0 + __ffs(leaders) - 1;
+    const int64_t slot = a.slots[t], page = slot >> shift;
+    const int first = static_cast<int>(slot & (P - 1));
     uint8_t* scale = scales + page * a.c.kv_heads + head;
-    if (first != 0) {
-      const int old = static_cast<int>(*scale) - 127;
-      if (old >= E) {
-        E = old;
-      } else {
-        const float down = pow2f(max(old - E, -126));
-        for (int i = lane; i < first * (D / 4); i += 32) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
-          const uint32_t c = *p;
-          *p = rescale2(c & 0xFFFFu, down) | rescale2(c >> 16, down) << 16;
-        }
+    const int old = first != 0 ? static_cast<int>(*scale) - 127 : -128;
+    int run = 0;  // rows of this page, this one included
+    for (int base = 0; base < P - first; base += 32) {
+      const int i = base + lane;
+      const bool in = i < P - first && t + i < a.tokens && a.slots[t + i] == slot + i;
+      const uint32_t votes = __ballot_sync(kAll, in);
+      const int n = votes == kAll ? 32 : __ffs(~votes) - 1;
+      run += n;
+      if (n < 32) break;
+    }
+    const uint16_t* x = a.x[which] + t * stride + head * a.head_stride[which];
+    uint8_t* codes = (which ? a.c.v : a.c.k) + ((page * a.c.kv_heads + head) << shift) * D;
+    int E = mx_exponent(rows_amax<D>(x, stride, run, lane), false);
+    if (old >= E) {
+      E = old;
+    } else if (first != 0) {
+      const float down = pow2f(max(old - E, -126));
+      for (int i = lane; i < first * (D / 4); i += 32) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
+        const uint32_t c = *p;
+        *p = rescale2(c & 0xFFFFu, down) | rescale2(c >> 16, down) << 16;
       }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = static_cast<uint8_t>(E + 127);
+    if (lane == 0 && E != old) *scale = static_cast<uint8_t>(E + 127);
+    // The rows again (from the caches by now), encoded.
     const float inv = pow2f(-E);
-    for (int i = lane; i < run * kChunks; i += 32) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x + (i / kChunks) * a.token_stride[which] + (i % kChunks) * 8);
-      uint2 o;
-      o.x = encode2(w.x, inv) | encode2(w.y, inv) << 16;
-      o.y = encode2(w.z, inv) | encode2(w.w, inv) << 16;
-      *reinterpret_cast<uint2*>(codes + (first + i / kChunks) * D + (i % kChunks) * 8) = o;
+    for (int base = lane; base < run * kChunks; base += 32 * kUnroll) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int i = base + 32 * j;
+        if (i < run * kChunks) w[j] = *reinterpret_cast<const uint4*>(x + (i / kChunks) * stride + (i % kChunks) * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int i = base + 32 * j;
+        uint2 o;
+        o.x = encode2(w[j].x, inv) | encode2(w[j].y, inv) << 16;
+        o.y = encode2(w[j].z, inv) | encode2(w[j].w, inv) << 16;
+        if (i < run * kChunks) *reinterpret_cast<uint2*>(codes + (first + i / kChunks) * D + (i % kChunks) * 8) = o;
+      }
     }
   }
+}
+
+template <int D>
+cudaError_t launch_dim(const AppendArgs& a, int shift, cudaStream_t stream) {
+  // Windows of one token where that already gives every SM work (a decode step), up to 32 for long prompts, whose pages
+  // start only every page_tokens tokens.
+  const int columns = (2 * a.c.kv_heads + kAppendWarps - 1) / kAppendWarps;
+  int window = 1;
+  while (window < 32 && static_cast<int64_t>(a.tokens) * columns > window * kAppendCtas) window *= 2;
+  const dim3 grid((a.tokens + window - 1) / window, columns);
+  kv_append_kernel<D><<<grid, 32 * kAppendWarps, 0, stream>>>(a, shift, window);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -104,13 +147,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   int shift = 4;
   while ((1 << shift) < a.c.page_tokens) ++shift;
-  if (a.c.head_dim == 64)
-    kv_append_kernel<64><<<a.tokens, 32 * kAppendWarps, 0, stream>>>(a, shift);
-  else if (a.c.head_dim == 128)
-    kv_append_kernel<128><<<a.tokens, 32 * kAppendWarps, 0, stream>>>(a, shift);
-  else
-    kv_append_kernel<256><<<a.tokens, 32 * kAppendWarps, 0, stream>>>(a, shift);
-  return cudaGetLastError();
+  if (a.c.head_dim == 64) return launch_dim<64>(a, shift, stream);
+  if (a.c.head_dim == 128) return launch_dim<128>(a, shift, stream);
+  return launch_dim<256>(a, shift, stream);
 }
 
 }  // namespace moe
