@@ -11,43 +11,35 @@
 namespace moe {
 namespace {
 
-constexpr int kPlanThreads = 256;
-constexpr int kPlanPerThread = MOE_KV_MAX_REQUESTS / kPlanThreads;
+// A thread to a request: kPlanThreads at least as many as the requests.
+static_assert(MOE_KV_MAX_REQUESTS <= 1024, "a CTA has a thread for every request");
 
-struct PlanSums {
-  long long tokens, pages;
-};
-
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan_t a, int shift) {
-  __shared__ long long s_start[MOE_KV_MAX_REQUESTS + 1];  // new tokens before request r
-  __shared__ long long s_pages[MOE_KV_MAX_REQUESTS];      // new pages before request r
-  __shared__ int s_context[MOE_KV_MAX_REQUESTS];
-  __shared__ long long s_warp[2][kPlanThreads / 32];
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ long long s_start[kPlanThreads + 1];  // new tokens before request r
+  __shared__ long long s_pages[kPlanThreads];      // new pages before request r
+  __shared__ int s_context[kPlanThreads];
+  __shared__ long long s_warp[2][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = a.page_tokens;
 
-  long long tok[kPlanPerThread], pag[kPlanPerThread], tsum = 0, psum = 0;
+  long long tsum = 0, psum = 0;  // of request tid
   int flags = 0, longest = 0;
-#pragma unroll
-  for (int i = 0; i < kPlanPerThread; ++i) {
-    const int r = tid * kPlanPerThread + i;
-    int c = 0, q = 0;
-    if (r < a.requests) {
-      c = a.context_lens[r];
-      q = a.query_lens[r];
-      if (c < 0 || q < 0 || static_cast<long long>(c) + q > 0x7FFFFFFF - P) {
-        flags |= 1;
-        c = q = 0;
-      }
-      s_context[r] = c;
-      longest = max(longest, c + q);
-      if (((c + q + P - 1) >> shift) > a.table_width) flags |= 4;
-      if (blockIdx.x == 0) a.seq_lens[r] = c + q;
+  const long long head = *a.free_head;
+  if (tid < a.requests) {
+    int c = a.context_lens[tid], q = a.query_lens[tid];
+    if (c < 0 || q < 0 || static_cast<long long>(c) + q > 0x7FFFFFFF - P) {
+      flags |= 1;
+      c = q = 0;
     }
-    tok[i] = tsum;
-    pag[i] = psum;
-    tsum += q;
-    psum += ((c + q + P - 1) >> shift) - ((c + P - 1) >> shift);
+    s_context[tid] = c;
+    longest = c + q;
+    const int held = (c + P - 1) >> shift, needed = (c + q + P - 1) >> shift;
+    if (needed > a.table_width) flags |= 4;
+    if (blockIdx.x == 0) a.seq_lens[tid] = c + q;
+    tsum = q;
+    psum = needed - held;
   }
   long long tin = tsum, pin = psum;  // inclusive sums over the warp
 #pragma unroll
@@ -63,39 +55,34 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan
     s_warp[1][warp] = pin;
   }
   __syncthreads();
-  long long tbase = tin - tsum, pbase = pin - psum, total = 0, pages = 0;
+  // Every warp sums the warps' totals for itself: lane w, warp w's.
+  long long tw = lane < kWarps ? s_warp[0][lane] : 0, pw = lane < kWarps ? s_warp[1][lane] : 0;
+  long long tbase = lane < warp ? tw : 0, pbase = lane < warp ? pw : 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) {
-      tbase += s_warp[0][w];
-      pbase += s_warp[1][w];
-    }
-    total += s_warp[0][w];
-    pages += s_warp[1][w];
+  for (int d = 16; d >= 1; d >>= 1) {
+    tw += __shfl_xor_sync(0xFFFFFFFFu, tw, d);
+    pw += __shfl_xor_sync(0xFFFFFFFFu, pw, d);
+    tbase += __shfl_xor_sync(0xFFFFFFFFu, tbase, d);
+    pbase += __shfl_xor_sync(0xFFFFFFFFu, pbase, d);
   }
-#pragma unroll
-  for (int i = 0; i < kPlanPerThread; ++i) {
-    const int r = tid * kPlanPerThread + i;
-    if (r < a.requests) {
-      s_start[r] = tbase + tok[i];
-      s_pages[r] = pbase + pag[i];
-      if (blockIdx.x == 0)
-        a.query_start[r] = static_cast<int>(min(tbase + tok[i], 0x7FFFFFFFll));
-    }
+  const long long total = tw, pages = pw;
+  if (tid < a.requests) {
+    s_start[tid] = tbase + tin - tsum;
+    s_pages[tid] = pbase + pin - psum;
+    if (blockIdx.x == 0) a.query_start[tid] = static_cast<int>(min(s_start[tid], 0x7FFFFFFFll));
   }
   if (tid == 0) s_start[a.requests] = total;
-  const long long head = *a.free_head;
   if (blockIdx.x == 0) {
     if (total > a.tokens) flags |= 2;
     if (head < 0 || head + pages > a.free_count) flags |= pages ? 8 : 0;
-    flags = __syncthreads_or(flags & 1) | __syncthreads_or(flags & 2) * 2 |
-            __syncthreads_or(flags & 4) * 4 | __syncthreads_or(flags & 8) * 8;
+    flags = (__syncthreads_or(flags & 1) ? 1 : 0) | (__syncthreads_or(flags & 2) ? 2 : 0) |
+            (__syncthreads_or(flags & 4) ? 4 : 0) | (__syncthreads_or(flags & 8) ? 8 : 0);
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    __shared__ int s_longest[kPlanThreads / 32];
+    __shared__ int s_longest[kWarps];
     if (lane == 0) s_longest[warp] = longest;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
+      for (int w = 1; w < kWarps; ++w) longest = max(longest, s_longest[w]);
       a.query_start[a.requests] = static_cast<int>(min(total, 0x7FFFFFFFll));
       a.counts[0] = static_cast<int>(min(total, 0x7FFFFFFFll));
       a.counts[1] = static_cast<int>(min(head + pages, 0x7FFFFFFFll));
@@ -141,9 +128,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan
 cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream) {
   int shift = 4;
   while ((1 << shift) < a.page_tokens) ++shift;
-  int grid = (a.tokens + kPlanThreads * 4 - 1) / (kPlanThreads * 4);
-  grid = grid < 1 ? 1 : (grid > 152 ? 152 : grid);
-  kv_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(a, shift);
+  // Every CTA takes the sums again, so no more of them than two to an SM.
+  const int threads = a.requests <= 256 ? 256 : 1024;
+  int grid = (a.tokens + threads - 1) / threads;
+  grid = grid < 1 ? 1 : (grid > 304 ? 304 : grid);
+  if (threads == 256) kv_plan_kernel<256><<<grid, 256, 0, stream>>>(a, shift);
+  else kv_plan_kernel<1024><<<grid, 1024, 0, stream>>>(a, shift);
   return cudaGetLastError();
 }
 
