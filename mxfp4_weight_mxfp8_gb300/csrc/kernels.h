@@ -190,10 +190,15 @@ struct AttendArgs {
   uint8_t* workspace;
 };
 
+struct AttendMaps {
+  CUtensorMap k, v;          // [pages * kv_heads][page_tokens][head_dim]; a box is a page's span of a head
+};
+
 cudaError_t launch_route(const moe_route_t& a, cudaStream_t stream);
 cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_attend_rows(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
 
 // Sets this thread's error detail (moe_last_error_detail) and returns `status`.
 int fail(int status, const char* format, ...);

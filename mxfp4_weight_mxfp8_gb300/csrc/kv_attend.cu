@@ -24,40 +24,20 @@
 // Roles: a producer warp looks up pages and streams tiles by TMA through a ring,
 // a warp issues the MMAs, four warps do the softmax (thread = token) and hold
 // the output (thread = dimension).
-#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <atomic>
 
-#include "kernels.h"
-#include "ptx.cuh"
+#include "kv_attend.cuh"
 
 namespace moe {
 namespace {
 
-using namespace ptx;
-
-constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kTile = 128;        // cache tokens of a tile
-constexpr int kCompute = 128;     // compute threads: warps 0-3
-constexpr int kProducerWarp = 4;
+constexpr int kProducerWarp = 4;  // after the compute warps 0-3
 constexpr int kIssueWarp = 5;
 constexpr int kThreads = 192;
-constexpr int kItemTiles = 2;     // what starting and joining an item costs, in tiles
-constexpr int kMaxPages = 8;      // pages of a tile
-constexpr int kMaxCtas = 512;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
 constexpr float kNear = 8.0f;        // log2 distance of a tile's maximum from the running one
-constexpr uint64_t kWaitNs = 2000000000ull;
-
-// Workspace: the status word, arrival counters (zero between calls: for the
-// runs of pieces that start with an item, for its other runs, for the item;
-// each under the CTA of the first piece), two partial results for each CTA.
-constexpr int kCounterOffset = 256;
-constexpr int kPartialOffset = MOE_KV_WORKSPACE_HEADER;
-static_assert(kCounterOffset + 3 * kMaxCtas * 4 <= kPartialOffset, "counters fit");
 
 template <int D, int RT>
 struct Shape {
@@ -87,23 +67,6 @@ struct Shape {
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand images on swizzle boundaries");
 };
 
-// ---------------------------------------------------------------- tensor core
-// D[tmem] (+)= A[smem] x B[smem], e4m3 operands, FP32 accumulation; K = 32.
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// M = 128 rows of A, N columns; A transposed (its rows contiguous) or not.
-__host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed) {
-  return (1u << 4)                                // FP32 accumulator; A and B e4m3 (0)
-         | ((a_transposed ? 1u : 0u) << 15)       // A is M-major
-         | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
-         | ((128u >> 4) << 24);                   // M / 16
-}
-
 // Eight consecutive TMEM columns of this thread's lane as floats, without the wait.
 __device__ __forceinline__ void tmem_load_8_async(uint32_t taddr, float (&r)[8]) {
   asm volatile(
@@ -119,157 +82,6 @@ __device__ __forceinline__ void tmem_wait_8(float (&r)[8]) {
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
                :
                : "memory");
-}
-
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// ------------------------------------------------------------------- numerics
-// 2^x; what underflows FP32's normal range is zero.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 2^(b - 127) of an E8M0 byte.
-__device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
-
-// Warp maximum (NaN loses).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t codes) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
-}
-
-// hi and lo e4m3 codes of two values of magnitude up to 256: v = hi + lo / 16.
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(v0, v1);
-  const float2 f = unpack2(hi);
-  lo = pack2((v0 - f.x) * 16.0f, (v1 - f.y) * 16.0f);
-}
-
-// The same in half precision, for values of which 11 bits are enough: a weight is held to fewer by its codes.
-__device__ __forceinline__ void split2_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  const __half2 v = __floats2half2_rn(v0, v1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
-  const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-  const __half2 rest = __hmul2(__hsub2(v, f), __float2half2_rn(16.0f));
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
-
-// Byte offset of 16-byte chunk c of row n in an image of kSpan-byte rows, as the swizzle of that width places it.
-template <int kSpan>
-__device__ __forceinline__ uint32_t chunk_at(int n, int c) {
-  return kSpan == 128 ? n * 128 + ((c ^ (n & 7)) << 4) : n * 64 + ((c ^ ((n >> 1) & 3)) << 4);
-}
-
-// ----------------------------------------------------------------------- work
-// a / b of numbers that mostly fit 32 bits, where the division is far shorter.
-__device__ __forceinline__ long long divide(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// A request's share of the work.
-struct Request {
-  int first, n, seq;       // first query row's token, query tokens, visible length
-  int end;                 // tokens that the table has room for
-  int tile0, tiles;        // first tile that some query sees, their number (one at least)
-  int row_tiles;
-  Request() = default;
-  __device__ Request(const AttendArgs& a, int shift, int r, int rows) {
-    first = min(max(a.b.query_start[r], 0), a.b.tokens);
-    n = min(max(a.b.query_start[r + 1], first), a.b.tokens) - first;
-    seq = a.b.seq_lens[r];
-    const long long room = static_cast<long long>(a.b.table_width) << shift;
-    end = static_cast<int>(min(static_cast<long long>(max(seq, 0)), room));
-    tile0 = a.window > 0 ? static_cast<int>(min(max(0ll, static_cast<long long>(seq) - n - a.window + 1), static_cast<long long>(end))) / kTile : 0;
-    tiles = max(1, (end + kTile - 1) / kTile - tile0);
-    row_tiles = static_cast<int>((static_cast<long long>(n) * a.group + rows - 1) / rows);
-  }
-  __device__ long long work(int heads) const { return static_cast<long long>(heads) * row_tiles * (tiles + kItemTiles); }
-};
-
-// A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
-struct Segment {
-  Request q;
-  int r, head, row_tile;
-  int begin, end;          // tiles of the request, from q.tile0 on
-  int length;              // in the units that the work is dealt in: kItemTiles for the item, then its tiles
-  bool first, whole;       // the item starts here; and ends here too
-  long long item;          // the item's first unit among all
-
-  __device__ __forceinline__ void cut(long long x, long long stop, int from) {
-    const int units = q.tiles + kItemTiles;
-    const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
-    item = x - from;
-    length = to - from;
-    whole = length == units;
-    first = from == 0;
-    begin = max(0, from - kItemTiles);
-    end = max(0, to - kItemTiles);
-  }
-
-  // The segment at unit x of a run that ends at `stop`.
-  __device__ void find(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
-    int lo = 0, hi = a.b.requests;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    r = lo;
-    q = Request(a, shift, r, rows);
-    const int units = q.tiles + kItemTiles;
-    const long long local = x - prefix[lo], index = divide(local, units);
-    row_tile = static_cast<int>(divide(index, a.c.kv_heads));
-    head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
-    cut(x, stop, static_cast<int>(local - index * units));
-  }
-
-  // The one after it, at unit x < stop: an item's start.
-  __device__ __forceinline__ void next(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
-    if (++head == a.c.kv_heads) {
-      head = 0;
-      if (++row_tile == q.row_tiles) {
-        row_tile = 0;
-        do ++r;
-        while (prefix[r + 1] == x);  // requests without rows
-        q = Request(a, shift, r, rows);
-      }
-    }
-    cut(x, stop, 0);
-  }
-};
-
-struct Maps {
-  CUtensorMap k, v;  // [pages * heads][page_tokens][head_dim]
-};
-
-// Bounded wait for a barrier's phase: false, and the error reported, when it runs out. A role that sees that issues
-// nothing more, waits (bounded again) for what it has in flight, and goes to the CTA's end.
-__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, int32_t* status) {
-  const uint64_t began = global_timer_ns();
-  while (!mbar_wait_hint(bar, parity, 20000)) {
-    if (global_timer_ns() - began > kWaitNs) {
-      report(status, MOE_ERR_DEVICE_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return mbar_test(bar, parity) || wait_more(bar, parity, status);
 }
 
 // Barrier of the compute warps; true everywhere if any thread brings true.
@@ -318,7 +130,7 @@ __device__ __forceinline__ void row_sums(float (&v)[kRows], float* red, int lane
 
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
-    kv_attend_kernel(const AttendArgs a, const __grid_constant__ Maps maps, int shift) {
+    kv_attend_kernel(const AttendArgs a, const __grid_constant__ AttendMaps maps, int shift) {
   using X = Shape<D, RT>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -336,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
   if (tid == 0) {
@@ -352,34 +163,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
-  // Prefix sums of the requests' work.
-  {
-    const int per = (a.b.requests + kThreads - 1) / kThreads;
-    long long sum = 0;
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r < a.b.requests) sum += Request(a, shift, r, X::kRows).work(a.c.kv_heads);
-    }
-    long long in = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long u = __shfl_up_sync(kAll, in, d);
-      if (lane >= d) in += u;
-    }
-    if (lane == 31) s_sum[warp] = in;
-    __syncthreads();
-    long long at = in - sum;
-    for (int w = 0; w < warp; ++w) at += s_sum[w];
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r < a.b.requests) {
-        prefix[r] = at;
-        at += Request(a, shift, r, X::kRows).work(a.c.kv_heads);
-        if (r == a.b.requests - 1) prefix[r + 1] = at;
-      }
-    }
-    __syncthreads();
-  }
+  sum_work<kThreads, X::kRows>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   constexpr int kLeast = 2;
   const long long ctas = min(static_cast<long long>(gridDim.x), (total + kLeast - 1) / kLeast);
@@ -395,69 +179,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * X::kCols;
 
   if (warp == kProducerWarp) {
-    const uint64_t policy = policy_evict_first();
-    const int per_tile = kTile >> shift, in_tile = lane & (per_tile - 1);  // pages of a tile; this lane's
-    const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
-    int k = 0;
-    bool alive = true;
-    Segment s;
-    s.find(a, prefix, shift, X::kRows, start, stop);
-    for (long long x = start; alive;) {
-      const Request& q = s.q;
-      int page = -1;
-      uint32_t entry = 0, top = 0;
-      bool fresh = false;  // a batch whose scales are not read yet
-      for (int tile = s.begin; tile < s.end; ++tile, ++k) {
-        const int batch = (tile - s.begin) & (batch_tiles - 1);
-        if (batch == 0) {
-          const long long token = static_cast<long long>(q.tile0 + tile) * kTile + (lane << shift);
-          page = -1;
-          if (token < q.end && tile + lane / per_tile < s.end) page = a.b.block_table[s.r * a.b.table_stride + (token >> shift)];
-          if (page >= a.c.pages) page = -1;
-          fresh = true;
-        }
-        const int stage = k % X::kStages;
-        if (k >= X::kStages) alive = __all_sync(kAll, wait(empty + stage, (k / X::kStages - 1) & 1, status));
-        if (!alive) break;
-        // The copies first; the barrier's phase stays open until lane 0 arrives.
-        const bool mine = lane / per_tile == batch;
-        const int boxes = __popc(__ballot_sync(kAll, mine && page >= 0));
-        if (mine && page >= 0) {
-          uint8_t* dst = sm + X::kRing + stage * X::kStageBytes + (in_tile << shift) * X::kSpan;
-#pragma unroll
-          for (int h = 0; h < X::kHalves; ++h) {
-            tma_load_3d(dst + h * (kTile * X::kSpan), &maps.k, h * X::kSpan, 0, page * a.c.kv_heads + s.head, full + stage, policy);
-            tma_load_3d(dst + X::kTileBytes + h * (kTile * X::kSpan), &maps.v, h * X::kSpan, 0, page * a.c.kv_heads + s.head,
-                        full + stage, policy);
-          }
-        }
-        if (fresh) {
-          fresh = false;
-          entry = 0;
-          if (page >= 0) {
-            const long long at = static_cast<long long>(page) * a.c.kv_heads + s.head;
-            entry = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8 | 1u << 16;
-          }
-          top = (entry >> 8) & 0xFFu;  // the tile's largest value scale
-          for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
-        }
-        uint32_t* m = meta + stage * (kMaxPages + 1);
-        if (mine) {
-          m[in_tile] = entry;
-          if (in_tile == 0) m[kMaxPages] = top;
-        }
-        __syncwarp();  // the entries are written before lane 0 arrives
-        if (lane == 0) {
-          if (boxes) mbar_arrive_expect_tx(full + stage, boxes * (2 * D << shift));
-          else mbar_arrive(full + stage);
-        }
-      }
-      x += s.length;
-      if (x >= stop) break;
-      s.next(a, prefix, shift, X::kRows, x, stop);
-    }
-    // The copies in flight land before the CTA ends (at once, unless another role gave up).
-    for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
+    produce<X, D>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
@@ -798,107 +520,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           mine[X::kRows * D + tid] = m;
           mine[X::kRows * D + X::kRows + tid] = sum;
         }
-        // The CTAs of this item: c0 .. c1, by the bounds of their runs.
-        const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
-        const int c1 = static_cast<int>(divide((s.item + rq.tiles + kItemTiles) * ctas - 1, total));
-        // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
-        // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces.
-        float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * X::kPartialFloats;  // the first piece
-        float* piece0 = partials + static_cast<int64_t>(c0 * 2) * X::kPartialFloats;      // piece i: 2 i slots on
-        auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * X::kPartialFloats; };
-        const int pieces = c1 - c0 + 1;
-        int width = 8;
-        while (width * width < pieces) ++width;
-        int from = (static_cast<int>(blockIdx.x) - c0) / width * width, stride = 1, count = min(width, pieces - from);
-        uint32_t* counter = from == 0 ? counters + c0 : counters + kMaxCtas + c0 + from;
-        for (;;) {
-          compute_sync();
-          if (tid == 0) {
-            // Releases the CTA's stores (ordered before it by the barrier), acquires the other pieces'.
-            const uint32_t before = atom_add_acq_rel_gpu(counter, 1);
-            s_last = before == static_cast<uint32_t>(count - 1);
-            if (s_last) *counter = 0;
-          }
-          compute_sync();
-          if (!s_last) break;
-          // A thread joins four dimensions of some rows, several pieces' loads in flight together.
-          constexpr int kQuads = D / 4, kUnits = X::kRows * kQuads / kCompute, kBatch = kUnits >= 4 ? 2 : 8 / kUnits;
-          float4 o[kUnits];
-          float top[kUnits], total_l[kUnits];
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            top[u] = -INFINITY;
-            total_l[u] = 0.0f;
-          }
-          for (int c = 0; c < count; c += kBatch) {
-            float pm[kBatch][kUnits], pl[kBatch][kUnits];
-            float4 pv[kBatch][kUnits];
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-              const bool in = c + e < count;
-              const float* src = piece(from + (in ? c + e : c) * stride);
-#pragma unroll
-              for (int u = 0; u < kUnits; ++u) {
-                const int i = (u * kCompute + tid) / kQuads, c4 = (u * kCompute + tid) % kQuads * 4;
-                pm[e][u] = __ldcg(src + X::kRows * D + i);
-                pl[e][u] = __ldcg(src + X::kRows * D + X::kRows + i);
-                pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + i * D + c4));
-                if (!in) pm[e][u] = -INFINITY;
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-              float mn = top[u];
-#pragma unroll
-              for (int e = 0; e < kBatch; ++e) mn = fmaxf(mn, pm[e][u]);
-              const float ref = mn > -INFINITY ? mn : 0.0f, f = exp2_fast(top[u] - ref);
-              total_l[u] *= f;
-              o[u].x *= f;
-              o[u].y *= f;
-              o[u].z *= f;
-              o[u].w *= f;
-#pragma unroll
-              for (int e = 0; e < kBatch; ++e) {
-                if (e > 0 && c + e >= count) continue;
-                const float g = exp2_fast(pm[e][u] - ref);
-                total_l[u] = fmaf(pl[e][u], g, total_l[u]);
-                o[u].x = fmaf(pv[e][u].x, g, o[u].x);
-                o[u].y = fmaf(pv[e][u].y, g, o[u].y);
-                o[u].z = fmaf(pv[e][u].z, g, o[u].z);
-                o[u].w = fmaf(pv[e][u].w, g, o[u].w);
-              }
-              top[u] = mn;
-            }
-          }
-          const bool last = stride > 1 || count == pieces;
-          if (!last) compute_sync();  // the first piece of the run has been read everywhere: the run's result takes its place
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            const int i = (u * kCompute + tid) / kQuads, c4 = (u * kCompute + tid) % kQuads * 4;
-            if (!last) {
-              float* dst = piece(from);
-              *reinterpret_cast<float4*>(dst + i * D + c4) = o[u];
-              if (c4 == 0) {
-                dst[X::kRows * D + i] = top[u];
-                dst[X::kRows * D + X::kRows + i] = total_l[u];
-              }
-              continue;
-            }
-            if (i >= rows) continue;
-            const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
-            const int at = row0 + i, tok = at / a.group;
-            const int64_t dst = static_cast<int64_t>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
-            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv), __floats2bfloat162_rn(o[u].z * inv, o[u].w * inv)};
-            *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
-            if (a.lse != nullptr && c4 == 0) a.lse[dst] = total_l[u] == 0.0f ? -INFINITY : (top[u] + log2f(total_l[u])) * kLn2;
-          }
-          if (last) break;
-          from = 0;
-          stride = width;
-          count = (pieces + width - 1) / width;
-          counter = counters + 2 * kMaxCtas + c0;
-        }
+        join_item<X::kRows, D>(a, s, rows, ctas, total, tid, &s_last);
       }
       x += s.length;
       if (x >= stop) break;
@@ -937,13 +559,10 @@ cudaError_t encode_map(CUtensorMap* map, const uint8_t* data, const moe_kv_cache
 }
 
 template <int D, int RT>
-cudaError_t launch_shape(const AttendArgs& a, const Maps& maps, int shift, cudaStream_t stream) {
-  int device = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
   const int smem = Shape<D, RT>::smem(a.b.requests);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kv_attend_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv_attend_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Shape<D, RT>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
   const int resident = sms * Shape<D, RT>::kCtasPerSm, grid = resident < kMaxCtas ? resident : kMaxCtas;
@@ -952,13 +571,15 @@ cudaError_t launch_shape(const AttendArgs& a, const Maps& maps, int shift, cudaS
 }
 
 template <int D>
-cudaError_t launch_dim(const AttendArgs& a, const Maps& maps, int shift, cudaStream_t stream) {
-  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average.
+cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
+  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average; many more than that are the 128-row
+  // form's (up to head_dim 128: a thread of it holds a row's output).
   const long long rows = static_cast<long long>(a.b.tokens) * a.group;
-  if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, stream);
-  if (rows <= 16ll * a.b.requests || D == 256) return launch_shape<D, 2>(a, maps, shift, stream);
-  if (rows <= 24ll * a.b.requests) return launch_shape<D, D == 256 ? 2 : 3>(a, maps, shift, stream);
-  return launch_shape<D, D == 256 ? 2 : 4>(a, maps, shift, stream);
+  if (D <= 128 && rows > 48ll * a.b.requests) return launch_kv_attend_rows(a, maps, shift, sms, stream);
+  if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, sms, stream);
+  if (rows <= 16ll * a.b.requests || D == 256) return launch_shape<D, 2>(a, maps, shift, sms, stream);
+  if (rows <= 24ll * a.b.requests) return launch_shape<D, D == 256 ? 2 : 3>(a, maps, shift, sms, stream);
+  return launch_shape<D, D == 256 ? 2 : 4>(a, maps, shift, sms, stream);
 }
 
 }  // namespace
@@ -966,13 +587,16 @@ cudaError_t launch_dim(const AttendArgs& a, const Maps& maps, int shift, cudaStr
 cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t stream) {
   int shift = 4;
   while ((1 << shift) < a.c.page_tokens) ++shift;
-  Maps maps;
+  AttendMaps maps;
   cudaError_t e = encode_map(&maps.k, a.c.k, a.c);
   if (e == cudaSuccess) e = encode_map(&maps.v, a.c.v, a.c);
+  int device = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return e;
-  if (a.c.head_dim == 64) return launch_dim<64>(a, maps, shift, stream);
-  if (a.c.head_dim == 128) return launch_dim<128>(a, maps, shift, stream);
-  return launch_dim<256>(a, maps, shift, stream);
+  if (a.c.head_dim == 64) return launch_dim<64>(a, maps, shift, sms, stream);
+  if (a.c.head_dim == 128) return launch_dim<128>(a, maps, shift, sms, stream);
+  return launch_dim<256>(a, maps, shift, sms, stream);
 }
 
 }  // namespace moe
