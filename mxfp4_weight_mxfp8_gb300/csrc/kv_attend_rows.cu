@@ -52,17 +52,40 @@ struct RowsShape {
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
 
-__device__ __forceinline__ void tmem_load_32(uint32_t taddr, float (&r)[32]) {
+// Sixteen consecutive TMEM columns of this thread's lane, without the wait.
+__device__ __forceinline__ void tmem_load_16_async(uint32_t taddr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
-        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
-        "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// The wait for tcgen05.ld, tied to the registers that it completes.
+__device__ __forceinline__ void tmem_wait_16(float (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+               :
+               : "memory");
+}
+
+// Runs f(column, values) over kColumns columns from `taddr`, 16 at a time, the next ones on their way meanwhile.
+template <int kColumns, class F>
+__device__ __forceinline__ void for_columns(uint32_t taddr, F&& f) {
+  float u[16], v[16];
+  tmem_load_16_async(taddr, u);
+#pragma unroll 1
+  for (int c = 0; c < kColumns; c += 32) {
+    tmem_wait_16(u);
+    tmem_load_16_async(taddr + c + 16, v);
+    f(c, u);
+    tmem_wait_16(v);
+    if (c + 32 < kColumns) tmem_load_16_async(taddr + c + 32, u);
+    f(c + 16, v);
+  }
 }
 
 // Codes of two values: e4m3 hi and e5m2 lo, v = hi + lo.
@@ -278,12 +301,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!failed) failed = !wait(o_full + group, i & 1, status);
         __syncwarp();
         tc_fence_after_sync();
+        float u[16], v[16];
+        tmem_load_16_async(lanes + 128, u);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_load_32(lanes + 128 + c, o);
+          tmem_wait_16(u);
+          tmem_load_16_async(lanes + 128 + c + 16, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(o[j], pend, acc[c + j]);
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(u[j], pend, acc[c + j]);
+          tmem_wait_16(v);
+          if (c + 32 < D) tmem_load_16_async(lanes + 128 + c + 32, u);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + 16 + j] = fmaf(v[j], pend, acc[c + 16 + j]);
         }
       };
       for (int at = k + ((k & 1) != group); at < last; at += 2, ++turn) {
@@ -299,26 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = base < all_lo || base + kTile - 1 > all_hi || !present;
         // Two passes over the scores: the row's maximum, then its weights.
         float top = -INFINITY;
+        for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
+          const uint32_t entry = mt[c >> shift];
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float v[32];
-          tmem_load_32(lanes + c, v);
-#pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            const uint32_t entry = mt[(c + h) >> shift];
-            if (edge) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int token = base + c + h + j;
-                if (token < lo || token > hi || !(entry >> 16)) v[h + j] = -INFINITY;
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int token = base + c + j;
+              if (token < lo || token > hi || !(entry >> 16)) v[j] = -INFINITY;
             }
-            float big = v[h];
-#pragma unroll
-            for (int j = 1; j < 16; ++j) big = fmaxf(big, v[h + j]);
-            if (big > -INFINITY) top = fmaxf(top, big * (factor * scale_of(entry & 0xFFu)));
           }
-        }
+          float big[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
+          const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+          if (most_here > -INFINITY) top = fmaxf(top, most_here * (factor * scale_of(entry & 0xFFu)));
+        });
         const float mn = fmaxf(m, top), safe = mn > -INFINITY ? mn : 0.0f;
         const float ref = top > -INFINITY ? top : 0.0f;
         const float keep = exp2_fast(m - safe), add = exp2_fast(top - safe);
@@ -332,47 +356,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int most = static_cast<int>(mt[kMaxPages]);
         pend = add * scale_of(most) * (1.0f / 256.0f);
         pending = true;
+        for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
+          const uint32_t entry = mt[c >> shift];
+          const float f = factor * scale_of(entry & 0xFFu);
+          // Times 256 and the page's value scale over the tile's largest, both in the exponent.
+          const int up = 8 + max(static_cast<int>((entry >> 8) & 0xFFu) - most, -100);
+          const float off = static_cast<float>(up) - ref;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float v[32];
-          tmem_load_32(lanes + c, v);
+          for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
+          if (edge) {
 #pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            const uint32_t entry = mt[(c + h) >> shift];
-            const float f = factor * scale_of(entry & 0xFFu);
-            // Times 256 and the page's value scale over the tile's largest, both in the exponent.
-            const int up = 8 + max(static_cast<int>((entry >> 8) & 0xFFu) - most, -100);
-            const float off = static_cast<float>(up) - ref;
-            float sum = 0.0f;
-            uint32_t his[4], los[4];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float p[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                p[e] = exp2_fast(fmaf(v[h + j + e], f, off));
-                if (edge) {
-                  const int token = base + c + h + j + e;
-                  if (token < lo || token > hi || !(entry >> 16)) p[e] = 0.0f;
-                }
-                sum += p[e];
-              }
-              uint32_t ph, pl;
-              split2_wide_half(p[0], p[1], ph, pl);
-              if (j % 4 == 0) {
-                his[j / 4] = ph;
-                los[j / 4] = pl;
-              } else {
-                his[j / 4] |= ph << 16;
-                los[j / 4] |= pl << 16;
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int token = base + c + j;
+              if (token < lo || token > hi || !(entry >> 16)) v[j] = 0.0f;
             }
-            l = fmaf(sum, add * pow2f(-up), l);
-            uint8_t* dst = weights + chunk_at<128>(row, (c + h) / 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(his[0], his[1], his[2], his[3]);
-            *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(los[0], los[1], los[2], los[3]);
           }
-        }
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t his[8], los[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sum[j & 3] += v[2 * j] + v[2 * j + 1];
+            split2_wide_half(v[2 * j], v[2 * j + 1], his[j], los[j]);
+          }
+          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), add * pow2f(-up), l);
+          uint8_t* dst = weights + chunk_at<128>(row, c / 16);
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(his[0] | his[1] << 16, his[2] | his[3] << 16, his[4] | his[5] << 16, his[6] | his[7] << 16);
+          *reinterpret_cast<uint4*>(dst + kRows * kTile) =
+              make_uint4(los[0] | los[1] << 16, los[2] | los[3] << 16, los[4] | los[5] << 16, los[6] | los[7] << 16);
+        });
         if (edge) {
           // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
           // taken out too, and noted for those. (Thread `row` here takes the tile's token of that number.)
