@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           }
         }
         pend_f = __any_sync(kAll, add != 1.0f);
-        pend_vs = scale_of(mt[kMaxPages]) * (1.0f / 256.0f);
+        pend_vs = scale_of(mt[kMaxPages] & 0xFFu) * (1.0f / 256.0f);
         // Weights against their reference, times 256 and the page's value scale over the tile's largest.
-        const int drop = static_cast<int>((entry >> 8) & 0xFFu) - static_cast<int>(mt[kMaxPages]);
+        const int drop = static_cast<int>((entry >> 8) & 0xFFu) - static_cast<int>(mt[kMaxPages] & 0xFFu);
         const float up = 256.0f * pow2f(max(drop, -126));
         uint8_t* prow = sm + X::kP + tid % 16;
 #pragma unroll

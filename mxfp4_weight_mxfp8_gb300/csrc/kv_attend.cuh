@@ -295,7 +295,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
       uint32_t* m = meta + stage * (kMaxPages + 1);
       if (mine) {
         m[in_tile] = entry;
-        if (in_tile == 0) m[kMaxPages] = top;
+        if (in_tile == 0) m[kMaxPages] = top | (boxes == per_tile) << 8;  // and whether every page is there
       }
       __syncwarp();  // the entries are written before lane 0 arrives
       if (lane == 0) {

@@ -7,9 +7,10 @@
 // its maximum and sum need no other thread. Queries and weights are split
 // into e4m3 hi + e5m2 lo, two products into one accumulator: hi + lo hold the
 // 8 significant bits of a BF16 query exactly down to 2^-16 of its row's largest
-// magnitude, and a weight, relative to the tile's largest of its row, within 2^-8
-// of itself (BF16's own rounding). Each tile's output joins the running one
-// in FP32 registers with the tile's own maximum and value scale.
+// magnitude, and a weight of 2^-10 of its row's reference or more within 2^-8 of
+// itself (BF16's own rounding; below that within 2^-18 of the reference). The
+// reference is a maximum of the row's scores seen so far, raised only when a
+// weight outgrows it. Each tile's output joins the running one in FP32 registers.
 //
 // Two warpgroups take a CTA's tiles in turn, one in its softmax while the
 // other's products run; their results are joined in shared memory.
@@ -21,8 +22,8 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kGroups = 2;                        // compute warpgroups: warps 0-3, 4-7
 constexpr int kProducerWarp = 4 * kGroups;
-constexpr int kIssueWarp = kProducerWarp + 1;
-constexpr int kThreads = 128 * (kGroups + 1);    // whole warpgroups: two warps of the last one idle
+constexpr int kIssueWarp = kProducerWarp + 1;       // one for each warpgroup
+constexpr int kThreads = 128 * (kGroups + 1);    // whole warpgroups: one warp of the last one idles
 // Registers a thread: 168 at launch; the last warpgroup gives of its own to the others (2 x 224 + 56 = 3 x 168).
 constexpr int kComputeRegs = 224, kIssueRegs = 56;
 
@@ -44,11 +45,13 @@ struct RowsShape {
   static constexpr int kNan = kJoinMl + kRows * 8;                   // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kPrefix = kBars + (2 * kStages + 3 * kGroups + 2) * 8;  // full, empty, s_full, o_full, p_ready, q_ready, drained
+  static constexpr int kPrefix = kBars + (2 * kStages + 4 * kGroups + 1) * 8;  // full, empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
   static_assert(kPartialOffset + 2ll * 256 * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES || D == 128, "workspace");
   static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
 };
+constexpr int kUp = 4;               // weights are held times 2^4, so one may grow to 2^4.75 times its reference's before
+constexpr float kHighest = 430.0f;   // it leaves e4m3
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
 
@@ -131,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = empty + X::kStages;   // [group]: scores of its tile in TMEM
   uint64_t* o_full = s_full + kGroups;     // [group]: its tile's output in TMEM
   uint64_t* p_ready = o_full + kGroups;    // [group]: its tile's weights in shared memory
-  uint64_t* q_ready = p_ready + kGroups;
-  uint64_t* drained = q_ready + 1;
+  uint64_t* drained = p_ready + kGroups;   // [group]: every product issued has completed
+  uint64_t* q_ready = drained + kGroups;
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
   __shared__ long long s_sum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -149,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(o_full + i, 1);
       mbar_init(p_ready + i, kCompute);
+      mbar_init(drained + i, 1);
     }
     mbar_init(q_ready, kCompute * kGroups);
-    mbar_init(drained, 1);
     fence_mbar_init();
   }
   sum_work<kThreads, kRows>(a, shift, prefix, s_sum);
@@ -171,24 +174,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducerWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == kProducerWarp) {
     produce<X, D>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
-  } else if (warp == kIssueWarp) {
+  } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
-    int k = 0, segments = 0;  // k: the CTA's tile, group k & 1's (k >> 1)-th
+    const int w = warp - kIssueWarp;  // the warpgroup whose products this warp issues
+    int k = 0, segments = 0, turn = 0;  // k: the CTA's first tile of the segment; turn: the group's own count
     bool alive = true;
     auto scores = [&](int i) {
       alive = __all_sync(kAll, wait(full + i % X::kStages, (i / X::kStages) & 1, status));
       if (!alive) return;
       tc_fence_after_sync();
       if (lane == 0) {
-        const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes, d = tmem + (i & 1) * X::kGroupTmem;
+        const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int st = 0; st < D / 32; ++st)
-            mma_f8(d, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode), smem_desc(keys + st * 32, 16, kGroup, kMode),
-                   idesc_f8(kTile, false, false, part == 1), part + st > 0);
-        tc_commit(s_full + (i & 1));
+            mma_f8(tmem + w * X::kGroupTmem, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode),
+                   smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1), part + st > 0);
+        tc_commit(s_full + w);
       }
       __syncwarp();
     };
@@ -196,41 +200,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     s.find(a, prefix, shift, kRows, start, stop);
     for (long long x = start; alive;) {
       const int last = k + s.end - s.begin;
-      if (s.begin < s.end) {
-        alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
-        if (alive) scores(k);
-        if (alive && k + 1 < last) scores(k + 1);
-      }
-      for (; k < last && alive; ++k) {
-        const int w = k & 1;
-        alive = __all_sync(kAll, wait(p_ready + w, (k >> 1) & 1, status));
+      if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
+      int i = k + ((k & 1) != w);
+      if (alive && i < last) scores(i);
+      for (; i < last && alive; i += 2, ++turn) {
+        alive = __all_sync(kAll, wait(p_ready + w, turn & 1, status));
         if (!alive) break;
-        // The group's scores have been read: its next tile's go first, unless its keys are still on their way.
-        const bool more = k + 2 < last;
-        const bool early = more && __all_sync(kAll, mbar_test(full + (k + 2) % X::kStages, ((k + 2) / X::kStages) & 1));
-        if (early) scores(k + 2);
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vals = ring + (k % X::kStages) * X::kStageBytes + X::kTileBytes, p = p_at + w * 2 * kRows * kTile;
+          const uint32_t vals = ring + (i % X::kStages) * X::kStageBytes + X::kTileBytes, p = p_at + w * 2 * kRows * kTile;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int st = 0; st < kTile / 32; ++st)
               mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
                      smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1), part + st > 0);
-          tc_commit(empty + k % X::kStages);
+          tc_commit(empty + i % X::kStages);
           tc_commit(o_full + w);
         }
         __syncwarp();
-        if (more && !early && alive) scores(k + 2);
+        // The group's scores have been read: its next tile's follow, while the group takes this output.
+        if (i + 2 < last) scores(i + 2);
       }
+      k = last;
       x += s.length;
       if (x >= stop) break;
       s.next(a, prefix, shift, kRows, x, stop);
     }
     if (lane == 0) {
-      tc_commit(drained);
-      wait(drained, 0, status);
+      tc_commit(drained + w);
+      wait(drained + w, 0, status);
     }
     __syncwarp();
   } else if (warp < kProducerWarp) {
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (long long x = start;;) {
       const int row0 = s.row_tile * kRows, before = s.q.seq - s.q.n;
       const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n) * a.group - row0));
-      float acc[D], m = -INFINITY, l = 0.0f;
+      float acc[D], l = 0.0f, m = row < rows ? -INFINITY : 0.0f;  // m: the reference of the weights, not always the maximum
 #pragma unroll
       for (int i = 0; i < D; ++i) acc[i] = 0.0f;
       const int last = k + s.end - s.begin;
@@ -295,26 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0, all_lo = a.window > 0 ? max(0, any_hi - a.window + 1) : 0;
       mixed = any_lo != all_lo || any_hi != all_hi;
       const float factor = s.begin < s.end ? row_f[row] : 0.0f;
-      float pend = 0.0f;  // factor of the output still in TMEM
-      bool pending = false;
-      auto take_output = [&](int i) {  // the group's i-th product joins the running output
-        if (!failed) failed = !wait(o_full + group, i & 1, status);
-        __syncwarp();
-        tc_fence_after_sync();
-        float u[16], v[16];
-        tmem_load_16_async(lanes + 128, u);
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          tmem_wait_16(u);
-          tmem_load_16_async(lanes + 128 + c + 16, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(u[j], pend, acc[c + j]);
-          tmem_wait_16(v);
-          if (c + 32 < D) tmem_load_16_async(lanes + 128 + c + 32, u);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + 16 + j] = fmaf(v[j], pend, acc[c + 16 + j]);
-        }
-      };
       for (int at = k + ((k & 1) != group); at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
@@ -323,68 +302,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + s.begin + at - k) * kTile;
-        uint32_t present = 1;
-        for (int i = 0; i < kTile >> shift; ++i) present &= mt[i] >> 16;
-        const bool edge = base < all_lo || base + kTile - 1 > all_hi || !present;
-        // Two passes over the scores: the row's maximum, then its weights.
-        float top = -INFINITY;
-        for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
-          const uint32_t entry = mt[c >> shift];
-          if (edge) {
+        const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
+        const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
+        // One pass over the scores while no weight outgrows its reference by more than the codes hold (2^4.75); else, and
+        // on the first tile, one for the maxima before it.
+        bool find = __any_sync(kAll, m == -INFINITY);
+        for (int tries = 0; tries < 2; ++tries) {
+          if (find) {
+            float top = m;
+            for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
+              const uint32_t entry = mt[c >> shift];
+              if (edge) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int token = base + c + j;
-              if (token < lo || token > hi || !(entry >> 16)) v[j] = -INFINITY;
-            }
+                for (int j = 0; j < 16; ++j) {
+                  const int token = base + c + j;
+                  if (token < lo || token > hi || !(entry >> 16)) v[j] = -INFINITY;
+                }
+              }
+              float big[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
+              const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+              if (most_here > -INFINITY) top = fmaxf(top, most_here * (factor * scale_of(entry & 0xFFu)));
+            });
+            const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < D; ++i) acc[i] *= keep;
           }
-          float big[4];
+          const float ref = m > -INFINITY ? m : 0.0f;
+          float part = 0.0f, high = 0.0f;
+          for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
+            const uint32_t entry = mt[c >> shift];
+            const float f = factor * scale_of(entry & 0xFFu);
+            // Times 2^kUp and the page's value scale over the tile's largest, both in the exponent.
+            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - most, -100);
+            const float off = static_cast<float>(up) - ref;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
-          const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-          if (most_here > -INFINITY) top = fmaxf(top, most_here * (factor * scale_of(entry & 0xFFu)));
-        });
-        const float mn = fmaxf(m, top), safe = mn > -INFINITY ? mn : 0.0f;
-        const float ref = top > -INFINITY ? top : 0.0f;
-        const float keep = exp2_fast(m - safe), add = exp2_fast(top - safe);
-        m = mn;
-        if (pending) take_output(turn - 1);
-        if (__any_sync(kAll, keep != 1.0f)) {
-          l *= keep;
+            for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
+            if (edge) {
 #pragma unroll
-          for (int i = 0; i < D; ++i) acc[i] *= keep;
+              for (int j = 0; j < 16; ++j) {
+                const int token = base + c + j;
+                if (token < lo || token > hi || !(entry >> 16)) v[j] = 0.0f;
+              }
+            }
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t his[8], los[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              sum[j & 3] += v[2 * j] + v[2 * j + 1];
+              high = fmaxf(high, fmaxf(v[2 * j], v[2 * j + 1]));
+              split2_wide_half(v[2 * j], v[2 * j + 1], his[j], los[j]);
+            }
+            part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __uint_as_float(static_cast<uint32_t>(127 - up) << 23), part);
+            uint8_t* dst = weights + chunk_at<128>(row, c / 16);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(his[0] | his[1] << 16, his[2] | his[3] << 16, his[4] | his[5] << 16, his[6] | his[7] << 16);
+            *reinterpret_cast<uint4*>(dst + kRows * kTile) =
+                make_uint4(los[0] | los[1] << 16, los[2] | los[3] << 16, los[4] | los[5] << 16, los[6] | los[7] << 16);
+          });
+          find = __any_sync(kAll, high > kHighest);
+          if (!find || tries == 1) {
+            l += part;
+            break;
+          }
         }
-        const int most = static_cast<int>(mt[kMaxPages]);
-        pend = add * scale_of(most) * (1.0f / 256.0f);
-        pending = true;
-        for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
-          const uint32_t entry = mt[c >> shift];
-          const float f = factor * scale_of(entry & 0xFFu);
-          // Times 256 and the page's value scale over the tile's largest, both in the exponent.
-          const int up = 8 + max(static_cast<int>((entry >> 8) & 0xFFu) - most, -100);
-          const float off = static_cast<float>(up) - ref;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int token = base + c + j;
-              if (token < lo || token > hi || !(entry >> 16)) v[j] = 0.0f;
-            }
-          }
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t his[8], los[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sum[j & 3] += v[2 * j] + v[2 * j + 1];
-            split2_wide_half(v[2 * j], v[2 * j + 1], his[j], los[j]);
-          }
-          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), add * pow2f(-up), l);
-          uint8_t* dst = weights + chunk_at<128>(row, c / 16);
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(his[0] | his[1] << 16, his[2] | his[3] << 16, his[4] | his[5] << 16, his[6] | his[7] << 16);
-          *reinterpret_cast<uint4*>(dst + kRows * kTile) =
-              make_uint4(los[0] | los[1] << 16, los[2] | los[3] << 16, los[4] | los[5] << 16, los[6] | los[7] << 16);
-        });
         if (edge) {
           // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
           // taken out too, and noted for those. (Thread `row` here takes the tile's token of that number.)
@@ -422,8 +406,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_shared();
         tc_fence_before_sync();
         mbar_arrive(p_ready + group);
+        // The tile's product joins the running output.
+        if (!failed) failed = !wait(o_full + group, turn & 1, status);
+        __syncwarp();
+        tc_fence_after_sync();
+        const float into = scale_of(most) * (1.0f / (1 << kUp));
+        float u[16], v[16];
+        tmem_load_16_async(lanes + 128, u);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          tmem_wait_16(u);
+          tmem_load_16_async(lanes + 128 + c + 16, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(u[j], into, acc[c + j]);
+          tmem_wait_16(v);
+          if (c + 32 < D) tmem_load_16_async(lanes + 128 + c + 32, u);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + 16 + j] = fmaf(v[j], into, acc[c + 16 + j]);
+        }
       }
-      if (pending) take_output(turn - 1);
       k = last;
 
       // The second group's rows join the first's.
