@@ -2,30 +2,33 @@
 // (moe_kv_attend in include/moe.h; kv_attend.cu has the decode form).
 //
 // Here the 128 query rows of an item are the tensor core's 128-row operand and
-// a tile's 128 tokens the columns: S[row][token] = Q x K^T and O[row][dim] =
-// P x V (V read transposed, as it lies in the page), so a thread owns a row and
-// its maximum and sum need no other thread. Queries and weights are split
-// into e4m3 hi + e5m2 lo, two products into one accumulator: hi + lo hold the
-// 8 significant bits of a BF16 query exactly down to 2^-16 of its row's largest
-// magnitude, and a weight of 2^-10 of its row's reference or more within 2^-8 of
-// itself (BF16's own rounding; below that within 2^-18 of the reference). The
-// reference is a maximum of the row's scores seen so far, raised only when a
-// weight outgrows it. Each tile's output joins the running one in FP32 registers.
+// a tile's 128 tokens the columns: S[row][token] = Q x K^T and O[row][dim] +=
+// P x V (V read transposed, as it lies in the page), so a row's weights need
+// no other row. Queries and weights are split into e4m3 hi + e5m2 lo, two
+// products into one accumulator: hi + lo hold the 8 significant bits of a BF16
+// query exactly down to 2^-16 of its row's largest magnitude, and a weight of
+// 2^-10 of its row's reference or more within 2^-8 of itself (BF16's own
+// rounding; below that within 2^-18 of the reference). The reference is a
+// maximum of the row's scores seen so far, and one for the value scales: while
+// no weight outgrows them, the output stays in TMEM, accumulated in FP32 by the
+// tensor core itself, and the scores are read once. Only when one does (and
+// on an item's first tile) the maxima are taken first and the output is rescaled.
 //
-// Two warpgroups take a CTA's tiles in turn, one in its softmax while the
-// other's products run; their results are joined in shared memory.
+// Two groups take a CTA's tiles in turn, one in its softmax while the other's
+// products run; in a group two warpgroups share the rows, each with half of the
+// columns (two threads to a row). The groups' results are joined in shared memory.
 #include "kv_attend.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kGroups = 2;                        // compute warpgroups: warps 0-3, 4-7
-constexpr int kProducerWarp = 4 * kGroups;
-constexpr int kIssueWarp = kProducerWarp + 1;       // one for each warpgroup
-constexpr int kThreads = 128 * (kGroups + 1);    // whole warpgroups: one warp of the last one idles
-// Registers a thread: 168 at launch; the last warpgroup gives of its own to the others (2 x 224 + 56 = 3 x 168).
-constexpr int kComputeRegs = 224, kIssueRegs = 56;
+constexpr int kGroups = 2;                        // each two warpgroups: threads 0-255, 256-511
+constexpr int kGroupThreads = 2 * kCompute;
+constexpr int kAllCompute = kGroups * kGroupThreads;
+constexpr int kProducerWarp = kAllCompute / 32;
+constexpr int kIssueWarp = kProducerWarp + 1;     // one for each group
+constexpr int kThreads = kAllCompute + 96;
 
 template <int D>
 struct RowsShape {
@@ -41,8 +44,9 @@ struct RowsShape {
   static constexpr int kQ = kRing + kStages * kStageBytes;           // hi, lo
   static constexpr int kP = kQ + 2 * kRows * D;                      // [group] hi, lo
   static constexpr int kRowF = kP + kGroups * 2 * kRows * kTile;     // [row] factor
-  static constexpr int kJoinMl = kRowF + kRows * 4;                  // [row] the second group's maximum and sum
-  static constexpr int kNan = kJoinMl + kRows * 8;                   // [row][D / 32]: outputs that saw a NaN apart
+  static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
+  static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [row] the second group's reference; its value scale's
+  static constexpr int kNan = kRefs + kRows * 4 + 16;                // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
   static constexpr int kPrefix = kBars + (2 * kStages + 4 * kGroups + 1) * 8;  // full, empty, s_full, o_full, p_ready, drained, q_ready
@@ -106,20 +110,33 @@ __device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& h
   lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2);
 }
 
-__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void all_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 
-// Barrier of both warpgroups; true everywhere if any thread brings true.
-__device__ __forceinline__ bool both_any(bool mine) {
+// Barrier of a group's threads, or of both groups'; true everywhere if any thread brings true.
+template <int kCount>
+__device__ __forceinline__ bool sync_any(int id, bool mine) {
   uint32_t any;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0;\n"
-      "barrier.cta.red.or.pred q, 3, 256, p;\n"
+      "{ .reg .pred p, q; setp.ne.u32 p, %2, 0;\n"
+      "barrier.cta.red.or.pred q, %1, %3, p;\n"
       "selp.u32 %0, 1, 0, q; }"
       : "=r"(any)
-      : "r"(static_cast<uint32_t>(mine))
+      : "r"(id), "r"(static_cast<uint32_t>(mine)), "n"(kCount)
       : "memory");
   return any != 0;
 }
+
+// Sixteen columns back into TMEM.
+__device__ __forceinline__ void tmem_store_16(uint32_t taddr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"f"(r[0]),
+      "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]),
+      "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -140,6 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long s_sum[kThreads / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
+  __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
+  __shared__ long long s_unit;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
@@ -151,10 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(o_full + i, 1);
-      mbar_init(p_ready + i, kCompute);
+      mbar_init(p_ready + i, kGroupThreads);
       mbar_init(drained + i, 1);
     }
-    mbar_init(q_ready, kCompute * kGroups);
+    mbar_init(q_ready, kAllCompute);
     fence_mbar_init();
   }
   sum_work<kThreads, kRows>(a, shift, prefix, s_sum);
@@ -171,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem;  // group g: scores at 256 g, output at 256 g + 128
 
-  if (warp >= kProducerWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == kProducerWarp) {
     produce<X, D>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
@@ -203,9 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
       int i = k + ((k & 1) != w);
       if (alive && i < last) scores(i);
-      for (; i < last && alive; i += 2, ++turn) {
+      for (bool first = true; i < last && alive; i += 2, ++turn, first = false) {
         alive = __all_sync(kAll, wait(p_ready + w, turn & 1, status));
         if (!alive) break;
+        // The group's scores have been read: its next tile's go first, unless its keys are still on their way.
+        const bool more = i + 2 < last;
+        const bool early = more && __all_sync(kAll, mbar_test(full + (i + 2) % X::kStages, ((i + 2) / X::kStages) & 1));
+        if (early) scores(i + 2);
         tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t vals = ring + (i % X::kStages) * X::kStageBytes + X::kTileBytes, p = p_at + w * 2 * kRows * kTile;
@@ -214,13 +236,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int st = 0; st < kTile / 32; ++st)
               mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
-                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1), part + st > 0);
+                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1),
+                     !first || part + st > 0);
           tc_commit(empty + i % X::kStages);
           tc_commit(o_full + w);
         }
         __syncwarp();
-        // The group's scores have been read: its next tile's follow, while the group takes this output.
-        if (i + 2 < last) scores(i + 2);
+        if (more && !early && alive) scores(i + 2);
       }
       k = last;
       x += s.length;
@@ -233,31 +255,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp < kProducerWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
-    const int group = warp >> 2, row = tid & (kCompute - 1);
+    const int group = tid / kGroupThreads, half = (tid / kCompute) & 1, row = tid & (kCompute - 1);
+    const int in_group = tid & (kGroupThreads - 1);
+    constexpr int kHalfTile = kTile / 2, kHalfD = D / 2;
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
-    float2* join_ml = reinterpret_cast<float2*>(sm + X::kJoinMl);
+    float* tops = reinterpret_cast<float*>(sm + X::kTops);
+    float* refs = reinterpret_cast<float*>(sm + X::kRefs);
+    int* ref_scale = reinterpret_cast<int*>(refs + kRows);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     float* join = reinterpret_cast<float*>(sm + X::kP);
     uint8_t* weights = sm + X::kP + group * 2 * kRows * kTile;
     const uint32_t lanes = tmem + group * X::kGroupTmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const uint32_t s_at = lanes + half * kHalfTile, o_at = lanes + 128 + half * kHalfD;
     int k = 0, turn = 0;   // the CTA's tile; the group's own count
-    bool failed = false;   // a wait of this thread's ran out; no more waits, agreed on at the segment's end
-    Segment s;
-    s.find(a, prefix, shift, kRows, start, stop);
-    for (long long x = start;;) {
+    bool failed = false;   // a wait ran out: no more waits; agreed on at the barriers
+    if (tid == 0) {
+      s_unit = start;
+      s_segment.find(a, prefix, shift, kRows, start, stop);
+    }
+    all_sync();
+    const Segment& s = s_segment;
+    for (;;) {
       const int row0 = s.row_tile * kRows, before = s.q.seq - s.q.n;
       const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n) * a.group - row0));
-      float acc[D], l = 0.0f, m = row < rows ? -INFINITY : 0.0f;  // m: the reference of the weights, not always the maximum
-#pragma unroll
-      for (int i = 0; i < D; ++i) acc[i] = 0.0f;
       const int last = k + s.end - s.begin;
-      bool mixed = false;
       if (s.begin < s.end) {
         // Queries: hi image, lo image, each row scaled by a power of two so that its largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
 #pragma unroll 2
-        for (int i = tid; i < kRows * kChunks; i += kCompute * kGroups) {
+        for (int i = tid; i < kRows * kChunks; i += kAllCompute) {
           const int r = i / kChunks, c = i % kChunks, at = row0 + r, tok = at / a.group;
           uint4 w = make_uint4(0, 0, 0, 0);
           if (r < rows)
@@ -282,40 +308,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c == 0)
             row_f[r] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : fabsf(a.scale) * kLog2e * pow2f(e);
         }
-        for (int i = tid; i < kRows * D / 32; i += kCompute * kGroups) nans[i] = 0;
+        for (int i = tid; i < kRows * D / 32; i += kAllCompute) nans[i] = 0;
         fence_proxy_async_shared();
         mbar_arrive(q_ready);
-        both_sync();
+        all_sync();
       }
       const int tok = (row0 + row) / a.group;
       const int hi = row < rows ? before + tok : -1, lo = row < rows && a.window > 0 ? max(0, hi - a.window + 1) : 0;
       // Tokens that any of the rows sees, and that all see.
       const int any_hi = before + (row0 + rows - 1) / a.group, all_hi = before + row0 / a.group;
       const int any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0, all_lo = a.window > 0 ? max(0, any_hi - a.window + 1) : 0;
-      mixed = any_lo != all_lo || any_hi != all_hi;
+      const bool mixed = any_lo != all_lo || any_hi != all_hi;
       const float factor = s.begin < s.end ? row_f[row] : 0.0f;
-      for (int at = k + ((k & 1) != group); at < last; at += 2, ++turn) {
+      float l = 0.0f, m = row < rows ? -INFINITY : 0.0f;  // m: the reference of the row's weights
+      int m_scale = 0;                                    // the reference of the value scales
+      bool written = false;                               // the group's output in TMEM is this item's
+      int at = k + ((k & 1) != group);
+      for (; at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
         if (!failed) failed = !wait(full + stage, (at / X::kStages) & 1, status);
         __syncwarp();
         tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
-        const int base = (s.q.tile0 + s.begin + at - k) * kTile;
+        const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
         const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
         const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
-        // One pass over the scores while no weight outgrows its reference by more than the codes hold (2^4.75); else, and
-        // on the first tile, one for the maxima before it.
-        bool find = __any_sync(kAll, m == -INFINITY);
-        for (int tries = 0; tries < 2; ++tries) {
+        bool find = !written || most > m_scale || (m == -INFINITY && hi >= base && lo < base + kTile);
+        find = sync_any<kGroupThreads>(4 + group, find);
+        for (int tries = 0;; ++tries) {
           if (find) {
-            float top = m;
-            for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
-              const uint32_t entry = mt[c >> shift];
+            // The references are raised: the maxima of the row's two halves, and what is there already follows.
+            float top = -INFINITY;
+            for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
+              const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
               if (edge) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                  const int token = base + c + j;
+                  const int token = base_half + c + j;
                   if (token < lo || token > hi || !(entry >> 16)) v[j] = -INFINITY;
                 }
               }
@@ -325,50 +355,75 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
               if (most_here > -INFINITY) top = fmaxf(top, most_here * (factor * scale_of(entry & 0xFFu)));
             });
+            float* mine = tops + (group * 2 + half) * kRows + row;
+            *mine = top;
+            sync_any<kGroupThreads>(4 + group, false);
+            top = fmaxf(m, fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
             const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
-            m = top;
+            const int scale = max(m_scale, most);
             l *= keep;
+            if (written) {
+              if (!failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
+              __syncwarp();
+              tc_fence_after_sync();
+              const float f = keep * exp2_fast(static_cast<float>(m_scale - scale));
+#pragma unroll 1
+              for (int c = 0; c < kHalfD; c += 16) {
+                float o[16];
+                tmem_load_16_async(o_at + c, o);
+                tmem_wait_16(o);
 #pragma unroll
-            for (int i = 0; i < D; ++i) acc[i] *= keep;
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_store_16(o_at + c, o);
+              }
+              tmem_wait_stores();
+            }
+            m = top;
+            m_scale = scale;
           }
+          // The last tile's weights have been used: these take their place.
+          if (written && !failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
           const float ref = m > -INFINITY ? m : 0.0f;
           float part = 0.0f, high = 0.0f;
-          for_columns<kTile>(lanes, [&](int c, float (&v)[16]) {
-            const uint32_t entry = mt[c >> shift];
+          for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
+            const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
             const float f = factor * scale_of(entry & 0xFFu);
-            // Times 2^kUp and the page's value scale over the tile's largest, both in the exponent.
-            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - most, -100);
+            // Times 2^kUp and the page's value scale over its reference, both in the exponent.
+            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -100);
             const float off = static_cast<float>(up) - ref;
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
             if (edge) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int token = base + c + j;
+                const int token = base_half + c + j;
                 if (token < lo || token > hi || !(entry >> 16)) v[j] = 0.0f;
               }
             }
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t his[8], los[8];
+            uint32_t his[4], los[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              sum[j & 3] += v[2 * j] + v[2 * j + 1];
-              high = fmaxf(high, fmaxf(v[2 * j], v[2 * j + 1]));
-              split2_wide_half(v[2 * j], v[2 * j + 1], his[j], los[j]);
+            for (int j = 0; j < 8; j += 2) {
+              sum[j / 2] = (v[2 * j] + v[2 * j + 1]) + (v[2 * j + 2] + v[2 * j + 3]);
+              high = fmaxf(high, fmaxf(fmaxf(v[2 * j], v[2 * j + 1]), fmaxf(v[2 * j + 2], v[2 * j + 3])));
+              uint32_t h0, l0, h1, l1;
+              split2_wide_half(v[2 * j], v[2 * j + 1], h0, l0);
+              split2_wide_half(v[2 * j + 2], v[2 * j + 3], h1, l1);
+              his[j / 2] = h0 | h1 << 16;
+              los[j / 2] = l0 | l1 << 16;
             }
             part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __uint_as_float(static_cast<uint32_t>(127 - up) << 23), part);
-            uint8_t* dst = weights + chunk_at<128>(row, c / 16);
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(his[0] | his[1] << 16, his[2] | his[3] << 16, his[4] | his[5] << 16, his[6] | his[7] << 16);
-            *reinterpret_cast<uint4*>(dst + kRows * kTile) =
-                make_uint4(los[0] | los[1] << 16, los[2] | los[3] << 16, los[4] | los[5] << 16, los[6] | los[7] << 16);
+            uint8_t* dst = weights + chunk_at<128>(row, (half * kHalfTile + c) / 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(his[0], his[1], his[2], his[3]);
+            *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(los[0], los[1], los[2], los[3]);
           });
-          find = __any_sync(kAll, high > kHighest);
+          find = sync_any<kGroupThreads>(4 + group, high > kHighest);
           if (!find || tries == 1) {
             l += part;
             break;
           }
         }
+        written = true;
         if (edge) {
           // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
           // taken out too, and noted for those. (Thread `row` here takes the tile's token of that number.)
@@ -377,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool seen = token >= any_lo && token <= any_hi && (mt[row >> shift] >> 16);
           if (!seen || mixed) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = half; c < D / 16; c += 2) {
               uint4* cell = reinterpret_cast<uint4*>(value + c * 16);
               if (!seen) {
                 *cell = make_uint4(0, 0, 0, 0);
@@ -406,84 +461,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_shared();
         tc_fence_before_sync();
         mbar_arrive(p_ready + group);
-        // The tile's product joins the running output.
-        if (!failed) failed = !wait(o_full + group, turn & 1, status);
+      }
+      // The group's output, this thread's half of the row.
+      float acc[kHalfD];
+      if (written) {
+        if (!failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
         __syncwarp();
         tc_fence_after_sync();
-        const float into = scale_of(most) * (1.0f / (1 << kUp));
-        float u[16], v[16];
-        tmem_load_16_async(lanes + 128, u);
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          tmem_wait_16(u);
-          tmem_load_16_async(lanes + 128 + c + 16, v);
+        for (int c = 0; c < kHalfD; c += 16) {
+          float o[16];
+          tmem_load_16_async(o_at + c, o);
+          tmem_wait_16(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(u[j], into, acc[c + j]);
-          tmem_wait_16(v);
-          if (c + 32 < D) tmem_load_16_async(lanes + 128 + c + 32, u);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + 16 + j] = fmaf(v[j], into, acc[c + 16 + j]);
+          for (int j = 0; j < 16; ++j) acc[c + j] = o[j];
         }
+        tc_fence_before_sync();
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHalfD; ++i) acc[i] = 0.0f;
       }
       k = last;
 
       // The second group's rows join the first's.
-      failed = both_any(failed);
+      failed = sync_any<kAllCompute>(3, failed);
       if (failed) break;
+      tops[(group * 2 + half) * kRows + row] = l;
       if (group == 1) {
-        join_ml[row] = make_float2(m, l);
+        if (half == 0) refs[row] = m;
+        if (in_group == 0) *ref_scale = m_scale;
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c)
-          *reinterpret_cast<float4*>(join + row * D + ((c ^ (row & 15)) << 2)) =
+        for (int c = 0; c < kHalfD / 4; ++c)
+          *reinterpret_cast<float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2)) =
               make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
       }
-      both_sync();
+      all_sync();
       if (group == 0) {
-        const float2 other = join_ml[row];
-        const float mn = fmaxf(m, other.x), safe = mn > -INFINITY ? mn : 0.0f;
-        const float f0 = exp2_fast(m - safe), f1 = exp2_fast(other.x - safe);
+        const float l0 = tops[row] + tops[kRows + row], l1 = tops[2 * kRows + row] + tops[3 * kRows + row];
+        const float m1 = refs[row], mn = fmaxf(m, m1), safe = mn > -INFINITY ? mn : 0.0f;
+        const float f0 = exp2_fast(m - safe), f1 = exp2_fast(m1 - safe);
+        l = l0 * f0 + l1 * f1;
         m = mn;
-        l = l * f0 + other.y * f1;
+        const float g0 = f0 * scale_of(m_scale) * (1.0f / (1 << kUp)), g1 = f1 * scale_of(*ref_scale) * (1.0f / (1 << kUp));
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(join + row * D + ((c ^ (row & 15)) << 2));
-          acc[4 * c] = acc[4 * c] * f0 + v.x * f1;
-          acc[4 * c + 1] = acc[4 * c + 1] * f0 + v.y * f1;
-          acc[4 * c + 2] = acc[4 * c + 2] * f0 + v.z * f1;
-          acc[4 * c + 3] = acc[4 * c + 3] * f0 + v.w * f1;
+        for (int c = 0; c < kHalfD / 4; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2));
+          acc[4 * c] = acc[4 * c] * g0 + v.x * g1;
+          acc[4 * c + 1] = acc[4 * c + 1] * g0 + v.y * g1;
+          acc[4 * c + 2] = acc[4 * c + 2] * g0 + v.z * g1;
+          acc[4 * c + 3] = acc[4 * c + 3] * g0 + v.w * g1;
         }
         if (mixed && s.begin < s.end) {
 #pragma unroll
-          for (int i = 0; i < D; ++i)
-            if (nans[row * (D / 32) + i / 32] >> (i % 32) & 1) acc[i] = __uint_as_float(0x7FC00000u);
+          for (int i = 0; i < kHalfD; ++i) {
+            const int dim = half * kHalfD + i;
+            if (nans[row * (D / 32) + dim / 32] >> (dim % 32) & 1) acc[i] = __uint_as_float(0x7FC00000u);
+          }
         }
         if (s.whole) {
           if (row < rows) {
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             const int64_t dst = static_cast<int64_t>(s.q.first + tok) * a.q_heads + s.head * a.group + row0 + row - tok * a.group;
 #pragma unroll
-            for (int c = 0; c < D; c += 8) {
+            for (int c = 0; c < kHalfD; c += 8) {
               __nv_bfloat162 w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(acc[c + 2 * j] * inv, acc[c + 2 * j + 1] * inv);
-              *reinterpret_cast<uint4*>(a.out + dst * D + c) = *reinterpret_cast<uint4*>(w);
+              *reinterpret_cast<uint4*>(a.out + dst * D + half * kHalfD + c) = *reinterpret_cast<uint4*>(w);
             }
-            if (a.lse != nullptr) a.lse[dst] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (a.lse != nullptr && half == 0) a.lse[dst] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
           }
         } else {
           float* mine = partials + static_cast<int64_t>(blockIdx.x * 2 + (s.first ? 1 : 0)) * X::kPartialFloats;
 #pragma unroll
-          for (int c = 0; c < D; c += 4)
-            *reinterpret_cast<float4*>(mine + row * D + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-          mine[kRows * D + row] = m;
-          mine[kRows * D + kRows + row] = l;
-          join_item<kRows, D>(a, s, rows, ctas, total, tid, &s_last);
+          for (int c = 0; c < kHalfD; c += 4)
+            *reinterpret_cast<float4*>(mine + row * D + half * kHalfD + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+          if (half == 0) {
+            mine[kRows * D + row] = m;
+            mine[kRows * D + kRows + row] = l;
+          }
+          sync_any<kGroupThreads>(4, false);  // both halves' stores, ahead of the first warpgroup's release of them
+          if (half == 0) join_item<kRows, D>(a, s, rows, ctas, total, tid, &s_last);
         }
       }
-      x += s.length;
-      if (x >= stop) break;
-      s.next(a, prefix, shift, kRows, x, stop);
-      both_sync();  // the join's room, the rows' factors and the join word are free again
+      all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
+      if (tid == 0) {
+        s_unit += s_segment.length;
+        if (s_unit < stop) s_segment.next(a, prefix, shift, kRows, s_unit, stop);
+      }
+      all_sync();
+      if (s_unit >= stop) break;
     }
   }
   tc_fence_before_sync();
