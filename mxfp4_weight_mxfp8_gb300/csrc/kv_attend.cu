@@ -47,6 +47,7 @@ struct Shape {
   static constexpr int kSpan = D >= 128 ? 128 : 64;       // bytes of a row in one box: the swizzle's width
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kKeyStride = kStageBytes, kValuesAt = kTileBytes, kValueStride = kStageBytes;
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : 5) : (D == 128 && RT != 2 ? 2 : 3);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * X::kCols;
 
   if (warp == kProducerWarp) {
-    produce<X, D>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
+    produce<X, D, 3>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).

@@ -240,8 +240,10 @@ __device__ void sum_work(const AttendArgs& a, int shift, long long* prefix, long
   __syncthreads();
 }
 
-// The producer warp: looks up the pages of the CTA's tiles and streams them through the ring.
-template <class X, int D>
+// A producer warp: looks up the pages of the CTA's tiles and streams their keys (kWhich 1), values (2) or both (3)
+// through the ring. With the values go the pages' entries: key scale, value scale << 8, present << 16; and after a
+// tile's, its largest value scale and, << 8, whether every page is there.
+template <class X, int D, int kWhich>
 __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int shift, long long start,
                         long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
   const int lane = threadIdx.x & 31;
@@ -273,16 +275,16 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
       const bool mine = lane / per_tile == batch;
       const int boxes = __popc(__ballot_sync(kAll, mine && page >= 0));
       if (mine && page >= 0) {
-        uint8_t* dst = sm + X::kRing + stage * X::kStageBytes + (in_tile << shift) * X::kSpan;
+        uint8_t* keys = sm + X::kRing + stage * X::kKeyStride + (in_tile << shift) * X::kSpan;
+        uint8_t* vals = sm + X::kRing + X::kValuesAt + stage * X::kValueStride + (in_tile << shift) * X::kSpan;
+        const int row = page * a.c.kv_heads + s.head;
 #pragma unroll
         for (int h = 0; h < X::kHalves; ++h) {
-          tma_load_3d(dst + h * (kTile * X::kSpan), &maps.k, h * X::kSpan, 0, page * a.c.kv_heads + s.head, full + stage,
-                    policy);
-          tma_load_3d(dst + X::kTileBytes + h * (kTile * X::kSpan), &maps.v, h * X::kSpan, 0, page * a.c.kv_heads + s.head,
-                      full + stage, policy);
+          if (kWhich & 1) tma_load_3d(keys + h * (kTile * X::kSpan), &maps.k, h * X::kSpan, 0, row, full + stage, policy);
+          if (kWhich & 2) tma_load_3d(vals + h * (kTile * X::kSpan), &maps.v, h * X::kSpan, 0, row, full + stage, policy);
         }
       }
-      if (fresh) {
+      if ((kWhich & 2) && fresh) {
         fresh = false;
         entry = 0;
         if (page >= 0) {
@@ -292,14 +294,16 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
         top = (entry >> 8) & 0xFFu;  // the tile's largest value scale
         for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
       }
-      uint32_t* m = meta + stage * (kMaxPages + 1);
-      if (mine) {
-        m[in_tile] = entry;
-        if (in_tile == 0) m[kMaxPages] = top | (boxes == per_tile) << 8;  // and whether every page is there
+      if (kWhich & 2) {
+        uint32_t* m = meta + stage * (kMaxPages + 1);
+        if (mine) {
+          m[in_tile] = entry;
+          if (in_tile == 0) m[kMaxPages] = top | (boxes == per_tile) << 8;
+        }
+        __syncwarp();  // the entries are written before lane 0 arrives
       }
-      __syncwarp();  // the entries are written before lane 0 arrives
       if (lane == 0) {
-        if (boxes) mbar_arrive_expect_tx(full + stage, boxes * (2 * D << shift));
+        if (boxes) mbar_arrive_expect_tx(full + stage, boxes * ((kWhich == 3 ? 2 : 1) * D << shift));
         else mbar_arrive(full + stage);
       }
     }

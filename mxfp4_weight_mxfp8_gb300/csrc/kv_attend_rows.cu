@@ -26,9 +26,9 @@ constexpr int kRows = 128;
 constexpr int kGroups = 2;                        // each two warpgroups: threads 0-255, 256-511
 constexpr int kGroupThreads = 2 * kCompute;
 constexpr int kAllCompute = kGroups * kGroupThreads;
-constexpr int kProducerWarp = kAllCompute / 32;
-constexpr int kIssueWarp = kProducerWarp + 1;     // one for each group
-constexpr int kThreads = kAllCompute + 96;
+constexpr int kProducerWarp = kAllCompute / 32;   // one for the keys, one for the values
+constexpr int kIssueWarp = kProducerWarp + 2;     // one for each group
+constexpr int kThreads = kAllCompute + 128;
 
 template <int D>
 struct RowsShape {
@@ -36,12 +36,13 @@ struct RowsShape {
   static constexpr int kHalves = 1;
   static constexpr int kSpan = D;                 // 128 or 64: one box, one swizzle span a row
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = D == 128 ? 3 : 5;
   static constexpr int kPartialFloats = kRows * (D + 2);
   static constexpr int kGroupTmem = 256;          // scores 128 columns, output D
+  // Keys and values in rings of their own: a tile's keys are done with long before its values.
+  static constexpr int kKeyStride = kTileBytes, kValuesAt = kStages * kTileBytes, kValueStride = kTileBytes;
   static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + kStages * kStageBytes;           // hi, lo
+  static constexpr int kQ = kRing + 2 * kStages * kTileBytes;        // hi, lo
   static constexpr int kP = kQ + 2 * kRows * D;                      // [group] hi, lo
   static constexpr int kRowF = kP + kGroups * 2 * kRows * kTile;     // [row] factor
   static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
@@ -49,7 +50,7 @@ struct RowsShape {
   static constexpr int kNan = kRefs + kRows * 4 + 16;                // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kPrefix = kBars + (2 * kStages + 4 * kGroups + 1) * 8;  // full, empty, s_full, o_full, p_ready, drained, q_ready
+  static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
   static_assert(kPartialOffset + 2ll * 256 * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES || D == 128, "workspace");
   static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
@@ -112,7 +113,7 @@ __device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& h
 
 __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 
-// Barrier of a group's threads, or of both groups'; true everywhere if any thread brings true.
+// Barrier of the two warps that share rows, or of more; true everywhere if any thread brings true.
 template <int kCount>
 __device__ __forceinline__ bool sync_any(int id, bool mine) {
   uint32_t any;
@@ -146,9 +147,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* meta = reinterpret_cast<uint32_t*>(sm + X::kMeta);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + X::kBars);
-  uint64_t* empty = full + X::kStages;
-  uint64_t* s_full = empty + X::kStages;   // [group]: scores of its tile in TMEM
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + X::kBars);
+  uint64_t* k_empty = k_full + X::kStages;
+  uint64_t* v_full = k_empty + X::kStages;
+  uint64_t* v_empty = v_full + X::kStages;
+  uint64_t* s_full = v_empty + X::kStages;   // [group]: scores of its tile in TMEM
   uint64_t* o_full = s_full + kGroups;     // [group]: its tile's output in TMEM
   uint64_t* p_ready = o_full + kGroups;    // [group]: its tile's weights in shared memory
   uint64_t* drained = p_ready + kGroups;   // [group]: every product issued has completed
@@ -164,8 +167,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < X::kStages; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(s_full + i, 1);
@@ -191,7 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;  // group g: scores at 256 g, output at 256 g + 128
 
   if (warp == kProducerWarp) {
-    produce<X, D>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
+    produce<X, D, 1>(a, maps, prefix, shift, start, stop, sm, meta, k_full, k_empty, status);
+  } else if (warp == kProducerWarp + 1) {
+    produce<X, D, 2>(a, maps, prefix, shift, start, stop, sm, meta, v_full, v_empty, status);
   } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
@@ -199,17 +206,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0, segments = 0, turn = 0;  // k: the CTA's first tile of the segment; turn: the group's own count
     bool alive = true;
     auto scores = [&](int i) {
-      alive = __all_sync(kAll, wait(full + i % X::kStages, (i / X::kStages) & 1, status));
+      alive = __all_sync(kAll, wait(k_full + i % X::kStages, (i / X::kStages) & 1, status));
       if (!alive) return;
       tc_fence_after_sync();
       if (lane == 0) {
-        const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes;
+        const uint32_t keys = ring + (i % X::kStages) * X::kKeyStride;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int st = 0; st < D / 32; ++st)
             mma_f8(tmem + w * X::kGroupTmem, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode),
                    smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1), part + st > 0);
+        tc_commit(k_empty + i % X::kStages);
         tc_commit(s_full + w);
       }
       __syncwarp();
@@ -224,13 +232,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool first = true; i < last && alive; i += 2, ++turn, first = false) {
         alive = __all_sync(kAll, wait(p_ready + w, turn & 1, status));
         if (!alive) break;
-        // The group's scores have been read: its next tile's go first, unless its keys are still on their way.
-        const bool more = i + 2 < last;
-        const bool early = more && __all_sync(kAll, mbar_test(full + (i + 2) % X::kStages, ((i + 2) / X::kStages) & 1));
-        if (early) scores(i + 2);
+        // The group's scores have been read: its next tile's go first.
+        if (i + 2 < last) scores(i + 2);
+        alive = alive && __all_sync(kAll, wait(v_full + i % X::kStages, (i / X::kStages) & 1, status));
+        if (!alive) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vals = ring + (i % X::kStages) * X::kStageBytes + X::kTileBytes, p = p_at + w * 2 * kRows * kTile;
+          const uint32_t vals = ring + X::kValuesAt + (i % X::kStages) * X::kValueStride, p = p_at + w * 2 * kRows * kTile;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -238,11 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
                      smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1),
                      !first || part + st > 0);
-          tc_commit(empty + i % X::kStages);
+          tc_commit(v_empty + i % X::kStages);
           tc_commit(o_full + w);
         }
         __syncwarp();
-        if (more && !early && alive) scores(i + 2);
       }
       k = last;
       x += s.length;
@@ -257,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kProducerWarp) {
     const int group = tid / kGroupThreads, half = (tid / kCompute) & 1, row = tid & (kCompute - 1);
     const int in_group = tid & (kGroupThreads - 1);
+    const int pair = 4 + group * 4 + (warp & 3);  // the barrier of the two warps that share this row
     constexpr int kHalfTile = kTile / 2, kHalfD = D / 2;
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
     float* tops = reinterpret_cast<float*>(sm + X::kTops);
@@ -327,15 +335,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
-        if (!failed) failed = !wait(full + stage, (at / X::kStages) & 1, status);
+        if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);
         __syncwarp();
         tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
         const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
         const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
-        bool find = !written || most > m_scale || (m == -INFINITY && hi >= base && lo < base + kTile);
-        find = sync_any<kGroupThreads>(4 + group, find);
+        // Past the item's first tile only an edge can bring a row its first token.
+        bool find = !written || most > m_scale;
+        if (edge && !find) find = sync_any<64>(pair, m == -INFINITY && hi >= base && lo < base + kTile);
         for (int tries = 0;; ++tries) {
           if (find) {
             // The references are raised: the maxima of the row's two halves, and what is there already follows.
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
             float* mine = tops + (group * 2 + half) * kRows + row;
             *mine = top;
-            sync_any<kGroupThreads>(4 + group, false);
+            sync_any<64>(pair, false);
             top = fmaxf(m, fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
             const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
             const int scale = max(m_scale, most);
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(dst) = make_uint4(his[0], his[1], his[2], his[3]);
             *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(los[0], los[1], los[2], los[3]);
           });
-          find = sync_any<kGroupThreads>(4 + group, high > kHighest);
+          find = sync_any<64>(pair, high > kHighest);
           if (!find || tries == 1) {
             l += part;
             break;
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
           // taken out too, and noted for those. (Thread `row` here takes the tile's token of that number.)
-          uint8_t* value = sm + X::kRing + stage * X::kStageBytes + X::kTileBytes + row * X::kSpan;
+          uint8_t* value = sm + X::kRing + X::kValuesAt + stage * X::kValueStride + row * X::kSpan;
           const int token = base + row;
           const bool seen = token >= any_lo && token <= any_hi && (mt[row >> shift] >> 16);
           if (!seen || mixed) {
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mine[kRows * D + row] = m;
             mine[kRows * D + kRows + row] = l;
           }
-          sync_any<kGroupThreads>(4, false);  // both halves' stores, ahead of the first warpgroup's release of them
+          sync_any<kGroupThreads>(4 + 8, false);  // both halves' stores, ahead of the first warpgroup's release of them
           if (half == 0) join_item<kRows, D>(a, s, rows, ctas, total, tid, &s_last);
         }
       }
