@@ -1,29 +1,25 @@
 // Causal attention of new tokens over the paged 8-bit cache (moe_kv_attend in
 // include/moe.h).
 //
-// The work is cut into tiles of 128 cache tokens of one item: a request, a
-// cache head and 8 * RT of its query rows (token-major, the head's query heads
-// within a token). All tiles in a row, [request][row tile][head][tile], are
-// dealt to the CTAs in equal runs, so a long context is split over many CTAs
-// and short ones share one; an item that spans CTAs is joined by the last of
-// them to finish, in CTA order.
-//
-// Both products run on the tensor cores with the cache's codes as they are, as
-// the 128-row operand: S^T[token][row] = K x Q^T and O^T[dim][row] = V^T x P^T
-// (V read transposed, token-major as it lies in the page). The few query rows are the
-// narrow operand. A query value is split into two e4m3 numbers, hi + lo / 16,
-// which take two columns: together they hold the 8 significant bits of a BF16
-// exactly down to 2^-14 of the row's largest magnitude, and below that within
-// 2^-22 of it. The weights are split the same way: p = exp2(s - ref), times
-// 256, within 2^-9 of p or 2^-22 of the reference; their sum is taken of the
-// unsplit values. ref is the row's running maximum where the tile's own is
-// within 2^8 of it, else the tile's own: neither a dominant token nor an
-// uneven page scale costs the others' precision. Each tile's product joins the
-// running output in FP32 registers.
+// An item is 8 * RT query rows of a request and cache head (kv_attend.cuh has
+// the work split). Both products run on the tensor cores with the cache's
+// codes as they are, as the 128-row operand: S^T[token][row] = K x Q^T and
+// O^T[dim][row] += V^T x P^T (V read transposed, token-major as it lies in the
+// page). The few query rows are the narrow operand. Queries and weights are
+// split into e4m3 hi + e5m2 lo, two products into one accumulator: hi + lo hold
+// the 8 significant bits of a BF16 query exactly down to 2^-16 of its row's
+// largest magnitude, and a weight of 2^-12 of its row's reference or more within
+// 2^-8 of itself (BF16's own rounding; below that within 2^-20 of the
+// reference); the sum of the weights is taken of the unsplit values. Weights
+// carry their token's value scale, and the reference is a maximum of such
+// products seen so far: while none outgrows it, the output stays in TMEM,
+// accumulated in FP32 by the tensor core, and a tile needs no maxima. Only when
+// one does (and on an item's first tile) they are taken first and the output is
+// rescaled.
 //
 // Roles: a producer warp looks up pages and streams tiles by TMA through a ring,
-// a warp issues the MMAs, four warps do the softmax (thread = token) and hold
-// the output (thread = dimension).
+// a warp issues the MMAs, four warps do the softmax (thread = token) and read
+// the output at the end (thread = dimension).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -36,13 +32,13 @@ namespace {
 constexpr int kProducerWarp = 4;  // after the compute warps 0-3
 constexpr int kIssueWarp = 5;
 constexpr int kThreads = 192;
-constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
-constexpr float kNear = 8.0f;        // log2 distance of a tile's maximum from the running one
+constexpr int kUp = 6;               // weights are held times 2^6, so one may grow to 2^2.75 times its reference's before
+constexpr float kHighest = 430.0f;   // it leaves e4m3
 
 template <int D, int RT>
 struct Shape {
   static constexpr int kRows = 8 * RT;
-  static constexpr int kCols = 2 * kRows;                 // N: hi and lo of each row
+  static constexpr int kCols = RT <= 2 ? 16 : 32;         // N, a multiple of 16: the rows, and columns nobody reads
   static constexpr int kHalves = D >= 128 ? D / 128 : 1;  // 128-byte spans of a cache row
   static constexpr int kSpan = D >= 128 ? 128 : 64;       // bytes of a row in one box: the swizzle's width
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
@@ -53,9 +49,9 @@ struct Shape {
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + kStages * kStageBytes;
-  static constexpr int kP = kQ + kCols * D;
-  static constexpr int kRed = kP + kCols * kTile;         // [row][warp] maxima, then sums
+  static constexpr int kQ = kRing + kStages * kStageBytes;  // hi, lo
+  static constexpr int kP = kQ + 2 * kCols * D;             // hi, lo
+  static constexpr int kRed = kP + 2 * kCols * kTile;       // [row][warp] maxima, then sums
   static constexpr int kRowF = kRed + kRows * 16;         // [row] factor
   static constexpr int kRowLo = kRowF + kRows * 4;        // [row] first and last visible token
   static constexpr int kRowHi = kRowLo + kRows * 4;
@@ -67,6 +63,13 @@ struct Shape {
   static_assert(kPartialOffset + 2ll * kMaxCtas * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand images on swizzle boundaries");
 };
+
+// Eight columns back into TMEM.
+__device__ __forceinline__ void tmem_store_8(uint32_t taddr, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]),
+               "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "r"(taddr)
+               : "memory");
+}
 
 // Eight consecutive TMEM columns of this thread's lane as floats, without the wait.
 __device__ __forceinline__ void tmem_load_8_async(uint32_t taddr, float (&r)[8]) {
@@ -148,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   __shared__ long long s_sum[kThreads / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
+  __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
+  __shared__ long long s_unit;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
-    constexpr uint32_t kScoreDesc = idesc_f8(X::kCols, false), kOutDesc = idesc_f8(X::kCols, true);
+    // (The narrow operand carries the split: hi, then lo.)
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
     int k = 0, segments = 0;
     bool alive = true;
@@ -196,11 +201,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       if (lane == 0) {
         const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes, d = tmem + (i & 1) * X::kCols;
 #pragma unroll
-        for (int st = 0; st < D / 32; ++st) {
-          const int h = st * 32 / X::kSpan, at = st * 32 % X::kSpan;
-          mma_f8(d, smem_desc(keys + h * kTile * X::kSpan + at, 16, kGroup, kMode),
-                 smem_desc(q_at + h * X::kCols * X::kSpan + at, 16, kGroup, kMode), kScoreDesc, st > 0);
-        }
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int st = 0; st < D / 32; ++st) {
+            const int h = st * 32 / X::kSpan, at = st * 32 % X::kSpan;
+            mma_f8(d, smem_desc(keys + h * kTile * X::kSpan + at, 16, kGroup, kMode),
+                   smem_desc(q_at + part * X::kCols * D + h * X::kCols * X::kSpan + at, 16, kGroup, kMode),
+                   idesc_f8(X::kCols, false, false, false, part == 1), part + st > 0);
+          }
         tc_commit(s_full + (i & 1));
       }
       __syncwarp();
@@ -225,9 +233,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
           for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
-            for (int st = 0; st < kTile / 32; ++st)
-              mma_f8(tmem_o + h * X::kCols, smem_desc(vals + (h * kTile + st * 32) * X::kSpan, 0, kGroup, kMode),
-                     smem_desc(p_at + st * 32, 16, 1024, 2), kOutDesc, st > 0);
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int st = 0; st < kTile / 32; ++st)
+                mma_f8(tmem_o + h * X::kCols, smem_desc(vals + (h * kTile + st * 32) * X::kSpan, 0, kGroup, kMode),
+                       smem_desc(p_at + part * X::kCols * kTile + st * 32, 16, 1024, 2), idesc_f8(X::kCols, true, false, false, part == 1),
+                       tile > s.begin || part + st > 0);
           tc_commit(empty + k % X::kStages);
           tc_commit(o_full);
         }
@@ -251,23 +262,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21), lanes_o = tmem_o + (static_cast<uint32_t>(warp) << 21);
     int k = 0;
-    bool failed = false;  // a wait of this thread's ran out; agreed on at the barriers
-    Segment s;
-    s.find(a, prefix, shift, X::kRows, start, stop);
-    for (long long x = start;;) {
-      const Request rq = s.q;
+    bool failed = false, dead = false;  // a wait of this thread's ran out; one of any thread's did, all agreed
+    if (tid == 0) {
+      s_unit = start;
+      s_segment.find(a, prefix, shift, X::kRows, start, stop);
+    }
+    compute_sync();
+    const Segment& s = s_segment;
+    for (;;) {
+      const Request& rq = s.q;
       const int row0 = s.row_tile * X::kRows;
       const int rows = min(X::kRows, static_cast<int>(min(static_cast<long long>(rq.n) * a.group - row0, 1ll << 30)));
-      float acc[X::kHalves][X::kRows], l[X::kRows], m = -INFINITY;  // m: of row `lane`
+      float l[X::kRows], ref[X::kRows];  // sums of this token's weights, less the row's reference
+      float m = -INFINITY;               // reference of row `lane`
+      int m_scale = 0;                   // reference of the value scales
 #pragma unroll
-      for (int i = 0; i < X::kRows; ++i) {
-        l[i] = 0.0f;
-#pragma unroll
-        for (int h = 0; h < X::kHalves; ++h) acc[h][i] = 0.0f;
-      }
+      for (int i = 0; i < X::kRows; ++i) l[i] = ref[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
       if (s.begin < s.end) {
-        // Queries: hi rows, then lo rows, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
+        // Queries: hi image, lo image, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
 #pragma unroll
         for (int base = 0; base < X::kRows * kChunks; base += kCompute) {
@@ -289,12 +302,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            split2(__uint_as_float(v[j] << 16) * down, __uint_as_float(v[j] & 0xFFFF0000u) * down, hi[j], lo[j]);
+            split2_wide(__uint_as_float(v[j] << 16) * down, __uint_as_float(v[j] & 0xFFFF0000u) * down, hi[j], lo[j]);
           if (row >= X::kRows) continue;  // whole warps, past the loop's shuffles
           const int span = c * 8 / X::kSpan, in = c * 8 % X::kSpan;
           uint8_t* dst = sm + X::kQ + span * (X::kCols * X::kSpan) + in % 16;
           *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(row, in / 16)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(X::kRows + row, in / 16)) =
+          *reinterpret_cast<uint2*>(dst + X::kCols * D + chunk_at<X::kSpan>(row, in / 16)) =
               make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           if (c == 0) {
             row_f[row] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : a.scale * kLog2e * pow2f(e);
@@ -317,26 +330,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         all_hi = row_hi[0];
         mixed = any_lo != all_lo || any_hi != all_hi;
       }
-      float pend[X::kRows], pend_vs = 0.0f;  // factors of the output still in TMEM
-      bool pend_f = false;
-      auto take_output = [&](int i) {  // tile i's product joins the running output
-        failed |= !wait(o_full, i & 1, status);
-        __syncwarp();
-        tc_fence_after_sync();
-#pragma unroll
-        for (int h = 0; h < X::kHalves; ++h)
-#pragma unroll
-          for (int part = 0; part < X::kRows; part += 8) {
-            float o[8], u[8];  // hi columns, lo columns
-            tmem_load_8_async(lanes_o + h * X::kCols + part, o);
-            tmem_load_8_async(lanes_o + h * X::kCols + X::kRows + part, u);
-            tmem_wait_8(o);
-            tmem_wait_8(u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[h][part + j] = fmaf(fmaf(u[j], kLo, o[j]), pend_f ? pend[part + j] * pend_vs : pend_vs, acc[h][part + j]);
-          }
-      };
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
         const int stage = k % X::kStages;
         failed |= !wait(s_full + (k & 1), (k >> 1) & 1, status);
@@ -345,96 +338,113 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const uint32_t entry = mt[tid >> shift];
-        const int base = (rq.tile0 + tile) * kTile, token = base + tid;
-        // Edge: some row does not see some token of the tile (every page that all rows see is there, or masked).
-        bool edge = base < all_lo || base + kTile - 1 > all_hi;
-        edge = __any_sync(kAll, edge || !(entry >> 16));
+        const int base = (rq.tile0 + tile) * kTile, token = base + tid, most = static_cast<int>(mt[kMaxPages] & 0xFFu);
+        // Edge: some row does not see some token of the tile.
+        const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
         const float ks = scale_of(entry & 0xFFu);
-        float sc[X::kRows];
+        bool find = tile == s.begin || most > m_scale;
+        if (edge)  // a row's first token
+          find |= __any_sync(kAll, lane < X::kRows && m == -INFINITY && row_hi[min(lane, X::kRows - 1)] >= base &&
+                                       row_lo[min(lane, X::kRows - 1)] < base + kTile);
+        for (int tries = 0;; ++tries) {
+          // Scores of this token, times log2 e.
+          float sc[X::kRows];
 #pragma unroll
-        for (int part = 0; part < X::kRows; part += 8) {
-          float u[8], w[8];  // hi columns, lo columns
-          tmem_load_8_async(lanes + (k & 1) * X::kCols + part, u);
-          tmem_load_8_async(lanes + (k & 1) * X::kCols + X::kRows + part, w);
-          tmem_wait_8(u);
-          tmem_wait_8(w);
+          for (int part = 0; part < X::kRows; part += 8) {
+            float u[8];
+            tmem_load_8_async(lanes + (k & 1) * X::kCols + part, u);
+            tmem_wait_8(u);
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(row_f + part + j);
-            const float fs[4] = {f.x, f.y, f.z, f.w};
+            for (int j = 0; j < 8; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(row_f + part + j);
+              const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[part + j + e] = fmaf(w[j + e], kLo, u[j + e]) * (fs[e] * ks);
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < X::kRows; ++i)
-            if (token < row_lo[i] || token > row_hi[i] || !(entry >> 16)) sc[i] = -INFINITY;
-        }
-        // The tile's maximum of each row: over the warp, then over the four warps.
-        float top = -INFINITY;  // of row `lane`
-#pragma unroll
-        for (int i = 0; i < X::kRows; ++i) {
-          const float v = warp_max(sc[i]);
-          if (lane == i) top = v;
-        }
-        if (lane < X::kRows) red[lane * 4 + warp] = top;
-        failed = compute_any(failed);
-        if (failed) break;
-        float ref = 0.0f, keep = 1.0f, add = 1.0f;
-        if (lane < X::kRows) {
-          const float4 v = *reinterpret_cast<const float4*>(red + lane * 4);
-          top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-          const float mn = fmaxf(m, top);
-          if (mn > -INFINITY) {
-            const bool near = top >= mn - kNear;
-            keep = exp2_fast(m - mn);
-            ref = near ? mn : top;
-            add = near ? 1.0f : exp2_fast(top - mn);
-            if (!(top > -INFINITY)) {
-              ref = 0.0f;
-              add = 0.0f;
+              for (int e = 0; e < 4; ++e) sc[part + j + e] = u[j + e] * (fs[e] * ks);
             }
           }
-          m = mn;
-        }
-        if (tile > s.begin) take_output(k - 1);
-        const bool rescale = __any_sync(kAll, keep != 1.0f);
-        if (rescale) {
+          if (edge) {
 #pragma unroll
-          for (int i = 0; i < X::kRows; ++i) {
-            const float f = __shfl_sync(kAll, keep, i);
-            l[i] *= f;
-#pragma unroll
-            for (int h = 0; h < X::kHalves; ++h) acc[h][i] *= f;
+            for (int i = 0; i < X::kRows; ++i)
+              if (token < row_lo[i] || token > row_hi[i] || !(entry >> 16)) sc[i] = -INFINITY;
           }
-        }
-        pend_f = __any_sync(kAll, add != 1.0f);
-        pend_vs = scale_of(mt[kMaxPages] & 0xFFu) * (1.0f / 256.0f);
-        // Weights against their reference, times 256 and the page's value scale over the tile's largest.
-        const int drop = static_cast<int>((entry >> 8) & 0xFFu) - static_cast<int>(mt[kMaxPages] & 0xFFu);
-        const float up = 256.0f * pow2f(max(drop, -126));
-        uint8_t* prow = sm + X::kP + tid % 16;
+          if (find) {
+            // The references are raised: the largest value scale, and each row's largest score with its token's value
+            // scale (less the largest); what is there already follows.
+            const int scale = max(m_scale, most), rise = min(scale - m_scale, kFar);
+            const float drop = static_cast<float>(max(static_cast<int>((entry >> 8) & 0xFFu) - scale, -kFar));
+            float top = -INFINITY;  // of row `lane`
 #pragma unroll
-        for (int i = 0; i < X::kRows; i += 2) {
-          float p[2];
+            for (int i = 0; i < X::kRows; ++i) {
+              const float v = warp_max(sc[i] + drop);
+              if (lane == i) top = v;
+            }
+            if (lane < X::kRows) red[lane * 4 + warp] = top;
+            dead = compute_any(failed);
+            if (dead) break;
+            float keep_l = 1.0f, keep_o = 1.0f;
+            if (lane < X::kRows) {
+              const float4 v = *reinterpret_cast<const float4*>(red + lane * 4);
+              top = fmaxf(m - static_cast<float>(rise), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+              keep_l = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
+              keep_o = m > -INFINITY ? exp2_fast(m - top + static_cast<float>(m_scale - scale)) : 0.0f;
+              m = top;
+            }
+            m_scale = scale;
+            const float mine = m > -INFINITY ? m : 0.0f;
+            float keeps[X::kRows];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[e] = exp2_fast(sc[i + e] - __shfl_sync(kAll, ref, i + e));
-            if (pend_f) {
-              pend[i + e] = __shfl_sync(kAll, add, i + e);
-              l[i + e] = fmaf(p[e], pend[i + e], l[i + e]);
-            } else {
-              l[i + e] += p[e];
+            for (int i = 0; i < X::kRows; ++i) {
+              ref[i] = __shfl_sync(kAll, mine, i);
+              keeps[i] = __shfl_sync(kAll, keep_o, i);
+              l[i] *= __shfl_sync(kAll, keep_l, i);
+            }
+            if (tile > s.begin) {
+              failed |= !wait(o_full, (k - 1) & 1, status);
+              __syncwarp();
+              tc_fence_after_sync();
+#pragma unroll
+              for (int h = 0; h < X::kHalves; ++h)
+#pragma unroll
+                for (int part = 0; part < X::kRows; part += 8) {
+                  float o[8];
+                  tmem_load_8_async(lanes_o + h * X::kCols + part, o);
+                  tmem_wait_8(o);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) o[j] *= keeps[part + j];
+                  tmem_store_8(lanes_o + h * X::kCols + part, o);
+                }
+              tmem_wait_stores();
             }
           }
-          uint32_t hi, lo;
-          split2_half(p[0] * up, p[1] * up, hi, lo);
-          prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
-          prow[chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(hi >> 8);
-          prow[chunk_at<128>(X::kRows + i, tid / 16)] = static_cast<uint8_t>(lo);
-          prow[chunk_at<128>(X::kRows + i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
+          // Weights: less their reference, times 2^kUp and the page's value scale over its reference, both in the exponent.
+          const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -kFar);
+          const float offset = static_cast<float>(up), down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          if (tile > s.begin) failed |= !wait(o_full, (k - 1) & 1, status);  // the last tile's have been used
+          float high = 0.0f, sums[X::kRows];
+          uint8_t* prow = sm + X::kP + tid % 16;
+#pragma unroll
+          for (int i = 0; i < X::kRows; i += 2) {
+            const float p0 = exp2_fast(sc[i] + (offset - ref[i])), p1 = exp2_fast(sc[i + 1] + (offset - ref[i + 1]));
+            sums[i] = p0;
+            sums[i + 1] = p1;
+            high = fmaxf(high, fmaxf(p0, p1));
+            uint32_t hi, lo;
+            split2_wide_half(p0, p1, hi, lo);
+            prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
+            prow[chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(hi >> 8);
+            prow[X::kCols * kTile + chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(lo);
+            prow[X::kCols * kTile + chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
+          }
+          // Every thread's weights are held against the same references: another round for all if one outgrew its own.
+          // (Or a wait of its ran out: the other round agrees on that.)
+          find = compute_any(high > kHighest || failed);
+          if (!find || tries == 1) {
+#pragma unroll
+            for (int i = 0; i < X::kRows; ++i) l[i] = fmaf(sums[i], down, l[i]);
+            break;
+          }
         }
+        if (dead) break;
         if (edge) {
           // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
           // taken out too, and noted for those.
@@ -469,7 +479,30 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         tc_fence_before_sync();
         mbar_arrive(p_ready);
       }
-      if (s.begin < s.end && !failed) take_output(k - 1);
+      // The output: this thread's dimension of each row.
+      float acc[X::kHalves][X::kRows];
+      if (s.begin < s.end && !failed) {
+        failed |= !wait(o_full, (k - 1) & 1, status);
+        __syncwarp();
+        tc_fence_after_sync();
+        const float out_scale = scale_of(m_scale) * (1.0f / (1 << kUp));
+#pragma unroll
+        for (int h = 0; h < X::kHalves; ++h)
+#pragma unroll
+          for (int part = 0; part < X::kRows; part += 8) {
+            float o[8];
+            tmem_load_8_async(lanes_o + h * X::kCols + part, o);
+            tmem_wait_8(o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[h][part + j] = o[j] * out_scale;
+          }
+        tc_fence_before_sync();
+      } else {
+#pragma unroll
+        for (int h = 0; h < X::kHalves; ++h)
+#pragma unroll
+          for (int i = 0; i < X::kRows; ++i) acc[h][i] = 0.0f;
+      }
 
       // The segment's sums over the tokens, and its rows.
       failed = compute_any(failed);
@@ -523,10 +556,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         }
         join_item<X::kRows, D>(a, s, rows, ctas, total, tid, &s_last);
       }
-      x += s.length;
-      if (x >= stop) break;
-      s.next(a, prefix, shift, X::kRows, x, stop);
-      compute_sync();  // red, the rows' limits and the join word are free again
+      compute_sync();  // red, the rows' limits, the join word and the segment are free again
+      if (tid == 0) {
+        s_unit += s_segment.length;
+        if (s_unit < stop) s_segment.next(a, prefix, shift, X::kRows, s_unit, stop);
+      }
+      compute_sync();
+      if (s_unit >= stop) break;
     }
   }
   tc_fence_before_sync();

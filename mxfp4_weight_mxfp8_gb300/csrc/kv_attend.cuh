@@ -27,6 +27,7 @@ constexpr int kItemTiles = 2;     // what starting and joining an item costs, in
 constexpr int kMaxPages = 8;      // pages of a tile
 constexpr int kMaxCtas = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFar = 100;              // a value scale this many powers of two below the largest counts as no smaller
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -47,11 +48,13 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
-// M = 128 rows of A, N columns of B, FP32 accumulator; B e4m3, A e4m3 or e5m2; either transposed (its rows contiguous).
-__host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed, bool b_transposed = false, bool a_e5m2 = false) {
-  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((a_transposed ? 1u : 0u) << 15) | ((b_transposed ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+// M = 128 rows of A, N columns of B, FP32 accumulator; either transposed (its rows contiguous), either e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed, bool b_transposed, bool a_e5m2, bool b_e5m2) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_transposed ? 1u : 0u) << 15) |
+         ((b_transposed ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
+
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -80,20 +83,19 @@ __device__ __forceinline__ float2 unpack2(uint32_t codes) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
 }
 
-// hi and lo e4m3 codes of two values of magnitude up to 256: v = hi + lo / 16.
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+// Codes of two values: e4m3 hi and e5m2 lo, v = hi + lo.
+__device__ __forceinline__ void split2_wide(float v0, float v1, uint32_t& hi, uint32_t& lo) {
   hi = pack2(v0, v1);
   const float2 f = unpack2(hi);
-  lo = pack2((v0 - f.x) * 16.0f, (v1 - f.y) * 16.0f);
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(v0 - f.x, v1 - f.y), __NV_SATFINITE, __NV_E5M2);
 }
 
-// The same in half precision, for values of which 11 bits are enough: a weight is held to fewer by its codes.
-__device__ __forceinline__ void split2_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+// The same in half precision, for weights.
+__device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
   const __half2 v = __floats2half2_rn(v0, v1);
   hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
-  const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-  const __half2 rest = __hmul2(__hsub2(v, f), __float2half2_rn(16.0f));
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+  const __half2 rest = __hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3)));
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2);
 }
 
 __device__ __forceinline__ uint32_t nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }

@@ -8,10 +8,10 @@
 // products into one accumulator: hi + lo hold the 8 significant bits of a BF16
 // query exactly down to 2^-16 of its row's largest magnitude, and a weight of
 // 2^-10 of its row's reference or more within 2^-8 of itself (BF16's own
-// rounding; below that within 2^-18 of the reference). The reference is a
-// maximum of the row's scores seen so far, and one for the value scales: while
-// no weight outgrows them, the output stays in TMEM, accumulated in FP32 by the
-// tensor core itself, and the scores are read once. Only when one does (and
+// rounding; below that within 2^-18 of the reference). Weights carry their
+// token's value scale, and the reference is a maximum of such products seen so
+// far: while none outgrows it, the output stays in TMEM, accumulated in FP32 by
+// the tensor core itself, and the scores are read once. Only when one does (and
 // on an item's first tile) the maxima are taken first and the output is rescaled.
 //
 // Two groups take a CTA's tiles in turn, one in its softmax while the other's
@@ -96,21 +96,6 @@ __device__ __forceinline__ void for_columns(uint32_t taddr, F&& f) {
   }
 }
 
-// Codes of two values: e4m3 hi and e5m2 lo, v = hi + lo.
-__device__ __forceinline__ void split2_wide(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(v0, v1);
-  const float2 f = unpack2(hi);
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(v0 - f.x, v1 - f.y), __NV_SATFINITE, __NV_E5M2);
-}
-
-// The same in half precision, for weights.
-__device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  const __half2 v = __floats2half2_rn(v0, v1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
-  const __half2 rest = __hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3)));
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2);
-}
-
 __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 
 // Barrier of the two warps that share rows, or of more; true everywhere if any thread brings true.
@@ -136,8 +121,6 @@ __device__ __forceinline__ void tmem_store_16(uint32_t taddr, const float (&r)[1
       "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(taddr)
       : "memory");
 }
-
-__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -216,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int st = 0; st < D / 32; ++st)
             mma_f8(tmem + w * X::kGroupTmem, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode),
-                   smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1), part + st > 0);
+                   smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1, false), part + st > 0);
         tc_commit(k_empty + i % X::kStages);
         tc_commit(s_full + w);
       }
@@ -244,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int st = 0; st < kTile / 32; ++st)
               mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
-                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1),
+                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1, false),
                      !first || part + st > 0);
           tc_commit(v_empty + i % X::kStages);
           tc_commit(o_full + w);
@@ -347,7 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge && !find) find = sync_any<64>(pair, m == -INFINITY && hi >= base && lo < base + kTile);
         for (int tries = 0;; ++tries) {
           if (find) {
-            // The references are raised: the maxima of the row's two halves, and what is there already follows.
+            // The references are raised: the largest value scale, and the row's largest score with its token's value scale
+            // (less the largest), over both halves; what is there already follows.
+            const int scale = max(m_scale, most), rise = min(scale - m_scale, kFar);
             float top = -INFINITY;
             for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
               const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
@@ -362,20 +347,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
               const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-              if (most_here > -INFINITY) top = fmaxf(top, most_here * (factor * scale_of(entry & 0xFFu)));
+              const float drop = static_cast<float>(max(static_cast<int>((entry >> 8) & 0xFFu) - scale, -kFar));
+              if (most_here > -INFINITY) top = fmaxf(top, fmaf(most_here, factor * scale_of(entry & 0xFFu), drop));
             });
             float* mine = tops + (group * 2 + half) * kRows + row;
             *mine = top;
             sync_any<64>(pair, false);
-            top = fmaxf(m, fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
+            top = fmaxf(m - static_cast<float>(rise), fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
             const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
-            const int scale = max(m_scale, most);
             l *= keep;
             if (written) {
               if (!failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
               __syncwarp();
               tc_fence_after_sync();
-              const float f = keep * exp2_fast(static_cast<float>(m_scale - scale));
+              const float f = m > -INFINITY ? exp2_fast(m - top + static_cast<float>(m_scale - scale)) : 0.0f;
 #pragma unroll 1
               for (int c = 0; c < kHalfD; c += 16) {
                 float o[16];
@@ -398,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
             const float f = factor * scale_of(entry & 0xFFu);
             // Times 2^kUp and the page's value scale over its reference, both in the exponent.
-            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -100);
+            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -kFar);
             const float off = static_cast<float>(up) - ref;
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
