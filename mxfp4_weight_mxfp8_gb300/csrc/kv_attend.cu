@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   uint64_t* q_ready = p_ready + 1;        // a segment's queries in shared memory
   uint64_t* drained = q_ready + 1;        // every MMA issued has completed
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
-  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
@@ -169,10 +169,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
-  sum_work<kThreads, X::kRows>(a, shift, prefix, s_sum);
+  const int weight = sum_work<kThreads, X::kRows, D == 64 ? 4 : 2>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
-  constexpr int kLeast = 2;
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kLeast - 1) / kLeast);
+  const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
   if (warp == kIssueWarp) {
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * X::kCols;
 
   if (warp == kProducerWarp) {
-    produce<X, D, 3>(a, maps, prefix, shift, start, stop, sm, meta, full, empty, status);
+    produce<X, D, 3>(a, maps, prefix, weight, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       __syncwarp();
     };
     Segment s;
-    s.find(a, prefix, shift, X::kRows, start, stop);
+    s.find(a, prefix, weight, shift, X::kRows, start, stop);
     for (long long x = start; alive;) {
       if (s.begin < s.end) {
         alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     bool failed = false, dead = false;  // a wait of this thread's ran out; one of any thread's did, all agreed
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, shift, X::kRows, start, stop);
+      s_segment.find(a, prefix, weight, shift, X::kRows, start, stop);
     }
     compute_sync();
     const Segment& s = s_segment;

@@ -23,7 +23,6 @@ using namespace ptx;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kTile = 128;        // cache tokens of a tile
 constexpr int kCompute = 128;     // threads of a compute warpgroup
-constexpr int kItemTiles = 2;     // what starting and joining an item costs, in tiles
 constexpr int kMaxPages = 8;      // pages of a tile
 constexpr int kMaxCtas = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -130,7 +129,7 @@ struct Request {
     tiles = max(1, (end + kTile - 1) / kTile - tile0);
     row_tiles = static_cast<int>((static_cast<long long>(n) * a.group + rows - 1) / rows);
   }
-  __device__ long long work(int heads) const { return static_cast<long long>(heads) * row_tiles * (tiles + kItemTiles); }
+  __device__ long long items(int heads) const { return static_cast<long long>(heads) * row_tiles; }
 };
 
 // A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
@@ -138,20 +137,21 @@ struct Segment {
   Request q;
   int r, head, row_tile;
   int begin, end;          // tiles of the request, from q.tile0 on
-  int length;              // in the units that the work is dealt in: kItemTiles for the item, then its tiles
+  int weight;              // what starting and joining an item counts as, in tiles
+  int length;              // in the units that the work is dealt in: `weight` for the item, then its tiles
   bool first, whole;       // the item starts here; and ends here too
   long long item;          // the item's first unit among all
 
   // The item's tiles from unit `from` on, as far as the run goes and this row tile's queries see.
   __device__ __forceinline__ void cut(const AttendArgs& a, int rows, long long x, long long stop, int from) {
-    const int units = q.tiles + kItemTiles;
+    const int units = q.tiles + weight;
     const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
     item = x - from;
     length = to - from;
     whole = length == units;
     first = from == 0;
-    begin = max(0, from - kItemTiles);
-    end = max(0, to - kItemTiles);
+    begin = max(0, from - weight);
+    end = max(0, to - weight);
     const int before = q.seq - q.n;  // position of the request's first query
     const int last = min(q.n - 1, static_cast<int>((static_cast<long long>(row_tile + 1) * rows - 1) / a.group));
     end = min(end, (min(q.end, max(0, before + last + 1)) + kTile - 1) / kTile - q.tile0);
@@ -163,7 +163,9 @@ struct Segment {
   }
 
   // The segment at unit x of a run that ends at `stop`.
-  __device__ void find(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
+  __device__ void find(const AttendArgs& a, const long long* prefix, int item_weight, int shift, int rows, long long x,
+                       long long stop) {
+    weight = item_weight;
     int lo = 0, hi = a.b.requests;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -172,7 +174,7 @@ struct Segment {
     }
     r = lo;
     q = Request(a, shift, r, rows);
-    const int units = q.tiles + kItemTiles;
+    const int units = q.tiles + weight;
     const long long local = x - prefix[lo], index = divide(local, units);
     row_tile = static_cast<int>(divide(index, a.c.kv_heads));
     head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
@@ -211,43 +213,64 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* st
   return mbar_test(bar, parity) || wait_more(bar, parity, status);
 }
 
-// Prefix sums of the requests' work, by the whole CTA of kThreads threads.
-template <int kThreads, int kRows>
-__device__ void sum_work(const AttendArgs& a, int shift, long long* prefix, long long* s_sum) {
+// Prefix sums of the requests' work, by the whole CTA of kThreads threads; returns what an item counts as: nothing
+// while there are no more tiles than CTAs, so that each gets one, else kItemTiles.
+template <int kThreads, int kRows, int kItemTiles>
+__device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long long (*s_sum)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.b.requests + kThreads - 1) / kThreads;
-  long long sum = 0;
+  long long tiles = 0, items = 0;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
-    if (r < a.b.requests) sum += Request(a, shift, r, kRows).work(a.c.kv_heads);
+    if (r < a.b.requests) {
+      const Request q(a, shift, r, kRows);
+      items += q.items(a.c.kv_heads);
+      tiles += q.items(a.c.kv_heads) * q.tiles;
+    }
   }
-  long long in = sum;
+  long long tiles_in = tiles, items_in = items;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long u = __shfl_up_sync(kAll, in, d);
-    if (lane >= d) in += u;
+    const long long u = __shfl_up_sync(kAll, tiles_in, d), v = __shfl_up_sync(kAll, items_in, d);
+    if (lane >= d) {
+      tiles_in += u;
+      items_in += v;
+    }
   }
-  if (lane == 31) s_sum[warp] = in;
+  if (lane == 31) {
+    s_sum[warp][0] = tiles_in;
+    s_sum[warp][1] = items_in;
+  }
   __syncthreads();
-  long long at = in - sum;
-  for (int w = 0; w < warp; ++w) at += s_sum[w];
+  long long all = 0, tiles_at = tiles_in - tiles, items_at = items_in - items;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    all += s_sum[w][0];
+    if (w < warp) {
+      tiles_at += s_sum[w][0];
+      items_at += s_sum[w][1];
+    }
+  }
+  const int weight = all > gridDim.x ? kItemTiles : 0;
+  long long at = tiles_at + items_at * weight;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r < a.b.requests) {
       prefix[r] = at;
-      at += Request(a, shift, r, kRows).work(a.c.kv_heads);
+      const Request q(a, shift, r, kRows);
+      at += q.items(a.c.kv_heads) * (q.tiles + weight);
       if (r == a.b.requests - 1) prefix[r + 1] = at;
     }
   }
   __syncthreads();
+  return weight;
 }
 
 // A producer warp: looks up the pages of the CTA's tiles and streams their keys (kWhich 1), values (2) or both (3)
 // through the ring. With the values go the pages' entries: key scale, value scale << 8, present << 16; and after a
 // tile's, its largest value scale and, << 8, whether every page is there.
 template <class X, int D, int kWhich>
-__device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int shift, long long start,
-                        long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
+__device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int weight, int shift,
+                        long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
   const int lane = threadIdx.x & 31;
   const uint64_t policy = policy_evict_first();
   const int per_tile = kTile >> shift, in_tile = lane & (per_tile - 1);  // pages of a tile; this lane's
@@ -255,7 +278,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   int k = 0;
   bool alive = true;
   Segment s;
-  s.find(a, prefix, shift, X::kRows, start, stop);
+  s.find(a, prefix, weight, shift, X::kRows, start, stop);
   for (long long x = start; alive;) {
     const Request& q = s.q;
     int page = -1;
@@ -327,7 +350,7 @@ __device__ void join_item(const AttendArgs& a, const Segment& s, int rows, long 
   const int row0 = s.row_tile * kRows;
   // The CTAs of this item: c0 .. c1, by the bounds of their runs.
   const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
-  const int c1 = static_cast<int>(divide((s.item + rq.tiles + kItemTiles) * ctas - 1, total));
+  const int c1 = static_cast<int>(divide((s.item + rq.tiles + s.weight) * ctas - 1, total));
   // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
   // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces.
   float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * kPartialFloats;  // the first piece

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drained = p_ready + kGroups;   // [group]: every product issued has completed
   uint64_t* q_ready = drained + kGroups;
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
-  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_ready, kAllCompute);
     fence_mbar_init();
   }
-  sum_work<kThreads, kRows>(a, shift, prefix, s_sum);
+  const int weight = sum_work<kThreads, kRows, D == 64 ? 4 : 2>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kItemTiles) / (kItemTiles + 1));
+  const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
   if (warp == kIssueWarp) {
@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;  // group g: scores at 256 g, output at 256 g + 128
 
   if (warp == kProducerWarp) {
-    produce<X, D, 1>(a, maps, prefix, shift, start, stop, sm, meta, k_full, k_empty, status);
+    produce<X, D, 1>(a, maps, prefix, weight, shift, start, stop, sm, meta, k_full, k_empty, status);
   } else if (warp == kProducerWarp + 1) {
-    produce<X, D, 2>(a, maps, prefix, shift, start, stop, sm, meta, v_full, v_empty, status);
+    produce<X, D, 2>(a, maps, prefix, weight, shift, start, stop, sm, meta, v_full, v_empty, status);
   } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     Segment s;
-    s.find(a, prefix, shift, kRows, start, stop);
+    s.find(a, prefix, weight, shift, kRows, start, stop);
     for (long long x = start; alive;) {
       const int last = k + s.end - s.begin;
       if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool failed = false;   // a wait ran out: no more waits; agreed on at the barriers
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, shift, kRows, start, stop);
+      s_segment.find(a, prefix, weight, shift, kRows, start, stop);
     }
     all_sync();
     const Segment& s = s_segment;
