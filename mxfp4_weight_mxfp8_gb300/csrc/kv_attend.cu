@@ -6,11 +6,12 @@
 // codes as they are, as the 128-row operand: S^T[token][row] = K x Q^T and
 // O^T[dim][row] += V^T x P^T (V read transposed, token-major as it lies in the
 // page). The few query rows are the narrow operand. Queries and weights are
-// split into e4m3 hi + e5m2 lo, two products into one accumulator: hi + lo hold
-// the 8 significant bits of a BF16 query exactly down to 2^-16 of its row's
-// largest magnitude, and a weight of 2^-12 of its row's reference or more within
-// 2^-8 of itself (BF16's own rounding; below that within 2^-20 of the
-// reference); the sum of the weights is taken of the unsplit values. Weights
+// split into two e4m3 numbers, hi + lo / 16, which take two columns of the one
+// product (the wide operand is read from shared memory once for both): together
+// they hold the 8 significant bits of a BF16 query exactly down to 2^-14 of its
+// row's largest magnitude, and a weight of 2^-12 of its row's reference or more
+// within 2^-9 of itself (below that within 2^-21 of the reference); the sum of
+// the weights is taken of the unsplit values. Weights
 // carry their token's value scale, and the reference is a maximum of such
 // products seen so far: while none outgrows it, the output stays in TMEM,
 // accumulated in FP32 by the tensor core, and a tile needs no maxima. Only when
@@ -32,13 +33,14 @@ namespace {
 constexpr int kProducerWarp = 4;  // after the compute warps 0-3
 constexpr int kIssueWarp = 5;
 constexpr int kThreads = 192;
+constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
 constexpr int kUp = 6;               // weights are held times 2^6, so one may grow to 2^2.75 times its reference's before
 constexpr float kHighest = 430.0f;   // it leaves e4m3
 
 template <int D, int RT>
 struct Shape {
   static constexpr int kRows = 8 * RT;
-  static constexpr int kCols = RT <= 2 ? 16 : 32;         // N, a multiple of 16: the rows, and columns nobody reads
+  static constexpr int kCols = 2 * kRows;                 // N: hi and lo of each row
   static constexpr int kHalves = D >= 128 ? D / 128 : 1;  // 128-byte spans of a cache row
   static constexpr int kSpan = D >= 128 ? 128 : 64;       // bytes of a row in one box: the swizzle's width
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
@@ -49,9 +51,9 @@ struct Shape {
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + kStages * kStageBytes;  // hi, lo
-  static constexpr int kP = kQ + 2 * kCols * D;             // hi, lo
-  static constexpr int kRed = kP + 2 * kCols * kTile;       // [row][warp] maxima, then sums
+  static constexpr int kQ = kRing + kStages * kStageBytes;  // hi rows, lo rows
+  static constexpr int kP = kQ + kCols * D;                 // hi rows, lo rows
+  static constexpr int kRed = kP + kCols * kTile;           // [row][warp] maxima, then sums
   static constexpr int kRowF = kRed + kRows * 16;         // [row] factor
   static constexpr int kRowLo = kRowF + kRows * 4;        // [row] first and last visible token
   static constexpr int kRowHi = kRowLo + kRows * 4;
@@ -189,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
     // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
-    // (The narrow operand carries the split: hi, then lo.)
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
     int k = 0, segments = 0;
     bool alive = true;
@@ -200,14 +201,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       if (lane == 0) {
         const uint32_t keys = ring + (i % X::kStages) * X::kStageBytes, d = tmem + (i & 1) * X::kCols;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int st = 0; st < D / 32; ++st) {
-            const int h = st * 32 / X::kSpan, at = st * 32 % X::kSpan;
-            mma_f8(d, smem_desc(keys + h * kTile * X::kSpan + at, 16, kGroup, kMode),
-                   smem_desc(q_at + part * X::kCols * D + h * X::kCols * X::kSpan + at, 16, kGroup, kMode),
-                   idesc_f8(X::kCols, false, false, false, part == 1), part + st > 0);
-          }
+        for (int st = 0; st < D / 32; ++st) {
+          const int h = st * 32 / X::kSpan, at = st * 32 % X::kSpan;
+          mma_f8(d, smem_desc(keys + h * kTile * X::kSpan + at, 16, kGroup, kMode),
+                 smem_desc(q_at + h * X::kCols * X::kSpan + at, 16, kGroup, kMode), idesc_f8(X::kCols, false), st > 0);
+        }
         tc_commit(s_full + (i & 1));
       }
       __syncwarp();
@@ -232,12 +230,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
           for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int st = 0; st < kTile / 32; ++st)
-                mma_f8(tmem_o + h * X::kCols, smem_desc(vals + (h * kTile + st * 32) * X::kSpan, 0, kGroup, kMode),
-                       smem_desc(p_at + part * X::kCols * kTile + st * 32, 16, 1024, 2), idesc_f8(X::kCols, true, false, false, part == 1),
-                       tile > s.begin || part + st > 0);
+            for (int st = 0; st < kTile / 32; ++st)
+              mma_f8(tmem_o + h * X::kCols, smem_desc(vals + (h * kTile + st * 32) * X::kSpan, 0, kGroup, kMode),
+                     smem_desc(p_at + st * 32, 16, 1024, 2), idesc_f8(X::kCols, true), tile > s.begin || st > 0);
           tc_commit(empty + k % X::kStages);
           tc_commit(o_full);
         }
@@ -279,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       for (int i = 0; i < X::kRows; ++i) l[i] = ref[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
       if (s.begin < s.end) {
-        // Queries: hi image, lo image, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
+        // Queries: hi rows, then lo rows, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
 #pragma unroll
         for (int base = 0; base < X::kRows * kChunks; base += kCompute) {
@@ -301,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            split2_wide(__uint_as_float(v[j] << 16) * down, __uint_as_float(v[j] & 0xFFFF0000u) * down, hi[j], lo[j]);
+            split2(__uint_as_float(v[j] << 16) * down, __uint_as_float(v[j] & 0xFFFF0000u) * down, hi[j], lo[j]);
           if (row >= X::kRows) continue;  // whole warps, past the loop's shuffles
           const int span = c * 8 / X::kSpan, in = c * 8 % X::kSpan;
           uint8_t* dst = sm + X::kQ + span * (X::kCols * X::kSpan) + in % 16;
           *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(row, in / 16)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(dst + X::kCols * D + chunk_at<X::kSpan>(row, in / 16)) =
+          *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(X::kRows + row, in / 16)) =
               make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           if (c == 0) {
             row_f[row] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : a.scale * kLog2e * pow2f(e);
@@ -350,15 +345,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           float sc[X::kRows];
 #pragma unroll
           for (int part = 0; part < X::kRows; part += 8) {
-            float u[8];
+            float u[8], w[8];  // hi columns, lo columns
             tmem_load_8_async(lanes + (k & 1) * X::kCols + part, u);
+            tmem_load_8_async(lanes + (k & 1) * X::kCols + X::kRows + part, w);
             tmem_wait_8(u);
+            tmem_wait_8(w);
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
               const float4 f = *reinterpret_cast<const float4*>(row_f + part + j);
               const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sc[part + j + e] = u[j + e] * (fs[e] * ks);
+              for (int e = 0; e < 4; ++e) sc[part + j + e] = fmaf(w[j + e], kLo, u[j + e]) * (fs[e] * ks);
             }
           }
           if (edge) {
@@ -404,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
               for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
-                for (int part = 0; part < X::kRows; part += 8) {
+                for (int part = 0; part < X::kCols; part += 8) {
                   float o[8];
                   tmem_load_8_async(lanes_o + h * X::kCols + part, o);
                   tmem_wait_8(o);
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) o[j] *= keeps[part + j];
+                  for (int j = 0; j < 8; ++j) o[j] *= keeps[(part + j) % X::kRows];
                   tmem_store_8(lanes_o + h * X::kCols + part, o);
                 }
               tmem_wait_stores();
@@ -428,11 +425,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
             sums[i + 1] = p1;
             high = fmaxf(high, fmaxf(p0, p1));
             uint32_t hi, lo;
-            split2_wide_half(p0, p1, hi, lo);
+            split2_half(p0, p1, hi, lo);
             prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
             prow[chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(hi >> 8);
-            prow[X::kCols * kTile + chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(lo);
-            prow[X::kCols * kTile + chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
+            prow[chunk_at<128>(X::kRows + i, tid / 16)] = static_cast<uint8_t>(lo);
+            prow[chunk_at<128>(X::kRows + i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
           }
           // Every thread's weights are held against the same references: another round for all if one outgrew its own.
           // (Or a wait of its ran out: the other round agrees on that.)
@@ -489,11 +486,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
           for (int part = 0; part < X::kRows; part += 8) {
-            float o[8];
+            float o[8], u[8];  // hi columns, lo columns
             tmem_load_8_async(lanes_o + h * X::kCols + part, o);
+            tmem_load_8_async(lanes_o + h * X::kCols + X::kRows + part, u);
             tmem_wait_8(o);
+            tmem_wait_8(u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[h][part + j] = o[j] * out_scale;
+            for (int j = 0; j < 8; ++j) acc[h][part + j] = fmaf(u[j], kLo, o[j]) * out_scale;
           }
         tc_fence_before_sync();
       } else {

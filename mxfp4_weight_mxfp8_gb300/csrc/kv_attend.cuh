@@ -47,9 +47,9 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
-// M = 128 rows of A, N columns of B, FP32 accumulator; either transposed (its rows contiguous), either e4m3 or e5m2.
-__host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed, bool b_transposed, bool a_e5m2, bool b_e5m2) {
-  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_transposed ? 1u : 0u) << 15) |
+// M = 128 rows of A, N columns of B, FP32 accumulator; either transposed (its rows contiguous); B e4m3, A e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed, bool b_transposed = false, bool a_e5m2 = false) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((a_transposed ? 1u : 0u) << 15) |
          ((b_transposed ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
@@ -80,6 +80,22 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t codes) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
+}
+
+// Codes of two values of magnitude up to 448: e4m3 hi and lo, v = hi + lo / 16.
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(v0, v1);
+  const float2 f = unpack2(hi);
+  lo = pack2((v0 - f.x) * 16.0f, (v1 - f.y) * 16.0f);
+}
+
+// The same in half precision, for weights: 11 bits are more than the codes hold.
+__device__ __forceinline__ void split2_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  const __half2 v = __floats2half2_rn(v0, v1);
+  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
+  const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
+  const __half2 rest = __hmul2(__hsub2(v, f), __float2half2_rn(16.0f));
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Codes of two values: e4m3 hi and e5m2 lo, v = hi + lo.

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int st = 0; st < D / 32; ++st)
             mma_f8(tmem + w * X::kGroupTmem, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode),
-                   smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1, false), part + st > 0);
+                   smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1), part + st > 0);
         tc_commit(k_empty + i % X::kStages);
         tc_commit(s_full + w);
       }
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int st = 0; st < kTile / 32; ++st)
               mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
-                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1, false),
+                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1),
                      !first || part + st > 0);
           tc_commit(v_empty + i % X::kStages);
           tc_commit(o_full + w);
