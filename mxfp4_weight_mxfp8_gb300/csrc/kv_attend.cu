@@ -57,7 +57,8 @@ struct Shape {
   static constexpr int kRowF = kRed + kRows * 16;         // [row] factor
   static constexpr int kRowLo = kRowF + kRows * 4;        // [row] first and last visible token
   static constexpr int kRowHi = kRowLo + kRows * 4;
-  static constexpr int kNan = kRowHi + kRows * 4;         // [row][D / 32]: outputs that saw a NaN apart
+  static constexpr int kRowDst = kRowHi + kRows * 4;      // [row] its place among the outputs' rows
+  static constexpr int kNan = kRowDst + kRows * 8;        // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;      // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
   static constexpr int kPrefix = kBars + (2 * kStages + 6) * 8;  // full, empty, s_full[2], o_full, p_ready, q_ready, drained
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
     int* row_lo = reinterpret_cast<int*>(sm + X::kRowLo);
     int* row_hi = reinterpret_cast<int*>(sm + X::kRowHi);
+    long long* row_dst = reinterpret_cast<long long*>(sm + X::kRowDst);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21), lanes_o = tmem_o + (static_cast<uint32_t>(warp) << 21);
     int k = 0;
@@ -273,6 +275,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
       for (int i = 0; i < X::kRows; ++i) l[i] = ref[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
+      if (tid < X::kRows) {
+        const int at = row0 + tid, tok = at / a.group, last = tid < rows ? rq.seq - rq.n + tok : -1;
+        row_hi[tid] = last;
+        row_lo[tid] = tid < rows && a.window > 0 ? max(0, last - a.window + 1) : 0;
+        row_dst[tid] = static_cast<long long>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
+      }
       if (s.begin < s.end) {
         // Queries: hi rows, then lo rows, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
@@ -303,12 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(row, in / 16)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
           *reinterpret_cast<uint2*>(dst + chunk_at<X::kSpan>(X::kRows + row, in / 16)) =
               make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-          if (c == 0) {
-            row_f[row] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : a.scale * kLog2e * pow2f(e);
-            const int last = used ? rq.seq - rq.n + tok : -1;
-            row_hi[row] = last;
-            row_lo[row] = used && a.window > 0 ? max(0, last - a.window + 1) : 0;
-          }
+          if (c == 0) row_f[row] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : a.scale * kLog2e * pow2f(e);
         }
         for (int i = tid; i < X::kRows * D / 32; i += kCompute) nans[i] = 0;
         fence_proxy_async_shared();
@@ -387,14 +390,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
             }
             m_scale = scale;
             const float mine = m > -INFINITY ? m : 0.0f;
-            float keeps[X::kRows];
 #pragma unroll
-            for (int i = 0; i < X::kRows; ++i) {
-              ref[i] = __shfl_sync(kAll, mine, i);
-              keeps[i] = __shfl_sync(kAll, keep_o, i);
-              l[i] *= __shfl_sync(kAll, keep_l, i);
-            }
+            for (int i = 0; i < X::kRows; ++i) ref[i] = __shfl_sync(kAll, mine, i);
             if (tile > s.begin) {
+              float keeps[X::kRows];
+#pragma unroll
+              for (int i = 0; i < X::kRows; ++i) {
+                keeps[i] = __shfl_sync(kAll, keep_o, i);
+                l[i] *= __shfl_sync(kAll, keep_l, i);
+              }
               failed |= !wait(o_full, (k - 1) & 1, status);
               __syncwarp();
               tc_fence_after_sync();
@@ -523,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       }
       const bool holds = D >= 128 || tid < D;  // this thread's dimension (D = 64: the upper lanes repeat the lower)
       auto store_row = [&](int i, float v0, float v1, float inv, float lse) {
-        const int at = row0 + i, tok = at / a.group;
-        const int64_t dst = static_cast<int64_t>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
+        const int64_t dst = row_dst[i];
         if (holds) {
           a.out[dst * D + tid] = __bfloat16_as_ushort(__float2bfloat16(v0 * inv));
           if (X::kHalves == 2) a.out[dst * D + 128 + tid] = __bfloat16_as_ushort(__float2bfloat16(v1 * inv));
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           mine[X::kRows * D + tid] = m;
           mine[X::kRows * D + X::kRows + tid] = sum;
         }
-        join_item<X::kRows, D>(a, s, rows, ctas, total, tid, &s_last);
+        join_item<X::kRows, D>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       }
       compute_sync();  // red, the rows' limits, the join word and the segment are free again
       if (tid == 0) {

@@ -356,14 +356,15 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
 }
 
-// A piece of an item has been stored: joins the item's pieces once they are all there. By one warpgroup (barrier 1).
+// A piece of an item has been stored: joins the item's pieces once they are all there. By one warpgroup (barrier 1);
+// row_dst: the rows' places among the outputs' rows.
 template <int kRows, int D>
-__device__ void join_item(const AttendArgs& a, const Segment& s, int rows, long long ctas, long long total, int tid, int* s_last) {
+__device__ void join_item(const AttendArgs& a, const Segment& s, const long long* row_dst, int rows, long long ctas, long long total,
+                          int tid, int* s_last) {
   constexpr int kPartialFloats = kRows * (D + 2);
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
   const Request& rq = s.q;
-  const int row0 = s.row_tile * kRows;
   // The CTAs of this item: c0 .. c1, by the bounds of their runs.
   const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
   const int c1 = static_cast<int>(divide((s.item + rq.tiles + s.weight) * ctas - 1, total));
@@ -455,8 +456,7 @@ __device__ void join_item(const AttendArgs& a, const Segment& s, int rows, long 
         }
         if (i >= rows) continue;
         const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
-        const int at = row0 + i, tok = at / a.group;
-        const int64_t dst = static_cast<int64_t>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
+        const int64_t dst = row_dst[i];
         __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv), __floats2bfloat162_rn(o[u].z * inv, o[u].w * inv)};
         *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
         if (a.lse != nullptr && c4 == 0) a.lse[dst] = total_l[u] == 0.0f ? -INFINITY : (top[u] + log2f(total_l[u])) * kLn2;

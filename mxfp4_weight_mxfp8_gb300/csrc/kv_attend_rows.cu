@@ -47,7 +47,8 @@ struct RowsShape {
   static constexpr int kRowF = kP + kGroups * 2 * kRows * kTile;     // [row] factor
   static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
   static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [row] the second group's reference; its value scale's
-  static constexpr int kNan = kRefs + kRows * 4 + 16;                // [row][D / 32]: outputs that saw a NaN apart
+  static constexpr int kRowDst = kRefs + kRows * 4 + 16;             // [row] its place among the outputs' rows
+  static constexpr int kNan = kRowDst + kRows * 8;                  // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
   static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* tops = reinterpret_cast<float*>(sm + X::kTops);
     float* refs = reinterpret_cast<float*>(sm + X::kRefs);
     int* ref_scale = reinterpret_cast<int*>(refs + kRows);
+    long long* row_dst = reinterpret_cast<long long*>(sm + X::kRowDst);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     float* join = reinterpret_cast<float*>(sm + X::kP);
     uint8_t* weights = sm + X::kP + group * 2 * kRows * kTile;
@@ -305,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         all_sync();
       }
       const int tok = (row0 + row) / a.group;
+      if (tid < kRows) row_dst[row] = static_cast<long long>(s.q.first + tok) * a.q_heads + s.head * a.group + row0 + row - tok * a.group;
       const int hi = row < rows ? before + tok : -1, lo = row < rows && a.window > 0 ? max(0, hi - a.window + 1) : 0;
       // Tokens that any of the rows sees, and that all see.
       const int any_hi = before + (row0 + rows - 1) / a.group, all_hi = before + row0 / a.group;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s.whole) {
           if (row < rows) {
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-            const int64_t dst = static_cast<int64_t>(s.q.first + tok) * a.q_heads + s.head * a.group + row0 + row - tok * a.group;
+            const int64_t dst = row_dst[row];
 #pragma unroll
             for (int c = 0; c < kHalfD; c += 8) {
               __nv_bfloat162 w[4];
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mine[kRows * D + kRows + row] = l;
           }
           sync_any<kGroupThreads>(4 + 8, false);  // both halves' stores, ahead of the first warpgroup's release of them
-          if (half == 0) join_item<kRows, D>(a, s, rows, ctas, total, tid, &s_last);
+          if (half == 0) join_item<kRows, D>(a, s, row_dst, rows, ctas, total, tid, &s_last);
         }
       }
       all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
