@@ -35,7 +35,7 @@ constexpr int kIssueWarp = 5;
 constexpr int kThreads = 192;
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
 constexpr int kUp = 6;               // weights are held times 2^6, so one may grow to 2^2.75 times its reference's before
-constexpr float kHighest = 430.0f;   // it leaves e4m3
+constexpr float kHighest = 8.75f;    // it leaves e4m3 at 2^8.75 (430)
 
 template <int D, int RT>
 struct Shape {
@@ -46,15 +46,17 @@ struct Shape {
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kKeyStride = kStageBytes, kValuesAt = kTileBytes, kValueStride = kStageBytes;
-  static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 ? 3 : 2;
-  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : 5) : (D == 128 && RT != 2 ? 2 : 3);
+  // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring.
+  static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 || (D == 64 && RT == 3) ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 4 ? 5 : 3) : D == 128 ? 2 : 3;
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kStages * kStageBytes;  // hi rows, lo rows
   static constexpr int kP = kQ + kCols * D;                 // hi rows, lo rows
   static constexpr int kRed = kP + kCols * kTile;           // [row][warp] maxima, then sums
-  static constexpr int kRowF = kRed + kRows * 16;         // [row] factor
+  static constexpr int kRef = kRed + kRows * 16;          // [warp][row] the weights' references
+  static constexpr int kRowF = kRef + kRows * 16;         // [row] factor
   static constexpr int kRowLo = kRowF + kRows * 4;        // [row] first and last visible token
   static constexpr int kRowHi = kRowLo + kRows * 4;
   static constexpr int kRowDst = kRowHi + kRows * 4;      // [row] its place among the outputs' rows
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     __syncwarp();
   } else {
     float* red = reinterpret_cast<float*>(sm + X::kRed);
+    float* refs = reinterpret_cast<float*>(sm + X::kRef) + warp * X::kRows;
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
     int* row_lo = reinterpret_cast<int*>(sm + X::kRowLo);
     int* row_hi = reinterpret_cast<int*>(sm + X::kRowHi);
@@ -269,11 +272,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       const Request& rq = s.q;
       const int row0 = s.row_tile * X::kRows;
       const int rows = min(X::kRows, static_cast<int>(min(static_cast<long long>(rq.n) * a.group - row0, 1ll << 30)));
-      float l[X::kRows], ref[X::kRows];  // sums of this token's weights, less the row's reference
+      float l[X::kRows];                 // sums of this thread's tokens' weights against the references
       float m = -INFINITY;               // reference of row `lane`
       int m_scale = 0;                   // reference of the value scales
 #pragma unroll
-      for (int i = 0; i < X::kRows; ++i) l[i] = ref[i] = 0.0f;
+      for (int i = 0; i < X::kRows; ++i) l[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
       if (tid < X::kRows) {
         const int at = row0 + tid, tok = at / a.group, last = tid < rows ? rq.seq - rq.n + tok : -1;
@@ -389,9 +392,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               m = top;
             }
             m_scale = scale;
-            const float mine = m > -INFINITY ? m : 0.0f;
-#pragma unroll
-            for (int i = 0; i < X::kRows; ++i) ref[i] = __shfl_sync(kAll, mine, i);
+            if (lane < X::kRows) refs[lane] = m > -INFINITY ? m : 0.0f;
+            __syncwarp();
             if (tile > s.begin) {
               float keeps[X::kRows];
 #pragma unroll
@@ -416,18 +418,31 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               tmem_wait_stores();
             }
           }
-          // Weights: less their reference, times 2^kUp and the page's value scale over its reference, both in the exponent.
+          // Less their reference, times 2^kUp and the page's value scale over its reference, all in the exponent.
           const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -kFar);
-          const float offset = static_cast<float>(up), down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          const float offset = static_cast<float>(up);
+          float high = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < X::kRows; i += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(refs + i);
+            sc[i] += offset - r.x;
+            sc[i + 1] += offset - r.y;
+            sc[i + 2] += offset - r.z;
+            sc[i + 3] += offset - r.w;
+            high = fmaxf(high, fmaxf(fmaxf(sc[i], sc[i + 1]), fmaxf(sc[i + 2], sc[i + 3])));
+          }
+          // Every thread's weights are held against the same references: another round for all if one outgrew its own.
+          // (Or a wait of its ran out: the other round agrees on that.)
+          find = compute_any(high > kHighest || failed);
+          if (find && tries == 0) continue;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
           if (tile > s.begin) failed |= !wait(o_full, (k - 1) & 1, status);  // the last tile's have been used
-          float high = 0.0f, sums[X::kRows];
           uint8_t* prow = sm + X::kP + tid % 16;
 #pragma unroll
           for (int i = 0; i < X::kRows; i += 2) {
-            const float p0 = exp2_fast(sc[i] + (offset - ref[i])), p1 = exp2_fast(sc[i + 1] + (offset - ref[i + 1]));
-            sums[i] = p0;
-            sums[i + 1] = p1;
-            high = fmaxf(high, fmaxf(p0, p1));
+            const float p0 = exp2_fast(sc[i]), p1 = exp2_fast(sc[i + 1]);
+            l[i] = fmaf(p0, down, l[i]);
+            l[i + 1] = fmaf(p1, down, l[i + 1]);
             uint32_t hi, lo;
             split2_half(p0, p1, hi, lo);
             prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
@@ -435,14 +450,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
             prow[chunk_at<128>(X::kRows + i, tid / 16)] = static_cast<uint8_t>(lo);
             prow[chunk_at<128>(X::kRows + i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
           }
-          // Every thread's weights are held against the same references: another round for all if one outgrew its own.
-          // (Or a wait of its ran out: the other round agrees on that.)
-          find = compute_any(high > kHighest || failed);
-          if (!find || tries == 1) {
-#pragma unroll
-            for (int i = 0; i < X::kRows; ++i) l[i] = fmaf(sums[i], down, l[i]);
-            break;
-          }
+          break;
         }
         if (dead) break;
         if (edge) {
