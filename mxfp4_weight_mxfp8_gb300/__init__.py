@@ -26,7 +26,7 @@ __all__ = [
     "MAX_BATCH", "moe_device_supported", "moe_small_batch_build", "SMALL_NONE", "SMALL_PACKED", "SMALL_WIDE", "moe_debug_kernel_span", "moe_read_kernel_span",
     "moe_kernel_path", "PATH_GRID", "PATH_SMALL", "PATH_CLUSTER", "PATH_SMALL_WIDE",
     "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
-    "MOE_KV_WORKSPACE_BYTES", "MOE_KV_MAX_REQUESTS",
+    "MOE_KV_WORKSPACE_BYTES", "MOE_KV_WORKSPACE_HEADER", "MOE_KV_MAX_REQUESTS",
 ]
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
@@ -35,6 +35,7 @@ MOE_NOALLOC_SCRATCH_BYTES = 8 << 20  # static scratch of moe_run_noalloc
 TOPK, UNIT_ROWS, MAX_BATCH = 16, 8, 256
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 MOE_KV_WORKSPACE_BYTES = 32 << 20  # workspace of moe_kv_attend
+MOE_KV_WORKSPACE_HEADER = 8192  # its bytes that must start as zero
 MOE_KV_MAX_REQUESTS = 1024
 
 

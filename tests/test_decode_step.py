@@ -643,6 +643,86 @@ def test_attend_uneven_scores_and_scales(moe, page, dim):
     check_attend(moe, cache, q * 2.0 ** -70, table, start, seq, scale=dim ** -0.5 * 2.0 ** 70)
 
 
+FORMS = [(1, 4), (2, 12), (3, 24), (40, 8), (90, 4)]  # query rows of a request, query heads on one cache head
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", FORMS)
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128)])
+def test_attend_growing_scores_and_scales(moe, page, dim, rows, q_heads):
+    """Scores that rise along the context by far more than a weight may outgrow its reference, value scales that rise and fall."""
+    rng = np.random.default_rng(rows * dim)
+    n = 900
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    k, v, ks, vs = cache
+    direction = rng.standard_normal(dim)
+    for t in range(n):
+        k[table[0, t // page], 0, t % page] = e4m3_encode(direction * (10 + 80 * t / n) + rng.standard_normal(dim) * 10)
+    for j in range(-(-n // page)):
+        ks[table[0, j]], vs[table[0, j]] = 121, 118 + (7 * j) % 11
+    q = bf16(direction * 1.5 + 0.3 * rng.standard_normal((rows, q_heads, dim)))
+    scale = 24.0 / (direction @ direction)  # the last scores about 20
+    check_attend(moe, cache, q, table, start, seq, scale=scale * 0.75)
+    check_attend(moe, cache, -q, table, start, seq, scale=scale * 0.75)
+    check_attend(moe, cache, q, table, start, seq, scale=scale * 0.75, window=300)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", FORMS)
+def test_attend_uneven_scales_in_every_form(moe, rows, q_heads):
+    rng = np.random.default_rng(rows)
+    page, dim, n = 32, 128, 700
+    cache, table, start, seq = make_batch(rng, [(n, rows), (100, rows)], page, 1, dim)
+    k, v, ks, vs = cache
+    for r, j, byte in ((0, 1, 90), (0, 2, 140), (0, 5, 0), (0, 20, 135), (1, 0, 0), (1, 1, 60), (1, 2, 121)):
+        vs[table[r, j], 0] = byte
+        if byte == 0:
+            v[table[r, j], 0] = 0
+    q = bf16(rng.standard_normal((2 * rows, q_heads, dim)))
+    check_attend(moe, cache, q, table, start, seq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", FORMS[2:])
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 0), (128, 20)])
+def test_attend_nan_in_the_cache_reaches_only_the_rows_that_see_it(moe, dim, window, rows, q_heads):
+    rng = np.random.default_rng(dim + rows)
+    n, page = 200, 16
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    q = bf16(rng.standard_normal((rows, q_heads, dim)))
+    clean, clean_lse = run_attend(moe, cache, q.cuda(), table, start, seq, window=window)
+    k, v, _, _ = cache
+    t = n - rows + 1  # the second row's own position: the first row does not see it
+    v[table[0, t // page], 0, t % page, 5] = 0x7F
+    v[table[0, t // page], 0, t % page, dim - 1] = 0xFF
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq, window=window)
+    sees = (np.arange(rows) >= 1) & (np.arange(rows) - 1 < (window or rows))
+    hit = np.zeros(dim, bool)
+    hit[[5, dim - 1]] = True
+    assert np.isnan(out[sees][:, :, hit]).all() and not np.isnan(out[sees][:, :, ~hit]).any()
+    assert not np.isnan(out[~sees]).any() and np.allclose(out[~sees], clean[~sees], rtol=2.0 ** -6, atol=1e-2)
+    assert np.array_equal(lse, clean_lse)
+    k[table[0, t // page], 0, t % page, 0] = 0x7F  # a key: whole rows
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq, window=window)
+    assert np.isnan(out[sees]).all() and np.isnan(lse[sees]).all()
+    assert not np.isnan(out[~sees]).any() and not np.isnan(lse[~sees]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (5, 24, 64), (200, 8, 128), (64, 16, 64), (9, 16, 256)])
+def test_attend_gives_the_same_bits_each_time(moe, rows, q_heads, dim):
+    """Work split over many CTAs and joined by whichever comes last: the order of the sums does not depend on it."""
+    rng = np.random.default_rng(rows)
+    cache, table, start, seq = make_batch(rng, [(5000, rows), (300, 1)], 64, 1, dim)
+    q = bf16(rng.standard_normal((rows + 1, q_heads, dim))).cuda()
+    workspace = torch.zeros(moe.MOE_KV_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    first = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+    for _ in range(10):
+        again = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+    assert moe.moe_kv_sync_status(workspace) == moe.MOE_OK and (workspace[:moe.MOE_KV_WORKSPACE_HEADER] == 0).all()
+
+
 @pytest.mark.gpu
 def test_attend_query_rows_with_nan_or_infinity(moe):
     rng = np.random.default_rng(2)
