@@ -563,6 +563,17 @@ int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, cons
  */
 int moe_kv_sync_status(void* workspace, void* stream);
 
+/*
+ * moe_kv_set_timeout - bound, in nanoseconds, of every wait inside
+ * moe_kv_attend on this workspace (default 2 s; 0 restores it).
+ * moe_kv_debug_withhold - test hook: the CTA of this number never copies its
+ * first tile, so its waits run out (-1 = off, the default): the call records
+ * MOE_ERR_DEVICE_TIMEOUT and finishes. After an error the header is zeroed
+ * (moe_kv_sync_status), these settings with it. Both synchronize the stream.
+ */
+int moe_kv_set_timeout(void* workspace, uint64_t nanoseconds, void* stream);
+int moe_kv_debug_withhold(void* workspace, int cta, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,7 @@ __all__ = [
     "MOE_ERR_STATE", "TOPK", "UNIT_ROWS", "MOE_NOALLOC_SCRATCH_BYTES", "moe_last_error_detail",
     "MAX_BATCH", "moe_device_supported", "moe_small_batch_build", "SMALL_NONE", "SMALL_PACKED", "SMALL_WIDE", "moe_debug_kernel_span", "moe_read_kernel_span",
     "moe_kernel_path", "PATH_GRID", "PATH_SMALL", "PATH_CLUSTER", "PATH_SMALL_WIDE",
-    "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "moe_kv_set_timeout", "moe_kv_debug_withhold", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
     "MOE_KV_WORKSPACE_BYTES", "MOE_KV_WORKSPACE_HEADER", "MOE_KV_MAX_REQUESTS",
 ]
 
@@ -113,6 +113,8 @@ def _load():
         "moe_kv_plan": ([ctypes.POINTER(_KvPlan), vp], i32),
         "moe_kv_append": ([ctypes.POINTER(_KvCache), vp, _i64, _i64, vp, _i64, _i64, vp, i32, vp], i32),
         "moe_kv_sync_status": ([vp, vp], i32),
+        "moe_kv_set_timeout": ([vp, u64, vp], i32),
+        "moe_kv_debug_withhold": ([vp, i32, vp], i32),
         "moe_kv_attend": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), vp, _i64, _i64, i32, ctypes.c_float,
                            i32, vp, vp, vp, vp], i32),
     }
@@ -487,6 +489,14 @@ def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, 
 def moe_kv_sync_status(workspace, stream=None) -> int:
     """Device status of the finished moe_kv_attend calls on this workspace (not raised)."""
     return _lib.moe_kv_sync_status(_ptr(workspace), _stream(stream))
+
+
+def moe_kv_set_timeout(workspace, nanoseconds: int, stream=None):
+    return _check(_lib.moe_kv_set_timeout(_ptr(workspace), nanoseconds, _stream(stream)), "moe_kv_set_timeout")
+
+
+def moe_kv_debug_withhold(workspace, cta: int, stream=None):
+    return _check(_lib.moe_kv_debug_withhold(_ptr(workspace), cta, _stream(stream)), "moe_kv_debug_withhold")
 
 
 class KvCache:

@@ -155,4 +155,22 @@ int moe_kv_sync_status(void* workspace, void* stream) {
   return e == cudaSuccess ? status : launched(e, "moe_kv_sync_status");
 }
 
+int moe_kv_set_timeout(void* workspace, uint64_t nanoseconds, void* stream) {
+  if (workspace == nullptr || !aligned(workspace, 16)) return refuse("null or misaligned workspace");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(static_cast<uint8_t*>(workspace) + 8, &nanoseconds, 8, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return launched(e, "moe_kv_set_timeout");
+}
+
+int moe_kv_debug_withhold(void* workspace, int cta, void* stream) {
+  if (workspace == nullptr || !aligned(workspace, 16)) return refuse("null or misaligned workspace");
+  if (cta < -1) return refuse("cta < -1");
+  const int32_t word = cta + 1;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(static_cast<uint8_t*>(workspace) + 4, &word, 4, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return launched(e, "moe_kv_debug_withhold");
+}
+
 }  // extern "C"

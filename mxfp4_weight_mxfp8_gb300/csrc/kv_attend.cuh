@@ -212,12 +212,20 @@ struct Segment {
   }
 };
 
+// The workspace header's first words.
+struct Header {
+  int32_t status;
+  int32_t withhold;      // test hook: the CTA (from 1) whose first tile is never copied
+  uint64_t timeout_ns;   // of one wait; 0: the default
+};
+
 // Bounded wait for a barrier's phase: false, and the error reported, when it runs out. A role that sees that issues
 // nothing more, waits (bounded again) for what it has in flight, and goes to the CTA's end.
 __device__ __forceinline__ bool wait_more(uint64_t* bar, uint32_t parity, int32_t* status) {
-  const uint64_t began = global_timer_ns();
+  const uint64_t began = global_timer_ns(), set = reinterpret_cast<const volatile Header*>(status)->timeout_ns;
+  const uint64_t limit = set ? set : kWaitNs;
   while (!mbar_wait_hint(bar, parity, 20000)) {
-    if (global_timer_ns() - began > kWaitNs) {
+    if (global_timer_ns() - began > limit) {
       report(status, MOE_ERR_DEVICE_TIMEOUT);
       return false;
     }
@@ -292,7 +300,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   const int per_tile = kTile >> shift, in_tile = lane & (per_tile - 1);  // pages of a tile; this lane's
   const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
   int k = 0;
-  bool alive = true;
+  bool alive = reinterpret_cast<const volatile Header*>(status)->withhold != static_cast<int>(blockIdx.x) + 1;
   Segment s;
   s.find(a, prefix, weight, shift, X::kRows, start, stop);
   for (long long x = start; alive;) {

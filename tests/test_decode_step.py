@@ -237,6 +237,15 @@ def test_attend_refusals(moe):
     assert raw.moe_kv_attend(c, moe._KvBatch(**{**batch, "tokens": 0}), *ok, None) == moe.MOE_OK
 
 
+def test_workspace_calls_refuse_bad_arguments(moe):
+    raw = moe.library()
+    for bad in (None, P + 4):
+        assert raw.moe_kv_sync_status(bad, None) == moe.MOE_ERR_ARG
+        assert raw.moe_kv_set_timeout(bad, 5, None) == moe.MOE_ERR_ARG
+        assert raw.moe_kv_debug_withhold(bad, 0, None) == moe.MOE_ERR_ARG
+    assert raw.moe_kv_debug_withhold(P, -2, None) == moe.MOE_ERR_ARG
+
+
 def test_python_calls_refuse_host_tensors(moe):
     x, ids, w = torch.zeros(2, 32), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 4)
     with pytest.raises(moe.MoeError) as e:
@@ -721,6 +730,25 @@ def test_attend_gives_the_same_bits_each_time(moe, rows, q_heads, dim):
         again = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
         assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
     assert moe.moe_kv_sync_status(workspace) == moe.MOE_OK and (workspace[:moe.MOE_KV_WORKSPACE_HEADER] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (64, 8, 64)])
+def test_attend_reports_a_wait_that_runs_out(moe, rows, q_heads, dim):
+    """One CTA's first tile is never copied: the call ends, says so, and the next one is unaffected."""
+    rng = np.random.default_rng(rows)
+    cache, table, start, seq = make_batch(rng, [(3000, rows)], 64, 1, dim)
+    q = bf16(rng.standard_normal((rows, q_heads, dim))).cuda()
+    workspace = torch.zeros(moe.MOE_KV_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    want = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+    moe.moe_kv_set_timeout(workspace, 2_000_000)
+    moe.moe_kv_debug_withhold(workspace, 1)
+    run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+    assert moe.moe_kv_sync_status(workspace) == moe.MOE_ERR_DEVICE_TIMEOUT
+    assert moe.moe_kv_sync_status(workspace) == moe.MOE_OK
+    got = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+    assert moe.moe_kv_sync_status(workspace) == moe.MOE_OK
+    assert np.array_equal(want[0], got[0]) and np.array_equal(want[1], got[1])
 
 
 @pytest.mark.gpu
