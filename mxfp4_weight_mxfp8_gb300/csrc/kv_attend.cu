@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           mine[X::kRows * D + tid] = m;
           mine[X::kRows * D + X::kRows + tid] = sum;
         }
-        join_item<X::kRows, D>(a, s, row_dst, rows, ctas, total, tid, &s_last);
+        join_item<X::kRows, D, kCompute, 1>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       }
       compute_sync();  // red, the rows' limits, the join word and the segment are free again
       if (tid == 0) {

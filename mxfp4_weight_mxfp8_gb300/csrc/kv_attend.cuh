@@ -364,15 +364,16 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
 }
 
-// A piece of an item has been stored: joins the item's pieces once they are all there. By one warpgroup (barrier 1);
-// row_dst: the rows' places among the outputs' rows.
-template <int kRows, int D>
+// A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
+// is kBarrier. row_dst: the rows' places among the outputs' rows.
+template <int kRows, int D, int kThreads, int kBarrier>
 __device__ void join_item(const AttendArgs& a, const Segment& s, const long long* row_dst, int rows, long long ctas, long long total,
                           int tid, int* s_last) {
   constexpr int kPartialFloats = kRows * (D + 2);
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
   const Request& rq = s.q;
+  auto sync = [] { asm volatile("bar.sync %0, %1;" ::"n"(kBarrier), "n"(kThreads) : "memory"); };
   // The CTAs of this item: c0 .. c1, by the bounds of their runs.
   const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
   const int c1 = static_cast<int>(divide((s.item + rq.tiles + s.weight) * ctas - 1, total));
@@ -387,17 +388,17 @@ __device__ void join_item(const AttendArgs& a, const Segment& s, const long long
   int from = (static_cast<int>(blockIdx.x) - c0) / width * width, stride = 1, count = min(width, pieces - from);
   uint32_t* counter = from == 0 ? counters + c0 : counters + kMaxCtas + c0 + from;
   for (;;) {
-    compute_sync();
+    sync();
     if (tid == 0) {
       // Releases the CTA's stores (ordered before it by the barrier), acquires the other pieces'.
       const uint32_t before = atom_add_acq_rel_gpu(counter, 1);
       *s_last = before == static_cast<uint32_t>(count - 1);
       if (*s_last) *counter = 0;
     }
-    compute_sync();
+    sync();
     if (!*s_last) break;
     // A thread joins four dimensions of some rows, several pieces' loads in flight together.
-    constexpr int kQuads = D / 4, kAllUnits = kRows * kQuads / kCompute, kUnits = kAllUnits % 4 == 0 ? 4 : kAllUnits % 2 == 0 ? 2 : 1;
+    constexpr int kQuads = D / 4, kAllUnits = kRows * kQuads / kThreads, kUnits = kAllUnits % 4 == 0 ? 4 : kAllUnits % 2 == 0 ? 2 : 1;
     constexpr int kBatch = 8 / kUnits;
     const bool last = stride > 1 || count == pieces;
     for (int group = 0; group < kAllUnits; group += kUnits) {
@@ -418,7 +419,7 @@ __device__ void join_item(const AttendArgs& a, const Segment& s, const long long
           const float* src = piece(from + (in ? c + e : c) * stride);
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
-            const int i = ((group + u) * kCompute + tid) / kQuads, c4 = ((group + u) * kCompute + tid) % kQuads * 4;
+            const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
             pm[e][u] = __ldcg(src + kRows * D + i);
             pl[e][u] = __ldcg(src + kRows * D + kRows + i);
             pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + i * D + c4));
@@ -449,10 +450,10 @@ __device__ void join_item(const AttendArgs& a, const Segment& s, const long long
           top[u] = mn;
         }
       }
-      if (!last) compute_sync();  // the first piece of the run has been read everywhere: the run's result takes its place
+      if (!last) sync();  // the first piece of the run has been read everywhere: the run's result takes its place
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int i = ((group + u) * kCompute + tid) / kQuads, c4 = ((group + u) * kCompute + tid) % kQuads * 4;
+        const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
         if (!last) {
           float* dst = piece(from);
           *reinterpret_cast<float4*>(dst + i * D + c4) = o[u];

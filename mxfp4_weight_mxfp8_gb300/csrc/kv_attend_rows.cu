@@ -56,6 +56,7 @@ struct RowsShape {
   static_assert(kPartialOffset + 2ll * 256 * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES || D == 128, "workspace");
   static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
 };
+constexpr int kItemTiles = 4;        // what starting and joining an item costs, in tiles
 constexpr int kUp = 4;               // weights are held times 2^4, so one may grow to 2^4.75 times its reference's before
 constexpr float kHighest = 430.0f;   // it leaves e4m3
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_ready, kAllCompute);
     fence_mbar_init();
   }
-  const int weight = sum_work<kThreads, kRows, D == 64 ? 4 : 2>(a, shift, prefix, s_sum);
+  const int weight = sum_work<kThreads, kRows, kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
@@ -320,10 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int at = k + ((k & 1) != group);
       for (; at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
-        if (!failed) failed = !wait(s_full + group, turn & 1, status);
-        if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);
+        if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);  // (for the entries; well before the scores)
         __syncwarp();
-        tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
         const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
@@ -331,6 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Past the item's first tile only an edge can bring a row its first token.
         bool find = !written || most > m_scale;
         if (edge && !find) find = sync_any<64>(pair, m == -INFINITY && hi >= base && lo < base + kTile);
+        if (!failed) failed = !wait(s_full + group, turn & 1, status);
+        __syncwarp();
+        tc_fence_after_sync();
         for (int tries = 0;; ++tries) {
           if (find) {
             // The references are raised: the largest value scale, and the row's largest score with its token's value scale
@@ -537,10 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mine[kRows * D + row] = m;
             mine[kRows * D + kRows + row] = l;
           }
-          sync_any<kGroupThreads>(4 + 8, false);  // both halves' stores, ahead of the first warpgroup's release of them
-          if (half == 0) join_item<kRows, D>(a, s, row_dst, rows, ctas, total, tid, &s_last);
         }
       }
+      if (!s.whole) join_item<kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
       if (tid == 0) {
         s_unit += s_segment.length;
