@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.begin < s.end) {
         // Queries: hi image, lo image, each row scaled by a power of two so that its largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
-#pragma unroll 2
+#pragma unroll
         for (int i = tid; i < kRows * kChunks; i += kAllCompute) {
           const int r = i / kChunks, c = i % kChunks, at = row0 + r, tok = at / a.group;
           uint4 w = make_uint4(0, 0, 0, 0);
