@@ -1,7 +1,7 @@
 // C entries of the decode step around the layer: argument checks, launches.
 #include <cmath>
 
-#include "kernels.h"
+#include "decode.h"
 
 namespace {
 

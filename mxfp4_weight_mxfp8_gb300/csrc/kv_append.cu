@@ -8,7 +8,7 @@
 // again), one pass that encodes.
 // Scales are powers of two, so growing one loses only what the smaller codes'
 // last places hold.
-#include "kernels.h"
+#include "decode.h"
 
 namespace moe {
 namespace {

@@ -12,7 +12,7 @@
 
 #include <cuda_fp16.h>
 
-#include "kernels.h"
+#include "decode.h"
 #include "ptx.cuh"
 
 namespace moe {

@@ -6,7 +6,7 @@
 // in it. A page is entered in the table by the token that starts it (a page
 // taken by this call always starts with a new token), so nothing waits for
 // anything but the sums, which every CTA takes for itself.
-#include "kernels.h"
+#include "decode.h"
 
 namespace moe {
 namespace {

@@ -9,6 +9,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "decode.h"
 #include "kernels.h"
 
 using moe::Geometry;

@@ -9,7 +9,7 @@
 // the keys that reach it are sorted one to a lane.
 #include <cuda_fp16.h>
 
-#include "kernels.h"
+#include "decode.h"
 
 namespace moe {
 namespace {
