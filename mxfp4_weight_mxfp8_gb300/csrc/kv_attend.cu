@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
-  __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
+  __shared__ Segment<X::kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       }
       __syncwarp();
     };
-    Segment s;
-    s.find(a, prefix, weight, shift, X::kRows, start, stop);
+    Segment<X::kRows> s;
+    s.find(a, prefix, weight, shift, start, stop);
     for (long long x = start; alive;) {
       if (s.begin < s.end) {
         alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       }
       x += s.length;
       if (x >= stop) break;
-      s.next(a, prefix, shift, X::kRows, x, stop);
+      s.next(a, prefix, shift, x, stop);
     }
     if (lane == 0) {
       tc_commit(drained);
@@ -264,10 +264,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     bool failed = false, dead = false;  // a wait of this thread's ran out; one of any thread's did, all agreed
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, weight, shift, X::kRows, start, stop);
+      s_segment.find(a, prefix, weight, shift, start, stop);
     }
     compute_sync();
-    const Segment& s = s_segment;
+    const Segment<X::kRows>& s = s_segment;
     for (;;) {
       const Request& rq = s.q;
       const int row0 = s.row_tile * X::kRows;
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       compute_sync();  // red, the rows' limits, the join word and the segment are free again
       if (tid == 0) {
         s_unit += s_segment.length;
-        if (s_unit < stop) s_segment.next(a, prefix, shift, X::kRows, s_unit, stop);
+        if (s_unit < stop) s_segment.next(a, prefix, shift, s_unit, stop);
       }
       compute_sync();
       if (s_unit >= stop) break;

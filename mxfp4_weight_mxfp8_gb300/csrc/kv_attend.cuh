@@ -148,10 +148,51 @@ struct Request {
   __device__ long long items(int heads) const { return static_cast<long long>(heads) * row_tiles; }
 };
 
+// The tiles that each row tile of a request sees. In the 128-row form, which prompts take, they are counted exactly: a
+// row tile's 128 rows advance the visible tokens by 128 / group, so row tile j sees the tiles from max(0, low + j) / group
+// to before (high + j) / group. In the decode form, whose row tiles differ by a few tokens, each counts them all.
+template <int kRows>
+struct RowTiles {
+  long long low = 0, high = 0;
+  int group;
+  __device__ __forceinline__ RowTiles(const AttendArgs& a, const Request& q) : group(a.group) {
+    if constexpr (kRows != kTile) return;
+    const long long before = max(0, q.seq - q.n);
+    high = (before * group + kTile + kTile * group - 1) >> 7;
+    low = a.window > 0 ? (before - a.window + 1) * group >> 7 : -(1ll << 40);
+  }
+  // The sum of i / group over 0 <= i < x.
+  __device__ __forceinline__ long long sum(long long x) const {
+    if (x <= group) return 0;
+    const long long n = divide(x, group);
+    return n * (n - 1) / 2 * group + n * (x - n * group);
+  }
+  // The tiles of the row tiles before j (j < row_tiles).
+  __device__ __forceinline__ long long before(const Request& q, int j) const {
+    if constexpr (kRows != kTile) return static_cast<long long>(j) * q.tiles;
+    return sum(high + j) - sum(high) - (sum(low + j) - sum(low));
+  }
+  __device__ __forceinline__ int first(const Request& q, int j) const {
+    if constexpr (kRows != kTile) return q.tile0;
+    return static_cast<int>(divide(max(0ll, low + j), group));
+  }
+  __device__ __forceinline__ int count(const Request& q, int j) const {
+    if constexpr (kRows != kTile) return q.tiles;
+    const int from = first(q, j), to = static_cast<int>(divide(high + j, group));
+    return max(1, (j + 1 == q.row_tiles ? min(to, q.tile0 + q.tiles) : to) - from);
+  }
+  __device__ __forceinline__ long long all(const Request& q) const {
+    return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + count(q, q.row_tiles - 1);
+  }
+};
+static_assert(kTile == 128, "RowTiles' shifts");
+
 // A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
+template <int kRows>
 struct Segment {
   Request q;
   int r, head, row_tile;
+  int tile_first, units;   // the item's first tile, from q.tile0 on; its length in the units of the work
   int begin, end;          // tiles of the request, from q.tile0 on
   int weight;              // what starting and joining an item counts as, in tiles
   int length;              // in the units that the work is dealt in: `weight` for the item, then its tiles
@@ -159,27 +200,31 @@ struct Segment {
   long long item;          // the item's first unit among all
 
   // The item's tiles from unit `from` on, as far as the run goes and this row tile's queries see.
-  __device__ __forceinline__ void cut(const AttendArgs& a, int rows, long long x, long long stop, int from) {
-    const int units = q.tiles + weight;
+  __device__ __forceinline__ void cut(const AttendArgs& a, long long x, long long stop, int from) {
     const int to = static_cast<int>(min(static_cast<long long>(units), from + (stop - x)));
     item = x - from;
     length = to - from;
     whole = length == units;
     first = from == 0;
-    begin = max(0, from - weight);
-    end = max(0, to - weight);
+    begin = tile_first + max(0, from - weight);
+    end = tile_first + max(0, to - weight);
     const int before = q.seq - q.n;  // position of the request's first query
-    const int last = min(q.n - 1, static_cast<int>((static_cast<long long>(row_tile + 1) * rows - 1) / a.group));
+    const int last = min(q.n - 1, static_cast<int>((static_cast<long long>(row_tile + 1) * kRows - 1) / a.group));
     end = min(end, (min(q.end, max(0, before + last + 1)) + kTile - 1) / kTile - q.tile0);
     if (a.window > 0) {
-      const long long from_token = static_cast<long long>(before) + static_cast<long long>(row_tile) * rows / a.group - a.window + 1;
+      const long long from_token = static_cast<long long>(before) + static_cast<long long>(row_tile) * kRows / a.group - a.window + 1;
       begin = max(begin, static_cast<int>(max(from_token, 0ll) / kTile) - q.tile0);
     }
     if (begin >= end) begin = end = 0;
   }
 
+  __device__ __forceinline__ void take(const RowTiles<kRows>& t) {
+    tile_first = t.first(q, row_tile) - q.tile0;
+    units = t.count(q, row_tile) + weight;
+  }
+
   // The segment at unit x of a run that ends at `stop`.
-  __device__ void find(const AttendArgs& a, const long long* prefix, int item_weight, int shift, int rows, long long x,
+  __device__ void find(const AttendArgs& a, const long long* prefix, int item_weight, int shift, long long x,
                        long long stop) {
     weight = item_weight;
     int lo = 0, hi = a.b.requests;
@@ -189,26 +234,36 @@ struct Segment {
       else hi = mid;
     }
     r = lo;
-    q = Request(a, shift, r, rows);
-    const int units = q.tiles + weight;
-    const long long local = x - prefix[lo], index = divide(local, units);
-    row_tile = static_cast<int>(divide(index, a.c.kv_heads));
-    head = static_cast<int>(index - static_cast<long long>(row_tile) * a.c.kv_heads);
-    cut(a, rows, x, stop, static_cast<int>(local - index * units));
+    q = Request(a, shift, r, kRows);
+    const RowTiles<kRows> t(a, q);
+    const long long local = x - prefix[lo];
+    lo = 0;
+    hi = q.row_tiles;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((t.before(q, mid) + static_cast<long long>(mid) * weight) * a.c.kv_heads <= local) lo = mid;
+      else hi = mid;
+    }
+    row_tile = lo;
+    take(t);
+    const long long in_row_tile = local - (t.before(q, lo) + static_cast<long long>(lo) * weight) * a.c.kv_heads;
+    head = static_cast<int>(divide(in_row_tile, units));
+    cut(a, x, stop, static_cast<int>(in_row_tile - static_cast<long long>(head) * units));
   }
 
   // The one after it, at unit x < stop: an item's start.
-  __device__ __forceinline__ void next(const AttendArgs& a, const long long* prefix, int shift, int rows, long long x, long long stop) {
+  __device__ __forceinline__ void next(const AttendArgs& a, const long long* prefix, int shift, long long x, long long stop) {
     if (++head == a.c.kv_heads) {
       head = 0;
       if (++row_tile == q.row_tiles) {
         row_tile = 0;
         do ++r;
         while (prefix[r + 1] == x);  // requests without rows
-        q = Request(a, shift, r, rows);
+        q = Request(a, shift, r, kRows);
       }
+      take(RowTiles<kRows>(a, q));
     }
-    cut(a, rows, x, stop, 0);
+    cut(a, x, stop, 0);
   }
 };
 
@@ -249,7 +304,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
     if (r < a.b.requests) {
       const Request q(a, shift, r, kRows);
       items += q.items(a.c.kv_heads);
-      tiles += q.items(a.c.kv_heads) * q.tiles;
+      tiles += RowTiles<kRows>(a, q).all(q) * a.c.kv_heads;
     }
   }
   long long tiles_in = tiles, items_in = items;
@@ -281,7 +336,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
     if (r < a.b.requests) {
       prefix[r] = at;
       const Request q(a, shift, r, kRows);
-      at += q.items(a.c.kv_heads) * (q.tiles + weight);
+      at += (RowTiles<kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
       if (r == a.b.requests - 1) prefix[r + 1] = at;
     }
   }
@@ -301,8 +356,8 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
   int k = 0;
   bool alive = reinterpret_cast<const volatile Header*>(status)->withhold != static_cast<int>(blockIdx.x) + 1;
-  Segment s;
-  s.find(a, prefix, weight, shift, X::kRows, start, stop);
+  Segment<X::kRows> s;
+  s.find(a, prefix, weight, shift, start, stop);
   for (long long x = start; alive;) {
     const Request& q = s.q;
     int page = -1;
@@ -358,7 +413,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
     }
     x += s.length;
     if (x >= stop) break;
-    s.next(a, prefix, shift, X::kRows, x, stop);
+    s.next(a, prefix, shift, x, stop);
   }
   // The copies in flight land before the CTA ends (at once, unless another role gave up).
   for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
@@ -367,16 +422,15 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
 // is kBarrier. row_dst: the rows' places among the outputs' rows.
 template <int kRows, int D, int kThreads, int kBarrier>
-__device__ void join_item(const AttendArgs& a, const Segment& s, const long long* row_dst, int rows, long long ctas, long long total,
+__device__ void join_item(const AttendArgs& a, const Segment<kRows>& s, const long long* row_dst, int rows, long long ctas, long long total,
                           int tid, int* s_last) {
   constexpr int kPartialFloats = kRows * (D + 2);
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
-  const Request& rq = s.q;
   auto sync = [] { asm volatile("bar.sync %0, %1;" ::"n"(kBarrier), "n"(kThreads) : "memory"); };
   // The CTAs of this item: c0 .. c1, by the bounds of their runs.
   const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
-  const int c1 = static_cast<int>(divide((s.item + rq.tiles + s.weight) * ctas - 1, total));
+  const int c1 = static_cast<int>(divide((s.item + s.units) * ctas - 1, total));
   // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
   // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces.
   float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * kPartialFloats;  // the first piece

@@ -53,10 +53,9 @@ struct RowsShape {
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
   static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
-  static_assert(kPartialOffset + 2ll * 256 * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES || D == 128, "workspace");
   static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
 };
-constexpr int kItemTiles = 4;        // what starting and joining an item costs, in tiles
+constexpr int kItemTiles = 6;        // what starting and joining an item costs, in tiles
 constexpr int kUp = 4;               // weights are held times 2^4, so one may grow to 2^4.75 times its reference's before
 constexpr float kHighest = 430.0f;   // it leaves e4m3
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
-  __shared__ Segment s_segment;  // the compute warps', kept by one of their threads
+  __shared__ Segment<kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
@@ -207,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    Segment s;
-    s.find(a, prefix, weight, shift, kRows, start, stop);
+    Segment<kRows> s;
+    s.find(a, prefix, weight, shift, start, stop);
     for (long long x = start; alive;) {
       const int last = k + s.end - s.begin;
       if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       k = last;
       x += s.length;
       if (x >= stop) break;
-      s.next(a, prefix, shift, kRows, x, stop);
+      s.next(a, prefix, shift, x, stop);
     }
     if (lane == 0) {
       tc_commit(drained + w);
@@ -265,10 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool failed = false;   // a wait ran out: no more waits; agreed on at the barriers
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, weight, shift, kRows, start, stop);
+      s_segment.find(a, prefix, weight, shift, start, stop);
     }
     all_sync();
-    const Segment& s = s_segment;
+    const Segment<kRows>& s = s_segment;
     for (;;) {
       const int row0 = s.row_tile * kRows, before = s.q.seq - s.q.n;
       const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n) * a.group - row0));
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
       if (tid == 0) {
         s_unit += s_segment.length;
-        if (s_unit < stop) s_segment.next(a, prefix, shift, kRows, s_unit, stop);
+        if (s_unit < stop) s_segment.next(a, prefix, shift, s_unit, stop);
       }
       all_sync();
       if (s_unit >= stop) break;
