@@ -192,6 +192,7 @@ template <int kRows>
 struct Segment {
   Request q;
   int r, head, row_tile;
+  int token, within;       // the row tile's first query token, its first row among that token's
   int tile_first, units;   // the item's first tile, from q.tile0 on; its length in the units of the work
   int begin, end;          // tiles of the request, from q.tile0 on
   int weight;              // what starting and joining an item counts as, in tiles
@@ -219,6 +220,9 @@ struct Segment {
   }
 
   __device__ __forceinline__ void take(const RowTiles<kRows>& t) {
+    const long long row0 = static_cast<long long>(row_tile) * kRows;
+    token = static_cast<int>(divide(row0, t.group));
+    within = static_cast<int>(row0 - static_cast<long long>(token) * t.group);
     tile_first = t.first(q, row_tile) - q.tile0;
     units = t.count(q, row_tile) + weight;
   }

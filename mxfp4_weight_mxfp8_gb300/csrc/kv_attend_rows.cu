@@ -46,8 +46,8 @@ struct RowsShape {
   static constexpr int kP = kQ + 2 * kRows * D;                      // [group] hi, lo
   static constexpr int kRowF = kP + kGroups * 2 * kRows * kTile;     // [row] factor
   static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
-  static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [row] the second group's reference; its value scale's
-  static constexpr int kRowDst = kRefs + kRows * 4 + 16;             // [row] its place among the outputs' rows
+  static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [group][row] references, then [group] the value scales'
+  static constexpr int kRowDst = kRefs + kGroups * kRows * 4 + 16;   // [row] its place among the outputs' rows
   static constexpr int kNan = kRowDst + kRows * 8;                  // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
     float* tops = reinterpret_cast<float*>(sm + X::kTops);
     float* refs = reinterpret_cast<float*>(sm + X::kRefs);
-    int* ref_scale = reinterpret_cast<int*>(refs + kRows);
+    int* ref_scale = reinterpret_cast<int*>(refs + kGroups * kRows);
     long long* row_dst = reinterpret_cast<long long*>(sm + X::kRowDst);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
     float* join = reinterpret_cast<float*>(sm + X::kP);
@@ -268,20 +268,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     all_sync();
     const Segment<kRows>& s = s_segment;
+    // x / group for a row x from a row tile's first token on.
+    const uint32_t inverse = a.group > 1 ? 0xFFFFFFFFu / a.group + 1 : 0;
+    auto per_group = [&](int x) { return inverse ? static_cast<int>(__umulhi(x, inverse)) : x; };
     for (;;) {
-      const int row0 = s.row_tile * kRows, before = s.q.seq - s.q.n;
-      const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n) * a.group - row0));
+      const int before = s.q.seq - s.q.n;
+      const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n - s.token) * a.group - s.within));
       const int last = k + s.end - s.begin;
       if (s.begin < s.end) {
         // Queries: hi image, lo image, each row scaled by a power of two so that its largest magnitude lies in [128, 256).
         constexpr int kChunks = D / 8;
 #pragma unroll
         for (int i = tid; i < kRows * kChunks; i += kAllCompute) {
-          const int r = i / kChunks, c = i % kChunks, at = row0 + r, tok = at / a.group;
+          const int r = i / kChunks, c = i % kChunks, tok = per_group(s.within + r);
           uint4 w = make_uint4(0, 0, 0, 0);
           if (r < rows)
-            w = *reinterpret_cast<const uint4*>(a.q + (s.q.first + tok) * a.q_token_stride +
-                                                (s.head * a.group + at - tok * a.group) * a.q_head_stride + c * 8);
+            w = *reinterpret_cast<const uint4*>(a.q + (s.q.first + s.token + tok) * a.q_token_stride +
+                                                (s.head * a.group + s.within + r - tok * a.group) * a.q_head_stride + c * 8);
           const uint32_t v[4] = {w.x, w.y, w.z, w.w};
           uint32_t top = 0;
 #pragma unroll
@@ -306,11 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(q_ready);
         all_sync();
       }
-      const int tok = (row0 + row) / a.group;
-      if (tid < kRows) row_dst[row] = static_cast<long long>(s.q.first + tok) * a.q_heads + s.head * a.group + row0 + row - tok * a.group;
+      const int in_tile = per_group(s.within + row), tok = s.token + in_tile;
+      if (tid < kRows)
+        row_dst[row] = static_cast<long long>(s.q.first + tok) * a.q_heads + s.head * a.group + s.within + row - in_tile * a.group;
       const int hi = row < rows ? before + tok : -1, lo = row < rows && a.window > 0 ? max(0, hi - a.window + 1) : 0;
       // Tokens that any of the rows sees, and that all see.
-      const int any_hi = before + (row0 + rows - 1) / a.group, all_hi = before + row0 / a.group;
+      const int all_hi = before + s.token, any_hi = all_hi + per_group(s.within + rows - 1);
       const int any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0, all_lo = a.window > 0 ? max(0, any_hi - a.window + 1) : 0;
       const bool mixed = any_lo != all_lo || any_hi != all_hi;
       const float factor = s.begin < s.end ? row_f[row] : 0.0f;
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
                 const int dim = chunk * 16 + b;
                 for (int i = 0; i < rows; ++i) {
-                  const int last_seen = before + (row0 + i) / a.group;
+                  const int last_seen = all_hi + per_group(s.within + i);
                   if (token <= last_seen && (a.window == 0 || token > last_seen - a.window))
                     atomicOr(nans + i * (D / 32) + dim / 32, 1u << (dim % 32));
                 }
@@ -481,64 +485,81 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       k = last;
 
-      // The second group's rows join the first's.
+      // The groups' outputs are joined: each takes a half of its threads' columns, and gives the other half away.
       failed = sync_any<kAllCompute>(3, failed);
       if (failed) break;
+      constexpr int kOwn = kHalfD / 2;
+      const int column = half * kHalfD + group * kOwn;
       tops[(group * 2 + half) * kRows + row] = l;
-      if (group == 1) {
-        if (half == 0) refs[row] = m;
-        if (in_group == 0) *ref_scale = m_scale;
+      if (half == 0) refs[group * kRows + row] = m;
+      if (in_group == 0) ref_scale[group] = m_scale;
+      auto cell = [&](int c) { return reinterpret_cast<float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2)); };
+      float own[kOwn];
+      if (group == 0) {
 #pragma unroll
-        for (int c = 0; c < kHalfD / 4; ++c)
-          *reinterpret_cast<float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2)) =
-              make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+        for (int c = 0; c < kOwn / 4; ++c)
+          *cell(kOwn / 4 + c) = make_float4(acc[kOwn + 4 * c], acc[kOwn + 4 * c + 1], acc[kOwn + 4 * c + 2], acc[kOwn + 4 * c + 3]);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) own[i] = acc[i];
+      } else {
+#pragma unroll
+        for (int c = 0; c < kOwn / 4; ++c) *cell(c) = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) own[i] = acc[kOwn + i];
       }
       all_sync();
-      if (group == 0) {
+      {
         const float l0 = tops[row] + tops[kRows + row], l1 = tops[2 * kRows + row] + tops[3 * kRows + row];
-        const float m1 = refs[row], mn = fmaxf(m, m1), safe = mn > -INFINITY ? mn : 0.0f;
-        const float f0 = exp2_fast(m - safe), f1 = exp2_fast(m1 - safe);
+        const float m0 = refs[row], m1 = refs[kRows + row], mn = fmaxf(m0, m1), safe = mn > -INFINITY ? mn : 0.0f;
+        const float f0 = exp2_fast(m0 - safe), f1 = exp2_fast(m1 - safe);
         l = l0 * f0 + l1 * f1;
         m = mn;
-        const float g0 = f0 * scale_of(m_scale) * (1.0f / (1 << kUp)), g1 = f1 * scale_of(*ref_scale) * (1.0f / (1 << kUp));
+        const float g0 = f0 * scale_of(ref_scale[0]) * (1.0f / (1 << kUp)), g1 = f1 * scale_of(ref_scale[1]) * (1.0f / (1 << kUp));
+        const float mine = group == 0 ? g0 : g1, other = group == 0 ? g1 : g0;
 #pragma unroll
-        for (int c = 0; c < kHalfD / 4; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2));
-          acc[4 * c] = acc[4 * c] * g0 + v.x * g1;
-          acc[4 * c + 1] = acc[4 * c + 1] * g0 + v.y * g1;
-          acc[4 * c + 2] = acc[4 * c + 2] * g0 + v.z * g1;
-          acc[4 * c + 3] = acc[4 * c + 3] * g0 + v.w * g1;
+        for (int c = 0; c < kOwn / 4; ++c) {
+          const float4 v = *cell(group * (kOwn / 4) + c);
+          own[4 * c] = own[4 * c] * mine + v.x * other;
+          own[4 * c + 1] = own[4 * c + 1] * mine + v.y * other;
+          own[4 * c + 2] = own[4 * c + 2] * mine + v.z * other;
+          own[4 * c + 3] = own[4 * c + 3] * mine + v.w * other;
         }
         if (mixed && s.begin < s.end) {
 #pragma unroll
-          for (int i = 0; i < kHalfD; ++i) {
-            const int dim = half * kHalfD + i;
-            if (nans[row * (D / 32) + dim / 32] >> (dim % 32) & 1) acc[i] = __uint_as_float(0x7FC00000u);
+          for (int i = 0; i < kOwn; ++i) {
+            const int dim = column + i;
+            if (nans[row * (D / 32) + dim / 32] >> (dim % 32) & 1) own[i] = __uint_as_float(0x7FC00000u);
           }
         }
-        if (s.whole) {
-          if (row < rows) {
-            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-            const int64_t dst = row_dst[row];
+        const float inv = !s.whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll
-            for (int c = 0; c < kHalfD; c += 8) {
-              __nv_bfloat162 w[4];
+        for (int c = 0; c < kOwn / 4; ++c)
+          *cell(group * (kOwn / 4) + c) = make_float4(own[4 * c] * inv, own[4 * c + 1] * inv, own[4 * c + 2] * inv, own[4 * c + 3] * inv);
+      }
+      all_sync();
+      // Out in whole rows (a thread's own row, 16 bytes at a time, would take an eighth of a wavefront's width a store).
+      auto joined = [&](int r, int c) {
+        return *reinterpret_cast<const float4*>(join + r * D + c / (kHalfD / 4) * kHalfD + ((c % (kHalfD / 4) ^ (r & 7)) << 2));
+      };
+      if (s.whole) {
+        if (a.lse != nullptr && tid < rows) a.lse[row_dst[tid]] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(acc[c + 2 * j] * inv, acc[c + 2 * j + 1] * inv);
-              *reinterpret_cast<uint4*>(a.out + dst * D + half * kHalfD + c) = *reinterpret_cast<uint4*>(w);
-            }
-            if (a.lse != nullptr && half == 0) a.lse[dst] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-          }
-        } else {
-          float* mine = partials + static_cast<int64_t>(blockIdx.x * 2 + (s.first ? 1 : 0)) * X::kPartialFloats;
-#pragma unroll
-          for (int c = 0; c < kHalfD; c += 4)
-            *reinterpret_cast<float4*>(mine + row * D + half * kHalfD + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-          if (half == 0) {
-            mine[kRows * D + row] = m;
-            mine[kRows * D + kRows + row] = l;
-          }
+        for (int i = tid; i < kRows * D / 8; i += kAllCompute) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          const float4 v0 = joined(r, 2 * c), v1 = joined(r, 2 * c + 1);
+          __nv_bfloat162 w[4] = {__floats2bfloat162_rn(v0.x, v0.y), __floats2bfloat162_rn(v0.z, v0.w),
+                                 __floats2bfloat162_rn(v1.x, v1.y), __floats2bfloat162_rn(v1.z, v1.w)};
+          if (r < rows) *reinterpret_cast<uint4*>(a.out + row_dst[r] * D + c * 8) = *reinterpret_cast<uint4*>(w);
         }
+      } else {
+        float* piece = partials + static_cast<int64_t>(blockIdx.x * 2 + (s.first ? 1 : 0)) * X::kPartialFloats;
+        if (tid < kRows) {
+          piece[kRows * D + tid] = m;
+          piece[kRows * D + kRows + tid] = l;
+        }
+#pragma unroll
+        for (int i = tid; i < kRows * D / 4; i += kAllCompute)
+          *reinterpret_cast<float4*>(piece + i * 4) = joined(i / (D / 4), i % (D / 4));
       }
       if (!s.whole) join_item<kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
