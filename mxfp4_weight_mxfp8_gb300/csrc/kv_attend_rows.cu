@@ -56,6 +56,7 @@ struct RowsShape {
   static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
 };
 constexpr int kItemTiles = 6;        // what starting and joining an item costs, in tiles
+constexpr int kLongUnits = 16;       // longer items may be cut anywhere
 constexpr int kUp = 4;               // weights are held times 2^4, so one may grow to 2^4.75 times its reference's before
 constexpr float kHighest = 430.0f;   // it leaves e4m3
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
@@ -123,6 +124,16 @@ __device__ __forceinline__ void tmem_store_16(uint32_t taddr, const float (&r)[1
       : "memory");
 }
 
+// Where a CTA's run of units ends and the next one's starts: inside an item only if the item is long, else at its nearer
+// end (a piece costs an item's start and the join, some kItemTiles tiles).
+__device__ long long snap(const AttendArgs& a, const long long* prefix, int weight, int shift, long long x, long long total) {
+  if (weight == 0 || x <= 0 || x >= total) return x;
+  Segment<kRows> s;
+  s.find(a, prefix, weight, shift, x, x + 1);
+  if (s.units > kLongUnits) return x;
+  return 2 * (x - s.item) >= s.units ? s.item + s.units : s.item;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attend_rows_kernel(const AttendArgs a, const __grid_constant__ AttendMaps maps, int shift) {
@@ -146,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_last;
   __shared__ Segment<kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
+  __shared__ long long s_run[2];  // the CTA's units
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
@@ -169,7 +181,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
-  const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
+  if (tid == 0 || tid == 32) {
+    const int i = tid == 0 ? 0 : 1;
+    s_run[i] = snap(a, prefix, weight, shift, total * (blockIdx.x + i) / ctas, total);
+  }
+  __syncthreads();
+  const long long start = s_run[0], stop = s_run[1];
+  if (start >= stop) return;
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, kGroups * X::kGroupTmem);
     tmem_relinquish();
