@@ -348,6 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
         const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
         const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
+        // The row's visible tokens among this thread's 16 from column c on, as bits.
+        auto visible = [&](int c, uint32_t entry) {
+          const int from = min(max(lo - base_half - c, 0), 16), to = entry >> 16 ? min(max(hi - base_half - c, -1), 15) : -1;
+          return 0xFFFFu >> (15 - to) & 0xFFFFu << from;
+        };
         // Past the item's first tile only an edge can bring a row its first token.
         bool find = !written || most > m_scale;
         if (edge && !find) find = sync_any<64>(pair, m == -INFINITY && hi >= base && lo < base + kTile);
@@ -363,11 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
               const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
               if (edge) {
+                const uint32_t seen = visible(c, entry);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const int token = base_half + c + j;
-                  if (token < lo || token > hi || !(entry >> 16)) v[j] = -INFINITY;
-                }
+                for (int j = 0; j < 16; ++j)
+                  if (!(seen & 1u << j)) v[j] = -INFINITY;
               }
               float big[4];
 #pragma unroll
@@ -414,11 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
             if (edge) {
+              const uint32_t seen = visible(c, entry);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int token = base_half + c + j;
-                if (token < lo || token > hi || !(entry >> 16)) v[j] = 0.0f;
-              }
+              for (int j = 0; j < 16; ++j)
+                if (!(seen & 1u << j)) v[j] = 0.0f;
             }
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t his[4], los[4];
@@ -543,11 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           own[4 * c + 3] = own[4 * c + 3] * mine + v.w * other;
         }
         if (mixed && s.begin < s.end) {
+          const uint32_t bad = nans[row * (D / 32) + column / 32] >> (column % 32);  // (its lowest kOwn bits)
 #pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            const int dim = column + i;
-            if (nans[row * (D / 32) + dim / 32] >> (dim % 32) & 1) own[i] = __uint_as_float(0x7FC00000u);
-          }
+          for (int i = 0; i < kOwn; ++i)
+            if (bad & 1u << i) own[i] = __uint_as_float(0x7FC00000u);
         }
         const float inv = !s.whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll
