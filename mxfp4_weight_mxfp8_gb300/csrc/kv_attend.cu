@@ -47,8 +47,8 @@ struct Shape {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kKeyStride = kStageBytes, kValuesAt = kTileBytes, kValueStride = kStageBytes;
   // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring.
-  static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 || (D == 64 && RT == 3) ? 3 : 2;
-  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 4 ? 5 : 3) : D == 128 ? 2 : 3;
+  static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 ? 2 : 3;
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
