@@ -21,6 +21,20 @@
 // Roles: a producer warp looks up pages and streams tiles by TMA through a ring,
 // a warp issues the MMAs, four warps do the softmax (thread = token) and read
 // the output at the end (thread = dimension).
+//
+// The cache's bytes bound large decode steps: 64 requests of up to 8192 tokens
+// (64 query heads on 8 of 128) take 90.7 us for 532 MB, 5.86 TB/s, 86 % of a
+// copy's rate; the tile loop itself runs at about that rate, the rest is the
+// first tile's latency (6 us: launch, work sums, lookups, TMA, DRAM) and the
+// last pieces' join (5). Two requests of 100 to 131 thousand tokens take 48.8 us
+// for 244 MB: the same, with longer joins. One request of 777 tokens takes 10.5
+// us, all latency. With several rows a request and a window (40 requests, up to
+// 24 rows, 1024 tokens of 64: 37.4 us for 35 MB) an item's start and end bound
+// it, some 8 thousand cycles next to 4 thousand for a tile.
+// What the tensor cores take off the loop: with both products on mma.sync (its
+// e4m3 form runs at 405 TFLOP/s on this part) the first such step took 3.2 ms;
+// the lo parts as further columns, not as a second product, read the wide
+// operand from shared memory once.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -46,7 +60,8 @@ struct Shape {
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kKeyStride = kStageBytes, kValuesAt = kTileBytes, kValueStride = kStageBytes;
-  // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring.
+  // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring (24 rows of 64 in 3 CTAs of
+  // 96 registers spill: 98.8 us for 64 requests of up to 4096 tokens, against 68.5 in 2).
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 ? 2 : 3;
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
@@ -618,8 +633,12 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
 
 template <int D>
 cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
-  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average; many more than that are the 128-row
-  // form's (up to head_dim 128: a thread of it holds a row's output).
+  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average: a wider tile costs its softmax and TMEM
+  // columns whether rows use them or not, a narrower one reads the cache again (8 rows: 90.7 us in tiles of 8, 93.7 in 16;
+  // 16 rows of 128, 64 requests of up to 4096 tokens: 67 us in 16, 90 in 24; 24 rows: 95 in 24, 112 in 32).
+  // Many more rows are the 128-row form's (up to head_dim 128: a thread of it holds half a row's output). The same requests
+  // with 28 rows each take 115 us here and 143 there, with 44 rows of 128 171 and 145, of 64 117 and 130; two long requests
+  // with 44 rows 59 and 82.
   const long long rows = static_cast<long long>(a.b.tokens) * a.group;
   if (D <= 128 && rows > 48ll * a.b.requests) return launch_kv_attend_rows(a, maps, shift, sms, stream);
   if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, sms, stream);

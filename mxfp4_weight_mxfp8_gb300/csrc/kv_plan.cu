@@ -6,6 +6,10 @@
 // in it. A page is entered in the table by the token that starts it (a page
 // taken by this call always starts with a new token), so nothing waits for
 // anything but the sums, which every CTA takes for itself.
+//
+// Latency bounds it: 64 requests with a token each take 2.7 us, about a launch;
+// 1000 requests with 300 thousand new tokens take 5.7 us, where the 3.4 MB
+// alone would take 0.5 and the sums (four dependent loads and two scans) 3.
 #include "decode.h"
 
 namespace moe {
@@ -128,10 +132,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan
 cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream) {
   int shift = 4;
   while ((1 << shift) < a.page_tokens) ++shift;
-  // Every CTA takes the sums again, so no more of them than two to an SM.
+  // A thread to a request: 256 threads while that is enough (64 requests: 2.7 us, against 3.6 with 1024). Every CTA
+  // takes the sums again, so one to an SM (1000 requests, 300 thousand tokens: 5.7 us; 6.5 with 100 CTAs, 7.0 with 304).
   const int threads = a.requests <= 256 ? 256 : 1024;
   int grid = (a.tokens + threads - 1) / threads;
-  grid = grid < 1 ? 1 : (grid > 304 ? 304 : grid);
+  grid = grid < 1 ? 1 : (grid > 152 ? 152 : grid);
   if (threads == 256) kv_plan_kernel<256><<<grid, 256, 0, stream>>>(a, shift);
   else kv_plan_kernel<1024><<<grid, 1024, 0, stream>>>(a, shift);
   return cudaGetLastError();
