@@ -1,5 +1,8 @@
 """GB300 (sm_103a) MXFP8-activation x MXFP4-weight top-16 MoE decode layer.
 
+Next to the layer: routing (``moe_route``) and the paged 8-bit cache with its
+attention (``moe_kv_plan``, ``moe_kv_append``, ``moe_kv_attend``, ``KvCache``).
+
 A thin ctypes binding over the C ABI declared in ``include/moe.h``: every
 function here only marshals arguments (tensor or array -> pointer, torch
 stream -> cudaStream_t) and raises ``MoeError`` on a non-zero status. All of
