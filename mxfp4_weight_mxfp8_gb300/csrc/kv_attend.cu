@@ -50,9 +50,6 @@ constexpr int kThreads = 192;
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
 constexpr int kUp = 6;               // weights are held times 2^6, so one may grow to 2^2.75 times its reference's before
 constexpr float kHighest = 8.75f;    // it leaves e4m3 at 2^8.75 (430)
-// What starting and joining an item costs, in tiles (64 ragged requests: 102 us with 0, 90.8 with 1, 90.7 with 2, 93.3
-// with 4; the windowed step: 56.9, 40.3, 37.5, 37.7).
-constexpr int kItemTiles = 2;
 
 template <int D, int RT>
 struct Shape {
@@ -67,6 +64,10 @@ struct Shape {
   // 96 registers spill: 98.8 us for 64 requests of up to 4096 tokens, against 68.5 in 2).
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 ? 2 : 3;
+  // What starting and joining an item costs, in tiles: more of them the wider the row tile and the shorter a tile's loads
+  // (64 ragged requests of 128: 8 rows take 90.7 us with 2, 93.4 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
+  // of 64: 8 rows 45 with 2, 39 with 4; 32 rows 95 and 79, 75 with 8).
+  static constexpr int kItemTiles = RT + (D == 64 ? 3 : 1);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
+  __shared__ int s_nans;         // the item has outputs noted in `nans`
   __shared__ Segment<X::kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
-  const int weight = sum_work<kThreads, X::kRows, kItemTiles>(a, shift, prefix, s_sum);
+  const int weight = sum_work<kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
@@ -286,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     }
     compute_sync();
     const Segment<X::kRows>& s = s_segment;
+    const uint32_t inverse = inverse_of(a.group);
     for (;;) {
       const Request& rq = s.q;
-      const int row0 = s.row_tile * X::kRows;
-      const int rows = min(X::kRows, static_cast<int>(min(static_cast<long long>(rq.n) * a.group - row0, 1ll << 30)));
+      const int rows = static_cast<int>(min(static_cast<long long>(rq.n - s.token) * a.group - s.within, static_cast<long long>(X::kRows)));
       float l[X::kRows];                 // sums of this thread's tokens' weights against the references
       float m = -INFINITY;               // reference of row `lane`
       int m_scale = 0;                   // reference of the value scales
@@ -297,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       for (int i = 0; i < X::kRows; ++i) l[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
       if (tid < X::kRows) {
-        const int at = row0 + tid, tok = at / a.group, last = tid < rows ? rq.seq - rq.n + tok : -1;
+        const int in_tile = per_group(s.within + tid, inverse), tok = s.token + in_tile, last = tid < rows ? rq.seq - rq.n + tok : -1;
         row_hi[tid] = last;
         row_lo[tid] = tid < rows && a.window > 0 ? max(0, last - a.window + 1) : 0;
-        row_dst[tid] = static_cast<long long>(rq.first + tok) * a.q_heads + s.head * a.group + at - tok * a.group;
+        row_dst[tid] = static_cast<long long>(rq.first + tok) * a.q_heads + s.head * a.group + s.within + tid - in_tile * a.group;
       }
       if (s.begin < s.end) {
         // Queries: hi rows, then lo rows, scaled by a power of two so that each row's largest magnitude lies in [128, 256).
@@ -308,12 +310,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
         for (int base = 0; base < X::kRows * kChunks; base += kCompute) {
           const int i = base + tid;
-          const int row = i / kChunks, c = i % kChunks, at = row0 + row, tok = at / a.group;
+          const int row = i / kChunks, c = i % kChunks, tok = per_group(s.within + row, inverse);
           const bool used = row < rows;
           uint4 w = make_uint4(0, 0, 0, 0);
           if (used)
-            w = *reinterpret_cast<const uint4*>(a.q + (rq.first + tok) * a.q_token_stride +
-                                                (s.head * a.group + at - tok * a.group) * a.q_head_stride + c * 8);
+            w = *reinterpret_cast<const uint4*>(a.q + (rq.first + s.token + tok) * a.q_token_stride +
+                                                (s.head * a.group + s.within + row - tok * a.group) * a.q_head_stride + c * 8);
           const uint32_t v[4] = {w.x, w.y, w.z, w.w};
           uint32_t top = 0;
 #pragma unroll
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           if (c == 0) row_f[row] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : a.scale * kLog2e * pow2f(e);
         }
         for (int i = tid; i < X::kRows * D / 32; i += kCompute) nans[i] = 0;
+        if (tid == 0) s_nans = 0;
         fence_proxy_async_shared();
         mbar_arrive(q_ready);
         compute_sync();
@@ -476,7 +479,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           // taken out too, and noted for those.
           uint8_t* row = sm + X::kRing + stage * X::kStageBytes + X::kTileBytes + tid * X::kSpan;
           const bool seen = token >= any_lo && token <= any_hi && (entry >> 16);
-          if (!seen || mixed) {
+          bool change = !seen;
+          if (seen && mixed) {
+#pragma unroll
+            for (int h = 0; h < X::kHalves; ++h)
+              change |= any_nan<X::kSpan / 16, 1>(reinterpret_cast<const uint4*>(row + h * (kTile * X::kSpan)));
+            if (change) s_nans = 1;
+          }
+          if (change) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint4* at = reinterpret_cast<uint4*>(row + (c * 16 / X::kSpan) * (kTile * X::kSpan) + c * 16 % X::kSpan);
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         const float4 v = *reinterpret_cast<const float4*>(red + lane * 4);
         sum = (v.x + v.y) + (v.z + v.w);
       }
-      if (mixed) {
+      if (s.begin < s.end && s_nans) {
 #pragma unroll
         for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
@@ -640,10 +650,10 @@ cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, i
   // columns whether rows use them or not, a narrower one reads the cache again (8 rows: 90.7 us in tiles of 8, 93.7 in 16;
   // 16 rows of 128, 64 requests of up to 4096 tokens: 67 us in 16, 90 in 24; 24 rows: 95 in 24, 112 in 32).
   // Many more rows are the 128-row form's (up to head_dim 128: a thread of it holds half a row's output). The same requests
-  // with 28 rows each take 115 us here and 143 there, with 44 rows of 128 171 and 145, of 64 117 and 130; two long requests
-  // with 44 rows 59 and 82.
+  // with 40 rows each take 140 us here and 144 there, with heads of 64 113 and 131; with 47 rows 166 and 147, 134 and 129;
+  // two requests of 30 thousand tokens with 40 rows 55 and 81.
   const long long rows = static_cast<long long>(a.b.tokens) * a.group;
-  if (D <= 128 && rows > 48ll * a.b.requests) return launch_kv_attend_rows(a, maps, shift, sms, stream);
+  if (D <= 128 && rows > 44ll * a.b.requests) return launch_kv_attend_rows(a, maps, shift, sms, stream);
   if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, sms, stream);
   if (rows <= 16ll * a.b.requests || D == 256) return launch_shape<D, 2>(a, maps, shift, sms, stream);
   if (rows <= 24ll * a.b.requests) return launch_shape<D, D == 256 ? 2 : 3>(a, maps, shift, sms, stream);

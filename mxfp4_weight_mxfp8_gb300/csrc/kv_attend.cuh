@@ -121,6 +121,25 @@ __device__ __forceinline__ uint32_t chunk_at(int n, int c) {
   return kSpan == 128 ? n * 128 + ((c ^ (n & 7)) << 4) : n * 64 + ((c ^ ((n >> 1) & 3)) << 4);
 }
 
+// Whether any of kChunks 16-byte chunks, kStep apart, holds a NaN code.
+template <int kChunks, int kStep>
+__device__ __forceinline__ bool any_nan(const uint4* p) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 w = p[i * kStep];
+    bad |= nan_code(w.x) | nan_code(w.y) | nan_code(w.z) | nan_code(w.w);
+  }
+  return bad != 0;
+}
+
+// x / group for rows x of a row tile (from its first token's first row on, so below 2048): `inverse` is 2^32 / group,
+// rounded up, or 0 for a group of one.
+__device__ __forceinline__ uint32_t inverse_of(int group) { return group > 1 ? 0xFFFFFFFFu / group + 1 : 0; }
+__device__ __forceinline__ int per_group(int x, uint32_t inverse) {
+  return inverse ? static_cast<int>(__umulhi(x, inverse)) : x;
+}
+
 // ----------------------------------------------------------------------- work
 // a / b of numbers that mostly fit 32 bits, where the division is far shorter.
 __device__ __forceinline__ long long divide(long long a, long long b) {

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long s_sum[kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
+  __shared__ int s_nans;         // the item has outputs noted in `nans`
   __shared__ Segment<kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   __shared__ long long s_run[2];  // the CTA's units
@@ -301,9 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     all_sync();
     const Segment<kRows>& s = s_segment;
-    // x / group for a row x from a row tile's first token on.
-    const uint32_t inverse = a.group > 1 ? 0xFFFFFFFFu / a.group + 1 : 0;
-    auto per_group = [&](int x) { return inverse ? static_cast<int>(__umulhi(x, inverse)) : x; };
+    const uint32_t inverse = inverse_of(a.group);
     for (;;) {
       const int before = s.q.seq - s.q.n;
       const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n - s.token) * a.group - s.within));
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kChunks = D / 8;
 #pragma unroll
         for (int i = tid; i < kRows * kChunks; i += kAllCompute) {
-          const int r = i / kChunks, c = i % kChunks, tok = per_group(s.within + r);
+          const int r = i / kChunks, c = i % kChunks, tok = per_group(s.within + r, inverse);
           uint4 w = make_uint4(0, 0, 0, 0);
           if (r < rows)
             w = *reinterpret_cast<const uint4*>(a.q + (s.q.first + s.token + tok) * a.q_token_stride +
@@ -338,16 +337,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_f[r] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.0f : fabsf(a.scale) * kLog2e * pow2f(e);
         }
         for (int i = tid; i < kRows * D / 32; i += kAllCompute) nans[i] = 0;
+        if (tid == 0) s_nans = 0;
         fence_proxy_async_shared();
         mbar_arrive(q_ready);
         all_sync();
       }
-      const int in_tile = per_group(s.within + row), tok = s.token + in_tile;
+      const int in_tile = per_group(s.within + row, inverse), tok = s.token + in_tile;
       if (tid < kRows)
         row_dst[row] = static_cast<long long>(s.q.first + tok) * a.q_heads + s.head * a.group + s.within + row - in_tile * a.group;
       const int hi = row < rows ? before + tok : -1, lo = row < rows && a.window > 0 ? max(0, hi - a.window + 1) : 0;
       // Tokens that any of the rows sees, and that all see.
-      const int all_hi = before + s.token, any_hi = all_hi + per_group(s.within + rows - 1);
+      const int all_hi = before + s.token, any_hi = all_hi + per_group(s.within + rows - 1, inverse);
       const int any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0, all_lo = a.window > 0 ? max(0, any_hi - a.window + 1) : 0;
       const bool mixed = any_lo != all_lo || any_hi != all_hi;
       const float factor = s.begin < s.end ? row_f[row] : 0.0f;
@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* value = sm + X::kRing + X::kValuesAt + stage * X::kValueStride + row * X::kSpan;
           const int token = base + row;
           const bool seen = token >= any_lo && token <= any_hi && (mt[row >> shift] >> 16);
-          if (!seen || mixed) {
+          if (!seen || (mixed && any_nan<D / 32, 2>(reinterpret_cast<const uint4*>(value) + half))) {
+            if (seen) s_nans = 1;
 #pragma unroll 1
             for (int c = half; c < D / 16; c += 2) {
               uint4* cell = reinterpret_cast<uint4*>(value + c * 16);
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
                 const int dim = chunk * 16 + b;
                 for (int i = 0; i < rows; ++i) {
-                  const int last_seen = all_hi + per_group(s.within + i);
+                  const int last_seen = all_hi + per_group(s.within + i, inverse);
                   if (token <= last_seen && (a.window == 0 || token > last_seen - a.window))
                     atomicOr(nans + i * (D / 32) + dim / 32, 1u << (dim % 32));
                 }
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           own[4 * c + 2] = own[4 * c + 2] * mine + v.z * other;
           own[4 * c + 3] = own[4 * c + 3] * mine + v.w * other;
         }
-        if (mixed && s.begin < s.end) {
+        if (s.begin < s.end && s_nans) {
           const uint32_t bad = nans[row * (D / 32) + column / 32] >> (column % 32);  // (its lowest kOwn bits)
 #pragma unroll
           for (int i = 0; i < kOwn; ++i)
