@@ -23,13 +23,13 @@
 // the output at the end (thread = dimension).
 //
 // The cache's bytes bound large decode steps: 64 requests of up to 8192 tokens
-// (64 query heads on 8 of 128) take 90.7 us for 532 MB, 5.86 TB/s, 86 % of a
+// (64 query heads on 8 of 128) take 91 us for 532 MB, 5.85 TB/s, 86 % of a
 // copy's rate; the tile loop itself runs at about that rate, the rest is the
 // first tile's latency (6 us: launch, work sums, lookups, TMA, DRAM) and the
-// last pieces' join (5). Two requests of 100 to 131 thousand tokens take 48.8 us
+// last pieces' join (5). Two requests of 100 to 131 thousand tokens take 48.7 us
 // for 244 MB: the same, with longer joins. One request of 777 tokens takes 10.5
 // us, all latency. With several rows a request and a window (40 requests, up to
-// 24 rows, 1024 tokens of 64: 37.4 us for 35 MB) an item's start and end bound
+// 24 rows, 1024 tokens of 64: 37 us for 35 MB) an item's start and end bound
 // it, some 8 thousand cycles next to 4 thousand for a tile.
 // What the tensor cores take off the loop: with both products on mma.sync (its
 // e4m3 form runs at 405 TFLOP/s on this part) the first such step took 3.2 ms;
@@ -65,7 +65,7 @@ struct Shape {
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 ? 2 : 3;
   // What starting and joining an item costs, in tiles: more of them the wider the row tile and the shorter a tile's loads
-  // (64 ragged requests of 128: 8 rows take 90.7 us with 2, 93.4 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
+  // (64 ragged requests of 128: 8 rows take 91 us with 2, 93.5 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
   // of 64: 8 rows 45 with 2, 39 with 4; 32 rows 95 and 79, 75 with 8).
   static constexpr int kItemTiles = RT + (D == 64 ? 3 : 1);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
@@ -479,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
           // taken out too, and noted for those.
           uint8_t* row = sm + X::kRing + stage * X::kStageBytes + X::kTileBytes + tid * X::kSpan;
           const bool seen = token >= any_lo && token <= any_hi && (entry >> 16);
-          bool change = !seen;
-          if (seen && mixed) {
+          bool look = !seen || mixed;
+          if (RT > 1 && look && seen) {  // (with 8 rows, mostly one token's, the code in the way costs more than it saves)
+            look = false;
 #pragma unroll
             for (int h = 0; h < X::kHalves; ++h)
-              change |= any_nan<X::kSpan / 16, 1>(reinterpret_cast<const uint4*>(row + h * (kTile * X::kSpan)));
-            if (change) s_nans = 1;
+              look |= any_nan<X::kSpan / 16, 1>(reinterpret_cast<const uint4*>(row + h * (kTile * X::kSpan)));
           }
-          if (change) {
+          if (look) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint4* at = reinterpret_cast<uint4*>(row + (c * 16 / X::kSpan) * (kTile * X::kSpan) + c * 16 % X::kSpan);
@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
                 if (((words[b >> 2] >> (8 * (b & 3))) & 0x7Fu) != 0x7Fu) continue;
                 words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
                 const int dim = chunk * 16 + b;
+                s_nans = 1;
                 for (int i = 0; i < rows; ++i)
                   if (token >= row_lo[i] && token <= row_hi[i]) atomicOr(nans + i * (D / 32) + dim / 32, 1u << (dim % 32));
               }
@@ -647,7 +648,7 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
 template <int D>
 cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
   // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average: a wider tile costs its softmax and TMEM
-  // columns whether rows use them or not, a narrower one reads the cache again (8 rows: 90.7 us in tiles of 8, 93.7 in 16;
+  // columns whether rows use them or not, a narrower one reads the cache again (8 rows: 91 us in tiles of 8, 94 in 16;
   // 16 rows of 128, 64 requests of up to 4096 tokens: 67 us in 16, 90 in 24; 24 rows: 95 in 24, 112 in 32).
   // Many more rows are the 128-row form's (up to head_dim 128: a thread of it holds half a row's output). The same requests
   // with 40 rows each take 140 us here and 144 there, with heads of 64 113 and 131; with 47 rows 166 and 147, 134 and 129;

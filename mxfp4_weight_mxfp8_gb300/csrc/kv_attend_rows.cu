@@ -19,7 +19,7 @@
 // columns (two threads to a row). The groups' results are joined in shared memory.
 //
 // The softmax bounds it: two chunks of up to 700 tokens on 3300 to 6000 earlier
-// ones (64 query heads on 8 of 128, 162 GFLOP) take 281 us, 576 TFLOP/s, where
+// ones (64 query heads on 8 of 128, 162 GFLOP) take 279 us, 579 TFLOP/s, where
 // both products with their lo parts keep the tensor pipe busy for a quarter of
 // that. A tile costs a group some 4 thousand cycles of conversions,
 // exponentials and sums and 1.7 thousand of waiting for its own products, the
@@ -29,7 +29,7 @@
 // image read twice as often); a tile's values before the next scores, 303.
 // Short items are bound by their starts and ends, some 20 thousand cycles
 // (queries 4, first scores and maxima 4, the groups' join and the output 6):
-// prompts of 1130 and 870 tokens without earlier ones take 151 us, 220 TFLOP/s.
+// prompts of 1130 and 870 tokens without earlier ones take 149 us, 224 TFLOP/s.
 #include "kv_attend.cuh"
 
 namespace moe {
@@ -469,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int token = base + row;
           const bool seen = token >= any_lo && token <= any_hi && (mt[row >> shift] >> 16);
           if (!seen || (mixed && any_nan<D / 32, 2>(reinterpret_cast<const uint4*>(value) + half))) {
-            if (seen) s_nans = 1;
 #pragma unroll 1
             for (int c = half; c < D / 16; c += 2) {
               uint4* cell = reinterpret_cast<uint4*>(value + c * 16);
@@ -487,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (((words[b >> 2] >> (8 * (b & 3))) & 0x7Fu) != 0x7Fu) continue;
                 words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
                 const int dim = chunk * 16 + b;
+                s_nans = 1;
                 for (int i = 0; i < rows; ++i) {
                   const int last_seen = all_hi + per_group(s.within + i, inverse);
                   if (token <= last_seen && (a.window == 0 || token > last_seen - a.window))
