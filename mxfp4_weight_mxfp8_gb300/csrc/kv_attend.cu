@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
 #pragma unroll
       for (int i = 0; i < X::kRows; ++i) l[i] = 0.0f;
       bool mixed = false;  // rows of this item see different tokens
+      bool blank = false;  // some row has seen no token yet
       if (tid < X::kRows) {
         const int in_tile = per_group(s.within + tid, inverse), tok = s.token + in_tile, last = tid < rows ? rq.seq - rq.n + tok : -1;
         row_hi[tid] = last;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
         const float ks = scale_of(entry & 0xFFu);
         bool find = tile == s.begin || most > m_scale;
-        if (edge)  // a row's first token
+        if (edge || blank)  // a row's first token
           find |= __any_sync(kAll, lane < X::kRows && m == -INFINITY && row_hi[min(lane, X::kRows - 1)] >= base &&
                                        row_lo[min(lane, X::kRows - 1)] < base + kTile);
         for (int tries = 0;; ++tries) {
@@ -413,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               m = top;
             }
             m_scale = scale;
+            blank = __any_sync(kAll, lane < rows && m == -INFINITY);
             if (lane < X::kRows) refs[lane] = m > -INFINITY ? m : 0.0f;
             __syncwarp();
             if (tile > s.begin) {

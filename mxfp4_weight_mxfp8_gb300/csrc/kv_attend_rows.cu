@@ -368,9 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int from = min(max(lo - base_half - c, 0), 16), to = entry >> 16 ? min(max(hi - base_half - c, -1), 15) : -1;
           return 0xFFFFu >> (15 - to) & 0xFFFFu << from;
         };
-        // Past the item's first tile only an edge can bring a row its first token.
-        bool find = !written || most > m_scale;
-        if (edge && !find) find = sync_any<64>(pair, m == -INFINITY && hi >= base && lo < base + kTile);
+        // Some row's first token may come with any of the group's tiles. (Both warps of the pair hold the same rows.)
+        bool find = !written || most > m_scale || __any_sync(kAll, m == -INFINITY && hi >= base && lo < base + kTile);
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
         __syncwarp();
         tc_fence_after_sync();

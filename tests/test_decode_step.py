@@ -606,6 +606,41 @@ def test_attend_matches_64_bits(moe, page, dim, heads, q_heads, window, lengths)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,group,heads,dim,page", [(8, 1, 24, 128, 16), (2, 8, 48, 128, 64), (3, 4, 48, 64, 64),
+                                                       (10, 2, 48, 64, 16), (40, 1, 24, 128, 64), (60, 2, 8, 128, 128),
+                                                       (100, 2, 4, 256, 64), (100, 1, 16, 64, 32)])
+def test_attend_windows_that_start_near_a_tile(moe, rows, group, heads, dim, page):
+    """The last query row's first token lies just before, at or after a tile's first one, many full tiles after it."""
+    rng = np.random.default_rng(rows + dim)
+    window = 900
+    lengths = [(first + window, rows) for first in (124, 126, 127, 128, 129, 131, 140, 250)]
+    cache, table, start, seq = make_batch(rng, lengths, page, 1, dim)
+    cache = [np.repeat(c, heads, axis=1) for c in cache]
+    q = bf16(rng.standard_normal((8 * rows, heads * group, dim)))
+    check_attend(moe, cache, q, table, start, seq, window=window)
+
+
+PROMPTS = [
+    (16, 64, 4, 28, 0, [(700, 700), (0, 0), (333, 200), (132, 129)]),
+    (64, 128, 2, 16, 100, [(900, 900), (640, 640)]),
+    (128, 128, 3, 3, 0, [(600, 600), (1000, 513), (128, 128), (1, 1)]),
+    (32, 64, 1, 16, 1000, [(3000, 700), (1500, 1500)]),
+    (16, 128, 2, 10, 1, [(500, 500), (300, 300)]),
+    (64, 256, 2, 16, 200, [(400, 400), (500, 300)]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,dim,heads,q_heads,window,lengths", PROMPTS)
+def test_attend_prompts(moe, page, dim, heads, q_heads, window, lengths):
+    """Many row tiles, each with tiles of its own number: short items whole, long ones cut between CTAs."""
+    rng = np.random.default_rng(dim + window)
+    cache, table, start, seq = make_batch(rng, lengths, page, heads, dim)
+    q = bf16(rng.standard_normal((int(start[-1]) + 1, q_heads, dim)))
+    check_attend(moe, cache, q, table, start, seq, window=window)
+
+
+@pytest.mark.gpu
 def test_attend_many_short_requests(moe):
     rng = np.random.default_rng(3)
     lengths = [(int(rng.integers(0, 70)), 1) for _ in range(300)]
