@@ -5,36 +5,34 @@
 // the work split). Both products run on the tensor cores with the cache's
 // codes as they are, as the 128-row operand: S^T[token][row] = K x Q^T and
 // O^T[dim][row] += V^T x P^T (V read transposed, token-major as it lies in the
-// page). The few query rows are the narrow operand. Queries and weights are
-// split into two e4m3 numbers, hi + lo / 16, which take two columns of the one
-// product (the wide operand is read from shared memory once for both): together
-// they hold the 8 significant bits of a BF16 query exactly down to 2^-14 of its
-// row's largest magnitude, and a weight of 2^-12 of its row's reference or more
-// within 2^-9 of itself (below that within 2^-21 of the reference); the sum of
-// the weights is taken of the unsplit values. Weights
-// carry their token's value scale, and the reference is a maximum of such
-// products seen so far: while none outgrows it, the output stays in TMEM,
-// accumulated in FP32 by the tensor core, and a tile needs no maxima. Only when
-// one does (and on an item's first tile) they are taken first and the output is
-// rescaled.
+// page). The few query rows are the narrow operand. Scores are taken of the
+// cache's codes as they are, queries split into two e4m3 numbers, hi + lo / 16,
+// which take two columns of the one product (the wide operand is read from
+// shared memory once for both): together they hold the 8 significant bits of a
+// BF16 query exactly down to 2^-14 of its row's largest magnitude, and what is
+// smaller within 2^-21 of that. Weights must keep their precision however small
+// they are (under a dominant token of no value the others are all of the
+// output), so they are two BF16 numbers, hi + lo, 16 bits at every magnitude,
+// in columns of their own again. For that the values are widened to BF16, code
+// times page scale, which is exact, in place in shared memory.
+// A row's weights are held against a reference, the largest score when it was
+// last raised: FP32 and BF16 have room for weights far above and below it, so a
+// tile needs no maxima and the output stays in TMEM, accumulated in FP32 by the
+// tensor core. Only when a weight outgrows the reference by 2^64 (and on an
+// item's first tile) the maxima are taken first and the output is rescaled.
 //
 // Roles: a producer warp looks up pages and streams tiles by TMA through a ring,
-// a warp issues the MMAs, four warps do the softmax (thread = token) and read
-// the output at the end (thread = dimension).
+// a warp issues the MMAs, four warps widen the values, do the softmax (thread =
+// token) and read the output at the end (thread = dimension).
 //
 // The cache's bytes bound large decode steps: 64 requests of up to 8192 tokens
-// (64 query heads on 8 of 128) take 91 us for 532 MB, 5.85 TB/s, 86 % of a
-// copy's rate; the tile loop itself runs at about that rate, the rest is the
-// first tile's latency (6 us: launch, work sums, lookups, TMA, DRAM) and the
-// last pieces' join (5). Two requests of 100 to 131 thousand tokens take 48.7 us
-// for 244 MB: the same, with longer joins. One request of 777 tokens takes 10.5
-// us, all latency. With several rows a request and a window (40 requests, up to
-// 24 rows, 1024 tokens of 64: 37 us for 35 MB) an item's start and end bound
-// it, some 8 thousand cycles next to 4 thousand for a tile.
-// What the tensor cores take off the loop: with both products on mma.sync (its
-// e4m3 form runs at 405 TFLOP/s on this part) the first such step took 3.2 ms;
-// the lo parts as further columns, not as a second product, read the wide
-// operand from shared memory once.
+// (64 query heads on 8 of 128) take 101 us for 532 MB, 5.24 TB/s, 77 % of a
+// copy's rate (the same loop without the widening takes 93). Two requests of 100
+// to 131 thousand tokens take 54 us for 244 MB: the same, with longer joins. One
+// request of 777 tokens takes 10.9 us, all latency. With several rows a request
+// and a window (40 requests, up to 24 rows, 1024 tokens of 64: 42 us for 35 MB)
+// an item's start and end bound it, some 8 thousand cycles next to 4 thousand
+// for a tile.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -46,10 +44,9 @@ namespace {
 
 constexpr int kProducerWarp = 4;  // after the compute warps 0-3
 constexpr int kIssueWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kWidenWarp = 6;     // the first of four, in shapes that have them
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
-constexpr int kUp = 6;               // weights are held times 2^6, so one may grow to 2^2.75 times its reference's before
-constexpr float kHighest = 8.75f;    // it leaves e4m3 at 2^8.75 (430)
+constexpr float kHighest = 64.0f;    // a weight may grow to 2^64 times its reference's: far from FP32's and BF16's ends
 
 template <int D, int RT>
 struct Shape {
@@ -60,10 +57,14 @@ struct Shape {
   static constexpr int kTileBytes = kTile * D;            // keys or values of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kKeyStride = kStageBytes, kValuesAt = kTileBytes, kValueStride = kStageBytes;
+  // Four warps of their own widen the values where one CTA fills an SM (prompts of 900 tokens, 16 heads on 8 of 256: 138 us,
+  // 169 without). Elsewhere they take the place of a CTA (16 rows of 128: 81 us, 74 without; 8 rows of 64: 64 and 53).
+  static constexpr bool kWideners = D == 256;
+  static constexpr int kThreads = kWideners ? 320 : 192;
   // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring (24 rows of 64 in 3 CTAs of
   // 96 registers spill: 98.8 us for 64 requests of up to 4096 tokens, against 68.5 in 2).
-  static constexpr int kCtasPerSm = D == 256 ? 1 : RT <= 2 ? 3 : 2;
-  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 ? 2 : 3;
+  static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 || (D == 64 && RT == 2) ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 && RT != 2 ? 2 : 3;
   // What starting and joining an item costs, in tiles: more of them the wider the row tile and the shorter a tile's loads
   // (64 ragged requests of 128: 8 rows take 91 us with 2, 93.5 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
   // of 64: 8 rows 45 with 2, 39 with 4; 32 rows 95 and 79, 75 with 8).
@@ -72,8 +73,8 @@ struct Shape {
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kStages * kStageBytes;  // hi rows, lo rows
-  static constexpr int kP = kQ + kCols * D;                 // hi rows, lo rows
-  static constexpr int kRed = kP + kCols * kTile;           // [row][warp] maxima, then sums
+  static constexpr int kP = kQ + kCols * D;                 // [64 tokens] hi rows, lo rows
+  static constexpr int kRed = kP + kCols * kTile * 2;       // [row][warp] maxima, then sums
   static constexpr int kRef = kRed + kRows * 16;          // [warp][row] the weights' references
   static constexpr int kRowF = kRef + kRows * 16;         // [row] factor
   static constexpr int kRowLo = kRowF + kRows * 4;        // [row] first and last visible token
@@ -82,7 +83,7 @@ struct Shape {
   static constexpr int kNan = kRowDst + kRows * 8;        // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;      // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kPrefix = kBars + (2 * kStages + 6) * 8;  // full, empty, s_full[2], o_full, p_ready, q_ready, drained
+  static constexpr int kPrefix = kBars + (2 * kStages + 8) * 8;  // full, empty, s_full[2], o_full, p_ready, q_ready, drained, v_ready[2]
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
   static_assert(kPartialOffset + 2ll * kMaxCtas * kPartialFloats * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand images on swizzle boundaries");
@@ -156,8 +157,53 @@ __device__ __forceinline__ void row_sums(float (&v)[kRows], float* red, int lane
   }
 }
 
+// A tile's values, widened in place to BF16 rows of 64 dimensions, the first ones over the tile's keys, which its scores
+// have used; thread `tid` takes the tile's token of that number. (From 128 dimensions on a token's wide rows lie over the
+// keys and its own codes; with 64 they lie over others', so all are read before any is written.) Values that no row sees
+// are dropped, whatever they hold; what is not finite and only some rows see is taken out and noted for those.
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
+__device__ __forceinline__ void widen_values(const Sight& sight, uint8_t* image, uint32_t entry, bool edge, int token, int tid,
+                                             uint32_t* nans, int* s_nans) {
+  using X = Shape<D, RT>;
+  uint32_t scale = (entry >> 8) & 0xFFu;
+  const uint32_t limit = finite_limit(scale);
+  const bool dropped = edge && (!sight.any(token) || !(entry >> 16)), careful = edge && sight.mixed;
+  if (dropped || (careful && scale == 255)) scale = 0;  // (all taken out)
+  const __nv_bfloat162 factor = scale2_of(scale);
+  auto load = [&](int c) {
+    return *reinterpret_cast<const uint4*>(image + X::kTileBytes + c / (X::kSpan / 16) * (kTile * X::kSpan) +
+                                           chunk_at<X::kSpan>(tid, c % (X::kSpan / 16)));
+  };
+  auto widened = [&](uint4 codes, int c) {
+    if (dropped) {
+      codes = make_uint4(0, 0, 0, 0);
+    } else if (careful && any_not_finite(codes, limit)) {
+      const uint32_t places = take_out(codes, limit) << (c % 2 * 16);
+      *s_nans = 1;
+#pragma unroll 1
+      for (int i = 0; i < sight.rows; ++i)
+        if (sight.sees(i, token)) atomicOr(nans + i * (D / 32) + c / 2, places);
+    }
+    uint8_t* dst = image + c / 4 * (kTile * 128);
+    const uint2 v0 = widen(codes.x, factor), v1 = widen(codes.y, factor), v2 = widen(codes.z, factor), v3 = widen(codes.w, factor);
+    *reinterpret_cast<uint4*>(dst + chunk_at<128>(tid, c % 4 * 2)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    *reinterpret_cast<uint4*>(dst + chunk_at<128>(tid, c % 4 * 2 + 1)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+  };
+  // (Rolled: unrolled, its code crowds the softmax's out of the instruction cache: 106 us for 64 ragged requests, not 101.)
+  constexpr int kBatch = D == 64 ? 4 : 2;
+#pragma unroll 1
+  for (int c = 0; c < D / 16; c += kBatch) {
+    uint4 codes[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) codes[i] = load(c + i);
+    if (D == 64) compute_sync();
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) widened(codes[i], c + i);
+  }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPerSm)
     kv_attend_kernel(const AttendArgs a, const __grid_constant__ AttendMaps maps, int shift) {
   using X = Shape<D, RT>;
   extern __shared__ uint8_t raw[];
@@ -171,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   uint64_t* p_ready = o_full + 1;         // a tile's weights in shared memory
   uint64_t* q_ready = p_ready + 1;        // a segment's queries in shared memory
   uint64_t* drained = q_ready + 1;        // every MMA issued has completed
+  uint64_t* v_ready = drained + 1;        // [2]: a tile's values widened by warps of their own
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
-  __shared__ long long s_sum[kThreads / 32][2];
+  __shared__ long long s_sum[X::kThreads / 32][2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ int s_nans;         // the item has outputs noted in `nans`
@@ -192,9 +239,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     mbar_init(p_ready, kCompute);
     mbar_init(q_ready, kCompute);
     mbar_init(drained, 1);
+    mbar_init(v_ready, kCompute);
+    mbar_init(v_ready + 1, kCompute);
     fence_mbar_init();
   }
-  const int weight = sum_work<kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
+  const int weight = sum_work<X::kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= ctas) return;
@@ -211,8 +260,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
   if (warp == kProducerWarp) {
     produce<X, D, 3>(a, maps, prefix, weight, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
-    // Operand descriptors: the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values M-major
-    // (D = 64: both 64-row halves of the operand read the same 64 dimensions).
+    // Operand descriptors: keys and queries in the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values
+    // M-major, 64 dimensions wide (D = 64: both 64-row halves of the operand read the same 64).
+    constexpr uint32_t kValueHalf = kTile * 128, kNext = D == 64 ? 0 : kValueHalf;
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
     const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
     int k = 0, segments = 0;
@@ -246,16 +296,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         const bool early = more && __all_sync(kAll, mbar_test(full + (k + 1) % X::kStages, ((k + 1) / X::kStages) & 1));
         if (early) scores(k + 1);
         alive = alive && __all_sync(kAll, wait(p_ready, k & 1, status));
+        if (X::kWideners) alive = alive && __all_sync(kAll, wait(v_ready + (k & 1), (k >> 1) & 1, status));
         if (!alive) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vals = ring + (k % X::kStages) * X::kStageBytes + X::kTileBytes;
+          const uint32_t vals = ring + (k % X::kStages) * X::kStageBytes;
 #pragma unroll
           for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
-            for (int st = 0; st < kTile / 32; ++st)
-              mma_f8(tmem_o + h * X::kCols, smem_desc(vals + (h * kTile + st * 32) * X::kSpan, 0, kGroup, kMode),
-                     smem_desc(p_at + st * 32, 16, 1024, 2), idesc_f8(X::kCols, true), tile > s.begin || st > 0);
+            for (int st = 0; st < kTile / 16; ++st)
+              mma_bf16(tmem_o + h * X::kCols, smem_desc(vals + 2 * h * kValueHalf + st * 2048, kNext, 1024, 2),
+                       smem_desc(p_at + st / 4 * (X::kCols * 128) + st % 4 * 32, 16, 1024, 2),
+                       idesc_bf16(X::kCols, true), tile > s.begin || st > 0);
           tc_commit(empty + k % X::kStages);
           tc_commit(o_full);
         }
@@ -271,6 +323,32 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       wait(drained, 0, status);
     }
     __syncwarp();
+  } else if (X::kWideners && warp >= kWidenWarp) {
+    const int at = tid - 32 * kWidenWarp;
+    const uint32_t inverse = inverse_of(a.group);
+    int k = 0, segments = 0;
+    bool alive = true;
+    Segment<X::kRows> s;
+    s.find(a, prefix, weight, shift, start, stop);
+    for (long long x = start; alive;) {
+      const Sight sight(a, s, inverse);
+      if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
+      for (int tile = s.begin; tile < s.end && alive; ++tile, ++k) {
+        const int stage = k % X::kStages;
+        alive = __all_sync(kAll, wait(full + stage, (k / X::kStages) & 1, status));
+        alive = alive && __all_sync(kAll, wait(s_full + (k & 1), (k >> 1) & 1, status));
+        if (!alive) break;
+        const uint32_t* mt = meta + stage * (kMaxPages + 1);
+        const int base = (s.q.tile0 + tile) * kTile;
+        widen_values<D, RT>(sight, sm + X::kRing + stage * X::kStageBytes, mt[at >> shift], sight.edge(base) || !(mt[kMaxPages] >> 8),
+                            base + at, at, reinterpret_cast<uint32_t*>(sm + X::kNan), &s_nans);
+        fence_proxy_async_shared();
+        mbar_arrive(v_ready + (k & 1));
+      }
+      x += s.length;
+      if (x >= stop) break;
+      s.next(a, prefix, shift, x, stop);
+    }
   } else {
     float* red = reinterpret_cast<float*>(sm + X::kRed);
     float* refs = reinterpret_cast<float*>(sm + X::kRef) + warp * X::kRows;
@@ -291,18 +369,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
     const uint32_t inverse = inverse_of(a.group);
     for (;;) {
       const Request& rq = s.q;
-      const int rows = static_cast<int>(min(static_cast<long long>(rq.n - s.token) * a.group - s.within, static_cast<long long>(X::kRows)));
+      const Sight sight(a, s, inverse);
+      const int rows = sight.rows;
       float l[X::kRows];                 // sums of this thread's tokens' weights against the references
       float m = -INFINITY;               // reference of row `lane`
-      int m_scale = 0;                   // reference of the value scales
 #pragma unroll
       for (int i = 0; i < X::kRows; ++i) l[i] = 0.0f;
-      bool mixed = false;  // rows of this item see different tokens
       bool blank = false;  // some row has seen no token yet
       if (tid < X::kRows) {
-        const int in_tile = per_group(s.within + tid, inverse), tok = s.token + in_tile, last = tid < rows ? rq.seq - rq.n + tok : -1;
+        const int in_tile = per_group(s.within + tid, inverse), tok = s.token + in_tile, last = tid < rows ? sight.last(tid) : -1;
         row_hi[tid] = last;
-        row_lo[tid] = tid < rows && a.window > 0 ? max(0, last - a.window + 1) : 0;
+        row_lo[tid] = tid < rows ? sight.first(last) : 0;
         row_dst[tid] = static_cast<long long>(rq.first + tok) * a.q_heads + s.head * a.group + s.within + tid - in_tile * a.group;
       }
       if (s.begin < s.end) {
@@ -343,15 +420,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         mbar_arrive(q_ready);
         compute_sync();
       }
-      // Tokens that any of the rows sees, and that all see.
-      int any_lo = 0, any_hi = -1, all_lo = 0, all_hi = 0x7FFFFFFF;
-      if (s.begin < s.end) {
-        any_lo = row_lo[0];
-        any_hi = row_hi[rows - 1];
-        all_lo = row_lo[rows - 1];
-        all_hi = row_hi[0];
-        mixed = any_lo != all_lo || any_hi != all_hi;
-      }
       for (int tile = s.begin; tile < s.end; ++tile, ++k) {
         const int stage = k % X::kStages;
         failed |= !wait(s_full + (k & 1), (k >> 1) & 1, status);
@@ -360,11 +428,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
         tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const uint32_t entry = mt[tid >> shift];
-        const int base = (rq.tile0 + tile) * kTile, token = base + tid, most = static_cast<int>(mt[kMaxPages] & 0xFFu);
-        // Edge: some row does not see some token of the tile.
-        const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
+        const int base = (rq.tile0 + tile) * kTile, token = base + tid;
+        const bool edge = sight.edge(base) || !(mt[kMaxPages] >> 8);
+        if (!X::kWideners)
+          widen_values<D, RT>(sight, sm + X::kRing + stage * X::kStageBytes, entry, edge, token, tid, nans, &s_nans);
         const float ks = scale_of(entry & 0xFFu);
-        bool find = tile == s.begin || most > m_scale;
+        bool find = tile == s.begin;
         if (edge || blank)  // a row's first token
           find |= __any_sync(kAll, lane < X::kRows && m == -INFINITY && row_hi[min(lane, X::kRows - 1)] >= base &&
                                        row_lo[min(lane, X::kRows - 1)] < base + kTile);
@@ -392,28 +461,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               if (token < row_lo[i] || token > row_hi[i] || !(entry >> 16)) sc[i] = -INFINITY;
           }
           if (find) {
-            // The references are raised: the largest value scale, and each row's largest score with its token's value
-            // scale (less the largest); what is there already follows.
-            const int scale = max(m_scale, most), rise = min(scale - m_scale, kFar);
-            const float drop = static_cast<float>(max(static_cast<int>((entry >> 8) & 0xFFu) - scale, -kFar));
+            // The references are raised to each row's largest score; what is there already follows.
             float top = -INFINITY;  // of row `lane`
 #pragma unroll
             for (int i = 0; i < X::kRows; ++i) {
-              const float v = warp_max(sc[i] + drop);
+              const float v = warp_max(sc[i]);
               if (lane == i) top = v;
             }
             if (lane < X::kRows) red[lane * 4 + warp] = top;
             dead = compute_any(failed);
             if (dead) break;
-            float keep_l = 1.0f, keep_o = 1.0f;
+            float keep = 1.0f;
             if (lane < X::kRows) {
               const float4 v = *reinterpret_cast<const float4*>(red + lane * 4);
-              top = fmaxf(m - static_cast<float>(rise), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-              keep_l = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
-              keep_o = m > -INFINITY ? exp2_fast(m - top + static_cast<float>(m_scale - scale)) : 0.0f;
+              top = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+              keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
               m = top;
             }
-            m_scale = scale;
             blank = __any_sync(kAll, lane < rows && m == -INFINITY);
             if (lane < X::kRows) refs[lane] = m > -INFINITY ? m : 0.0f;
             __syncwarp();
@@ -421,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               float keeps[X::kRows];
 #pragma unroll
               for (int i = 0; i < X::kRows; ++i) {
-                keeps[i] = __shfl_sync(kAll, keep_o, i);
-                l[i] *= __shfl_sync(kAll, keep_l, i);
+                keeps[i] = __shfl_sync(kAll, keep, i);
+                l[i] *= keeps[i];
               }
               failed |= !wait(o_full, (k - 1) & 1, status);
               __syncwarp();
@@ -441,79 +505,40 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
               tmem_wait_stores();
             }
           }
-          // Less their reference, times 2^kUp and the page's value scale over its reference, all in the exponent.
-          const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -kFar);
-          const float offset = static_cast<float>(up);
+          // Less their reference.
           float high = -INFINITY;
 #pragma unroll
           for (int i = 0; i < X::kRows; i += 4) {
             const float4 r = *reinterpret_cast<const float4*>(refs + i);
-            sc[i] += offset - r.x;
-            sc[i + 1] += offset - r.y;
-            sc[i + 2] += offset - r.z;
-            sc[i + 3] += offset - r.w;
+            sc[i] -= r.x;
+            sc[i + 1] -= r.y;
+            sc[i + 2] -= r.z;
+            sc[i + 3] -= r.w;
             high = fmaxf(high, fmaxf(fmaxf(sc[i], sc[i + 1]), fmaxf(sc[i + 2], sc[i + 3])));
           }
           // Every thread's weights are held against the same references: another round for all if one outgrew its own.
           // (Or a wait of its ran out: the other round agrees on that.)
           find = compute_any(high > kHighest || failed);
           if (find && tries == 0) continue;
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-          if (tile > s.begin) failed |= !wait(o_full, (k - 1) & 1, status);  // the last tile's have been used
-          uint8_t* prow = sm + X::kP + tid % 16;
+          if (tile > s.begin) failed |= !wait(o_full, (k - 1) & 1, status);  // the last tile's weights have been used
+          uint8_t* prow = sm + X::kP + tid / 64 * (X::kCols * 128) + tid % 8 * 2;
+          const int chunk = tid % 64 / 8;
+          auto put = [&](int row, uint32_t v) { *reinterpret_cast<uint16_t*>(prow + chunk_at<128>(row, chunk)) = static_cast<uint16_t>(v); };
 #pragma unroll
           for (int i = 0; i < X::kRows; i += 2) {
             const float p0 = exp2_fast(sc[i]), p1 = exp2_fast(sc[i + 1]);
-            l[i] = fmaf(p0, down, l[i]);
-            l[i + 1] = fmaf(p1, down, l[i + 1]);
+            l[i] += p0;
+            l[i + 1] += p1;
             uint32_t hi, lo;
-            split2_half(p0, p1, hi, lo);
-            prow[chunk_at<128>(i, tid / 16)] = static_cast<uint8_t>(hi);
-            prow[chunk_at<128>(i + 1, tid / 16)] = static_cast<uint8_t>(hi >> 8);
-            prow[chunk_at<128>(X::kRows + i, tid / 16)] = static_cast<uint8_t>(lo);
-            prow[chunk_at<128>(X::kRows + i + 1, tid / 16)] = static_cast<uint8_t>(lo >> 8);
+            split2_bf16(p0, p1, hi, lo);
+            put(i, hi);
+            put(i + 1, hi >> 16);
+            put(X::kRows + i, lo);
+            put(X::kRows + i + 1, lo >> 16);
           }
           break;
         }
         if (dead) break;
-        if (edge) {
-          // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
-          // taken out too, and noted for those.
-          uint8_t* row = sm + X::kRing + stage * X::kStageBytes + X::kTileBytes + tid * X::kSpan;
-          const bool seen = token >= any_lo && token <= any_hi && (entry >> 16);
-          bool look = !seen || mixed;
-          if (RT > 1 && look && seen) {  // (with 8 rows, mostly one token's, the code in the way costs more than it saves)
-            look = false;
-#pragma unroll
-            for (int h = 0; h < X::kHalves; ++h)
-              look |= any_nan<X::kSpan / 16, 1>(reinterpret_cast<const uint4*>(row + h * (kTile * X::kSpan)));
-          }
-          if (look) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(row + (c * 16 / X::kSpan) * (kTile * X::kSpan) + c * 16 % X::kSpan);
-              if (!seen) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 w = *at;
-              uint32_t words[4] = {w.x, w.y, w.z, w.w};
-              if (!(nan_code(w.x) | nan_code(w.y) | nan_code(w.z) | nan_code(w.w))) continue;
-              // Stored chunk c of the row holds the dimensions of chunk c ^ (the row's swizzle).
-              const int chunk = X::kSpan == 128 ? (c & ~7) | ((c ^ tid) & 7) : c ^ ((tid >> 1) & 3);
-#pragma unroll 1
-              for (int b = 0; b < 16; ++b) {
-                if (((words[b >> 2] >> (8 * (b & 3))) & 0x7Fu) != 0x7Fu) continue;
-                words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
-                const int dim = chunk * 16 + b;
-                s_nans = 1;
-                for (int i = 0; i < rows; ++i)
-                  if (token >= row_lo[i] && token <= row_hi[i]) atomicOr(nans + i * (D / 32) + dim / 32, 1u << (dim % 32));
-              }
-              *at = make_uint4(words[0], words[1], words[2], words[3]);
-            }
-          }
-        }
         fence_proxy_async_shared();
         tc_fence_before_sync();
         mbar_arrive(p_ready);
@@ -522,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
       float acc[X::kHalves][X::kRows];
       if (s.begin < s.end && !failed) {
         failed |= !wait(o_full, (k - 1) & 1, status);
+        if (X::kWideners) failed |= !wait(v_ready + ((k - 1) & 1), ((k - 1) >> 1) & 1, status);  // (for what they noted)
         __syncwarp();
         tc_fence_after_sync();
-        const float out_scale = scale_of(m_scale) * (1.0f / (1 << kUp));
 #pragma unroll
         for (int h = 0; h < X::kHalves; ++h)
 #pragma unroll
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RT>::kCtasPerSm)
             tmem_wait_8(o);
             tmem_wait_8(u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[h][part + j] = fmaf(u[j], kLo, o[j]) * out_scale;
+            for (int j = 0; j < 8; ++j) acc[h][part + j] = o[j] + u[j];
           }
         tc_fence_before_sync();
       } else {
@@ -643,7 +668,7 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
                              Shape<D, RT>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
   const int resident = sms * Shape<D, RT>::kCtasPerSm, grid = resident < kMaxCtas ? resident : kMaxCtas;
-  kv_attend_kernel<D, RT><<<grid, kThreads, smem, stream>>>(a, maps, shift);
+  kv_attend_kernel<D, RT><<<grid, Shape<D, RT>::kThreads, smem, stream>>>(a, maps, shift);
   return cudaGetLastError();
 }
 

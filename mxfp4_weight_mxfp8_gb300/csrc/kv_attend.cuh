@@ -53,6 +53,18 @@ __host__ __device__ constexpr uint32_t idesc_f8(int n, bool a_transposed, bool b
          ((b_transposed ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// The same with BF16 operands; K = 16.
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool a_transposed, bool b_transposed = false) {
+  return idesc_f8(n, a_transposed, b_transposed) | (1u << 7) | (1u << 10);
+}
+
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -89,13 +101,12 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_
   lo = pack2((v0 - f.x) * 16.0f, (v1 - f.y) * 16.0f);
 }
 
-// The same in half precision, for weights: 11 bits are more than the codes hold.
-__device__ __forceinline__ void split2_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  const __half2 v = __floats2half2_rn(v0, v1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
-  const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-  const __half2 rest = __hmul2(__hsub2(v, f), __float2half2_rn(16.0f));
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+// Two weights as BF16 hi and lo: 16 bits of each, whatever its magnitude.
+__device__ __forceinline__ void split2_bf16(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xFFFF0000u));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
 // Codes of two values: e4m3 hi and e5m2 lo, v = hi + lo.
@@ -114,6 +125,45 @@ __device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& h
 }
 
 __device__ __forceinline__ uint32_t nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+// Values in BF16 are the code times its page's scale, exact. What leaves BF16's range (scales of 2^120 and more) or is a
+// NaN is not finite there, and a weight of zero would not drop it: codes from a limit on, in magnitude. finite_limit is
+// what takes each byte's magnitude to 128 from there on.
+__device__ __forceinline__ uint32_t finite_limit(uint32_t scale) {
+  return (scale < 247 ? 1u : scale == 255 ? 128u : 8 + 8 * (scale - 247)) * 0x01010101u;
+}
+__device__ __forceinline__ uint32_t not_finite(uint32_t codes, uint32_t limit) {
+  return ((codes & 0x7F7F7F7Fu) + limit) & 0x80808080u;
+}
+__device__ __forceinline__ bool any_not_finite(const uint4& codes, uint32_t limit) {
+  return (not_finite(codes.x, limit) | not_finite(codes.y, limit) | not_finite(codes.z, limit) | not_finite(codes.w, limit)) != 0;
+}
+
+// 2^(b - 127) of an E8M0 byte, twice.
+__device__ __forceinline__ __nv_bfloat162 scale2_of(uint32_t b) {
+  const uint32_t one = b ? b << 7 : 0x0040u, both = one | one << 16;
+  return *reinterpret_cast<const __nv_bfloat162*>(&both);
+}
+
+// Four codes -> four values times `scale`.
+__device__ __forceinline__ uint2 widen(uint32_t codes, __nv_bfloat162 scale) {
+  const float2 a = unpack2(codes & 0xFFFFu), b = unpack2(codes >> 16);
+  const __nv_bfloat162 v0 = __hmul2(__floats2bfloat162_rn(a.x, a.y), scale), v1 = __hmul2(__floats2bfloat162_rn(b.x, b.y), scale);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+}
+
+// Takes the codes that are not finite out of a chunk of 16; their places as bits.
+__device__ __forceinline__ uint32_t take_out(uint4& codes, uint32_t limit) {
+  uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w}, places = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bad = not_finite(w[i], limit) >> 7;
+    w[i] &= ~(bad * 0xFFu);
+    places |= ((bad & 1u) | (bad >> 7 & 2u) | (bad >> 14 & 4u) | (bad >> 21 & 8u)) << (4 * i);
+  }
+  codes = make_uint4(w[0], w[1], w[2], w[3]);
+  return places;
+}
 
 // Byte offset of 16-byte chunk c of row n in an image of kSpan-byte rows, as the swizzle of that width places it.
 template <int kSpan>
@@ -287,6 +337,35 @@ struct Segment {
       take(RowTiles<kRows>(a, q));
     }
     cut(a, x, stop, 0);
+  }
+};
+
+// What a row tile's rows see: the tokens that any of them sees and those that all see. Rows of later tokens see later ones.
+struct Sight {
+  int any_lo, any_hi, all_lo, all_hi;
+  int rows;      // of the row tile
+  bool mixed;    // its rows see different tokens
+  int within, window;
+  uint32_t inverse;
+  template <int kRows>
+  __device__ __forceinline__ Sight(const AttendArgs& a, const Segment<kRows>& s, uint32_t inverse)
+      : within(s.within), window(a.window), inverse(inverse) {
+    rows = static_cast<int>(min(static_cast<long long>(s.q.n - s.token) * a.group - s.within, static_cast<long long>(kRows)));
+    all_hi = s.q.seq - s.q.n + s.token;
+    any_hi = last(rows - 1);
+    any_lo = first(all_hi);
+    all_lo = first(any_hi);
+    mixed = any_lo != all_lo || any_hi != all_hi;
+  }
+  // The last token that row i sees, and the first that a row with this last one sees.
+  __device__ __forceinline__ int last(int i) const { return all_hi + per_group(within + i, inverse); }
+  __device__ __forceinline__ int first(int last) const { return window > 0 ? max(0, last - window + 1) : 0; }
+  // Some row does not see some token of the tile from `base` on.
+  __device__ __forceinline__ bool edge(int base) const { return base < all_lo || base + kTile - 1 > all_hi; }
+  __device__ __forceinline__ bool any(int token) const { return token >= any_lo && token <= any_hi; }
+  __device__ __forceinline__ bool sees(int i, int token) const {
+    const int end = last(i);
+    return token <= end && token >= first(end);
   }
 };
 

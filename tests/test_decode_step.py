@@ -752,6 +752,67 @@ def test_attend_nan_in_the_cache_reaches_only_the_rows_that_see_it(moe, dim, win
     assert not np.isnan(out[~sees]).any() and not np.isnan(lse[~sees]).any()
 
 
+# Query rows of a request, query heads on one cache head: a row tile of 8, 16, 24 and 32 rows
+# (with heads of 256, of 16 rows in all but the first).
+TILES = [(2, 4), (2, 8), (3, 8), (4, 8)]
+
+
+def request_reference(cache, q, table, n, scale):
+    """attend_reference of one request without a window, whole rows at a time."""
+    k, v, ks, vs = cache
+    rows, q_heads, dim = q.shape
+    heads, page = k.shape[1], k.shape[2]
+    js = np.arange(n)
+    own = table[0, js // page]
+    out, lse, mass = np.zeros(q.shape), np.zeros((rows, q_heads)), np.zeros(q.shape)
+    seen = js <= (n - rows + np.arange(rows))[:, None]
+    for h in range(q_heads):
+        g = h // (q_heads // heads)
+        kk = VALUES[k[own, g, js % page]] * 2.0 ** (ks[own, g].astype(np.float64) - 127)[:, None]
+        vv = VALUES[v[own, g, js % page]] * 2.0 ** (vs[own, g].astype(np.float64) - 127)[:, None]
+        s = np.where(seen, q[:, h].astype(np.float64) @ kk.T * scale, -np.inf)
+        w = np.exp(s - s.max(1, keepdims=True))
+        lse[:, h] = s.max(1) + np.log(w.sum(1))
+        w /= w.sum(1, keepdims=True)
+        out[:, h], mass[:, h] = w @ vv, w @ np.abs(vv)
+    return out, lse, mass
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,gap,deviation", [(200, 25, 1.0), (1500, 13, 1.0), (1500, 15, 1.0), (8192, 14, 1.0), (8192, 40, 1.0),
+                                             (131071, 13, 1.0), (131071, 15, 0.5)])
+def test_attend_small_weights_under_a_dominant_token_without_value(moe, n, gap, deviation, dim, rows, q_heads):
+    """A first token takes most of every row's weight and has value 0: the output is the others' alone, whose weights lie
+    `gap` nats below. They count with their own precision, not with the dominant weight's: check_attend's bounds."""
+    if n > 10000 and (dim == 256 or rows * q_heads != 8):
+        pytest.skip("the longest contexts in the narrowest tile")
+    rng = np.random.default_rng(n + gap)
+    page = 64
+    pages = -(-n // page)
+    k, v = (np.zeros((pages, 1, page, dim), np.uint8) for _ in range(2))
+    ks, vs = np.full((pages, 1), 124, np.uint8), rng.integers(119, 124, (pages, 1)).astype(np.uint8)
+    mean = rng.standard_normal(dim)
+    for j in range(pages):
+        keys = rng.standard_normal((page, dim)) * 8  # times 2^-3
+        keys[:, 0] = 0  # the dominant token's own direction
+        k[j, 0] = e4m3_encode(keys)
+        v[j, 0] = e4m3_encode((rng.standard_normal((page, dim)) + mean) * 30)
+    k[0, 0, 0] = 0
+    k[0, 0, 0, 0] = e4m3_encode(np.array([gap * 8 * dim ** 0.5 / 16]))[0]
+    v[0, 0, 0] = 0
+    q = rng.standard_normal((rows, q_heads, dim)) * deviation
+    q[..., 0] = 16
+    q = bf16(q)
+    table, start, seq = np.arange(pages, dtype=np.int32)[None], np.array([0, rows], np.int32), np.array([n], np.int32)
+    out, lse = run_attend(moe, (k, v, ks, vs), q.cuda(), table, start, seq)
+    want, want_lse, mass = request_reference((k, v, ks, vs), q.float().numpy(), table, n, dim ** -0.5)
+    assert (np.abs(lse - want_lse) <= 1.6e-4).all()
+    assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
+    assert np.linalg.norm(out - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (5, 24, 64), (200, 8, 128), (64, 16, 64), (9, 16, 256)])
 def test_attend_gives_the_same_bits_each_time(moe, rows, q_heads, dim):
