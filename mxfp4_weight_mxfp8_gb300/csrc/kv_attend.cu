@@ -46,7 +46,6 @@ constexpr int kProducerWarp = 4;  // after the compute warps 0-3
 constexpr int kIssueWarp = 5;
 constexpr int kWidenWarp = 6;     // the first of four, in shapes that have them
 constexpr float kLo = 1.0f / 16.0f;  // lo parts are held 16 times as large
-constexpr float kHighest = 64.0f;    // a weight may grow to 2^64 times its reference's: far from FP32's and BF16's ends
 
 template <int D, int RT>
 struct Shape {
@@ -157,48 +156,24 @@ __device__ __forceinline__ void row_sums(float (&v)[kRows], float* red, int lane
   }
 }
 
-// A tile's values, widened in place to BF16 rows of 64 dimensions, the first ones over the tile's keys, which its scores
-// have used; thread `tid` takes the tile's token of that number. (From 128 dimensions on a token's wide rows lie over the
-// keys and its own codes; with 64 they lie over others', so all are read before any is written.) Values that no row sees
-// are dropped, whatever they hold; what is not finite and only some rows see is taken out and noted for those.
+// A tile's values, widened in place, the first dimensions over the tile's keys, which its scores have used; thread `tid`
+// takes the tile's token of that number. (From 128 dimensions on a token's wide rows lie over the keys and its own codes;
+// with 64 they lie over others', so all are read before any is written.)
 template <int D, int RT>
-__device__ __forceinline__ void widen_values(const Sight& sight, uint8_t* image, uint32_t entry, bool edge, int token, int tid,
-                                             uint32_t* nans, int* s_nans) {
+__device__ __forceinline__ void widen_values(const Widener<D / 32>& widener, uint8_t* image, int tid) {
   using X = Shape<D, RT>;
-  uint32_t scale = (entry >> 8) & 0xFFu;
-  const uint32_t limit = finite_limit(scale);
-  const bool dropped = edge && (!sight.any(token) || !(entry >> 16)), careful = edge && sight.mixed;
-  if (dropped || (careful && scale == 255)) scale = 0;  // (all taken out)
-  const __nv_bfloat162 factor = scale2_of(scale);
-  auto load = [&](int c) {
-    return *reinterpret_cast<const uint4*>(image + X::kTileBytes + c / (X::kSpan / 16) * (kTile * X::kSpan) +
-                                           chunk_at<X::kSpan>(tid, c % (X::kSpan / 16)));
-  };
-  auto widened = [&](uint4 codes, int c) {
-    if (dropped) {
-      codes = make_uint4(0, 0, 0, 0);
-    } else if (careful && any_not_finite(codes, limit)) {
-      const uint32_t places = take_out(codes, limit) << (c % 2 * 16);
-      *s_nans = 1;
-#pragma unroll 1
-      for (int i = 0; i < sight.rows; ++i)
-        if (sight.sees(i, token)) atomicOr(nans + i * (D / 32) + c / 2, places);
-    }
-    uint8_t* dst = image + c / 4 * (kTile * 128);
-    const uint2 v0 = widen(codes.x, factor), v1 = widen(codes.y, factor), v2 = widen(codes.z, factor), v3 = widen(codes.w, factor);
-    *reinterpret_cast<uint4*>(dst + chunk_at<128>(tid, c % 4 * 2)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-    *reinterpret_cast<uint4*>(dst + chunk_at<128>(tid, c % 4 * 2 + 1)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
-  };
   // (Rolled: unrolled, its code crowds the softmax's out of the instruction cache: 106 us for 64 ragged requests, not 101.)
   constexpr int kBatch = D == 64 ? 4 : 2;
 #pragma unroll 1
   for (int c = 0; c < D / 16; c += kBatch) {
     uint4 codes[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) codes[i] = load(c + i);
+    for (int i = 0; i < kBatch; ++i)
+      codes[i] = *reinterpret_cast<const uint4*>(image + X::kTileBytes + (c + i) / (X::kSpan / 16) * (kTile * X::kSpan) +
+                                                 chunk_at<X::kSpan>(tid, (c + i) % (X::kSpan / 16)));
     if (D == 64) compute_sync();
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) widened(codes[i], c + i);
+    for (int i = 0; i < kBatch; ++i) widener(codes[i], c + i, tid, image);
   }
 }
 
@@ -340,8 +315,9 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
         if (!alive) break;
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + tile) * kTile;
-        widen_values<D, RT>(sight, sm + X::kRing + stage * X::kStageBytes, mt[at >> shift], sight.edge(base) || !(mt[kMaxPages] >> 8),
-                            base + at, at, reinterpret_cast<uint32_t*>(sm + X::kNan), &s_nans);
+        const Widener<D / 32> widener(sight, mt[at >> shift], sight.edge(base) || mt[kMaxPages] == 0, base + at,
+                                      reinterpret_cast<uint32_t*>(sm + X::kNan), &s_nans);
+        widen_values<D, RT>(widener, sm + X::kRing + stage * X::kStageBytes, at);
         fence_proxy_async_shared();
         mbar_arrive(v_ready + (k & 1));
       }
@@ -429,9 +405,9 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const uint32_t entry = mt[tid >> shift];
         const int base = (rq.tile0 + tile) * kTile, token = base + tid;
-        const bool edge = sight.edge(base) || !(mt[kMaxPages] >> 8);
+        const bool edge = sight.edge(base) || mt[kMaxPages] == 0;
         if (!X::kWideners)
-          widen_values<D, RT>(sight, sm + X::kRing + stage * X::kStageBytes, entry, edge, token, tid, nans, &s_nans);
+          widen_values<D, RT>(Widener<D / 32>(sight, entry, edge, token, nans, &s_nans), sm + X::kRing + stage * X::kStageBytes, tid);
         const float ks = scale_of(entry & 0xFFu);
         bool find = tile == s.begin;
         if (edge || blank)  // a row's first token

@@ -26,7 +26,7 @@ constexpr int kCompute = 128;     // threads of a compute warpgroup
 constexpr int kMaxPages = 8;      // pages of a tile
 constexpr int kMaxCtas = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFar = 100;              // a value scale this many powers of two below the largest counts as no smaller
+constexpr float kHighest = 64.0f;      // a weight may grow to 2^64 times its reference's: far from FP32's and BF16's ends
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -58,6 +58,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
   asm volatile(
       "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A in TMEM, a row to a lane, two values to a column.
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -116,16 +124,6 @@ __device__ __forceinline__ void split2_wide(float v0, float v1, uint32_t& hi, ui
   lo = __nv_cvt_float2_to_fp8x2(make_float2(v0 - f.x, v1 - f.y), __NV_SATFINITE, __NV_E5M2);
 }
 
-// The same in half precision, for weights.
-__device__ __forceinline__ void split2_wide_half(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  const __half2 v = __floats2half2_rn(v0, v1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
-  const __half2 rest = __hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3)));
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2);
-}
-
-__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
-
 // Values in BF16 are the code times its page's scale, exact. What leaves BF16's range (scales of 2^120 and more) or is a
 // NaN is not finite there, and a weight of zero would not drop it: codes from a limit on, in magnitude. finite_limit is
 // what takes each byte's magnitude to 128 from there on.
@@ -169,18 +167,6 @@ __device__ __forceinline__ uint32_t take_out(uint4& codes, uint32_t limit) {
 template <int kSpan>
 __device__ __forceinline__ uint32_t chunk_at(int n, int c) {
   return kSpan == 128 ? n * 128 + ((c ^ (n & 7)) << 4) : n * 64 + ((c ^ ((n >> 1) & 3)) << 4);
-}
-
-// Whether any of kChunks 16-byte chunks, kStep apart, holds a NaN code.
-template <int kChunks, int kStep>
-__device__ __forceinline__ bool any_nan(const uint4* p) {
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const uint4 w = p[i * kStep];
-    bad |= nan_code(w.x) | nan_code(w.y) | nan_code(w.z) | nan_code(w.w);
-  }
-  return bad != 0;
 }
 
 // x / group for rows x of a row tile (from its first token's first row on, so below 2048): `inverse` is 2^32 / group,
@@ -369,6 +355,44 @@ struct Sight {
   }
 };
 
+// Widens one token's value codes to BF16 rows of 64 dimensions. Values that no row sees are dropped, whatever they hold;
+// what is not finite and only some rows see is taken out and noted for those, in `nans` ([row][kWords]).
+template <int kWords>
+struct Widener {
+  const Sight& sight;
+  uint32_t* nans;
+  int* any_nans;
+  int token;
+  bool dropped, careful;
+  uint32_t limit;
+  __nv_bfloat162 factor;
+  __device__ __forceinline__ Widener(const Sight& sight, uint32_t entry, bool edge, int token, uint32_t* nans, int* any_nans)
+      : sight(sight), nans(nans), any_nans(any_nans), token(token) {
+    uint32_t scale = (entry >> 8) & 0xFFu;
+    limit = finite_limit(scale);
+    dropped = edge && (!sight.any(token) || !(entry >> 16));
+    careful = edge && sight.mixed;
+    if (dropped || (careful && scale == 255)) scale = 0;  // (all taken out)
+    factor = scale2_of(scale);
+  }
+  // Chunk c of 16 dimensions, into row `row` of an image.
+  __device__ __forceinline__ void operator()(uint4 codes, int c, int row, uint8_t* image) const {
+    if (dropped) {
+      codes = make_uint4(0, 0, 0, 0);
+    } else if (careful && any_not_finite(codes, limit)) {
+      const uint32_t places = take_out(codes, limit) << (c % 2 * 16);
+      *any_nans = 1;
+#pragma unroll 1
+      for (int i = 0; i < sight.rows; ++i)
+        if (sight.sees(i, token)) atomicOr(nans + i * kWords + c / 2, places);
+    }
+    uint8_t* dst = image + c / 4 * (kTile * 128);
+    const uint2 v0 = widen(codes.x, factor), v1 = widen(codes.y, factor), v2 = widen(codes.z, factor), v3 = widen(codes.w, factor);
+    *reinterpret_cast<uint4*>(dst + chunk_at<128>(row, c % 4 * 2)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    *reinterpret_cast<uint4*>(dst + chunk_at<128>(row, c % 4 * 2 + 1)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+  }
+};
+
 // The workspace header's first words.
 struct Header {
   int32_t status;
@@ -448,7 +472,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
 
 // A producer warp: looks up the pages of the CTA's tiles and streams their keys (kWhich 1), values (2) or both (3)
 // through the ring. With the values go the pages' entries: key scale, value scale << 8, present << 16; and after a
-// tile's, its largest value scale and, << 8, whether every page is there.
+// tile's, whether every page is there.
 template <class X, int D, int kWhich>
 __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int weight, int shift,
                         long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
@@ -463,7 +487,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   for (long long x = start; alive;) {
     const Request& q = s.q;
     int page = -1;
-    uint32_t entry = 0, top = 0;
+    uint32_t entry = 0;
     bool fresh = false;  // a batch whose scales are not read yet
     for (int tile = s.begin; tile < s.end; ++tile, ++k) {
       const int batch = (tile - s.begin) & (batch_tiles - 1);
@@ -497,14 +521,12 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
           const long long at = static_cast<long long>(page) * a.c.kv_heads + s.head;
           entry = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8 | 1u << 16;
         }
-        top = (entry >> 8) & 0xFFu;  // the tile's largest value scale
-        for (int d = 1; d < per_tile; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
       }
       if (kWhich & 2) {
         uint32_t* m = meta + stage * (kMaxPages + 1);
         if (mine) {
           m[in_tile] = entry;
-          if (in_tile == 0) m[kMaxPages] = top | (boxes == per_tile) << 8;
+          if (in_tile == 0) m[kMaxPages] = boxes == per_tile;
         }
         __syncwarp();  // the entries are written before lane 0 arrives
       }

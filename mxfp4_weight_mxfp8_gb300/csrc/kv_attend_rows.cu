@@ -3,33 +3,30 @@
 //
 // Here the 128 query rows of an item are the tensor core's 128-row operand and
 // a tile's 128 tokens the columns: S[row][token] = Q x K^T and O[row][dim] +=
-// P x V (V read transposed, as it lies in the page), so a row's weights need
-// no other row. Queries and weights are split into e4m3 hi + e5m2 lo, two
-// products into one accumulator: hi + lo hold the 8 significant bits of a BF16
-// query exactly down to 2^-16 of its row's largest magnitude, and a weight of
-// 2^-10 of its row's reference or more within 2^-8 of itself (BF16's own
-// rounding; below that within 2^-18 of the reference). Weights carry their
-// token's value scale, and the reference is a maximum of such products seen so
-// far: while none outgrows it, the output stays in TMEM, accumulated in FP32 by
-// the tensor core itself, and the scores are read once. Only when one does (and
-// on an item's first tile) the maxima are taken first and the output is rescaled.
+// P x V, so a row's weights need no other row. Scores are taken of the cache's
+// codes as they are, queries split into e4m3 hi + e5m2 lo, two products into one
+// accumulator: together they hold the 8 significant bits of a BF16 query exactly
+// down to 2^-16 of its row's largest magnitude. Weights must keep their precision
+// however small they are (kv_attend.cu says why), so they are two BF16 numbers,
+// hi + lo, 16 bits at every magnitude, and two products again. They go back into
+// TMEM, in the place of the scores that they come from, and are read from there:
+// shared memory has no room for them. For that the values are widened to BF16,
+// code times page scale, which is exact. A row's weights are held against a
+// reference that has room for 2^64 times its weight; what outgrows it raises it,
+// and the weights and outputs so far follow.
 //
 // Two groups take a CTA's tiles in turn, one in its softmax while the other's
 // products run; in a group two warpgroups share the rows, each with half of the
 // columns (two threads to a row). The groups' results are joined in shared memory.
 //
-// The softmax bounds it: two chunks of up to 700 tokens on 3300 to 6000 earlier
-// ones (64 query heads on 8 of 128, 162 GFLOP) take 279 us, 579 TFLOP/s, where
-// both products with their lo parts keep the tensor pipe busy for a quarter of
-// that. A tile costs a group some 4 thousand cycles of conversions,
-// exponentials and sums and 1.7 thousand of waiting for its own products, the
-// other group's tile half hidden behind it; the schedulers issue in half of the
-// cycles. Steps of 64 tokens with their scores in turn in two halves hide those
-// products and measured 335 us (twice the waits and barriers, and the query
-// image read twice as often); a tile's values before the next scores, 303.
+// Softmax and widening bound it: two chunks of up to 700 tokens on 3300 to 6000
+// earlier ones (64 query heads on 8 of 128, 162 GFLOP) take 350 us, 462 TFLOP/s;
+// the schedulers issue in 47 % of the cycles, the tensor pipe is busy for 31 %.
+// A group waits for its own products (the next scores cannot start before its
+// weights have been used), the other group's tile half hidden behind it.
 // Short items are bound by their starts and ends, some 20 thousand cycles
 // (queries 4, first scores and maxima 4, the groups' join and the output 6):
-// prompts of 1130 and 870 tokens without earlier ones take 149 us, 224 TFLOP/s.
+// prompts of 1130 and 870 tokens without earlier ones take 162 us, 206 TFLOP/s.
 #include "kv_attend.cuh"
 
 namespace moe {
@@ -56,24 +53,24 @@ struct RowsShape {
   static constexpr int kKeyStride = kTileBytes, kValuesAt = kStages * kTileBytes, kValueStride = kTileBytes;
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + 2 * kStages * kTileBytes;        // hi, lo
-  static constexpr int kP = kQ + 2 * kRows * D;                      // [group] hi, lo
-  static constexpr int kRowF = kP + kGroups * 2 * kRows * kTile;     // [row] factor
+  static constexpr int kWide = kQ + 2 * kRows * D;                   // [group] its tile's values in BF16
+  static constexpr int kWideBytes = kTile * D * 2;
+  static constexpr int kRowF = kWide + kGroups * kWideBytes;         // [row] factor
   static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
-  static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [group][row] references, then [group] the value scales'
-  static constexpr int kRowDst = kRefs + kGroups * kRows * 4 + 16;   // [row] its place among the outputs' rows
+  static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [group][row] references
+  static constexpr int kRowDst = kRefs + kGroups * kRows * 4;        // [row] its place among the outputs' rows
   static constexpr int kNan = kRowDst + kRows * 8;                  // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
   static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
-  static_assert(kGroups * 2 * kRows * kTile >= kRows * D * 4, "the groups' join fits the weights' room");
+  static_assert(kGroups * kWideBytes >= kRows * D * 4, "the groups' join fits the wide values' room");
+  static_assert(kWide % 1024 == 0, "operand images on swizzle boundaries");
 };
 // What starting and joining an item costs, in tiles (the chunks: 286 us with 4, 281 with 6, 282 with 8; the prompts: 147,
 // 151, 151; with a window of 1000 on 4000 tokens: 219, 219, 237).
 constexpr int kItemTiles = 6;
 constexpr int kLongUnits = 16;       // longer items may be cut anywhere (one head to a group, 900 tokens: 46 -> 34.6 us)
-constexpr int kUp = 4;               // weights are held times 2^4, so one may grow to 2^4.75 times its reference's before
-constexpr float kHighest = 430.0f;   // it leaves e4m3
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
 
@@ -97,7 +94,7 @@ __device__ __forceinline__ void tmem_wait_16(float (&r)[16]) {
                : "memory");
 }
 
-// Runs f(column, values) over kColumns columns from `taddr`, 16 at a time, the next ones on their way meanwhile.
+// Runs f(column, values, others) over kColumns columns from `taddr`, 16 at a time; the others are on their way meanwhile.
 template <int kColumns, class F>
 __device__ __forceinline__ void for_columns(uint32_t taddr, F&& f) {
   float u[16], v[16];
@@ -106,10 +103,10 @@ __device__ __forceinline__ void for_columns(uint32_t taddr, F&& f) {
   for (int c = 0; c < kColumns; c += 32) {
     tmem_wait_16(u);
     tmem_load_16_async(taddr + c + 16, v);
-    f(c, u);
+    f(c, u, v);
     tmem_wait_16(v);
     if (c + 32 < kColumns) tmem_load_16_async(taddr + c + 32, u);
-    f(c + 16, v);
+    f(c + 16, v, u);
   }
 }
 
@@ -139,6 +136,47 @@ __device__ __forceinline__ void tmem_store_16(uint32_t taddr, const float (&r)[1
       : "memory");
 }
 
+// The largest of 16 (NaN loses).
+__device__ __forceinline__ float highest(const float (&v)[16]) {
+  float big[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
+  return fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+}
+
+// This row's weights of `groups` 16 tokens (8 columns of hi pairs, 8 of lo pairs) times a power of two.
+__device__ __forceinline__ void scale_weights(uint32_t taddr, int groups, float factor) {
+  tmem_wait_stores();
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g) {
+    float w[16];
+    tmem_load_16_async(taddr + 16 * g, w);
+    tmem_wait_16(w);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t pair = __float_as_uint(w[j]);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(pair << 16) * factor, __uint_as_float(pair & 0xFFFF0000u) * factor);
+      w[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&v));
+    }
+    tmem_store_16(taddr + 16 * g, w);
+  }
+}
+
+// This thread's kColumns columns of an output times a factor.
+template <int kColumns>
+__device__ __forceinline__ void scale_output(uint32_t taddr, float factor) {
+#pragma unroll 1
+  for (int c = 0; c < kColumns; c += 16) {
+    float o[16];
+    tmem_load_16_async(taddr + c, o);
+    tmem_wait_16(o);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] *= factor;
+    tmem_store_16(taddr + c, o);
+  }
+  tmem_wait_stores();
+}
+
 // Where a CTA's run of units ends and the next one's starts: inside an item only if the item is long, else at its nearer
 // end (a piece costs an item's start and the join, some kItemTiles tiles).
 __device__ long long snap(const AttendArgs& a, const long long* prefix, int weight, int shift, long long x, long long total) {
@@ -163,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = v_full + X::kStages;
   uint64_t* s_full = v_empty + X::kStages;   // [group]: scores of its tile in TMEM
   uint64_t* o_full = s_full + kGroups;     // [group]: its tile's output in TMEM
-  uint64_t* p_ready = o_full + kGroups;    // [group]: its tile's weights in shared memory
+  uint64_t* p_ready = o_full + kGroups;    // [group]: its tile's weights in TMEM, its values widened
   uint64_t* drained = p_ready + kGroups;   // [group]: every product issued has completed
   uint64_t* q_ready = drained + kGroups;
   long long* prefix = reinterpret_cast<long long*>(sm + X::kPrefix);
@@ -182,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 1);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, kGroupThreads);
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(s_full + i, 1);
@@ -211,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_tmem;  // group g: scores at 256 g, output at 256 g + 128
+  const uint32_t tmem = s_tmem;  // group g: scores at 256 g, then weights in their place; output at 256 g + 128
 
   if (warp == kProducerWarp) {
     produce<X, D, 1>(a, maps, prefix, weight, shift, start, stop, sm, meta, k_full, k_empty, status);
@@ -219,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     produce<X, D, 2>(a, maps, prefix, weight, shift, start, stop, sm, meta, v_full, v_empty, status);
   } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
     constexpr uint32_t kMode = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
-    const uint32_t q_at = smem_addr(sm + X::kQ), p_at = smem_addr(sm + X::kP), ring = smem_addr(sm + X::kRing);
+    const uint32_t q_at = smem_addr(sm + X::kQ), wide = smem_addr(sm + X::kWide), ring = smem_addr(sm + X::kRing);
     const int w = warp - kIssueWarp;  // the warpgroup whose products this warp issues
     int k = 0, segments = 0, turn = 0;  // k: the CTA's first tile of the segment; turn: the group's own count
     bool alive = true;
@@ -250,24 +288,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool first = true; i < last && alive; i += 2, ++turn, first = false) {
         alive = __all_sync(kAll, wait(p_ready + w, turn & 1, status));
         if (!alive) break;
-        // The group's scores have been read: its next tile's go first.
-        if (i + 2 < last) scores(i + 2);
-        alive = alive && __all_sync(kAll, wait(v_full + i % X::kStages, (i / X::kStages) & 1, status));
-        if (!alive) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vals = ring + X::kValuesAt + (i % X::kStages) * X::kValueStride, p = p_at + w * 2 * kRows * kTile;
+          const uint32_t own = tmem + w * X::kGroupTmem, vals = wide + w * X::kWideBytes;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int st = 0; st < kTile / 16; ++st)
 #pragma unroll
-            for (int st = 0; st < kTile / 32; ++st)
-              mma_f8(tmem + w * X::kGroupTmem + 128, smem_desc(p + part * kRows * kTile + st * 32, 16, 1024, 2),
-                     smem_desc(vals + st * 32 * X::kSpan, 0, kGroup, kMode), idesc_f8(D, false, true, part == 1),
-                     !first || part + st > 0);
-          tc_commit(v_empty + i % X::kStages);
+            for (int part = 0; part < 2; ++part)
+              mma_bf16_tmem(own + 128, own + st * 16 + part * 8, smem_desc(vals + st * 2048, kTile * 128, 1024, 2),
+                            idesc_bf16(D, false, true), !first || st + part > 0);
           tc_commit(o_full + w);
         }
         __syncwarp();
+        // The next scores take the place of these weights, once those have been used.
+        if (i + 2 < last) {
+          alive = __all_sync(kAll, wait(o_full + w, turn & 1, status));
+          if (alive) scores(i + 2);
+        }
       }
       k = last;
       x += s.length;
@@ -281,17 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kProducerWarp) {
     const int group = tid / kGroupThreads, half = (tid / kCompute) & 1, row = tid & (kCompute - 1);
-    const int in_group = tid & (kGroupThreads - 1);
     const int pair = 4 + group * 4 + (warp & 3);  // the barrier of the two warps that share this row
     constexpr int kHalfTile = kTile / 2, kHalfD = D / 2;
     float* row_f = reinterpret_cast<float*>(sm + X::kRowF);
     float* tops = reinterpret_cast<float*>(sm + X::kTops);
     float* refs = reinterpret_cast<float*>(sm + X::kRefs);
-    int* ref_scale = reinterpret_cast<int*>(refs + kGroups * kRows);
     long long* row_dst = reinterpret_cast<long long*>(sm + X::kRowDst);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
-    float* join = reinterpret_cast<float*>(sm + X::kP);
-    uint8_t* weights = sm + X::kP + group * 2 * kRows * kTile;
+    float* join = reinterpret_cast<float*>(sm + X::kWide);
+    uint8_t* wide = sm + X::kWide + group * X::kWideBytes;
     const uint32_t lanes = tmem + group * X::kGroupTmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t s_at = lanes + half * kHalfTile, o_at = lanes + 128 + half * kHalfD;
     int k = 0, turn = 0;   // the CTA's tile; the group's own count
@@ -304,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Segment<kRows>& s = s_segment;
     const uint32_t inverse = inverse_of(a.group);
     for (;;) {
-      const int before = s.q.seq - s.q.n;
-      const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(s.q.n - s.token) * a.group - s.within));
+      const Sight sight(a, s, inverse);
+      const int rows = sight.rows;
       const int last = k + s.end - s.begin;
       if (s.begin < s.end) {
         // Queries: hi image, lo image, each row scaled by a power of two so that its largest magnitude lies in [128, 256).
@@ -345,160 +380,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int in_tile = per_group(s.within + row, inverse), tok = s.token + in_tile;
       if (tid < kRows)
         row_dst[row] = static_cast<long long>(s.q.first + tok) * a.q_heads + s.head * a.group + s.within + row - in_tile * a.group;
-      const int hi = row < rows ? before + tok : -1, lo = row < rows && a.window > 0 ? max(0, hi - a.window + 1) : 0;
-      // Tokens that any of the rows sees, and that all see.
-      const int all_hi = before + s.token, any_hi = all_hi + per_group(s.within + rows - 1, inverse);
-      const int any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0, all_lo = a.window > 0 ? max(0, any_hi - a.window + 1) : 0;
-      const bool mixed = any_lo != all_lo || any_hi != all_hi;
+      const int hi = row < rows ? sight.last(row) : -1, lo = row < rows ? sight.first(hi) : 0;
       const float factor = s.begin < s.end ? row_f[row] : 0.0f;
       float l = 0.0f, m = row < rows ? -INFINITY : 0.0f;  // m: the reference of the row's weights
-      int m_scale = 0;                                    // the reference of the value scales
       bool written = false;                               // the group's output in TMEM is this item's
       int at = k + ((k & 1) != group);
       for (; at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
-        if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);  // (for the entries; well before the scores)
+        if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);
+        if (written && !failed) failed = !wait(o_full + group, (turn - 1) & 1, status);  // the last tile's values have been used
         __syncwarp();
+        tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
-        const int most = static_cast<int>(mt[kMaxPages] & 0xFFu);
-        const bool edge = base < all_lo || base + kTile - 1 > all_hi || !(mt[kMaxPages] >> 8);
+        const bool edge = sight.edge(base) || mt[kMaxPages] == 0;
+        {
+          // The values' wide form, while the scores are on their way: thread `row` takes the tile's token of that number.
+          const uint8_t* codes = sm + X::kRing + X::kValuesAt + stage * X::kValueStride;
+          const Widener<D / 32> widener(sight, mt[row >> shift], edge, base + row, nans, &s_nans);
+#pragma unroll 2
+          for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c)
+            widener(*reinterpret_cast<const uint4*>(codes + chunk_at<X::kSpan>(row, c)), c, row, wide);
+          fence_proxy_async_shared();
+        }
         // The row's visible tokens among this thread's 16 from column c on, as bits.
         auto visible = [&](int c, uint32_t entry) {
           const int from = min(max(lo - base_half - c, 0), 16), to = entry >> 16 ? min(max(hi - base_half - c, -1), 15) : -1;
           return 0xFFFFu >> (15 - to) & 0xFFFFu << from;
         };
         // Some row's first token may come with any of the group's tiles. (Both warps of the pair hold the same rows.)
-        bool find = !written || most > m_scale || __any_sync(kAll, m == -INFINITY && hi >= base && lo < base + kTile);
+        const bool find = !written || __any_sync(kAll, m == -INFINITY && hi >= base && lo < base + kTile);
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
         __syncwarp();
         tc_fence_after_sync();
-        for (int tries = 0;; ++tries) {
-          if (find) {
-            // The references are raised: the largest value scale, and the row's largest score with its token's value scale
-            // (less the largest), over both halves; what is there already follows.
-            const int scale = max(m_scale, most), rise = min(scale - m_scale, kFar);
-            float top = -INFINITY;
-            for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
-              const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
-              if (edge) {
-                const uint32_t seen = visible(c, entry);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (!(seen & 1u << j)) v[j] = -INFINITY;
-              }
-              float big[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) big[j] = fmaxf(fmaxf(v[4 * j], v[4 * j + 1]), fmaxf(v[4 * j + 2], v[4 * j + 3]));
-              const float most_here = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-              const float drop = static_cast<float>(max(static_cast<int>((entry >> 8) & 0xFFu) - scale, -kFar));
-              if (most_here > -INFINITY) top = fmaxf(top, fmaf(most_here, factor * scale_of(entry & 0xFFu), drop));
-            });
-            float* mine = tops + (group * 2 + half) * kRows + row;
-            *mine = top;
-            sync_any<64>(pair, false);
-            top = fmaxf(m - static_cast<float>(rise), fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
-            const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
-            l *= keep;
-            if (written) {
-              if (!failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
-              __syncwarp();
-              tc_fence_after_sync();
-              const float f = m > -INFINITY ? exp2_fast(m - top + static_cast<float>(m_scale - scale)) : 0.0f;
-#pragma unroll 1
-              for (int c = 0; c < kHalfD; c += 16) {
-                float o[16];
-                tmem_load_16_async(o_at + c, o);
-                tmem_wait_16(o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] *= f;
-                tmem_store_16(o_at + c, o);
-              }
-              tmem_wait_stores();
-            }
-            m = top;
-            m_scale = scale;
-          }
-          // The last tile's weights have been used: these take their place.
-          if (written && !failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
-          const float ref = m > -INFINITY ? m : 0.0f;
-          float part = 0.0f, high = 0.0f;
-          for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16]) {
+        if (find) {
+          // The reference is raised to the row's largest score, over both halves; what is there already follows.
+          float top = -INFINITY;
+          for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16], float (&)[16]) {
             const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
-            const float f = factor * scale_of(entry & 0xFFu);
-            // Times 2^kUp and the page's value scale over its reference, both in the exponent.
-            const int up = kUp + max(static_cast<int>((entry >> 8) & 0xFFu) - m_scale, -kFar);
-            const float off = static_cast<float>(up) - ref;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = exp2_fast(fmaf(v[j], f, off));
             if (edge) {
               const uint32_t seen = visible(c, entry);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (!(seen & 1u << j)) v[j] = 0.0f;
+                if (!(seen & 1u << j)) v[j] = -INFINITY;
             }
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t his[4], los[4];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              sum[j / 2] = (v[2 * j] + v[2 * j + 1]) + (v[2 * j + 2] + v[2 * j + 3]);
-              high = fmaxf(high, fmaxf(fmaxf(v[2 * j], v[2 * j + 1]), fmaxf(v[2 * j + 2], v[2 * j + 3])));
-              uint32_t h0, l0, h1, l1;
-              split2_wide_half(v[2 * j], v[2 * j + 1], h0, l0);
-              split2_wide_half(v[2 * j + 2], v[2 * j + 3], h1, l1);
-              his[j / 2] = h0 | h1 << 16;
-              los[j / 2] = l0 | l1 << 16;
-            }
-            part = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __uint_as_float(static_cast<uint32_t>(127 - up) << 23), part);
-            uint8_t* dst = weights + chunk_at<128>(row, (half * kHalfTile + c) / 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(his[0], his[1], his[2], his[3]);
-            *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(los[0], los[1], los[2], los[3]);
+            const float most = highest(v);
+            if (most > -INFINITY) top = fmaxf(top, most * (factor * scale_of(entry & 0xFFu)));
           });
-          find = sync_any<64>(pair, high > kHighest);
-          if (!find || tries == 1) {
-            l += part;
-            break;
-          }
+          tops[(group * 2 + half) * kRows + row] = top;
+          sync_any<64>(pair, false);
+          top = fmaxf(m, fmaxf(top, tops[(group * 2 + (half ^ 1)) * kRows + row]));
+          const float keep = m > -INFINITY ? exp2_fast(m - top) : 0.0f;
+          l *= keep;
+          if (written) scale_output<kHalfD>(o_at, keep);
+          m = top;
         }
+        const float ref = m > -INFINITY ? m : 0.0f;
+        float part = 0.0f, raised = 0.0f;
+        for_columns<kHalfTile>(s_at, [&](int c, float (&v)[16], float (&others)[16]) {
+          const uint32_t entry = mt[(half * kHalfTile + c) >> shift];
+          const float f = factor * scale_of(entry & 0xFFu), off = -(ref + raised);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = fmaf(v[j], f, off);
+          if (edge) {
+            const uint32_t seen = visible(c, entry);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (!(seen & 1u << j)) v[j] = -INFINITY;
+          }
+          const float high = highest(v);
+          if (__any_sync(kAll, high > kHighest)) {
+            // A weight outgrows the reference, which is raised; the tile's weights so far, which lie over their scores, follow.
+            tmem_wait_16(others);
+            const float up = high > kHighest ? high : 0.0f, keep = exp2_fast(-up);
+            scale_weights(s_at, c / 16, keep);
+            part *= keep;
+            raised += up;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] -= up;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = exp2_fast(v[j]);
+          float sum[4], out[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[j] = (v[4 * j] + v[4 * j + 1]) + (v[4 * j + 2] + v[4 * j + 3]);
+          part += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t hi_pair, lo_pair;
+            split2_bf16(v[2 * j], v[2 * j + 1], hi_pair, lo_pair);
+            out[j] = __uint_as_float(hi_pair);
+            out[8 + j] = __uint_as_float(lo_pair);
+          }
+          tmem_store_16(s_at + c, out);
+        });
+        if (sync_any<64>(pair, raised > 0.0f)) {
+          // Both halves of a row go to the larger of their references.
+          tops[(group * 2 + half) * kRows + row] = raised;
+          sync_any<64>(pair, false);
+          const float to = fmaxf(raised, tops[(group * 2 + (half ^ 1)) * kRows + row]);
+          const float own = exp2_fast(raised - to), keep = exp2_fast(-to);
+          scale_weights(s_at, kHalfTile / 16, own);
+          part *= own;
+          l *= keep;
+          if (written) scale_output<kHalfD>(o_at, keep);
+          m += to;
+        }
+        l += part;
         written = true;
-        if (edge) {
-          // Values that no row sees are dropped, whatever they hold. A NaN that only some rows see is
-          // taken out too, and noted for those. (Thread `row` here takes the tile's token of that number.)
-          uint8_t* value = sm + X::kRing + X::kValuesAt + stage * X::kValueStride + row * X::kSpan;
-          const int token = base + row;
-          const bool seen = token >= any_lo && token <= any_hi && (mt[row >> shift] >> 16);
-          if (!seen || (mixed && any_nan<D / 32, 2>(reinterpret_cast<const uint4*>(value) + half))) {
-#pragma unroll 1
-            for (int c = half; c < D / 16; c += 2) {
-              uint4* cell = reinterpret_cast<uint4*>(value + c * 16);
-              if (!seen) {
-                *cell = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 w = *cell;
-              uint32_t words[4] = {w.x, w.y, w.z, w.w};
-              if (!(nan_code(w.x) | nan_code(w.y) | nan_code(w.z) | nan_code(w.w))) continue;
-              // Stored chunk c of the token's row holds the dimensions of chunk c ^ (the row's swizzle).
-              const int chunk = X::kSpan == 128 ? (c ^ row) & 7 : c ^ ((row >> 1) & 3);
-#pragma unroll 1
-              for (int b = 0; b < 16; ++b) {
-                if (((words[b >> 2] >> (8 * (b & 3))) & 0x7Fu) != 0x7Fu) continue;
-                words[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
-                const int dim = chunk * 16 + b;
-                s_nans = 1;
-                for (int i = 0; i < rows; ++i) {
-                  const int last_seen = all_hi + per_group(s.within + i, inverse);
-                  if (token <= last_seen && (a.window == 0 || token > last_seen - a.window))
-                    atomicOr(nans + i * (D / 32) + dim / 32, 1u << (dim % 32));
-                }
-              }
-              *cell = make_uint4(words[0], words[1], words[2], words[3]);
-            }
-          }
-        }
-        fence_proxy_async_shared();
+        tmem_wait_stores();
         tc_fence_before_sync();
         mbar_arrive(p_ready + group);
+        mbar_arrive(v_empty + stage);  // (with the pages' entries, which the scores needed)
       }
       // The group's output, this thread's half of the row.
       float acc[kHalfD];
@@ -528,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int column = half * kHalfD + group * kOwn;
       tops[(group * 2 + half) * kRows + row] = l;
       if (half == 0) refs[group * kRows + row] = m;
-      if (in_group == 0) ref_scale[group] = m_scale;
       auto cell = [&](int c) { return reinterpret_cast<float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2)); };
       float own[kOwn];
       if (group == 0) {
@@ -550,8 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f0 = exp2_fast(m0 - safe), f1 = exp2_fast(m1 - safe);
         l = l0 * f0 + l1 * f1;
         m = mn;
-        const float g0 = f0 * scale_of(ref_scale[0]) * (1.0f / (1 << kUp)), g1 = f1 * scale_of(ref_scale[1]) * (1.0f / (1 << kUp));
-        const float mine = group == 0 ? g0 : g1, other = group == 0 ? g1 : g0;
+        const float mine = group == 0 ? f0 : f1, other = group == 0 ? f1 : f0;
 #pragma unroll
         for (int c = 0; c < kOwn / 4; ++c) {
           const float4 v = *cell(group * (kOwn / 4) + c);

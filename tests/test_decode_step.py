@@ -752,9 +752,9 @@ def test_attend_nan_in_the_cache_reaches_only_the_rows_that_see_it(moe, dim, win
     assert not np.isnan(out[~sees]).any() and not np.isnan(lse[~sees]).any()
 
 
-# Query rows of a request, query heads on one cache head: a row tile of 8, 16, 24 and 32 rows
+# Query rows of a request, query heads on one cache head: a row tile of 8, 16, 24 and 32 rows, then the 128-row form
 # (with heads of 256, of 16 rows in all but the first).
-TILES = [(2, 4), (2, 8), (3, 8), (4, 8)]
+TILES = [(2, 4), (2, 8), (3, 8), (4, 8), (16, 8)]
 
 
 def request_reference(cache, q, table, n, scale):
@@ -786,8 +786,8 @@ def request_reference(cache, q, table, n, scale):
 def test_attend_small_weights_under_a_dominant_token_without_value(moe, n, gap, deviation, dim, rows, q_heads):
     """A first token takes most of every row's weight and has value 0: the output is the others' alone, whose weights lie
     `gap` nats below. They count with their own precision, not with the dominant weight's: check_attend's bounds."""
-    if n > 10000 and (dim == 256 or rows * q_heads != 8):
-        pytest.skip("the longest contexts in the narrowest tile")
+    if n > 10000 and (dim == 256 or rows * q_heads not in (8, 128)):
+        pytest.skip("the longest contexts in the narrowest tile and in the 128-row form")
     rng = np.random.default_rng(n + gap)
     page = 64
     pages = -(-n // page)
@@ -811,6 +811,42 @@ def test_attend_small_weights_under_a_dominant_token_without_value(moe, n, gap, 
     assert (np.abs(lse - want_lse) <= 1.6e-4).all()
     assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
     assert np.linalg.norm(out - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES + [(150, 8)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("profile", ["rising", "falling", "mixed", "spikes"])
+def test_attend_scores_hundreds_of_nats_apart(moe, profile, dim, rows, q_heads):
+    """Weights that outgrow their reference by far more than FP32's range, from tile to tile and inside one.
+
+    Scores of up to 600: FP32's error of 4 * 600 u in each is 1.5e-4 of its weight, and 64 * 600 u bounds the log-sum-exp's."""
+    rng = np.random.default_rng(dim + rows)
+    n, page = 900, 32
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    k, _, ks, _ = cache
+    level = np.linspace(0, 448, n)
+    if profile == "falling":
+        level = level[::-1]
+    elif profile == "mixed":
+        level = rng.permutation(level)
+    elif profile == "spikes":  # in one half of a tile, then in the other; the last one before the end
+        level = np.zeros(n)
+        level[[130, 215, 300, 470, 530, 700]] = [100, 150, 150, 260, 200, 448]
+    for t in range(n):
+        k[table[0, t // page], 0, t % page] = e4m3_encode(rng.standard_normal(dim))
+        k[table[0, t // page], 0, t % page, 0] = e4m3_encode(level[t:t + 1])[0]
+    ks[:] = 127
+    q = rng.standard_normal((rows, q_heads, dim))
+    q[..., 0] = 16
+    q = bf16(q)
+    scale = 600 / (16 * 448)
+    for sign in (1, -1):
+        out, lse = run_attend(moe, cache, q.cuda() * sign, table, start, seq, scale=scale * sign)
+        want, want_lse, mass = request_reference(cache, q.float().numpy(), table, n, scale)
+        assert (np.abs(lse - want_lse) <= 64 * 600 * U).all()
+        assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
+        assert np.linalg.norm(out - want) <= 2.0 ** -8 * np.linalg.norm(want)
 
 
 @pytest.mark.gpu
