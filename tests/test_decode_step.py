@@ -850,6 +850,55 @@ def test_attend_scores_hundreds_of_nats_apart(moe, profile, dim, rows, q_heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES + [(150, 8)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("byte", [255, 254, 0])
+def test_attend_scales_of_pages_that_no_query_sees(moe, byte, dim, rows, q_heads):
+    """Pages of the table before a window (and so in its first tile) and after the last token, whatever their scales and codes."""
+    rng = np.random.default_rng(rows * dim)
+    page, window = 16, 150
+    lengths = [(n + rows, rows) for n in (300, 410, 523)]
+    cache, table, start, seq = make_batch(rng, lengths, page, 2, dim)
+    k, v, ks, vs = cache
+    nobodys = np.setdiff1d(np.arange(len(k)), table)[0]
+    for r, n in enumerate(seq):
+        first = max(0, n - rows - window + 1)  # the first query row's
+        for j in range(table.shape[1]):
+            if j < first // page or j * page >= n:
+                if table[r, j] < 0:
+                    table[r, j] = nobodys  # the table's later entries
+                ks[table[r, j]] = vs[table[r, j]] = byte
+                v[table[r, j]] = rng.integers(0, 256, v[0].shape)
+    q = bf16(rng.standard_normal((3 * rows, 2 * q_heads, dim)))
+    check_attend(moe, cache, q, table, start, seq, window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES + [(150, 8)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("large,others", [(230, None), (160, 40)])
+def test_attend_value_scales_far_apart(moe, large, others, dim, rows, q_heads):
+    """A page of huge values that every query sees and gives no weight to, more than 2^100 above the others."""
+    rng = np.random.default_rng(rows + dim)
+    n, page = 300 + rows, 16
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    k, _, ks, vs = cache
+    if others is not None:
+        vs[:] = others
+    k[table[0, : -(-n // page)], 0, :, 0] = 0
+    far = table[0, 3]
+    k[far], ks[far], vs[far] = 0, 127, large
+    k[far, 0, :, 0] = e4m3_encode(np.array([-400.0]))[0]
+    q = rng.standard_normal((rows, q_heads, dim))
+    q[..., 0] = 16
+    q = bf16(q)
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq)
+    want, want_lse, mass = request_reference(cache, q.float().numpy(), table, n, dim ** -0.5)
+    assert (np.abs(lse - want_lse) <= 1.6e-4).all()
+    assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (5, 24, 64), (200, 8, 128), (64, 16, 64), (9, 16, 256)])
 def test_attend_gives_the_same_bits_each_time(moe, rows, q_heads, dim):
     """Work split over many CTAs and joined by whichever comes last: the order of the sums does not depend on it."""
