@@ -479,8 +479,10 @@ typedef struct moe_kv_cache_t {
  *                8 free pages exhausted (4 and 8: the tokens concerned get
  *                slot -1, and the entries -1 where the row has them)
  * Rows of positions and slots past the last new token get 0 and -1.
- * requests <= MOE_KV_MAX_REQUESTS. The same inputs give the same outputs:
- * nothing but block_table is both read and written, and no entry both.
+ * seq_lens may be context_lens itself: lengths stepped in place. No other
+ * output may overlap an input (MOE_ERR_ARG). requests <=
+ * MOE_KV_MAX_REQUESTS. The same inputs give the same outputs: no entry of
+ * block_table is both read and written.
  */
 typedef struct moe_kv_plan_t {
   const int32_t* context_lens;

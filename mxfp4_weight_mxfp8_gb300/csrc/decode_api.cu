@@ -7,6 +7,11 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 int launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return MOE_OK;
   return moe::fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -78,6 +83,14 @@ int moe_kv_plan(const moe_kv_plan_t* p, void* stream) {
     return refuse("misaligned pointer");
   if (p->free_head >= p->counts && p->free_head < p->counts + 4)
     return refuse("free_head must not lie in this call's counts");
+  // Every CTA reads the inputs for itself, some when others have written: only lengths stepped in place are provided for.
+  const int64_t per = 4ll * p->requests;
+  const struct { const void* at; int64_t bytes; } in[] = {{p->context_lens, per}, {p->query_lens, per}, {p->free_pages, 4ll * p->free_count}, {p->free_head, 4}},
+      out[] = {{p->query_start, per + 4}, {p->seq_lens, per}, {p->positions, 4ll * p->tokens}, {p->slots, 8ll * p->tokens}, {p->counts, 16}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (overlap(o.at, o.bytes, i.at, i.bytes) && !(o.at == p->seq_lens && i.at == p->context_lens && p->seq_lens == p->context_lens))
+        return refuse("an output overlaps an input (only seq_lens may be context_lens)");
   return launched(moe::launch_kv_plan(*p, static_cast<cudaStream_t>(stream)), "moe_kv_plan");
 }
 

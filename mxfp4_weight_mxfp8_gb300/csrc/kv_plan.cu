@@ -18,8 +18,25 @@ namespace {
 // A thread to a request: kPlanThreads at least as many as the requests.
 static_assert(MOE_KV_MAX_REQUESTS <= 1024, "a CTA has a thread for every request");
 
+// A request's cached and new tokens; both 0 where they are no lengths.
+__device__ __forceinline__ bool lengths(const moe_kv_plan_t& a, int r, int& c, int& q) {
+  c = a.context_lens[r];
+  q = a.query_lens[r];
+  const bool ok = c >= 0 && q >= 0 && static_cast<long long>(c) + q <= 0x7FFFFFFF - a.page_tokens;
+  if (!ok) c = q = 0;
+  return ok;
+}
+
+// seq_lens over context_lens: every CTA of the plan has read those by now.
+__global__ void __launch_bounds__(1024) kv_lengths_kernel(const moe_kv_plan_t a) {
+  int c, q;
+  if (threadIdx.x >= a.requests) return;
+  lengths(a, threadIdx.x, c, q);
+  a.seq_lens[threadIdx.x] = c + q;
+}
+
 template <int kPlanThreads>
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan_t a, int shift) {
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan_t a, int shift, bool store_lengths) {
   constexpr int kWarps = kPlanThreads / 32;
   __shared__ long long s_start[kPlanThreads + 1];  // new tokens before request r
   __shared__ long long s_pages[kPlanThreads];      // new pages before request r
@@ -32,16 +49,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const moe_kv_plan
   int flags = 0, longest = 0;
   const long long head = *a.free_head;
   if (tid < a.requests) {
-    int c = a.context_lens[tid], q = a.query_lens[tid];
-    if (c < 0 || q < 0 || static_cast<long long>(c) + q > 0x7FFFFFFF - P) {
-      flags |= 1;
-      c = q = 0;
-    }
+    int c, q;
+    if (!lengths(a, tid, c, q)) flags |= 1;
     s_context[tid] = c;
     longest = c + q;
     const int held = (c + P - 1) >> shift, needed = (c + q + P - 1) >> shift;
     if (needed > a.table_width) flags |= 4;
-    if (blockIdx.x == 0) a.seq_lens[tid] = c + q;
+    if (store_lengths && blockIdx.x == 0) a.seq_lens[tid] = c + q;
     tsum = q;
     psum = needed - held;
   }
@@ -137,8 +151,11 @@ cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream) {
   const int threads = a.requests <= 256 ? 256 : 1024;
   int grid = (a.tokens + threads - 1) / threads;
   grid = grid < 1 ? 1 : (grid > 152 ? 152 : grid);
-  if (threads == 256) kv_plan_kernel<256><<<grid, 256, 0, stream>>>(a, shift);
-  else kv_plan_kernel<1024><<<grid, 1024, 0, stream>>>(a, shift);
+  // Lengths stepped in place are written by a launch of their own, unless one CTA does all (each thread its own request's).
+  const bool later = a.seq_lens == a.context_lens && grid > 1;
+  if (threads == 256) kv_plan_kernel<256><<<grid, 256, 0, stream>>>(a, shift, !later);
+  else kv_plan_kernel<1024><<<grid, 1024, 0, stream>>>(a, shift, !later);
+  if (later) kv_lengths_kernel<<<1, 1024, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

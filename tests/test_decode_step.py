@@ -205,6 +205,19 @@ def test_plan_refusals(moe):
         assert raw.moe_kv_plan(moe._KvPlan(**{**good, **change}), None) == moe.MOE_ERR_ARG, change
 
 
+def test_plan_refuses_outputs_over_inputs(moe):
+    names = ("context_lens", "query_lens", "free_pages", "free_head", "block_table", "query_start", "seq_lens", "positions",
+             "slots", "counts")
+    good = {n: P * (i + 1) for i, n in enumerate(names)}
+    good.update(table_stride=4, requests=2, page_tokens=16, table_width=4, free_count=3, tokens=5)
+    raw = moe.library()
+    for change in (dict(seq_lens=good["query_lens"]), dict(seq_lens=good["context_lens"] + 4), dict(query_start=good["context_lens"]),
+                   dict(positions=good["free_pages"] + 8), dict(slots=good["query_lens"]), dict(counts=good["free_pages"]),
+                   dict(query_start=good["query_lens"] - 8), dict(positions=good["free_head"] - 16), dict(free_head=good["seq_lens"])):
+        assert raw.moe_kv_plan(moe._KvPlan(**{**good, **change}), None) == moe.MOE_ERR_ARG, change
+        assert "overlaps an input" in moe.moe_last_error_detail(), change
+
+
 CACHE = dict(k=P, v=P, k_scale=P, v_scale=P, pages=4, page_tokens=64, kv_heads=2, head_dim=128)
 BAD_CACHES = (dict(k=None), dict(v_scale=None), dict(k=P + 8), dict(pages=0), dict(kv_heads=0), dict(page_tokens=48),
               dict(head_dim=96), dict(head_dim=512))
@@ -466,6 +479,36 @@ def test_plan_reports_what_does_not_fit(moe):
     t, out = run_plan(moe, [5, 0], [0, 0], 64, table[:2], [3], 0, 2)
     assert out["counts"].tolist() == [0, 0, 5, 0] and out["slots"].tolist() == [-1, -1]
     assert np.array_equal(t, table[:2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("requests,most", [(1, 1), (60, 4), (3, 4000), (300, 1), (900, 150)])
+def test_plan_steps_lengths_in_place(moe, requests, most):
+    """One tensor as context_lens and seq_lens, with one CTA and with many, which all read what one of them replaces."""
+    rng = np.random.default_rng(requests)
+    page = 16
+    context, query = rng.integers(0, 500, requests), rng.integers(0, most + 1, requests)
+    held, need = -(-context // page), -(-(context + query) // page)
+    table = np.full((requests, int(need.max()) + 1), -1, np.int32)
+    at = 0
+    for r in range(requests):
+        table[r, :held[r]] = np.arange(at, at + held[r])
+        at += held[r]
+    free, capacity = np.arange(at, int(need.sum()) + at, dtype=np.int32), int(query.sum()) + 5
+    want_t, start, positions, slots, head = plan_reference(context, query, page, table, free, 0, capacity)
+    want_t, start, positions, slots = (torch.from_numpy(a).cuda() for a in (want_t, start, positions, slots))
+
+    def dev(a, dt=torch.int32):
+        return torch.tensor(np.asarray(a), dtype=dt, device="cuda")
+
+    for _ in range(20):
+        lens, t = dev(context), dev(table)
+        out = dict(query_start=dev(np.zeros(requests + 1)), positions=dev(np.full(capacity, 99)),
+                   slots=dev(np.full(capacity, 99), torch.int64), counts=dev(np.zeros(4)))
+        moe.moe_kv_plan(lens, dev(query), page, t, dev(free), dev([0]), seq_lens=lens, **out)
+        assert torch.equal(lens, dev(context + query)) and torch.equal(t, want_t)
+        assert torch.equal(out["query_start"], start) and torch.equal(out["positions"], positions) and torch.equal(out["slots"], slots)
+        assert out["counts"].tolist() == [int(query.sum()), head, int((context + query).max()), 0]
 
 
 # ------------------------------------------------------------------- append
