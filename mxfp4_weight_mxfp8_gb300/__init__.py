@@ -480,6 +480,8 @@ def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, 
     shape = (tokens, heads, dim)
     batch = _BATCH.pack(table, table_stride, _dense(call, "query_start", query_start, _i32t, (requests + 1,), device),
                         _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device), width, requests, tokens)
+    if not 0 <= window < 1 << 31:  # (ctypes would take it modulo 2^32)
+        _refuse(call, "window must be 0 or a number of tokens below 2^31")
     room = workspace.shape
     if len(room) != 1 or room[0] < MOE_KV_WORKSPACE_BYTES:
         _refuse(call, f"workspace must be {MOE_KV_WORKSPACE_BYTES} bytes of uint8")

@@ -345,7 +345,9 @@ struct Sight {
   }
   // The last token that row i sees, and the first that a row with this last one sees.
   __device__ __forceinline__ int last(int i) const { return all_hi + per_group(within + i, inverse); }
-  __device__ __forceinline__ int first(int last) const { return window > 0 ? max(0, last - window + 1) : 0; }
+  __device__ __forceinline__ int first(int last) const {  // (in 64 bits: the window may be any, `last` below 0)
+    return window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(last) - window + 1)) : 0;
+  }
   // Some row does not see some token of the tile from `base` on.
   __device__ __forceinline__ bool edge(int base) const { return base < all_lo || base + kTile - 1 > all_hi; }
   __device__ __forceinline__ bool any(int token) const { return token >= any_lo && token <= any_hi; }

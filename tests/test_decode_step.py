@@ -709,6 +709,22 @@ def test_attend_rows_that_see_nothing_and_bad_table_entries(moe):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", [(8, 1), (8, 2), (8, 3), (8, 4), (16, 8)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 6])
+def test_attend_windows_without_an_end(moe, window, rows, q_heads):
+    """The largest windows, with query rows that stand before the sequence."""
+    rng = np.random.default_rng(rows)
+    cache, table, start, seq = make_batch(rng, [(150, rows), (70, rows)], 16, 1, 64)
+    seq[1] = 3  # five or more rows before it
+    q = bf16(rng.standard_normal((2 * rows, q_heads, 64)))
+    check_attend(moe, cache, q, table, start, seq, window=window)
+    for bad in (-1, 2 ** 31, 2 ** 32):
+        with pytest.raises(moe.MoeError) as e:
+            run_attend(moe, cache, q.cuda(), table, start, seq, window=bad)
+        assert e.value.code == moe.MOE_ERR_ARG
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("page,dim", [(16, 64), (64, 128), (128, 256)])
 def test_attend_uneven_scores_and_scales(moe, page, dim):
     """A dominant first token over many small weights, page scales far apart, a page of zeros, large scores."""
