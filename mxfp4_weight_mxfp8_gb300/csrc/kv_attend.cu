@@ -522,9 +522,12 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
       // The output: this thread's dimension of each row.
       float acc[X::kHalves][X::kRows];
       if (s.begin < s.end && !failed) {
-        failed |= !wait(o_full, (k - 1) & 1, status);
+        failed = !wait(o_full, (k - 1) & 1, status);
         if (X::kWideners) failed |= !wait(v_ready + ((k - 1) & 1), ((k - 1) >> 1) & 1, status);  // (for what they noted)
-        __syncwarp();
+      }
+      failed = compute_any(failed);  // agreed on before whole warps read TMEM: a wait may run out for some lanes only
+      if (failed) break;
+      if (s.begin < s.end) {
         tc_fence_after_sync();
 #pragma unroll
         for (int h = 0; h < X::kHalves; ++h)
@@ -547,8 +550,6 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
       }
 
       // The segment's sums over the tokens, and its rows.
-      failed = compute_any(failed);
-      if (failed) break;
       row_sums<X::kRows>(l, red, lane, warp);
       compute_sync();
       float sum = 0.0f;  // of row `lane`

@@ -992,6 +992,28 @@ def test_attend_reports_a_wait_that_runs_out(moe, rows, q_heads, dim):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cta", [1, 5])
+def test_attend_waits_that_run_out_in_every_form(moe, cta, dim, rows, q_heads):
+    """As above, in each row tile, at two CTAs in the middle of an item, with a wait of a millisecond. (The first CTA of many
+    may have nothing but an item's start, and no tile to withhold.)"""
+    rng = np.random.default_rng(rows)
+    cache, table, start, seq = make_batch(rng, [(3000, rows), (40, rows)], 64, 2, dim)
+    q = bf16(rng.standard_normal((2 * rows, 2 * q_heads, dim))).cuda()
+    workspace = torch.zeros(moe.MOE_KV_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    want = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+    for _ in range(3):
+        moe.moe_kv_set_timeout(workspace, 1_000_000)
+        moe.moe_kv_debug_withhold(workspace, cta)
+        run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+        assert moe.moe_kv_sync_status(workspace) == moe.MOE_ERR_DEVICE_TIMEOUT
+        got = run_attend(moe, cache, q, table, start, seq, workspace=workspace)
+        assert moe.moe_kv_sync_status(workspace) == moe.MOE_OK
+        assert np.array_equal(want[0], got[0]) and np.array_equal(want[1], got[1])
+
+
+@pytest.mark.gpu
 def test_attend_query_rows_with_nan_or_infinity(moe):
     rng = np.random.default_rng(2)
     cache, table, start, seq = make_batch(rng, [(90, 2)], 64, 2, 128)
