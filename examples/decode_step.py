@@ -106,7 +106,7 @@ def main(argv=None):
         x = y[step.query_start[1:].long() - 1]  # each request's last row goes on
         y = layer(x, step.plan(ones, a.requests))
         print(f"step {i}: lengths {step.seq_lens.tolist()}, pages taken {step.head.item()}, |y| {y.float().norm():.4f}")
-    if (moe.moe_sync_status(layer.experts.handle) != moe.MOE_OK or moe.moe_kv_sync_status(layer.cache.workspace) != moe.MOE_OK
+    if (moe.moe_sync_status(layer.experts.handle) != moe.MOE_OK or layer.cache.status() != moe.MOE_OK
             or step.counts[3].item() != 0):
         raise SystemExit("the device reported an error")
     layer.experts.close()

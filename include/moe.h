@@ -560,8 +560,9 @@ int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, cons
  * moe_kv_sync_status - synchronize `stream` and return (and clear) the status
  * word that moe_kv_attend's kernels write into the workspace: MOE_OK, or
  * MOE_ERR_DEVICE_TIMEOUT (a bounded wait for a copy ran out; the kernel still
- * finished, its outputs are not to be used). MOE_ERR_CUDA if the
- * synchronization itself fails.
+ * finished). Until then the calls after it on this workspace do nothing, so
+ * after an error the outputs of every call since the last MOE_OK are not to be
+ * used. MOE_ERR_CUDA if the synchronization itself fails.
  */
 int moe_kv_sync_status(void* workspace, void* stream);
 

@@ -511,7 +511,9 @@ class KvCache:
     block_table, query_start, seq_lens)`` returns the BF16 [T, q_heads,
     head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``), both
     on the current torch stream. Layers that run one after the other on one
-    stream can share a workspace.
+    stream can share a workspace. ``status()`` synchronizes and returns the
+    device status of the attend calls since it was last read: anything but
+    MOE_OK and none of their outputs is to be used.
     """
 
     def __init__(self, pages: int, kv_heads: int, page_tokens: int = 64, head_dim: int = 128, device="cuda",
@@ -544,6 +546,9 @@ class KvCache:
         moe_kv_attend(self.tensors, q, block_table, query_start, seq_lens, out, self.workspace, lse, scale, window,
                       stream)
         return (out, lse) if return_lse else out
+
+    def status(self, stream=None) -> int:
+        return moe_kv_sync_status(self.workspace, stream)
 
 
 class MoeLayer:

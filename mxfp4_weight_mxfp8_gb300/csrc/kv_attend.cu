@@ -200,10 +200,12 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   __shared__ int s_nans;         // the item has outputs noted in `nans`
   __shared__ Segment<X::kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
+  __shared__ int32_t s_status;   // the workspace's when the CTA started
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
   if (tid == 0) {
+    s_status = *static_cast<const volatile int32_t*>(status);
     for (int i = 0; i < X::kStages; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -221,7 +223,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   const int weight = sum_work<X::kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  if (blockIdx.x >= ctas) return;
+  // (An error that nobody has read yet: its call has left the arrival counters anyhow.)
+  if (blockIdx.x >= ctas || s_status != MOE_OK) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, X::kTmem);

@@ -211,11 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_nans;         // the item has outputs noted in `nans`
   __shared__ Segment<kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
+  __shared__ int32_t s_status;   // the workspace's when the CTA started
   __shared__ long long s_run[2];  // the CTA's units
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
   if (tid == 0) {
+    s_status = *static_cast<const volatile int32_t*>(status);
     for (int i = 0; i < X::kStages; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
@@ -234,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int weight = sum_work<kThreads, kRows, kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  if (blockIdx.x >= ctas) return;
+  // (An error that nobody has read yet: its call has left the arrival counters anyhow.)
+  if (blockIdx.x >= ctas || s_status != MOE_OK) return;
   if (tid == 0 || tid == 32) {
     const int i = tid == 0 ? 0 : 1;
     s_run[i] = snap(a, prefix, weight, shift, total * (blockIdx.x + i) / ctas, total);

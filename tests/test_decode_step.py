@@ -1014,6 +1014,33 @@ def test_attend_waits_that_run_out_in_every_form(moe, cta, dim, rows, q_heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (9, 16, 256), (64, 8, 64)])
+def test_attend_does_nothing_after_an_error_until_it_is_read(moe, rows, q_heads, dim):
+    """The call that failed leaves the items' arrival counters partly counted: no later call may join by them."""
+    rng = np.random.default_rng(rows)
+    cache, table, start, seq = make_batch(rng, [(3000, rows)], 64, 1, dim)
+    q = bf16(rng.standard_normal((rows, q_heads, dim))).cuda()
+    c = moe.KvCache(len(cache[0]), 1, 64, dim)
+    for t, a in zip(c.tensors, cache):
+        t.copy_(torch.from_numpy(a))
+    where = [torch.from_numpy(a).cuda() for a in (table, start, seq)]
+    want, want_lse = c.attend(q, *where, return_lse=True)
+    assert c.status() == moe.MOE_OK
+    moe.moe_kv_set_timeout(c.workspace, 1_000_000)
+    moe.moe_kv_debug_withhold(c.workspace, 3)
+    c.attend(q, *where)
+    moe.moe_kv_debug_withhold(c.workspace, -1)
+    counters = c.workspace[:moe.MOE_KV_WORKSPACE_HEADER].clone()
+    out = torch.full_like(q, 7.0)
+    for _ in range(2):
+        c.attend(q, *where, out=out)
+    assert (out == 7).all() and torch.equal(c.workspace[:moe.MOE_KV_WORKSPACE_HEADER], counters)
+    assert c.status() == moe.MOE_ERR_DEVICE_TIMEOUT and c.status() == moe.MOE_OK
+    got, lse = c.attend(q, *where, return_lse=True)
+    assert c.status() == moe.MOE_OK and torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.gpu
 def test_attend_query_rows_with_nan_or_infinity(moe):
     rng = np.random.default_rng(2)
     cache, table, start, seq = make_batch(rng, [(90, 2)], 64, 2, 128)
