@@ -12,6 +12,7 @@ Importing fails loudly when the library has not been built
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -504,13 +505,23 @@ def moe_kv_debug_withhold(workspace, cta: int, stream=None):
     return _check(_lib.moe_kv_debug_withhold(_ptr(workspace), cta, _stream(stream)), "moe_kv_debug_withhold")
 
 
+def _allocating_on(stream):
+    """Context in which torch allocates for this stream (a torch stream or a raw handle); None: the current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if _torch is None:
+        _use_torch()
+    return _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class KvCache:
     """A layer's paged cache: its tensors (e4m3 codes, E8M0 scales) and an attention workspace.
 
     ``append(k, v, slots)`` writes a step's keys and values, ``attend(q,
     block_table, query_start, seq_lens)`` returns the BF16 [T, q_heads,
     head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``), both
-    on the current torch stream. Layers that run one after the other on one
+    on the current torch stream or on ``stream``, which the outputs are then
+    allocated for too (the inputs are the caller's to keep). Layers that run one after the other on one
     stream can share a workspace. ``status()`` synchronizes and returns the
     device status of the attend calls since it was last read: anything but
     MOE_OK and none of their outputs is to be used.
@@ -540,9 +551,10 @@ class KvCache:
                return_lse: bool = False, stream=None):
         import torch
 
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+        with _allocating_on(stream):  # a block of the current stream's may still be in use there
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
         moe_kv_attend(self.tensors, q, block_table, query_start, seq_lens, out, self.workspace, lse, scale, window,
                       stream)
         return (out, lse) if return_lse else out

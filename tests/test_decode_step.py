@@ -1079,6 +1079,32 @@ def test_attend_strides_streams_and_repeats(moe):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_attend_on_a_stream_allocates_for_it(moe, raw):
+    """Outputs of a call on another stream lie in no block that the current stream has freed and still writes."""
+    rng = np.random.default_rng(3)
+    cache, table, start, seq = make_batch(rng, [(500, 40)], 64, 2, 128)
+    q = bf16(rng.standard_normal((40, 16, 128))).cuda()
+    c = moe.KvCache(len(cache[0]), 2, 64, 128)
+    for t, a in zip(c.tensors, cache):
+        t.copy_(torch.from_numpy(a))
+    where = [torch.from_numpy(a).cuda() for a in (table, start, seq)]
+    want, want_lse = c.attend(q, *where, return_lse=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    blocks = [torch.empty_like(t) for t in (want, want_lse)]
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    for b in blocks:
+        b.fill_(7.0)
+    freed = {b.data_ptr() for b in blocks}
+    del b, blocks
+    out, lse = c.attend(q, *where, return_lse=True, stream=side.cuda_stream if raw else side)
+    assert out.data_ptr() not in freed and lse.data_ptr() not in freed
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and c.status(side) == moe.MOE_OK
+
+
+@pytest.mark.gpu
 def test_cache_offsets_past_32_bits(moe):
     """Pages whose bytes lie past 2^32 in the cache, written and read."""
     pages, heads, page, dim = 70000, 8, 64, 128  # 4.6 GB of codes each
