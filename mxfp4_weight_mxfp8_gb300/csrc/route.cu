@@ -115,17 +115,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps, N <= 12 ? 6 : N <= 16 ? 4 : 
       x[i] = e < E ? load_logit<T>(row + e) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fmaxf(x[i], -INFINITY);  // NaN: masked
+    for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -INFINITY), 3.402823466e38f);  // NaN: masked; +inf: the largest number
     // A logit's score is exp(x - top) / sum, or its sigmoid.
     float top = 0.0f, sum = 1.0f;
     uint32_t key[N];
     if (!sigmoids) {
       top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] = fminf(x[i], 3.402823466e38f);
-        top = fmaxf(top, x[i]);
-      }
+      for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
       if (top == -INFINITY) top = 0.0f;

@@ -407,6 +407,21 @@ def test_route_ties_go_to_the_lowest_index(moe, experts, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_score", [(1, 1), (4, 1), (4, 2)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_infinity_counts_as_the_largest_number(moe, scoring, groups, group_score, bias):
+    """A logit of +inf ties with the largest FP32 number: the lower index first."""
+    x = torch.full((2, 40), -1.0)
+    x[0, 3], x[0, 7], x[0, 31] = 3.4028234663852886e38, math.inf, math.inf
+    x[1, 3], x[1, 7], x[1, 31] = math.inf, 3.4028234663852886e38, math.inf
+    kw = dict(scoring=scoring, bias=np.zeros(40, np.float32) if bias else None, groups=groups, group_topk=groups, group_score=group_score)
+    ids, w = run_route(moe, x.cuda(), 3, **kw)
+    assert ids.tolist() == [[3, 7, 31]] * 2
+    np.testing.assert_allclose(w, np.full((2, 3), 1 / 3), rtol=32 * U)
+
+
+@pytest.mark.gpu
 def test_route_strided_rows_and_row_independence(moe):
     g = torch.Generator().manual_seed(4)
     wide = torch.randn(70, 500, generator=g).cuda()
