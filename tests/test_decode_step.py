@@ -422,6 +422,38 @@ def test_route_infinity_counts_as_the_largest_number(moe, scoring, groups, group
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tokens,experts,k,kw", ROUTES + [
+    (2000, 384, 16, dict(scoring="sigmoid", bias=True, groups=8, group_topk=4, group_score=2)),
+    (2000, 256, 8, dict(scoring="softmax", bias=True, groups=4, group_topk=2, group_score=2))])
+def test_route_ids_are_those_of_the_32_bit_formula(moe, tokens, experts, k, kw):
+    """Every id equal to the formula's in FP32 on this device, sums by halving 1024 places, near and exact ties among them."""
+    g = torch.Generator().manual_seed(tokens + experts)
+    x = (torch.randn(tokens, experts, generator=g) * 2).to(torch.bfloat16).float().cuda()  # coarse: many equal logits
+    kw = dict(kw)
+    bias = (torch.randint(-50, 50, (experts,), generator=g) * 0.002).float().cuda() if kw.pop("bias", False) else None
+    if kw["scoring"] == "sigmoid":
+        score = 1.0 / (1.0 + torch.exp(-x))
+    else:
+        e = torch.exp(x - x.amax(1, keepdim=True))
+        total = torch.nn.functional.pad(e, (0, 1024 - experts))
+        while total.shape[1] > 1:
+            total = total[:, : total.shape[1] // 2] + total[:, total.shape[1] // 2:]
+        score = e / total
+    groups, by_sum = kw.get("groups", 1), kw.get("groups", 1) > 1 and kw["group_score"] == 2
+    key = score + bias if bias is not None else score if by_sum else x
+    if groups > 1:
+        part = key.view(tokens, groups, -1)
+        best = part.sort(dim=-1, descending=True).values
+        rank = best[..., 0] + best[..., 1] if by_sum else best[..., 0]
+        kept = torch.zeros_like(rank, dtype=torch.bool).scatter_(
+            1, rank.sort(dim=-1, descending=True, stable=True).indices[:, : kw["group_topk"]], True)
+        key = torch.where(kept[..., None], part, -math.inf).view(tokens, experts)
+    want = key.sort(dim=-1, descending=True, stable=True).indices[:, :k].int().cpu().numpy()
+    ids, _ = run_route(moe, x, k, bias=None if bias is None else bias.cpu().numpy(), **kw)
+    assert np.array_equal(ids, want)
+
+
+@pytest.mark.gpu
 def test_route_strided_rows_and_row_independence(moe):
     g = torch.Generator().manual_seed(4)
     wide = torch.randn(70, 500, generator=g).cuda()
@@ -970,6 +1002,72 @@ def test_attend_value_scales_far_apart(moe, large, others, dim, rows, q_heads):
     want, want_lse, mass = request_reference(cache, q.float().numpy(), table, n, dim ** -0.5)
     assert (np.abs(lse - want_lse) <= 1.6e-4).all()
     assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES + [(150, 8)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 3, 140])
+def test_attend_values_that_are_not_finite_reach_only_rows_that_see_them(moe, window, dim, rows, q_heads):
+    """NaN codes in every 32 dimensions at the second row's own token: the first row does not see it, nor do the rows whose
+    window has passed it."""
+    rng = np.random.default_rng(dim + rows)
+    n, page = 273 + rows, 16
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    _, v, _, _ = cache
+    q = bf16(rng.standard_normal((rows, q_heads, dim)))
+    clean, clean_lse = run_attend(moe, cache, q.cuda(), table, start, seq, window=window)
+    t = n - rows + 1
+    sees = (np.arange(rows) >= 1) & (np.arange(rows) - 1 < (window or rows))
+    hit = np.zeros(dim, bool)
+    hit[5::32] = hit[dim - 1] = True
+    v[table[0, t // page], 0, t % page, hit] = 0x7F
+    v[table[0, t // page], 0, t % page, dim - 1] = 0xFF
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq, window=window)
+    assert np.isnan(out[sees][:, :, hit]).all() and np.isfinite(out[sees][:, :, ~hit]).all()
+    assert np.array_equal(out[~sees], clean[~sees]) and np.array_equal(lse, clean_lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES + [(150, 8)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("byte", [247, 251, 255])
+def test_attend_values_past_the_largest_number_reach_only_rows_that_see_them(moe, byte, dim, rows, q_heads):
+    """The last token starts a page whose scale takes some of its codes (all, with byte 255) past FP32's largest number: the
+    last row's alone."""
+    rng = np.random.default_rng(dim + rows)
+    page, n = 16, 16 * 20 + 1
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    _, v, _, vs = cache
+    q = bf16(rng.standard_normal((rows, q_heads, dim)))
+    clean, clean_lse = run_attend(moe, cache, q.cuda(), table, start, seq)
+    last = table[0, n // page]
+    vs[last] = byte
+    big = rng.random(dim) < 0.3
+    v[last, 0, 0] = np.where(big, 0xF8, 0x01)  # -256 and 2^-9
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq)
+    assert np.array_equal(out[:-1], clean[:-1]) and np.array_equal(lse, clean_lse)
+    assert not np.isfinite(out[-1][:, big | (byte == 255)]).any() and np.isfinite(out[-1][:, ~(big | (byte == 255))]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (3, 8, 64), (40, 8, 128), (4, 8, 256)])
+def test_append_and_attend_head_major_rows(moe, rows, q_heads, dim):
+    """Keys, values and queries whose heads lie further apart than their tokens: the same as token-major ones."""
+    rng = np.random.default_rng(dim)
+    n, heads, page = 70, 3, 16
+    x = bf16(rng.standard_normal((2, n, heads, dim))).cuda()
+    slots = torch.arange(n, device="cuda") + 2 * page
+    q = bf16(rng.standard_normal((rows, heads * q_heads, dim))).cuda()
+    table = torch.arange(2, 9, dtype=torch.int32, device="cuda")[None]
+    start, seq = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, rows], [n]))
+    results = []
+    for major in (lambda t: t, lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)):
+        c = moe.KvCache(9, heads, page, dim)
+        c.append(major(x[0]), major(x[1]), slots)
+        results.append([*c.tensors, *c.attend(major(q), table, start, seq, return_lse=True)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
