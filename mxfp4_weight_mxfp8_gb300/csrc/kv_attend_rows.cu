@@ -46,7 +46,7 @@ struct RowsShape {
   static constexpr int kHalves = 1;
   static constexpr int kSpan = D;                 // 128 or 64: one box, one swizzle span a row
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kPartialFloats = kRows * (D + 2);
   static constexpr int kGroupTmem = 256;          // scores 128 columns, output D
   // Keys and values in rings of their own: a tile's keys are done with long before its values.
@@ -65,6 +65,9 @@ struct RowsShape {
   static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
   static_assert(kGroups * kWideBytes >= kRows * D * 4, "the groups' join fits the wide values' room");
+  // Each stage is always the same group's: a group waits for its own tiles only, and by a phase's parity would take a stage's
+  // tile before last for its last, had the other group's in between not come yet.
+  static_assert(kStages % kGroups == 0, "stages by groups");
   static_assert(kWide % 1024 == 0, "operand images on swizzle boundaries");
 };
 // What starting and joining an item costs, in tiles (the chunks: 286 us with 4, 281 with 6, 282 with 8; the prompts: 147,
