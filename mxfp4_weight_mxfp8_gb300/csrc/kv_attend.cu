@@ -64,6 +64,7 @@ struct Shape {
   // 96 registers spill: 98.8 us for 64 requests of up to 4096 tokens, against 68.5 in 2).
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 || (D == 64 && RT == 2) ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 && RT != 2 ? 2 : 3;
+  static constexpr int kKeyStages = kStages;
   // What starting and joining an item costs, in tiles: more of them the wider the row tile and the shorter a tile's loads
   // (64 ragged requests of 128: 8 rows take 91 us with 2, 93.5 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
   // of 64: 8 rows 45 with 2, 39 with 4; 32 rows 95 and 79, 75 with 8).

@@ -478,6 +478,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
 template <class X, int D, int kWhich>
 __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int weight, int shift,
                         long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
+  constexpr int kStages = kWhich == 1 ? X::kKeyStages : X::kStages;
   const int lane = threadIdx.x & 31;
   const uint64_t policy = policy_evict_first();
   const int per_tile = kTile >> shift, in_tile = lane & (per_tile - 1);  // pages of a tile; this lane's
@@ -500,8 +501,8 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
         if (page >= a.c.pages) page = -1;
         fresh = true;
       }
-      const int stage = k % X::kStages;
-      if (k >= X::kStages) alive = __all_sync(kAll, wait(empty + stage, (k / X::kStages - 1) & 1, status));
+      const int stage = k % kStages;
+      if (k >= kStages) alive = __all_sync(kAll, wait(empty + stage, (k / kStages - 1) & 1, status));
       if (!alive) break;
       // The copies first; the barrier's phase stays open until lane 0 arrives.
       const bool mine = lane / per_tile == batch;
@@ -542,7 +543,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
     s.next(a, prefix, shift, x, stop);
   }
   // The copies in flight land before the CTA ends (at once, unless another role gave up).
-  for (int i = max(0, k - X::kStages); i < k; ++i) wait(full + i % X::kStages, (i / X::kStages) & 1, status);
+  for (int i = max(0, k - kStages); i < k; ++i) wait(full + i % kStages, (i / kStages) & 1, status);
 }
 
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier

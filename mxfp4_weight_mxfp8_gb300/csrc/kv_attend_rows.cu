@@ -17,16 +17,19 @@
 //
 // Two groups take a CTA's tiles in turn, one in its softmax while the other's
 // products run; in a group two warpgroups share the rows, each with half of the
-// columns (two threads to a row). The groups' results are joined in shared memory.
+// columns (two threads to a row). At an item's end each thread takes a quarter of
+// its row's output from both groups' TMEM.
 //
 // Softmax and widening bound it: two chunks of up to 700 tokens on 3300 to 6000
-// earlier ones (64 query heads on 8 of 128, 162 GFLOP) take 350 us, 462 TFLOP/s;
-// the schedulers issue in 47 % of the cycles, the tensor pipe is busy for 31 %.
-// A group waits for its own products (the next scores cannot start before its
-// weights have been used), the other group's tile half hidden behind it.
-// Short items are bound by their starts and ends, some 20 thousand cycles
-// (queries 4, first scores and maxima 4, the groups' join and the output 6):
-// prompts of 1130 and 870 tokens without earlier ones take 162 us, 206 TFLOP/s.
+// earlier ones (64 query heads on 8 of 128, 162 GFLOP) take 313 us, 517 TFLOP/s.
+// A group's next scores cannot start before its weights have been used: it
+// waits for both products (some 2 thousand cycles, and widens its next values
+// meanwhile), the other group's tile half hidden behind it. Values widened only
+// then, into one buffer for each group, made it 350 us.
+// Short items are bound by their starts and ends (queries, first scores and
+// maxima, the output): prompts of 1130 and 870 tokens without earlier ones take
+// 139 us, 240 TFLOP/s; with the groups joined in shared memory, not by reading
+// each other's TMEM, 162.
 #include "kv_attend.cuh"
 
 namespace moe {
@@ -46,33 +49,33 @@ struct RowsShape {
   static constexpr int kHalves = 1;
   static constexpr int kSpan = D;                 // 128 or 64: one box, one swizzle span a row
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kPartialFloats = kRows * (D + 2);
   static constexpr int kGroupTmem = 256;          // scores 128 columns, output D
-  // Keys and values in rings of their own: a tile's keys are done with long before its values.
-  static constexpr int kKeyStride = kTileBytes, kValuesAt = kStages * kTileBytes, kValueStride = kTileBytes;
-  static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + 2 * kStages * kTileBytes;        // hi, lo
-  static constexpr int kWide = kQ + 2 * kRows * D;                   // [group] its tile's values in BF16
-  static constexpr int kWideBytes = kTile * D * 2;
-  static constexpr int kRowF = kWide + kGroups * kWideBytes;         // [row] factor
+  // Keys and values in rings of their own: a tile's keys are done with long before its values. A value stage holds the wide
+  // form, and the codes as they come: behind it, or (from 128 dimensions on) in its second half, where a token's wide row
+  // of the second 64 dimensions lies over its own codes.
+  static constexpr int kKeyStages = D == 128 ? 2 : 4, kStages = 4;
+  static constexpr int kWideBytes = kTile * D * 2, kKeyStride = kTileBytes, kValueStride = kWideBytes + (D == 128 ? 0 : kTileBytes);
+  static constexpr int kRing = 0, kWide = kKeyStages * kTileBytes;
+  static constexpr int kValuesAt = kWide + (D == 128 ? kTileBytes : kWideBytes);
+  static constexpr int kQ = kWide + kStages * kValueStride;          // hi, lo; an item's output on its way out
+  static constexpr int kRowF = kQ + 2 * kRows * D;                   // [row] factor
   static constexpr int kTops = kRowF + kRows * 4;                    // [group][half][row] maxima, then sums
   static constexpr int kRefs = kTops + kGroups * 2 * kRows * 4;      // [group][row] references
   static constexpr int kRowDst = kRefs + kGroups * kRows * 4;        // [row] its place among the outputs' rows
   static constexpr int kNan = kRowDst + kRows * 8;                  // [row][D / 32]: outputs that saw a NaN apart
   static constexpr int kMeta = kNan + kRows * D / 8;                 // [stage][kMaxPages + 1]
   static constexpr int kBars = (kMeta + kStages * (kMaxPages + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kPrefix = kBars + (4 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
+  static constexpr int kPrefix = kBars + (2 * kKeyStages + 2 * kStages + 4 * kGroups + 1) * 8;  // k_full, k_empty, v_full, v_empty, s_full, o_full, p_ready, drained, q_ready
   static constexpr int smem(int requests) { return kPrefix + (requests + 1) * 8 + 1024; }
-  static_assert(kGroups * kWideBytes >= kRows * D * 4, "the groups' join fits the wide values' room");
   // Each stage is always the same group's: a group waits for its own tiles only, and by a phase's parity would take a stage's
   // tile before last for its last, had the other group's in between not come yet.
-  static_assert(kStages % kGroups == 0, "stages by groups");
-  static_assert(kWide % 1024 == 0, "operand images on swizzle boundaries");
+  static_assert(kKeyStages % kGroups == 0 && kStages % kGroups == 0, "stages by groups");
+  static_assert(kWide % 1024 == 0 && kValueStride % 1024 == 0 && kQ % 1024 == 0, "operand images on swizzle boundaries");
 };
-// What starting and joining an item costs, in tiles (the chunks: 286 us with 4, 281 with 6, 282 with 8; the prompts: 147,
-// 151, 151; with a window of 1000 on 4000 tokens: 219, 219, 237).
-constexpr int kItemTiles = 6;
+// What starting and joining an item costs, in tiles (prompts without earlier tokens: 139 us with 4 and 5, 146 with 6, 153
+// with 8; one of 900 tokens with a window of 100: 104 with 4, 100 with 5; the chunks: 313 with any).
+constexpr int kItemTiles = 5;
 constexpr int kLongUnits = 16;       // longer items may be cut anywhere (one head to a group, 900 tokens: 46 -> 34.6 us)
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
@@ -199,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* meta = reinterpret_cast<uint32_t*>(sm + X::kMeta);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + X::kBars);
-  uint64_t* k_empty = k_full + X::kStages;
-  uint64_t* v_full = k_empty + X::kStages;
+  uint64_t* k_empty = k_full + X::kKeyStages;
+  uint64_t* v_full = k_empty + X::kKeyStages;
   uint64_t* v_empty = v_full + X::kStages;
   uint64_t* s_full = v_empty + X::kStages;   // [group]: scores of its tile in TMEM
   uint64_t* o_full = s_full + kGroups;     // [group]: its tile's output in TMEM
@@ -221,11 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     s_status = *static_cast<const volatile int32_t*>(status);
-    for (int i = 0; i < X::kStages; ++i) {
+    for (int i = 0; i < X::kKeyStages; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < X::kStages; ++i) {
       mbar_init(v_full + i, 1);
-      mbar_init(v_empty + i, kGroupThreads);
+      mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(s_full + i, 1);
@@ -268,18 +273,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0, segments = 0, turn = 0;  // k: the CTA's first tile of the segment; turn: the group's own count
     bool alive = true;
     auto scores = [&](int i) {
-      alive = __all_sync(kAll, wait(k_full + i % X::kStages, (i / X::kStages) & 1, status));
+      const int stage = i % X::kKeyStages;
+      alive = __all_sync(kAll, wait(k_full + stage, (i / X::kKeyStages) & 1, status));
       if (!alive) return;
       tc_fence_after_sync();
       if (lane == 0) {
-        const uint32_t keys = ring + (i % X::kStages) * X::kKeyStride;
+        const uint32_t keys = ring + stage * X::kKeyStride;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int st = 0; st < D / 32; ++st)
             mma_f8(tmem + w * X::kGroupTmem, smem_desc(q_at + part * kRows * D + st * 32, 16, kGroup, kMode),
                    smem_desc(keys + st * 32, 16, kGroup, kMode), idesc_f8(kTile, false, false, part == 1), part + st > 0);
-        tc_commit(k_empty + i % X::kStages);
+        tc_commit(k_empty + stage);
         tc_commit(s_full + w);
       }
       __syncwarp();
@@ -296,13 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!alive) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t own = tmem + w * X::kGroupTmem, vals = wide + w * X::kWideBytes;
+          const uint32_t own = tmem + w * X::kGroupTmem, vals = wide + i % X::kStages * X::kValueStride;
 #pragma unroll
           for (int st = 0; st < kTile / 16; ++st)
 #pragma unroll
             for (int part = 0; part < 2; ++part)
               mma_bf16_tmem(own + 128, own + st * 16 + part * 8, smem_desc(vals + st * 2048, kTile * 128, 1024, 2),
                             idesc_bf16(D, false, true), !first || st + part > 0);
+          tc_commit(v_empty + i % X::kStages);
           tc_commit(o_full + w);
         }
         __syncwarp();
@@ -331,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* refs = reinterpret_cast<float*>(sm + X::kRefs);
     long long* row_dst = reinterpret_cast<long long*>(sm + X::kRowDst);
     uint32_t* nans = reinterpret_cast<uint32_t*>(sm + X::kNan);
-    float* join = reinterpret_cast<float*>(sm + X::kWide);
-    uint8_t* wide = sm + X::kWide + group * X::kWideBytes;
+    uint8_t* staged = sm + X::kQ;  // an item's output
     const uint32_t lanes = tmem + group * X::kGroupTmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const int widen_row = (warp & 7) * 16 + lane / 2;  // the token of a tile that this thread widens, with its neighbour
     const uint32_t s_at = lanes + half * kHalfTile, o_at = lanes + 128 + half * kHalfD;
     int k = 0, turn = 0;   // the CTA's tile; the group's own count
     bool failed = false;   // a wait ran out: no more waits; agreed on at the barriers
@@ -394,19 +401,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; at < last; at += 2, ++turn) {
         const int stage = at % X::kStages;
         if (!failed) failed = !wait(v_full + stage, (at / X::kStages) & 1, status);
-        if (written && !failed) failed = !wait(o_full + group, (turn - 1) & 1, status);  // the last tile's values have been used
         __syncwarp();
-        tc_fence_after_sync();
         const uint32_t* mt = meta + stage * (kMaxPages + 1);
         const int base = (s.q.tile0 + s.begin + at - k) * kTile, base_half = base + half * kHalfTile;
         const bool edge = sight.edge(base) || mt[kMaxPages] == 0;
         {
-          // The values' wide form, while the scores are on their way: thread `row` takes the tile's token of that number.
-          const uint8_t* codes = sm + X::kRing + X::kValuesAt + stage * X::kValueStride;
-          const Widener<D / 32> widener(sight, mt[row >> shift], edge, base + row, nans, &s_nans);
-#pragma unroll 2
-          for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c)
-            widener(*reinterpret_cast<const uint4*>(codes + chunk_at<X::kSpan>(row, c)), c, row, wide);
+          // The values' wide form, while the group's products run: two lanes to a token, half of its dimensions each (the
+          // second in an order of its own, so that they meet no bank twice). Both read all before either writes.
+          uint8_t* image = sm + X::kWide + stage * X::kValueStride;
+          const uint8_t* codes = sm + X::kValuesAt + stage * X::kValueStride;
+          constexpr int kChunks = D / 32;
+          const int part = lane & 1;
+          const Widener<D / 32> widener(sight, mt[widen_row >> shift], edge, base + widen_row, nans, &s_nans);
+          uint4 w[kChunks];
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(codes + chunk_at<X::kSpan>(widen_row, part * kChunks + (i ^ (D == 128 ? part * 2 : 0))));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) widener(w[i], part * kChunks + (i ^ (D == 128 ? part * 2 : 0)), widen_row, image);
           fence_proxy_async_shared();
         }
         // The row's visible tokens among this thread's 16 from column c on, as bits.
@@ -497,91 +510,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_stores();
         tc_fence_before_sync();
         mbar_arrive(p_ready + group);
-        mbar_arrive(v_empty + stage);  // (with the pages' entries, which the scores needed)
       }
-      // The group's output, this thread's half of the row.
-      float acc[kHalfD];
-      if (written) {
-        if (!failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
-        __syncwarp();
-        tc_fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < kHalfD; c += 16) {
-          float o[16];
-          tmem_load_16_async(o_at + c, o);
-          tmem_wait_16(o);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = o[j];
-        }
-        tc_fence_before_sync();
-      } else {
-#pragma unroll
-        for (int i = 0; i < kHalfD; ++i) acc[i] = 0.0f;
-      }
+      // The groups' outputs are joined: a thread takes a quarter of its row's columns, from both groups' TMEM (a group may have
+      // had no tile).
+      if (written && !failed) failed = !wait(o_full + group, (turn - 1) & 1, status);
+      const bool any0 = k + (k & 1) < last, any1 = k + !(k & 1) < last;
       k = last;
-
-      // The groups' outputs are joined: each takes a half of its threads' columns, and gives the other half away.
-      failed = sync_any<kAllCompute>(3, failed);
-      if (failed) break;
-      constexpr int kOwn = kHalfD / 2;
-      const int column = half * kHalfD + group * kOwn;
       tops[(group * 2 + half) * kRows + row] = l;
       if (half == 0) refs[group * kRows + row] = m;
-      auto cell = [&](int c) { return reinterpret_cast<float4*>(join + row * D + half * kHalfD + ((c ^ (row & 7)) << 2)); };
+      tc_fence_before_sync();
+      failed = sync_any<kAllCompute>(3, failed);
+      if (failed) break;
+      tc_fence_after_sync();
+      constexpr int kOwn = kHalfD / 2;
+      const int column = half * kHalfD + group * kOwn;
+      const uint32_t out0 = tmem + (static_cast<uint32_t>(warp & 3) << 21) + 128 + column, out1 = out0 + X::kGroupTmem;
       float own[kOwn];
-      if (group == 0) {
-#pragma unroll
-        for (int c = 0; c < kOwn / 4; ++c)
-          *cell(kOwn / 4 + c) = make_float4(acc[kOwn + 4 * c], acc[kOwn + 4 * c + 1], acc[kOwn + 4 * c + 2], acc[kOwn + 4 * c + 3]);
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) own[i] = acc[i];
-      } else {
-#pragma unroll
-        for (int c = 0; c < kOwn / 4; ++c) *cell(c) = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) own[i] = acc[kOwn + i];
-      }
-      all_sync();
       {
         const float l0 = tops[row] + tops[kRows + row], l1 = tops[2 * kRows + row] + tops[3 * kRows + row];
         const float m0 = refs[row], m1 = refs[kRows + row], mn = fmaxf(m0, m1), safe = mn > -INFINITY ? mn : 0.0f;
         const float f0 = exp2_fast(m0 - safe), f1 = exp2_fast(m1 - safe);
         l = l0 * f0 + l1 * f1;
         m = mn;
-        const float mine = group == 0 ? f0 : f1, other = group == 0 ? f1 : f0;
 #pragma unroll
-        for (int c = 0; c < kOwn / 4; ++c) {
-          const float4 v = *cell(group * (kOwn / 4) + c);
-          own[4 * c] = own[4 * c] * mine + v.x * other;
-          own[4 * c + 1] = own[4 * c + 1] * mine + v.y * other;
-          own[4 * c + 2] = own[4 * c + 2] * mine + v.z * other;
-          own[4 * c + 3] = own[4 * c + 3] * mine + v.w * other;
+        for (int c = 0; c < kOwn; c += 16) {
+          float u[16], v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = v[j] = 0.0f;
+          if (any0) tmem_load_16_async(out0 + c, u);
+          if (any1) tmem_load_16_async(out1 + c, v);
+          tmem_wait_16(u);
+          tmem_wait_16(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) own[c + j] = u[j] * f0 + v[j] * f1;
         }
+        tc_fence_before_sync();
         if (s.begin < s.end && s_nans) {
           const uint32_t bad = nans[row * (D / 32) + column / 32] >> (column % 32);  // (its lowest kOwn bits)
 #pragma unroll
           for (int i = 0; i < kOwn; ++i)
             if (bad & 1u << i) own[i] = __uint_as_float(0x7FC00000u);
         }
-        const float inv = !s.whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-#pragma unroll
-        for (int c = 0; c < kOwn / 4; ++c)
-          *cell(group * (kOwn / 4) + c) = make_float4(own[4 * c] * inv, own[4 * c + 1] * inv, own[4 * c + 2] * inv, own[4 * c + 3] * inv);
       }
-      all_sync();
-      // Out in whole rows (a thread's own row, 16 bytes at a time, would take an eighth of a wavefront's width a store).
-      auto joined = [&](int r, int c) {
-        return *reinterpret_cast<const float4*>(join + r * D + c / (kHalfD / 4) * kHalfD + ((c % (kHalfD / 4) ^ (r & 7)) << 2));
-      };
       if (s.whole) {
+        // Out in whole rows, by way of the queries' room (a thread's own row, 16 bytes at a time, would take an eighth of a
+        // wavefront's width a store).
+        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
         if (a.lse != nullptr && tid < rows) a.lse[row_dst[tid]] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        auto cell = [&](int r, int c) { return reinterpret_cast<uint4*>(staged + r * (2 * D) + ((c ^ (r & 7)) << 4)); };
+#pragma unroll
+        for (int c = 0; c < kOwn; c += 8) {
+          __nv_bfloat162 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(own[c + 2 * j] * inv, own[c + 2 * j + 1] * inv);
+          *cell(row, (column + c) / 8) = *reinterpret_cast<uint4*>(w);
+        }
+        all_sync();
 #pragma unroll
         for (int i = tid; i < kRows * D / 8; i += kAllCompute) {
           const int r = i / (D / 8), c = i % (D / 8);
-          const float4 v0 = joined(r, 2 * c), v1 = joined(r, 2 * c + 1);
-          __nv_bfloat162 w[4] = {__floats2bfloat162_rn(v0.x, v0.y), __floats2bfloat162_rn(v0.z, v0.w),
-                                 __floats2bfloat162_rn(v1.x, v1.y), __floats2bfloat162_rn(v1.z, v1.w)};
-          if (r < rows) *reinterpret_cast<uint4*>(a.out + row_dst[r] * D + c * 8) = *reinterpret_cast<uint4*>(w);
+          if (r < rows) *reinterpret_cast<uint4*>(a.out + row_dst[r] * D + c * 8) = *cell(r, c);
         }
       } else {
         float* piece = partials + static_cast<int64_t>(blockIdx.x * 2 + (s.first ? 1 : 0)) * X::kPartialFloats;
@@ -590,11 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           piece[kRows * D + kRows + tid] = l;
         }
 #pragma unroll
-        for (int i = tid; i < kRows * D / 4; i += kAllCompute)
-          *reinterpret_cast<float4*>(piece + i * 4) = joined(i / (D / 4), i % (D / 4));
+        for (int c = 0; c < kOwn; c += 4)
+          *reinterpret_cast<float4*>(piece + row * D + column + c) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
       }
       if (!s.whole) join_item<kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
-      all_sync();  // the join's room, the rows' factors and the join word are free again, the segment is done with
+      all_sync();  // the output's room, the rows' factors and the join word are free again, the segment is done with
       if (tid == 0) {
         s_unit += s_segment.length;
         if (s_unit < stop) s_segment.next(a, prefix, shift, s_unit, stop);
