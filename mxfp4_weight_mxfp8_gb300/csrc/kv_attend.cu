@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
+  const int32_t found = tid == 0 ? *static_cast<const volatile int32_t*>(status) : 0;  // (on its way while the work is summed)
   if (tid == 0) {
-    s_status = *static_cast<const volatile int32_t*>(status);
     for (int i = 0; i < X::kStages; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -224,19 +224,21 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   const int weight = sum_work<X::kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  // (An error that nobody has read yet: its call has left the arrival counters anyhow.)
-  if (blockIdx.x >= ctas || s_status != MOE_OK) return;
+  if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, X::kTmem);
     tmem_relinquish();  // the SM's other CTA allocates its own
   }
+  if (tid == 0) s_status = found;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * X::kCols;
 
-  if (warp == kProducerWarp) {
+  if (s_status != MOE_OK) {
+    // An error that nobody has read yet: its call has left the arrival counters anyhow.
+  } else if (warp == kProducerWarp) {
     produce<X, D, 3>(a, maps, prefix, weight, shift, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: keys and queries in the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values

@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
   float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
 
+  const int32_t found = tid == 0 ? *static_cast<const volatile int32_t*>(status) : 0;  // (on its way while the work is summed)
   if (tid == 0) {
-    s_status = *static_cast<const volatile int32_t*>(status);
     for (int i = 0; i < X::kKeyStages; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
@@ -244,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int weight = sum_work<kThreads, kRows, kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  // (An error that nobody has read yet: its call has left the arrival counters anyhow.)
-  if (blockIdx.x >= ctas || s_status != MOE_OK) return;
+  if (blockIdx.x >= ctas) return;
   if (tid == 0 || tid == 32) {
     const int i = tid == 0 ? 0 : 1;
     s_run[i] = snap(a, prefix, weight, shift, total * (blockIdx.x + i) / ctas, total);
   }
+  if (tid == 0) s_status = found;
   __syncthreads();
   const long long start = s_run[0], stop = s_run[1];
-  if (start >= stop) return;
+  if (start >= stop || s_status != MOE_OK) return;  // (an error that nobody has read yet: the arrival counters are anyhow)
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, kGroups * X::kGroupTmem);
     tmem_relinquish();
