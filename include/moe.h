@@ -537,8 +537,10 @@ typedef struct moe_kv_batch_t {
  * all up to p). Query head h reads cache head h / (q_heads / kv_heads).
  *   out = sum_j w_j v_j,  w_j = exp(scale q.k_j - lse),
  *   lse = log sum_j exp(scale q.k_j)
- * in FP32; out is rounded to BF16 once. A query that sees nothing (p < 0) gets a
- * zero row and lse -inf. Cache rows that no query sees are never used,
+ * in FP32, but that a query element smaller than 2^-13 of its row's largest
+ * magnitude is held within 2^-21 of that, and each weight within 2^-16 of itself
+ * (down to 2^-100 of its row's largest); out is rounded to BF16 once. A query
+ * that sees nothing (p < 0) gets a zero row and lse -inf. Cache rows that no query sees are never used,
  * whatever they hold; a table entry outside the cache is seen by no query. A
  * query row that holds a NaN or an infinity gives a NaN row.
  *   q    device, BF16 [tokens, q_heads, head_dim], strides in elements

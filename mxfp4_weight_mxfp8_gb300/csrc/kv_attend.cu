@@ -2,37 +2,37 @@
 // include/moe.h).
 //
 // An item is 8 * RT query rows of a request and cache head (kv_attend.cuh has
-// the work split). Both products run on the tensor cores with the cache's
-// codes as they are, as the 128-row operand: S^T[token][row] = K x Q^T and
-// O^T[dim][row] += V^T x P^T (V read transposed, token-major as it lies in the
-// page). The few query rows are the narrow operand. Scores are taken of the
-// cache's codes as they are, queries split into two e4m3 numbers, hi + lo / 16,
-// which take two columns of the one product (the wide operand is read from
-// shared memory once for both): together they hold the 8 significant bits of a
-// BF16 query exactly down to 2^-14 of its row's largest magnitude, and what is
-// smaller within 2^-21 of that. Weights must keep their precision however small
-// they are (under a dominant token of no value the others are all of the
-// output), so they are two BF16 numbers, hi + lo, 16 bits at every magnitude,
-// in columns of their own again. For that the values are widened to BF16, code
-// times page scale, which is exact, in place in shared memory.
+// the work split). In both products the cache's tokens or dimensions are the
+// tensor core's 128-row operand: S^T[token][row] = K x Q^T and O^T[dim][row] +=
+// V^T x P^T (V read transposed, token-major as it lies in the page). The few
+// query rows are the narrow operand. Scores are taken of the keys' codes as they
+// are, queries split into two e4m3 numbers, hi + lo / 16, which take two columns
+// of the one product (the wide operand is read from shared memory once for
+// both): together they hold the 8 significant bits of a BF16 query exactly down
+// to 2^-13 of its row's largest magnitude, and what is smaller within 2^-21 of
+// that. Weights must keep their precision however small they are (under a
+// dominant token of no value the others are all of the output), so they are two
+// BF16 numbers, hi + lo, 16 bits at every magnitude, in columns of their own
+// again. For that the values are widened to BF16, code times page scale, which
+// is exact, in place in shared memory.
 // A row's weights are held against a reference, the largest score when it was
-// last raised: FP32 and BF16 have room for weights far above and below it, so a
-// tile needs no maxima and the output stays in TMEM, accumulated in FP32 by the
-// tensor core. Only when a weight outgrows the reference by 2^64 (and on an
-// item's first tile) the maxima are taken first and the output is rescaled.
+// last raised, so a tile needs no maxima and the output stays in TMEM, accumulated
+// in FP32 by the tensor core. Only when a weight outgrows the reference by 2^8
+// (and on an item's first tile) the maxima are taken first and the output is
+// rescaled.
 //
 // Roles: a producer warp looks up pages and streams tiles by TMA through a ring,
 // a warp issues the MMAs, four warps widen the values, do the softmax (thread =
 // token) and read the output at the end (thread = dimension).
 //
 // The cache's bytes bound large decode steps: 64 requests of up to 8192 tokens
-// (64 query heads on 8 of 128) take 101 us for 532 MB, 5.24 TB/s, 77 % of a
-// copy's rate (the same loop without the widening takes 93). Two requests of 100
-// to 131 thousand tokens take 54 us for 244 MB: the same, with longer joins. One
-// request of 777 tokens takes 10.9 us, all latency. With several rows a request
-// and a window (40 requests, up to 24 rows, 1024 tokens of 64: 42 us for 35 MB)
-// an item's start and end bound it, some 8 thousand cycles next to 4 thousand
-// for a tile.
+// (64 query heads on 8 of 128) take 102 us for 532 MB, 5.2 TB/s, 77 % of a
+// copy's rate, with the schedulers issuing in 57 % of the cycles: the widening's
+// instructions (the loop without them takes 93 us). Two requests of 100 to 131
+// thousand tokens take 55 us for 244 MB: the same, with longer joins. One request
+// of 777 tokens takes 11 us, all latency. With several rows a request and a
+// window (40 requests, up to 24 rows, 1024 tokens of 64: 43 us for 35 MB) an
+// item's start and end bound it, twice as long as a tile.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -61,13 +61,13 @@ struct Shape {
   static constexpr bool kWideners = D == 256;
   static constexpr int kThreads = kWideners ? 320 : 192;
   // As many CTAs as shared memory and registers hold with two tiles or more in each one's ring (24 rows of 64 in 3 CTAs of
-  // 96 registers spill: 98.8 us for 64 requests of up to 4096 tokens, against 68.5 in 2).
+  // 96 registers spill: 119 us for 64 requests of up to 4096 tokens, against 79 in 2).
   static constexpr int kCtasPerSm = D == 256 ? 1 : RT == 1 || (D == 64 && RT == 2) ? 3 : 2;
   static constexpr int kStages = D == 64 ? (RT == 1 ? 4 : RT == 2 ? 3 : 5) : D == 128 && RT != 2 ? 2 : 3;
   static constexpr int kKeyStages = kStages;
   // What starting and joining an item costs, in tiles: more of them the wider the row tile and the shorter a tile's loads
-  // (64 ragged requests of 128: 8 rows take 91 us with 2, 93.5 with 4; 24 rows 91 with 2, 76 with 4; 32 rows 112 and 96;
-  // of 64: 8 rows 45 with 2, 39 with 4; 32 rows 95 and 79, 75 with 8).
+  // (64 ragged requests of 128: 8 rows take 102 us with 2, 106 with 1 or 5; 24 rows 84 with 4, 88 with 7; of 64: 8 rows 54
+  // with 3 to 5, 61 with 1).
   static constexpr int kItemTiles = RT + (D == 64 ? 3 : 1);
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
@@ -657,12 +657,13 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
 
 template <int D>
 cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
-  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average: a wider tile costs its softmax and TMEM
-  // columns whether rows use them or not, a narrower one reads the cache again (8 rows: 91 us in tiles of 8, 94 in 16;
-  // 16 rows of 128, 64 requests of up to 4096 tokens: 67 us in 16, 90 in 24; 24 rows: 95 in 24, 112 in 32).
-  // Many more rows are the 128-row form's (up to head_dim 128: a thread of it holds half a row's output). The same requests
-  // with 40 rows each take 140 us here and 144 there, with heads of 64 113 and 131; with 47 rows 166 and 147, 134 and 129;
-  // two requests of 30 thousand tokens with 40 rows 55 and 81.
+  // Row tiles of 8, 16, 24 or 32, by the rows that a request has on average over the call, requests without rows and
+  // padding included (the host knows no more): a wider tile costs its softmax and TMEM columns whether rows use them or
+  // not, a narrower one reads the cache again (64 requests of up to 4096 tokens, heads of 128: 8 rows take 62 us in tiles
+  // of 8, 73 in 16; 16 rows 74 in 16, 83 in 24; 24 rows 84 in 24, 96 in 32).
+  // Many more rows are the 128-row form's (up to head_dim 128: there the two groups' scores and outputs fill the TMEM). The
+  // same requests with 40 rows each take 151 us here and 161 there, with heads of 64 138 and 131; with 48 rows 178 and 162,
+  // 166 and 131; two requests of 30 thousand tokens with 40 rows 62 and 91.
   const long long rows = static_cast<long long>(a.b.tokens) * a.group;
   if (D <= 128 && rows > 44ll * a.b.requests) return launch_kv_attend_rows(a, maps, shift, sms, stream);
   if (rows <= 8ll * a.b.requests) return launch_shape<D, 1>(a, maps, shift, sms, stream);

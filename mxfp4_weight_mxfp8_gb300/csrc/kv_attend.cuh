@@ -26,7 +26,7 @@ constexpr int kCompute = 128;     // threads of a compute warpgroup
 constexpr int kMaxPages = 8;      // pages of a tile
 constexpr int kMaxCtas = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kHighest = 64.0f;      // a weight may grow to 2^64 times its reference's: far from FP32's and BF16's ends
+constexpr float kHighest = 8.0f;       // a weight may grow to 2^8 times its reference's: room for sums of large values
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 

@@ -6,14 +6,14 @@
 // P x V, so a row's weights need no other row. Scores are taken of the cache's
 // codes as they are, queries split into e4m3 hi + e5m2 lo, two products into one
 // accumulator: together they hold the 8 significant bits of a BF16 query exactly
-// down to 2^-16 of its row's largest magnitude. Weights must keep their precision
-// however small they are (kv_attend.cu says why), so they are two BF16 numbers,
-// hi + lo, 16 bits at every magnitude, and two products again. They go back into
-// TMEM, in the place of the scores that they come from, and are read from there:
-// shared memory has no room for them. For that the values are widened to BF16,
-// code times page scale, which is exact. A row's weights are held against a
-// reference that has room for 2^64 times its weight; what outgrows it raises it,
-// and the weights and outputs so far follow.
+// down to 2^-13 of its row's largest magnitude, and what is smaller within 2^-21
+// of that. Weights must keep their precision however small they are (kv_attend.cu
+// says why), so they are two BF16 numbers, hi + lo, 16 bits at every magnitude,
+// and two products again. They go back into TMEM, in the place of the scores that
+// they come from, and are read from there: shared memory has no room for them.
+// For that the values are widened to BF16, code times page scale, which is exact.
+// A row's weights are held against a reference; one that outgrows it by 2^8
+// raises it, and the weights and outputs so far follow.
 //
 // Two groups take a CTA's tiles in turn, one in its softmax while the other's
 // products run; in a group two warpgroups share the rows, each with half of the

@@ -1071,6 +1071,53 @@ def test_append_and_attend_head_major_rows(moe, rows, q_heads, dim):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attend_large_values_under_growing_scores(moe, dim, rows, q_heads):
+    """Values of 2^110 whose scores grow by 60 over the context: no sum of theirs leaves FP32."""
+    rng = np.random.default_rng(dim + rows)
+    n, page = 700, 32
+    cache, table, start, seq = make_batch(rng, [(n, rows)], page, 1, dim)
+    k, _, ks, vs = cache
+    vs[:], ks[:] = 231, 127  # codes of about 60 times 2^104
+    for t in range(n):
+        k[table[0, t // page], 0, t % page] = e4m3_encode(rng.standard_normal(dim))
+        k[table[0, t // page], 0, t % page, 0] = e4m3_encode(np.array([448.0 * t / n]))[0]
+    q = rng.standard_normal((rows, q_heads, dim))
+    q[..., 0] = 16
+    q = bf16(q)
+    scale = 60 / (16 * 448)
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq, scale=scale)
+    want, want_lse, mass = request_reference(cache, q.float().numpy(), table, n, scale)
+    assert (np.abs(lse - want_lse) <= 64 * 60 * U).all()
+    assert (np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + 2 * mass)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,q_heads", TILES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("outlier", [2.0 ** 6, 2.0 ** 13])
+def test_attend_queries_with_an_outlier(moe, outlier, dim, rows, q_heads):
+    """One element far above a query row's others, where the keys are 0: the others keep 2^-21 of it, so a score is within
+    2^-21 outlier scale sum_d |k_d| of its own, a weight within twice that, and the outputs follow."""
+    rng = np.random.default_rng(dim + rows)
+    n = 300
+    cache, table, start, seq = make_batch(rng, [(n, rows)], 32, 1, dim)
+    k, _, ks, _ = cache
+    k[..., 0] = 0
+    q = rng.standard_normal((rows, q_heads, dim))
+    q[..., 0] = outlier * 1.5
+    q = bf16(q)
+    out, lse = run_attend(moe, cache, q.cuda(), table, start, seq)
+    want, want_lse, mass = request_reference(cache, q.float().numpy(), table, n, dim ** -0.5)
+    used = table[0, : -(-n // 32)]
+    keys = np.nan_to_num(np.abs(VALUES[k[used]])) * 2.0 ** (ks[used].astype(np.float64) - 127)[..., None, None]
+    held = 2.0 ** -21 * 1.5 * outlier * dim ** -0.5 * keys.sum(-1).max()
+    assert (np.abs(lse - want_lse) <= 2e-5 + held).all()
+    assert (np.abs(out - want) <= (2.0 ** -8 + 2 * held) * (np.abs(want) + 2 * mass)).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,q_heads,dim", [(1, 8, 128), (5, 24, 64), (200, 8, 128), (64, 16, 64), (9, 16, 256)])
 def test_attend_gives_the_same_bits_each_time(moe, rows, q_heads, dim):
     """Work split over many CTAs and joined by whichever comes last: the order of the sums does not depend on it."""
