@@ -8,7 +8,7 @@
 // anything but the sums, which every CTA takes for itself.
 //
 // Latency bounds it: 64 requests with a token each take 2.7 us, about a launch;
-// 1000 requests with 300 thousand new tokens take 5.7 us, where the 3.4 MB
+// 1000 requests with 300 thousand new tokens take 5.9 us, where the 3.4 MB
 // alone would take 0.5 and the sums (four dependent loads and two scans) 3.
 #include "decode.h"
 
@@ -147,7 +147,7 @@ cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream) {
   int shift = 4;
   while ((1 << shift) < a.page_tokens) ++shift;
   // A thread to a request: 256 threads while that is enough (64 requests: 2.7 us, against 3.6 with 1024). Every CTA
-  // takes the sums again, so one to an SM (1000 requests, 300 thousand tokens: 5.7 us; 6.5 with 100 CTAs, 7.0 with 304).
+  // takes the sums again, so one to an SM (1000 requests, 300 thousand tokens: 5.9 us; 6.5 with 100 CTAs, 7.0 with 304).
   const int threads = a.requests <= 256 ? 256 : 1024;
   int grid = (a.tokens + threads - 1) / threads;
   grid = grid < 1 ? 1 : (grid > 152 ? 152 : grid);

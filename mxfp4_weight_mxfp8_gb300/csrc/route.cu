@@ -11,7 +11,7 @@
 // Ids are the formula's bit for bit, so every key is computed as written: expf,
 // a correctly rounded reciprocal or quotient, one addition of the bias. That,
 // not memory, bounds large calls: 16381 tokens of 384 experts with a bias and
-// group limits take 25.3 us (1.08 TB/s; the 27 MB alone would take 4.0), with
+// group limits take 25.6 us (1.07 TB/s; the 27 MB alone would take 4.0), with
 // the schedulers issuing in 70 % of the cycles (about 1340 warp instructions a
 // token, a third of them the 384 sigmoids). One token takes 3.7 us and 64 take
 // 3.4, of which a launch is about 2.5.
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, N <= 12 ? 6 : N <= 16 ? 4 : 
 template <typename T, int N>
 cudaError_t launch_size(const moe_route_t& a, cudaStream_t stream) {
   // Warps that stay over their tokens, so the bias is read once; no more than are resident together (16381 tokens:
-  // 25.3 us, against 27.4 with a warp for every token).
+  // 25.6 us, against 27.4 with a warp for every token).
   const int ctas = (a.tokens + kRouteWarps - 1) / kRouteWarps, resident = kRouteSms * (N <= 12 ? 6 : N <= 16 ? 4 : 3);
   route_kernel<T, N><<<ctas < resident ? ctas : resident, 32 * kRouteWarps, 0, stream>>>(a);
   return cudaGetLastError();
