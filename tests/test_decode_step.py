@@ -884,16 +884,17 @@ def request_reference(cache, q, table, n, scale):
     return out, lse, mass
 
 
+SINKS = [(200, 25, 1.0), (1500, 13, 1.0), (1500, 15, 1.0), (8192, 14, 1.0), (8192, 40, 1.0)]
+LONG_SINKS = [(131071, 13, 1.0), (131071, 15, 0.5)]  # in the narrowest tile and in the 128-row form
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,q_heads", TILES)
-@pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("n,gap,deviation", [(200, 25, 1.0), (1500, 13, 1.0), (1500, 15, 1.0), (8192, 14, 1.0), (8192, 40, 1.0),
-                                             (131071, 13, 1.0), (131071, 15, 0.5)])
+@pytest.mark.parametrize("n,gap,deviation,dim,rows,q_heads",
+                         [(*s, d, *t) for s in SINKS for d in (64, 128, 256) for t in TILES]
+                         + [(*s, d, *t) for s in LONG_SINKS for d in (64, 128) for t in (TILES[0], TILES[-1])])
 def test_attend_small_weights_under_a_dominant_token_without_value(moe, n, gap, deviation, dim, rows, q_heads):
     """A first token takes most of every row's weight and has value 0: the output is the others' alone, whose weights lie
     `gap` nats below. They count with their own precision, not with the dominant weight's: check_attend's bounds."""
-    if n > 10000 and (dim == 256 or rows * q_heads not in (8, 128)):
-        pytest.skip("the longest contexts in the narrowest tile and in the 128-row form")
     rng = np.random.default_rng(n + gap)
     page = 64
     pages = -(-n // page)
