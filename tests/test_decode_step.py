@@ -558,6 +558,18 @@ def test_plan_steps_lengths_in_place(moe, requests, most):
         assert out["counts"].tolist() == [int(query.sum()), head, int((context + query).max()), 0]
 
 
+@pytest.mark.gpu
+def test_plan_empty_tensors_overlap_nothing(moe):
+    """Views of no elements that point into another tensor: no new tokens, no free pages."""
+    buf = torch.tensor([5, 0, 0, 7], dtype=torch.int32, device="cuda")
+    context, query, head = buf[:2], buf[1:3], buf[2:3]
+    start, seq, counts = (torch.full((n,), 9, dtype=torch.int32, device="cuda") for n in (3, 2, 4))
+    table = torch.full((2, 1), 3, dtype=torch.int32, device="cuda")
+    moe.moe_kv_plan(context, query, 16, table, buf[1:1], head, start, seq, buf[1:1], torch.empty(0, dtype=torch.int64, device="cuda"),
+                    counts)
+    assert start.tolist() == [0, 0, 0] and seq.tolist() == [5, 0] and counts.tolist() == [0, 0, 5, 0] and table.tolist() == [[3], [3]]
+
+
 # ------------------------------------------------------------------- append
 def bf16(a):
     return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(torch.bfloat16)
