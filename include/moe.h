@@ -579,6 +579,224 @@ int moe_kv_sync_status(void* workspace, void* stream);
 int moe_kv_set_timeout(void* workspace, uint64_t nanoseconds, void* stream);
 int moe_kv_debug_withhold(void* workspace, int cta, void* stream);
 
+/*
+ * moe_norm - residual addition and root-mean-square norm of rows, with an
+ * output in `dtype` and one in MXFP8 (either may be null, not both).
+ *   h[t, :] = x[t, :] + residual[t, :]                    (FP32)
+ *   y[t, :] = h * (weight + weight_offset) / sqrt(mean(h^2) + eps)
+ *   residual_out = h in residual_dtype; out = y in dtype
+ *   scales[t, b] = E + 127 with the smallest E >= -127 with max|y| <= 448 * 2^E
+ *   over the block b of 32 elements, codes = e4m3(y * 2^-E)
+ * Each output is rounded once, from FP32, to nearest even; the norm is of the
+ * unrounded h, the codes of the unrounded y. The rule of the scale is that of
+ * moe_quantize. A row with an infinity or a NaN gives what the formula gives:
+ * NaN there, 0 elsewhere under an infinity, NaN everywhere under a NaN (its
+ * codes too; a block's scale is of the numbers in it). Sums of squares past
+ * FP32's range are taken of the scaled row.
+ *   x             device, [tokens, hidden] of dtype, rows x_stride elements apart
+ *   residual      device, [tokens, hidden] of residual_dtype, or null
+ *   residual_out  device, the same type; may be `residual` itself (with its
+ *                 stride), or null. Without a residual it takes x rounded to
+ *                 residual_dtype.
+ *   weight        device, [hidden] of weight_dtype
+ *   out           device, [tokens, hidden] of dtype, rows out_stride apart, or
+ *                 null; may be x itself (with its stride)
+ *   codes, scales device, uint8 [tokens, hidden] and [tokens, hidden / 32]
+ *                 contiguous (codes 8-byte aligned), both or neither
+ * Otherwise no output overlaps an input or another output. 1 <= hidden <=
+ * MOE_MAX_HIDDEN, a multiple of 32 with codes; eps >= 1e-30. Rows that are not
+ * multiples of 16 bytes or not aligned to them are read element by element.
+ */
+typedef struct moe_norm_t {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t residual_stride;
+  void* residual_out;
+  int64_t residual_out_stride;
+  const void* weight;
+  void* out;
+  int64_t out_stride;
+  uint8_t* codes;
+  uint8_t* scales;
+  int dtype, residual_dtype, weight_dtype, tokens, hidden; /* enum moe_dtype */
+  float eps, weight_offset;
+} moe_norm_t;
+
+int moe_norm(const moe_norm_t* norm, void* stream);
+
+/*
+ * moe_norm_quantize - moe_norm whose MXFP8 output is a layer's activation plan:
+ * moe_quantize with the norm before it, from the unrounded y. codes and scales
+ * of `norm` must be null (they are the handle's), hidden the layer's, 1 <=
+ * tokens <= MOE_MAX_BATCH; out may be null. moe_group and moe_experts follow,
+ * with batch = tokens. Asynchronous on `stream`.
+ * Errors: as moe_norm and moe_quantize.
+ */
+int moe_norm_quantize(moe_handle h, const moe_norm_t* norm, void* stream);
+
+#define MOE_ROPE_MAX_DIM 512
+
+/*
+ * moe_rope - queries and keys rotated by their tokens' positions.
+ * Pair i of the first rotary_dim dimensions of a head (elements i and i +
+ * rotary_dim / 2, or 2i and 2i + 1 where `interleaved` is set) turns by the
+ * angle positions[t] * turns[i]:
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin),
+ * in FP32, rounded to BF16 once; the other dimensions are copied as they are.
+ * turns[i] is the pair's angle for one position in units of 2^-64 turns, so the
+ * product modulo 2^64 is the angle, exactly, however far the position.
+ *   positions   device, int32 [tokens] (moe_kv_plan)
+ *   turns       device, uint64 [rotary_dim / 2] (moe_rope_turns)
+ *   q, k        device, BF16 [tokens, heads, head_dim] with token and head
+ *               strides in elements, not negative; k null with k_heads 0
+ *   q_out, k_out  device, the same shapes; q itself and k itself (with their
+ *               strides) for rotating in place, where only the rotated
+ *               dimensions are touched. Otherwise no output overlaps an input
+ *               or the other output, and no output's rows overlap each other.
+ * head_dim up to MOE_ROPE_MAX_DIM, rotary_dim even, 2 .. head_dim; q_heads 1 .. 1024, k_heads
+ * 0 .. 1024. Rows not on 16-byte boundaries, and rotary_dim / 2 not a multiple of
+ * 8, are served element by element.
+ */
+typedef struct moe_rope_t {
+  const int32_t* positions;
+  const uint64_t* turns;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  void* k_out;
+  int64_t k_out_token_stride, k_out_head_stride;
+  int tokens, q_heads, k_heads, head_dim, rotary_dim, interleaved;
+  float amplitude;
+} moe_rope_t;
+
+int moe_rope(const moe_rope_t* rope, void* stream);
+
+/*
+ * moe_rope_turns - the table of moe_rope, on the host (no CUDA call).
+ *   f_i = base^(-2i / rotary_dim) radians a position, then by `scaling`:
+ *   MOE_ROPE_LINEAR: f_i / factor (factor 1: as it is)
+ *   MOE_ROPE_BANDS:  pairs that turn at least `high` times over `trained`
+ *     positions stay, those that turn at most `low` times take f_i / factor,
+ *     those between f_i (s + (1 - s) / factor), s = (turns - low) / (high - low)
+ *   MOE_ROPE_RAMP:   the same, s linear in the pair's index i instead, between the
+ *     indices (rounded up and down to whole ones) of the pairs that turn `low`
+ *     and `high` times
+ *   turns[i] = f_i / (2 pi) * 2^64, rounded, modulo 2^64.
+ * base > 1; factor, trained > 0; 0 < low < high (not looked at by LINEAR).
+ * Writes turns[rotary_dim / 2], host memory.
+ */
+enum moe_rope_scaling { MOE_ROPE_LINEAR = 0, MOE_ROPE_BANDS = 1, MOE_ROPE_RAMP = 2 };
+int moe_rope_turns(int rotary_dim, double base, int scaling, double factor, double trained, double low,
+                   double high, uint64_t* turns);
+
+/* ------------------------------------------------------------------------
+ * Pages that several requests hold. A request's pages are what its row of the
+ * block table names for its length: entries 0 .. ceil(length / page_tokens) - 1.
+ * Rows may name the same pages; nothing counts references. moe_kv_fork makes
+ * rows that go on from others, moe_kv_reclaim finds what no row holds any more
+ * (a request ends when its length is set to 0), moe_kv_copy moves what the two
+ * say has to be moved, once for each layer's cache.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * moe_kv_fork - block-table rows of requests that go on from others' caches:
+ * samples of one prompt, beams, a batch whose rows change places or leave.
+ * Request r goes on from row p = parents[r] (-1: an empty request): it holds p's
+ * length and names p's pages. Full pages are shared. A last page that is not
+ * full stays with the first request that goes on from p; each of the others
+ * takes a page from the free list (free_pages[*free_head], the next one, ...,
+ * in the requests' order), and moves[r] = {p's page, the page taken, the tokens
+ * in it}; moves[r] = {-1, -1, 0} for a request that takes none.
+ *   parents      int32 [requests]
+ *   block_table  int32 [rows, table_width], rows table_stride apart
+ *   seq_lens     int32 [rows]: tokens held (moe_kv_plan's seq_lens)
+ *   out_table    int32 [requests, table_width], rows out_stride apart: written
+ *                whole, -1 behind a request's pages
+ *   out_lens     int32 [requests]
+ *   moves        int32 [requests, 3], for moe_kv_copy
+ *   counts       int32 [4]: moves, the free list's head after this call (as
+ *                moe_kv_plan's), the longest length, and error bits: 1 a parent
+ *                or a length out of range (counted as -1, as 0), 4 a length
+ *                longer than its row (what is past it has no page), 8 free pages
+ *                exhausted (the entries concerned are -1, with no move)
+ * All device memory. No output overlaps an input or another output. requests
+ * and rows <= MOE_KV_MAX_REQUESTS. The same inputs give the same outputs.
+ */
+typedef struct moe_kv_fork_t {
+  const int32_t* parents;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* out_table;
+  int64_t out_stride;
+  int32_t* out_lens;
+  int32_t* moves;
+  int32_t* counts;
+  int rows, requests, page_tokens, table_width, free_count;
+} moe_kv_fork_t;
+
+int moe_kv_fork(const moe_kv_fork_t* fork, void* stream);
+
+/*
+ * moe_kv_copy - pages copied within a cache: for each move {from, to, tokens},
+ * the first `tokens` rows (at most page_tokens) of every head's keys and values
+ * and the page's scales. Moves with a page outside the cache, no tokens or from
+ * == to do nothing.
+ *   moves  device, int32 [capacity, 3]
+ *   count  device, int32 [1]: only the first *count moves are done; null: all
+ * No two moves have the same `to`, and no `to` is another move's `from`.
+ */
+int moe_kv_copy(const moe_kv_cache_t* cache, const int32_t* moves, const int32_t* count, int capacity,
+                void* stream);
+
+/*
+ * moe_kv_reclaim - the free list of a pool of `pages`, from the rows that hold
+ * them; and, with out_table and moves, the pool compacted.
+ *   block_table  int32 [requests, table_width], rows table_stride apart
+ *   seq_lens     int32 [requests]: tokens held; 0: the row holds nothing
+ *   free_pages   int32 [pages]: with n pages held, its last pages - n entries are
+ *                the others in rising order, the first n are not written
+ *   counts       int32 [4]: pages held (n), the free list's head (n: pass its
+ *                address as moe_kv_plan's free_head, `pages` as its free_count),
+ *                moves, and error bits: 1 a negative length (counted as 0), 2 an
+ *                entry held outside the pool (left out), 4 a length longer than
+ *                its row (the row's entries count)
+ *   workspace    MOE_KV_RECLAIM_BYTES(pages), 16-byte aligned, whatever it holds
+ * Compaction (both or neither null): the held pages from n on go to the free ones
+ * before n, both in rising order, so that the pool's first n pages are held.
+ *   out_table    int32 [requests, table_width], rows out_stride apart: the rows
+ *                with the new places, -1 behind a request's pages and for entries
+ *                outside the pool. May be block_table itself (with its stride).
+ *   moves        int32 [max(1, pages / 2), 3]: {from, to, page_tokens}, counts[2]
+ *                of them, for moe_kv_copy with count = &counts[2]; the rest is
+ *                not written
+ * All device memory. Otherwise no output overlaps an input or another output.
+ * requests <= MOE_KV_MAX_REQUESTS, pages <= 2^30. The same inputs give the same
+ * outputs.
+ */
+#define MOE_KV_RECLAIM_BYTES(pages) (1024 + 8 * (size_t)(pages))
+
+typedef struct moe_kv_reclaim_t {
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  int32_t* free_pages;
+  int32_t* counts;
+  int32_t* out_table;
+  int64_t out_stride;
+  int32_t* moves;
+  void* workspace;
+  int requests, page_tokens, table_width, pages;
+} moe_kv_reclaim_t;
+
+int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

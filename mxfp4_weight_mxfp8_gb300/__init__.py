@@ -1,7 +1,9 @@
 """GB300 (sm_103a) MXFP8-activation x MXFP4-weight top-16 MoE decode layer.
 
-Next to the layer: routing (``moe_route``) and the paged 8-bit cache with its
-attention (``moe_kv_plan``, ``moe_kv_append``, ``moe_kv_attend``, ``KvCache``).
+Next to the layer: routing (``moe_route``), norms (``moe_norm``), rotary positions
+(``moe_rope``) and the paged 8-bit cache with its attention (``moe_kv_plan``,
+``moe_kv_append``, ``moe_kv_attend``, ``KvCache``) and the pages that requests
+share (``moe_kv_fork``, ``moe_kv_reclaim``, ``moe_kv_copy``).
 
 A thin ctypes binding over the C ABI declared in ``include/moe.h``: every
 function here only marshals arguments (tensor or array -> pointer, torch
@@ -30,6 +32,8 @@ __all__ = [
     "MAX_BATCH", "moe_device_supported", "moe_small_batch_build", "SMALL_NONE", "SMALL_PACKED", "SMALL_WIDE", "moe_debug_kernel_span", "moe_read_kernel_span",
     "moe_kernel_path", "PATH_GRID", "PATH_SMALL", "PATH_CLUSTER", "PATH_SMALL_WIDE",
     "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "moe_kv_set_timeout", "moe_kv_debug_withhold", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "moe_norm", "moe_norm_quantize", "moe_rope", "moe_rope_turns", "ROPE_LINEAR", "ROPE_BANDS", "ROPE_RAMP",
+    "moe_kv_fork", "moe_kv_reclaim", "moe_kv_reclaim_bytes", "moe_kv_copy",
     "MOE_KV_WORKSPACE_BYTES", "MOE_KV_WORKSPACE_HEADER", "MOE_KV_MAX_REQUESTS",
 ]
 
@@ -68,6 +72,34 @@ class _KvPlan(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("context_lens", "query_lens", "free_pages", "free_head", "block_table")] + [
         ("table_stride", _i64)] + [(n, _vp) for n in ("query_start", "seq_lens", "positions", "slots", "counts")] + [
         (n, _i32) for n in ("requests", "page_tokens", "table_width", "free_count", "tokens")]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_stride", _i64), ("residual", _vp), ("residual_stride", _i64), ("residual_out", _vp),
+                ("residual_out_stride", _i64), ("weight", _vp), ("out", _vp), ("out_stride", _i64), ("codes", _vp),
+                ("scales", _vp)] + [(n, _i32) for n in ("dtype", "residual_dtype", "weight_dtype", "tokens", "hidden")] + [
+                    ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("positions", _vp), ("turns", _vp)] + [
+        (n + s, t) for n in ("q", "q_out", "k", "k_out")
+        for s, t in (("", _vp), ("_token_stride", _i64), ("_head_stride", _i64))] + [
+        (n, _i32) for n in ("tokens", "q_heads", "k_heads", "head_dim", "rotary_dim", "interleaved")] + [
+        ("amplitude", ctypes.c_float)]
+
+
+class _KvFork(ctypes.Structure):
+    _fields_ = [("parents", _vp), ("block_table", _vp), ("table_stride", _i64), ("seq_lens", _vp), ("free_pages", _vp),
+                ("free_head", _vp), ("out_table", _vp), ("out_stride", _i64)] + [
+        (n, _vp) for n in ("out_lens", "moves", "counts")] + [
+        (n, _i32) for n in ("rows", "requests", "page_tokens", "table_width", "free_count")]
+
+
+class _KvReclaim(ctypes.Structure):
+    _fields_ = [("block_table", _vp), ("table_stride", _i64), ("seq_lens", _vp), ("free_pages", _vp), ("counts", _vp),
+                ("out_table", _vp), ("out_stride", _i64), ("moves", _vp), ("workspace", _vp)] + [
+        (n, _i32) for n in ("requests", "page_tokens", "table_width", "pages")]
 
 
 class _KvCache(ctypes.Structure):
@@ -116,6 +148,13 @@ def _load():
         "moe_route": ([ctypes.POINTER(_Route), vp], i32),
         "moe_kv_plan": ([ctypes.POINTER(_KvPlan), vp], i32),
         "moe_kv_append": ([ctypes.POINTER(_KvCache), vp, _i64, _i64, vp, _i64, _i64, vp, i32, vp], i32),
+        "moe_norm": ([ctypes.POINTER(_Norm), vp], i32),
+        "moe_norm_quantize": ([vp, ctypes.POINTER(_Norm), vp], i32),
+        "moe_rope": ([ctypes.POINTER(_Rope), vp], i32),
+        "moe_rope_turns": ([i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + [vp], i32),
+        "moe_kv_fork": ([ctypes.POINTER(_KvFork), vp], i32),
+        "moe_kv_reclaim": ([ctypes.POINTER(_KvReclaim), vp], i32),
+        "moe_kv_copy": ([ctypes.POINTER(_KvCache), vp, vp, i32, vp], i32),
         "moe_kv_sync_status": ([vp, vp], i32),
         "moe_kv_set_timeout": ([vp, u64, vp], i32),
         "moe_kv_debug_withhold": ([vp, i32, vp], i32),
@@ -340,6 +379,8 @@ def _packed(name: str):
 
 
 _route, _plan, _append, _attend = (_packed(n) for n in ("moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend"))
+_norm, _norm_quantize, _rope = (_packed(n) for n in ("moe_norm", "moe_norm_quantize", "moe_rope"))
+_fork, _reclaim, _copy = (_packed(n) for n in ("moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy"))
 _torch = None
 _LOGITS: dict = {}
 
@@ -514,12 +555,185 @@ def _allocating_on(stream):
     return _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+# --- norms, positions, shared pages ------------------------------------------
+_NORM = struct.Struct("PqPqPqPPqPP5i2f0P")
+_ROPE = struct.Struct("PP" + "PqqPqq" * 2 + "6if0P")
+_FORK = struct.Struct("PPqPPPPqPPP5i0P")
+_RECLAIM = struct.Struct("PqPPPPqPP4i")
+
+
+def _matrix(call: str, name: str, t, rows: int, columns: int, device: int):
+    """(address, row stride) of a [rows, columns] tensor with unit stride along its rows."""
+    if t.get_device() == device and t.dim() == 2:
+        shape, (stride, unit) = t.shape, t.stride()
+        if shape[0] == rows and shape[1] == columns and (unit == 1 or columns == 1):
+            return t.data_ptr(), stride if rows > 1 else max(stride, columns)
+    _refuse(call, f"{name} must be a tensor of shape ({rows}, {columns}) on cuda:{device} with unit stride along its rows, "
+                  f"not {tuple(t.shape)} on {t.device}")
+
+
+def _norm_block(call: str, x, weight, out, eps, residual, residual_out, codes, scales, weight_offset, device: int):
+    if x.dim() != 2 or x.dtype not in _LOGITS or weight.dtype not in _LOGITS:
+        _refuse(call, "x must be [tokens, hidden], x and weight float32, bfloat16 or float16")
+    tokens, hidden = x.shape
+    kind = 0
+    for t in (residual, residual_out):
+        if t is not None:
+            kind = _LOGITS.get(t.dtype)
+            if kind is None or (residual is not None and t.dtype is not residual.dtype):
+                _refuse(call, "residual and residual_out must be of one type: float32, bfloat16 or float16")
+    if out is not None and out.dtype is not x.dtype:
+        _refuse(call, "out must be of x's type")
+    none = (0, hidden)
+    return _NORM.pack(
+        *_matrix(call, "x", x, tokens, hidden, device),
+        *(none if residual is None else _matrix(call, "residual", residual, tokens, hidden, device)),
+        *(none if residual_out is None else _matrix(call, "residual_out", residual_out, tokens, hidden, device)),
+        _dense(call, "weight", weight, weight.dtype, (hidden,), device),
+        *(none if out is None else _matrix(call, "out", out, tokens, hidden, device)),
+        0 if codes is None else _dense(call, "codes", codes, _u8t, (tokens, hidden), device),
+        0 if scales is None else _dense(call, "scales", scales, _u8t, (tokens, hidden // 32), device),
+        _LOGITS[x.dtype], kind, _LOGITS[weight.dtype], tokens, hidden, eps, weight_offset)
+
+
+def moe_norm(x, weight, out=None, eps: float = 1e-6, residual=None, residual_out=None, codes=None, scales=None,
+             weight_offset: float = 0.0, stream=None):
+    """Residual addition and root-mean-square norm of x [T, H] into out (x's type) and, in MXFP8, codes (uint8 [T, H])
+    and scales (uint8 [T, H / 32]); x + residual into residual_out. See include/moe.h."""
+    call = "moe_norm"
+    device, stream = _on(call, x, stream)
+    return _check(_norm(_norm_block(call, x, weight, out, eps, residual, residual_out, codes, scales, weight_offset, device),
+                        stream), call)
+
+
+def moe_norm_quantize(handle, x, weight, out=None, eps: float = 1e-6, residual=None, residual_out=None,
+                      weight_offset: float = 0.0, stream=None):
+    """moe_norm whose MXFP8 output is the layer's activation plan (moe_group and moe_experts follow)."""
+    call = "moe_norm_quantize"
+    device, stream = _on(call, x, stream)
+    return _check(_norm_quantize(handle, _norm_block(call, x, weight, out, eps, residual, residual_out, None, None,
+                                                     weight_offset, device), stream), call)
+
+
+ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 0, 1, 2
+
+
+def moe_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_LINEAR, factor: float = 1.0,
+                   trained: float = 8192.0, low: float = 1.0, high: float = 4.0, device=None):
+    """The table of moe_rope: int64 [rotary_dim / 2], angles of one position in units of 2^-64 turns; see include/moe.h."""
+    import torch
+
+    turns = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
+    _check(_lib.moe_rope_turns(rotary_dim, base, scaling, factor, trained, low, high, turns.data_ptr()), "moe_rope_turns")
+    return turns if device is None else turns.to(device)
+
+
+def _heads(call: str, name: str, t, device: int):
+    """(address, token stride, head stride, tokens, heads, dim) of a bfloat16 [tokens, heads, dim] tensor."""
+    if t.dtype is _bf16t and t.get_device() == device and t.dim() == 3:
+        (tokens, heads, dim), (token, head, unit) = t.shape, t.stride()
+        if unit == 1:
+            return t.data_ptr(), token if tokens > 1 else heads * dim, head if heads > 1 else dim, tokens, heads, dim
+    _refuse(call, f"{name} must be a bfloat16 [tokens, heads, dim] tensor on cuda:{device} with unit stride along its last "
+                  f"dimension, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def moe_rope(positions, turns, q, k=None, q_out=None, k_out=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """Rotates q and k (bfloat16 [T, heads, head_dim], any token and head strides) by `positions` into q_out and k_out,
+    or in place; `turns`: moe_rope_turns on the device. See include/moe.h."""
+    call = "moe_rope"
+    device, stream = _on(call, q, stream)
+    *q_in, tokens, heads, dim = _heads(call, "q", q, device)
+    q_to = q_in if q_out is None else _heads(call, "q_out", q_out, device)
+    if q_out is not None and q_out.shape != q.shape:
+        _refuse(call, "q_out must have q's shape")
+    k_in = k_to = (0, 0, 0)
+    k_heads = 0
+    if k is not None:
+        *k_in, k_tokens, k_heads, k_dim = _heads(call, "k", k, device)
+        if k_tokens != tokens or k_dim != dim:
+            _refuse(call, "k must have q's tokens and head_dim")
+        k_to = k_in if k_out is None else _heads(call, "k_out", k_out, device)
+        if k_out is not None and k_out.shape != k.shape:
+            _refuse(call, "k_out must have k's shape")
+    elif k_out is not None:
+        _refuse(call, "k_out without k")
+    pairs = turns.shape[0] if turns.dim() == 1 else 0
+    block = _ROPE.pack(_dense(call, "positions", positions, _i32t, (tokens,), device),
+                       _dense(call, "turns", turns, _i64t, (pairs,), device), *q_in, *q_to[:3], *k_in, *k_to[:3], tokens, heads,
+                       k_heads, dim, 2 * pairs, 1 if interleaved else 0, amplitude)
+    return _check(_rope(block, stream), call)
+
+
+def _moves(call: str, t, least: int, device: int):
+    if t.dim() != 2 or t.shape[1] != 3 or t.shape[0] < least:
+        _refuse(call, f"moves must be [{least} or more, 3]")
+    return _dense(call, "moves", t, _i32t, t.shape, device)
+
+
+def moe_kv_fork(parents, block_table, seq_lens, page_tokens: int, free_pages, free_head, out_table, out_lens, moves, counts,
+                stream=None):
+    """Rows of requests that go on from others' caches, and the moves that moe_kv_copy makes; see include/moe.h."""
+    call = "moe_kv_fork"
+    device, stream = _on(call, parents, stream)
+    requests, rows, free = parents.shape[0], seq_lens.shape[0], free_pages.shape[0]
+    table, table_stride, width = _table(call, block_table, rows, device)
+    out, out_stride, out_width = _table(call, out_table, requests, device)
+    if out_width != width:
+        _refuse(call, "out_table must be as wide as block_table")
+    block = _FORK.pack(_dense(call, "parents", parents, _i32t, (requests,), device), table, table_stride,
+                       _dense(call, "seq_lens", seq_lens, _i32t, (rows,), device),
+                       _dense(call, "free_pages", free_pages, _i32t, (free,), device),
+                       _dense(call, "free_head", free_head, _i32t, (1,), device), out, out_stride,
+                       _dense(call, "out_lens", out_lens, _i32t, (requests,), device),
+                       _dense(call, "moves", moves, _i32t, (requests, 3), device),
+                       _dense(call, "counts", counts, _i32t, (4,), device), rows, requests, page_tokens, width, free)
+    return _check(_fork(block, stream), call)
+
+
+def moe_kv_reclaim(block_table, seq_lens, page_tokens: int, free_pages, counts, workspace, out_table=None, moves=None,
+                   stream=None):
+    """The free list of a pool of free_pages.shape[0] pages; with out_table and moves, the pool compacted. `workspace`:
+    uint8 of moe_kv_reclaim_bytes(pages). See include/moe.h."""
+    call = "moe_kv_reclaim"
+    device, stream = _on(call, block_table, stream)
+    requests, pages = seq_lens.shape[0], free_pages.shape[0]
+    table, table_stride, width = _table(call, block_table, requests, device)
+    out, out_stride, out_width = (0, 0, width) if out_table is None else _table(call, out_table, requests, device)
+    if out_width != width:
+        _refuse(call, "out_table must be as wide as block_table")
+    room = workspace.shape
+    if len(room) != 1 or room[0] < moe_kv_reclaim_bytes(pages):
+        _refuse(call, f"workspace must be {moe_kv_reclaim_bytes(pages)} bytes of uint8")
+    block = _RECLAIM.pack(table, table_stride, _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device),
+                          _dense(call, "free_pages", free_pages, _i32t, (pages,), device),
+                          _dense(call, "counts", counts, _i32t, (4,), device), out, out_stride,
+                          0 if moves is None else _moves(call, moves, max(1, pages // 2), device),
+                          _dense(call, "workspace", workspace, _u8t, room, device), requests, page_tokens, width, pages)
+    return _check(_reclaim(block, stream), call)
+
+
+def moe_kv_reclaim_bytes(pages: int) -> int:
+    """Bytes of moe_kv_reclaim's workspace (MOE_KV_RECLAIM_BYTES)."""
+    return 1024 + 8 * pages
+
+
+def moe_kv_copy(cache, moves, count=None, stream=None):
+    """Copies pages within a cache given as its uint8 tensors (k, v, k_scale, v_scale): moves (int32 [n, 3]: from, to,
+    tokens), the first `count` (int32 [1]) of them or all; see include/moe.h."""
+    call = "moe_kv_copy"
+    device, stream = _on(call, moves, stream)
+    return _check(_copy(_cache_block(call, cache, device)[0], _moves(call, moves, 0, device),
+                        None if count is None else _dense(call, "count", count, _i32t, (1,), device), moves.shape[0], stream), call)
+
+
 class KvCache:
     """A layer's paged cache: its tensors (e4m3 codes, E8M0 scales) and an attention workspace.
 
     ``append(k, v, slots)`` writes a step's keys and values, ``attend(q,
     block_table, query_start, seq_lens)`` returns the BF16 [T, q_heads,
-    head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``), both
+    head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``),
+    ``copy(moves)`` moves pages within it (moe_kv_fork, moe_kv_reclaim), all
     on the current torch stream or on ``stream``, which the outputs are then
     allocated for too (the inputs are the caller's to keep). Layers that run one after the other on one
     stream can share a workspace. ``status()`` synchronizes and returns the
@@ -558,6 +772,9 @@ class KvCache:
         moe_kv_attend(self.tensors, q, block_table, query_start, seq_lens, out, self.workspace, lse, scale, window,
                       stream)
         return (out, lse) if return_lse else out
+
+    def copy(self, moves, count=None, stream=None):
+        moe_kv_copy(self.tensors, moves, count, stream)
 
     def status(self, stream=None) -> int:
         return moe_kv_sync_status(self.workspace, stream)

@@ -31,11 +31,21 @@ struct AttendMaps {
   CUtensorMap k, v;          // [pages * kv_heads][page_tokens][head_dim]; a box is a page's span of a head
 };
 
+cudaError_t launch_norm(const moe_norm_t& a, cudaStream_t stream);
+cudaError_t launch_rope(const moe_rope_t& a, cudaStream_t stream);
 cudaError_t launch_route(const moe_route_t& a, cudaStream_t stream);
 cudaError_t launch_kv_plan(const moe_kv_plan_t& a, cudaStream_t stream);
+cudaError_t launch_kv_fork(const moe_kv_fork_t& a, cudaStream_t stream);
+cudaError_t launch_kv_copy(const moe_kv_cache_t& c, const int32_t* moves, const int32_t* count, int capacity, cudaStream_t stream);
+cudaError_t launch_kv_reclaim(const moe_kv_reclaim_t& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_attend_rows(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
+
+// What moe_norm refuses (null: nothing); `plan`: its codes go to a layer's plan.
+const char* norm_fault(const moe_norm_t* n, bool plan);
+
+const char* rope_fault(const moe_rope_t* r);
 
 // Sets this thread's error detail (moe_last_error_detail) and returns `status`.
 int fail(int status, const char* format, ...);

@@ -12,6 +12,17 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
 }
 
+// A range of an argument's bytes.
+struct Bytes {
+  const void* at;
+  int64_t bytes;
+};
+
+bool overlap(const Bytes& a, const Bytes& b) { return overlap(a.at, a.bytes, b.at, b.bytes); }
+
+// Bytes of a table of int32 rows, from its first row's first to its last row's last.
+int64_t table_bytes(int rows, int64_t stride, int width) { return 4 * ((rows - 1) * stride + width); }
+
 int launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return MOE_OK;
   return moe::fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -66,6 +77,49 @@ int moe_route(const moe_route_t* r, void* stream) {
   return launched(moe::launch_route(*r, static_cast<cudaStream_t>(stream)), "moe_route");
 }
 
+int moe_norm(const moe_norm_t* n, void* stream) {
+  if (const char* fault = moe::norm_fault(n, false)) return refuse(fault);
+  if (n->tokens == 0) return MOE_OK;
+  return launched(moe::launch_norm(*n, static_cast<cudaStream_t>(stream)), "moe_norm");
+}
+
+int moe_rope(const moe_rope_t* r, void* stream) {
+  if (const char* fault = moe::rope_fault(r)) return refuse(fault);
+  if (r->tokens == 0) return MOE_OK;
+  return launched(moe::launch_rope(*r, static_cast<cudaStream_t>(stream)), "moe_rope");
+}
+
+int moe_rope_turns(int rotary_dim, double base, int scaling, double factor, double trained, double low, double high,
+                   uint64_t* turns) {
+  if (turns == nullptr) return refuse("null pointer");
+  if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > MOE_ROPE_MAX_DIM) return refuse("rotary_dim out of range");
+  if (!(base > 1.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor)) return refuse("base or factor out of range");
+  if (scaling != MOE_ROPE_LINEAR && scaling != MOE_ROPE_BANDS && scaling != MOE_ROPE_RAMP) return refuse("scaling");
+  if (scaling != MOE_ROPE_LINEAR && (!(trained > 0.0) || !std::isfinite(trained) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
+    return refuse("trained, low or high out of range");
+  const double tau = 6.283185307179586476925;
+  // The pair that turns n times over the trained length: trained * base^(-2i / rotary_dim) = tau n.
+  const auto index = [&](double n) { return rotary_dim * std::log(trained / (tau * n)) / (2.0 * std::log(base)); };
+  double from = 0.0, to = 1.0;
+  if (scaling == MOE_ROPE_RAMP) {
+    from = std::fmax(std::floor(index(high)), 0.0);
+    to = std::fmin(std::ceil(index(low)), rotary_dim / 2 - 1.0);
+    if (to <= from) to = from + 0.001;  // a step
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rotary_dim), keep = 0.0;
+    if (scaling == MOE_ROPE_BANDS) keep = (trained * f / tau - low) / (high - low);
+    if (scaling == MOE_ROPE_RAMP) keep = 1.0 - (i - from) / (to - from);
+    keep = std::fmin(std::fmax(keep, 0.0), 1.0);
+    f = f * keep + f / factor * (1.0 - keep);
+    double whole;
+    const double turn = std::modf(f / tau, &whole);
+    turns[i] = turn >= 0.5 ? 0 - static_cast<uint64_t>(std::nearbyint(std::ldexp(1.0 - turn, 64)))
+                           : static_cast<uint64_t>(std::nearbyint(std::ldexp(turn, 64)));
+  }
+  return MOE_OK;
+}
+
 int moe_kv_plan(const moe_kv_plan_t* p, void* stream) {
   if (p == nullptr) return refuse("null argument");
   if (p->requests < 1 || p->requests > MOE_KV_MAX_REQUESTS) return refuse("requests out of range");
@@ -92,6 +146,71 @@ int moe_kv_plan(const moe_kv_plan_t* p, void* stream) {
       if (overlap(o.at, o.bytes, i.at, i.bytes) && !(o.at == p->seq_lens && i.at == p->context_lens && p->seq_lens == p->context_lens))
         return refuse("an output overlaps an input (only seq_lens may be context_lens)");
   return launched(moe::launch_kv_plan(*p, static_cast<cudaStream_t>(stream)), "moe_kv_plan");
+}
+
+int moe_kv_fork(const moe_kv_fork_t* f, void* stream) {
+  if (f == nullptr) return refuse("null argument");
+  if (f->requests < 1 || f->requests > MOE_KV_MAX_REQUESTS || f->rows < 1 || f->rows > MOE_KV_MAX_REQUESTS)
+    return refuse("requests or rows out of range");
+  if (!page_size_ok(f->page_tokens)) return refuse("page_tokens must be 16, 32, 64 or 128");
+  if (f->free_count < 0 || f->table_width < 1 || f->table_stride < f->table_width || f->out_stride < f->table_width)
+    return refuse("free_count or table size out of range");
+  if (!f->parents || !f->block_table || !f->seq_lens || !f->free_head || !f->out_table || !f->out_lens || !f->moves || !f->counts ||
+      (f->free_count && !f->free_pages))
+    return refuse("null pointer");
+  const Bytes in[] = {{f->parents, 4ll * f->requests}, {f->block_table, table_bytes(f->rows, f->table_stride, f->table_width)},
+                      {f->seq_lens, 4ll * f->rows}, {f->free_pages, 4ll * f->free_count}, {f->free_head, 4}};
+  const Bytes out[] = {{f->out_table, table_bytes(f->requests, f->out_stride, f->table_width)}, {f->out_lens, 4ll * f->requests},
+                       {f->moves, 12ll * f->requests}, {f->counts, 16}};
+  for (const Bytes& o : out) {
+    if (!aligned(o.at, 4)) return refuse("misaligned pointer");
+    for (const Bytes& i : in)
+      if (overlap(o, i)) return refuse("an output overlaps an input");
+    for (const Bytes& p : out)
+      if (&p != &o && overlap(o, p)) return refuse("two outputs overlap");
+  }
+  for (const Bytes& i : in)
+    if (!aligned(i.at, 4)) return refuse("misaligned pointer");
+  return launched(moe::launch_kv_fork(*f, static_cast<cudaStream_t>(stream)), "moe_kv_fork");
+}
+
+int moe_kv_copy(const moe_kv_cache_t* cache, const int32_t* moves, const int32_t* count, int capacity, void* stream) {
+  if (const char* fault = cache_fault(cache)) return refuse(fault);
+  if (capacity < 0) return refuse("capacity < 0");
+  if (capacity == 0) return MOE_OK;
+  if (!moves) return refuse("null pointer");
+  if (!aligned(moves, 4) || !aligned(count, 4)) return refuse("misaligned pointer");
+  return launched(moe::launch_kv_copy(*cache, moves, count, capacity, static_cast<cudaStream_t>(stream)), "moe_kv_copy");
+}
+
+int moe_kv_reclaim(const moe_kv_reclaim_t* r, void* stream) {
+  if (r == nullptr) return refuse("null argument");
+  if (r->requests < 1 || r->requests > MOE_KV_MAX_REQUESTS) return refuse("requests out of range");
+  if (!page_size_ok(r->page_tokens)) return refuse("page_tokens must be 16, 32, 64 or 128");
+  if (r->pages < 1 || r->pages > 1 << 30) return refuse("pages out of range");
+  if (r->table_width < 1 || r->table_stride < r->table_width) return refuse("table size out of range");
+  if ((r->out_table == nullptr) != (r->moves == nullptr)) return refuse("out_table and moves come together");
+  if (r->out_table && r->out_stride < r->table_width) return refuse("table size out of range");
+  if (!r->block_table || !r->seq_lens || !r->free_pages || !r->counts || !r->workspace) return refuse("null pointer");
+  if (!aligned(r->workspace, 16)) return refuse("misaligned pointer");
+  const int64_t table = table_bytes(r->requests, r->table_stride, r->table_width);
+  const Bytes in[] = {{r->block_table, table}, {r->seq_lens, 4ll * r->requests}};
+  const Bytes out[] = {{r->free_pages, 4ll * r->pages}, {r->counts, 16},
+                       {r->workspace, static_cast<int64_t>(MOE_KV_RECLAIM_BYTES(r->pages))},
+                       {r->moves, r->moves ? 12ll * (r->pages > 1 ? r->pages / 2 : 1) : 0},
+                       {r->out_table, r->out_table ? table_bytes(r->requests, r->out_stride, r->table_width) : 0}};
+  const bool in_place = r->out_table == r->block_table && r->out_stride == r->table_stride;
+  for (const Bytes& o : out) {
+    if (!aligned(o.at, 4)) return refuse("misaligned pointer");
+    for (const Bytes& i : in)
+      if (overlap(o, i) && !(in_place && o.at == r->out_table && i.at == r->block_table))
+        return refuse("an output overlaps an input (only out_table may be block_table)");
+    for (const Bytes& p : out)
+      if (&p != &o && overlap(o, p)) return refuse("two outputs overlap");
+  }
+  for (const Bytes& i : in)
+    if (!aligned(i.at, 4)) return refuse("misaligned pointer");
+  return launched(moe::launch_kv_reclaim(*r, static_cast<cudaStream_t>(stream)), "moe_kv_reclaim");
 }
 
 int moe_kv_append(const moe_kv_cache_t* cache, const void* k, int64_t k_token_stride,

@@ -1,0 +1,335 @@
+// Pages that several requests hold: rows that go on from others, the free list,
+// pages moved (moe_kv_fork, moe_kv_reclaim, moe_kv_copy in include/moe.h).
+//
+// Fork: who takes a page is a prefix sum over the requests, which every CTA
+// takes for itself; the rows are copied a warp to a row. Reclaim: the pages that
+// some row holds are bits of a map; a page's place among the free ones is a
+// count of the bits before it. Copy: bytes.
+#include "decode.h"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+static_assert(MOE_KV_MAX_REQUESTS <= 1024, "a CTA has a thread for every request");
+
+__device__ __forceinline__ int pages_for(int tokens, int shift) {  // (any length up to 2^31 - 1)
+  return static_cast<int>((static_cast<uint32_t>(tokens) + (1u << shift) - 1) >> shift);
+}
+
+// ------------------------------------------------------------------------ fork
+template <int kForkThreads>
+__global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const moe_kv_fork_t a, int shift) {
+  constexpr int kWarps = kForkThreads / 32;
+  __shared__ int s_first[MOE_KV_MAX_REQUESTS];  // [row] the first request that goes on from it
+  __shared__ int s_parent[kForkThreads], s_len[kForkThreads], s_last[kForkThreads];  // [request]; s_last: its last page, where taken
+  __shared__ int s_warp[kWarps], s_longest[kWarps], s_moved[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = 1 << shift;
+  for (int i = tid; i < a.rows; i += kForkThreads) s_first[i] = 0x7FFFFFFF;
+  __syncthreads();
+  int p = -1, len = 0, flags = 0;
+  if (tid < a.requests) {
+    p = a.parents[tid];
+    if (p < -1 || p >= a.rows) {
+      flags |= 1;
+      p = -1;
+    }
+    if (p >= 0) {
+      atomicMin(s_first + p, tid);
+      len = a.seq_lens[p];
+      if (len < 0) {
+        flags |= 1;
+        len = 0;
+      }
+    }
+  }
+  const long long head = *a.free_head;
+  const int needed = pages_for(len, shift);
+  if (needed > a.table_width) flags |= 4;
+  int entry = -1;
+  if (len & (P - 1) && needed <= a.table_width) entry = a.block_table[p * a.table_stride + needed - 1];
+  __syncthreads();
+  const bool wants = entry >= 0 && s_first[p] != tid;
+  const uint32_t votes = __ballot_sync(kAll, wants);
+  if (lane == 0) s_warp[warp] = __popc(votes);
+  __syncthreads();
+  int total = lane < kWarps ? s_warp[lane] : 0, before = lane < warp ? total : 0;
+  total = __reduce_add_sync(kAll, total);
+  before = __reduce_add_sync(kAll, before) + __popc(votes & ((1u << lane) - 1));
+  int page = -1;
+  if (wants) {
+    const long long at = head + before;
+    if (at >= 0 && at < a.free_count) page = a.free_pages[at];
+  }
+  if (tid < a.requests) {
+    s_parent[tid] = p;
+    s_len[tid] = len;
+    s_last[tid] = wants ? page : -2;
+  }
+  const bool moved = wants && page >= 0;
+  if (blockIdx.x == 0) {
+    if (tid < a.requests) {
+      a.out_lens[tid] = len;
+      a.moves[3 * tid] = moved ? entry : -1;
+      a.moves[3 * tid + 1] = moved ? page : -1;
+      a.moves[3 * tid + 2] = moved ? len & (P - 1) : 0;
+    }
+    if (total && (head < 0 || head + total > a.free_count)) flags |= 8;
+    flags = __reduce_or_sync(kAll, flags);
+    const int longest = __reduce_max_sync(kAll, len), count = __popc(__ballot_sync(kAll, moved));
+    if (lane == 0) {
+      s_longest[warp] = longest;
+      s_moved[warp] = count | flags << 16;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int w = lane < kWarps ? s_moved[lane] : 0;
+      const int all = __reduce_add_sync(kAll, w & 0xFFFF), bits = __reduce_or_sync(kAll, w >> 16);
+      const int most = __reduce_max_sync(kAll, lane < kWarps ? s_longest[lane] : 0);
+      if (lane == 0) {
+        a.counts[0] = all;
+        a.counts[1] = static_cast<int>(min(head + total, 0x7FFFFFFFll));
+        a.counts[2] = most;
+        a.counts[3] = bits;
+      }
+    }
+  }
+  __syncthreads();
+
+  // The rows, a warp to 128 entries of one.
+  const int parts = (a.table_width + 127) / 128;
+  const long long units = static_cast<long long>(a.requests) * parts;
+  for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < units; u += static_cast<long long>(gridDim.x) * kWarps) {
+    const int r = static_cast<int>(u / parts), j0 = static_cast<int>(u - static_cast<long long>(r) * parts) * 128 + lane;
+    const int from = s_parent[r], n = pages_for(s_len[r], shift), last = s_last[r];
+    const int32_t* src = a.block_table + from * a.table_stride;
+    int32_t* dst = a.out_table + r * a.out_stride;
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + 32 * i;
+      v[i] = j < a.table_width && j < n ? src[j] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + 32 * i;
+      if (j < a.table_width) dst[j] = j == n - 1 && last != -2 ? last : v[i];
+    }
+  }
+}
+
+// --------------------------------------------------------------------- reclaim
+// Workspace: counts of the marking (error bits), then the map, a bit to a page, then (compaction) the place of each page that
+// leaves among those.
+struct Map {
+  uint32_t* errors;
+  uint32_t* bits;
+  int32_t* leaver;
+  int words;
+  __host__ __device__ explicit Map(const moe_kv_reclaim_t& a)
+      : errors(static_cast<uint32_t*>(a.workspace)), bits(errors + 128), words((a.pages + 31) / 32) {
+    leaver = reinterpret_cast<int32_t*>(bits + (words + 3) / 4 * 4);
+  }
+};
+
+constexpr int kReclaimThreads = 256;
+
+__global__ void __launch_bounds__(kReclaimThreads) kv_clear_kernel(const moe_kv_reclaim_t a) {
+  const Map m(a);
+  for (int i = blockIdx.x * kReclaimThreads + threadIdx.x; i < m.words; i += gridDim.x * kReclaimThreads) m.bits[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *m.errors = 0;
+}
+
+// The entries that a row's length covers.
+__device__ __forceinline__ int held_entries(const moe_kv_reclaim_t& a, int r, int shift, uint32_t& errors) {
+  const int len = a.seq_lens[r];
+  if (len < 0) errors |= 1;
+  const int n = pages_for(max(len, 0), shift);
+  if (n > a.table_width) errors |= 4;
+  return min(n, a.table_width);
+}
+
+__global__ void __launch_bounds__(kReclaimThreads) kv_mark_kernel(const moe_kv_reclaim_t a, int shift) {
+  const Map m(a);
+  uint32_t errors = 0;
+  const int r = blockIdx.y, n = held_entries(a, r, shift, errors);
+  const int32_t* row = a.block_table + r * a.table_stride;
+  for (int j = blockIdx.x * kReclaimThreads + threadIdx.x; j < n; j += gridDim.x * kReclaimThreads) {
+    const int page = row[j];
+    if (page < 0 || page >= a.pages) {
+      errors |= 2;
+      continue;
+    }
+    const uint32_t bit = 1u << (page & 31);
+    if (!(*static_cast<const volatile uint32_t*>(m.bits + (page >> 5)) & bit)) atomicOr(m.bits + (page >> 5), bit);
+  }
+  errors = __reduce_or_sync(kAll, errors);
+  if (errors && (threadIdx.x & 31) == 0) atomicOr(m.errors, errors);
+}
+
+// The sum of x over the CTA, everywhere.
+__device__ __forceinline__ long long block_sum(int x, int* s_part) {
+  x = __reduce_add_sync(kAll, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kReclaimThreads / 32; ++w) sum += s_part[w];
+  return sum;
+}
+
+// Each CTA lists the pages of a run of words: free ones, or what leaves and where it goes.
+template <bool kCompact>
+__global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_reclaim_t a, int shift, int words_per) {
+  __shared__ int s_part[kReclaimThreads / 32], s_scan[kReclaimThreads / 32];
+  const Map m(a);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int begin = blockIdx.x * words_per, end = min(begin + words_per, m.words);
+  int held = 0, before = 0;
+  for (int i = tid; i < m.words; i += kReclaimThreads) {
+    const int c = __popc(m.bits[i]);
+    held += c;
+    before += i < begin ? c : 0;
+  }
+  const int n = static_cast<int>(block_sum(held, s_part));
+  int at = static_cast<int>(block_sum(before, s_part));  // pages held before the CTA's first word
+  int kept = 0;                                          // held pages before page n, which stay
+  if (kCompact) {
+    for (int i = tid; i <= n >> 5 && i < m.words; i += kReclaimThreads)
+      kept += __popc(i < n >> 5 ? m.bits[i] : m.bits[i] & ((1u << (n & 31)) - 1));
+    kept = static_cast<int>(block_sum(kept, s_part));
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.counts[0] = a.counts[1] = n;
+    a.counts[2] = kCompact ? n - kept : 0;
+    a.counts[3] = static_cast<int>(*m.errors);
+  }
+  // Words, a lane to a page.
+  for (int base = begin; base < end; base += kReclaimThreads) {
+    const uint32_t word = base + tid < end ? m.bits[base + tid] : 0;
+    const int own = __popc(word);
+    int in = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kAll, in, d);
+      if (lane >= d) in += u;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = in;
+    __syncthreads();
+    int first = at, total = 0;
+#pragma unroll
+    for (int w = 0; w < kReclaimThreads / 32; ++w) {
+      first += w < warp ? s_scan[w] : 0;
+      total += s_scan[w];
+    }
+    first += in - own;  // held before this thread's word
+    at += total;
+    for (int k = 0; k < 32; ++k) {
+      const int index = base + warp * 32 + k;
+      if (index >= end) break;
+      const uint32_t bits = __shfl_sync(kAll, word, k);
+      const int page = index * 32 + lane, rank = __shfl_sync(kAll, first, k) + __popc(bits & ((1u << lane) - 1));  // held before it
+      const bool mine = bits >> lane & 1;
+      if (page >= a.pages) continue;
+      if (!kCompact) {
+        if (!mine) a.free_pages[n + (page - rank)] = page;
+      } else {
+        if (page >= n) {
+          a.free_pages[page] = page;
+          if (mine) {
+            m.leaver[page] = rank - kept;
+            a.moves[3ll * (rank - kept)] = page;
+          }
+        } else if (!mine) {
+          a.moves[3ll * (page - rank) + 1] = page;
+          a.moves[3ll * (page - rank) + 2] = 1 << shift;
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kReclaimThreads) kv_rename_kernel(const moe_kv_reclaim_t a, int shift) {
+  const Map m(a);
+  uint32_t errors = 0;
+  const int r = blockIdx.y, used = held_entries(a, r, shift, errors), n = a.counts[0];
+  const int32_t* row = a.block_table + r * a.table_stride;
+  int32_t* out = a.out_table + r * a.out_stride;
+  for (int j = blockIdx.x * kReclaimThreads + threadIdx.x; j < a.table_width; j += gridDim.x * kReclaimThreads) {
+    int page = j < used ? row[j] : -1;
+    if (page >= a.pages) page = -1;
+    if (page >= n) page = a.moves[3ll * m.leaver[page] + 1];
+    out[j] = max(page, -1);
+  }
+}
+
+// ------------------------------------------------------------------------ copy
+constexpr int kCopyThreads = 256;
+
+// A unit is a move's keys or values of one head; a CTA takes them in turn.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const moe_kv_cache_t c, const int32_t* moves, const int32_t* count, int capacity) {
+  const int n = count ? min(max(*count, 0), capacity) : capacity;
+  const long long page_bytes = static_cast<long long>(c.kv_heads) * c.page_tokens * c.head_dim;
+  const int head_bytes = c.page_tokens * c.head_dim;
+  for (long long u = blockIdx.x; u < 2ll * n; u += gridDim.x) {
+    const int32_t* move = moves + 3 * (u >> 1);
+    const int from = move[0], to = move[1], tokens = min(move[2], c.page_tokens);
+    if (from < 0 || to < 0 || from >= c.pages || to >= c.pages || from == to || tokens <= 0) continue;
+    uint8_t* data = u & 1 ? c.v : c.k;
+    uint8_t* scales = u & 1 ? c.v_scale : c.k_scale;
+    const uint4* src = reinterpret_cast<const uint4*>(data + from * page_bytes);
+    uint4* dst = reinterpret_cast<uint4*>(data + to * page_bytes);
+    const int words = tokens * c.head_dim / 16, stride = head_bytes / 16, all = words * c.kv_heads;
+    for (int i = threadIdx.x; i < all; i += kCopyThreads) {
+      const int h = i / words, w = h * stride + i - h * words;
+      dst[w] = src[w];
+    }
+    for (int h = threadIdx.x; h < c.kv_heads; h += kCopyThreads)
+      scales[static_cast<long long>(to) * c.kv_heads + h] = scales[static_cast<long long>(from) * c.kv_heads + h];
+  }
+}
+
+int shift_of(int page_tokens) {
+  int shift = 4;
+  while ((1 << shift) < page_tokens) ++shift;
+  return shift;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const moe_kv_fork_t& a, cudaStream_t stream) {
+  const int threads = a.requests <= 256 ? 256 : 1024;
+  const long long warps = static_cast<long long>(a.requests) * ((a.table_width + 127) / 128);
+  const long long ctas = (warps + threads / 32 - 1) / (threads / 32);
+  const int grid = static_cast<int>(ctas < 152 ? ctas : 152);
+  if (threads == 256) kv_fork_kernel<256><<<grid, 256, 0, stream>>>(a, shift_of(a.page_tokens));
+  else kv_fork_kernel<1024><<<grid, 1024, 0, stream>>>(a, shift_of(a.page_tokens));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_copy(const moe_kv_cache_t& c, const int32_t* moves, const int32_t* count, int capacity, cudaStream_t stream) {
+  const long long units = 2ll * capacity;
+  kv_copy_kernel<<<static_cast<int>(units < 152 * 8 ? units : 152 * 8), kCopyThreads, 0, stream>>>(c, moves, count, capacity);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_reclaim(const moe_kv_reclaim_t& a, cudaStream_t stream) {
+  const int shift = shift_of(a.page_tokens), words = (a.pages + 31) / 32;
+  const auto least = [](int x, int y) { return x < y ? x : y; };
+  kv_clear_kernel<<<least((words + kReclaimThreads - 1) / kReclaimThreads, 152), kReclaimThreads, 0, stream>>>(a);
+  const dim3 rows(least((a.table_width + kReclaimThreads - 1) / kReclaimThreads, 8), a.requests);
+  kv_mark_kernel<<<rows, kReclaimThreads, 0, stream>>>(a, shift);
+  const int ctas = least((words + 31) / 32, 152), words_per = (words + ctas - 1) / ctas, grid = (words + words_per - 1) / words_per;
+  if (a.out_table == nullptr) {
+    kv_list_kernel<false><<<grid, kReclaimThreads, 0, stream>>>(a, shift, words_per);
+    return cudaGetLastError();
+  }
+  kv_list_kernel<true><<<grid, kReclaimThreads, 0, stream>>>(a, shift, words_per);
+  kv_rename_kernel<<<rows, kReclaimThreads, 0, stream>>>(a, shift);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -514,6 +514,20 @@ int moe_quantize(moe_handle h, const void* x_bf16, int batch, void* stream) {
   return MOE_OK;
 }
 
+int moe_norm_quantize(moe_handle h, const moe_norm_t* norm, void* stream) {
+  if (h == nullptr) return MOE_ERR_ARG;
+  if (const char* fault = moe::norm_fault(norm, true)) return moe::fail(MOE_ERR_ARG, "%s", fault);
+  if (norm->hidden != h->g.H || check_batch(norm->tokens)) return moe::fail(MOE_ERR_ARG, "hidden or tokens not the layer's");
+  MOE_CHECK_DEVICE(h);
+  moe_norm_t n = *norm;
+  n.codes = h->plan_codes;
+  n.scales = h->plan_scales;
+  note_launch(h, static_cast<cudaStream_t>(stream));
+  MOE_CUDA(moe::launch_norm(n, static_cast<cudaStream_t>(stream)));
+  h->plan_batch = norm->tokens;
+  return MOE_OK;
+}
+
 int moe_group(moe_handle h, const int32_t* topk_ids, int batch, void* stream) {
   if (h == nullptr || topk_ids == nullptr || !aligned16(topk_ids) || check_batch(batch))
     return MOE_ERR_ARG;
