@@ -469,9 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float high = highest(v);
           if (__any_sync(kAll, high > kHighest)) {
-            // A weight outgrows the reference, which is raised; the tile's weights so far, which lie over their scores, follow.
+            // A weight outgrows the reference, which is raised, by a whole number: the tile's weights so far, which lie over
+            // their scores in BF16, follow by a power of two, so that they lose nothing.
             tmem_wait_16(others);
-            const float up = high > kHighest ? high : 0.0f, keep = exp2_fast(-up);
+            const float up = high > kHighest ? ceilf(high) : 0.0f, keep = exp2_fast(-up);
             scale_weights(s_at, c / 16, keep);
             part *= keep;
             raised += up;
