@@ -797,6 +797,44 @@ typedef struct moe_kv_reclaim_t {
 
 int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
 
+/*
+ * moe_kv_attend_shared - moe_kv_attend (without a window) for requests in groups
+ * that share a prefix: the pages of a group's prefix are read once for all of its
+ * requests, as one piece of attention with all their queries, and joined with
+ * what each request holds behind it. The results are moe_kv_attend's but for the
+ * order of the sums.
+ *   group_start  int32 [groups + 1]: group g is the requests group_start[g] ..
+ *                group_start[g + 1] - 1; the first is 0, the last requests
+ *   prefix_lens  int32 [groups]: tokens of the group's prefix. The block-table
+ *                rows of a group's requests name the same pages for them (the
+ *                first prefix_len / page_tokens entries, rounded down), as
+ *                moe_kv_fork leaves them; the page where the prefix ends inside
+ *                may be each request's own.
+ * Both device memory. Shared are the whole pages that every query of the group
+ * sees: prefix_len is held to the group's shortest cached context. Requests
+ * without queries take no part (their rows may hold anything), a prefix that one
+ * request reads, a length of 0 or below, and groups that do not cover the
+ * requests in order share nothing, and the call is moe_kv_attend's then.
+ *   scratch  device, moe_kv_shared_bytes(tokens, q_heads, head_dim) bytes, 16-byte
+ *            aligned, whatever they hold; the call's own while it runs
+ * Everything else as for moe_kv_attend, the workspace and its status too.
+ * 1 <= groups <= requests.
+ * moe_kv_shared_bytes: 0 for arguments that the call refuses.
+ */
+#define MOE_KV_SHARED_HEADER 65536
+
+typedef struct moe_kv_prefixes_t {
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int groups;
+} moe_kv_prefixes_t;
+
+size_t moe_kv_shared_bytes(int tokens, int q_heads, int head_dim);
+int moe_kv_attend_shared(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch,
+                         const moe_kv_prefixes_t* prefixes, const void* q, int64_t q_token_stride,
+                         int64_t q_head_stride, int q_heads, float scale, void* out, float* lse,
+                         void* workspace, void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

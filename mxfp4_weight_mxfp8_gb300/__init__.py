@@ -34,6 +34,7 @@ __all__ = [
     "moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend", "moe_kv_sync_status", "moe_kv_set_timeout", "moe_kv_debug_withhold", "KvCache", "SCORE_SOFTMAX", "SCORE_SIGMOID",
     "moe_norm", "moe_norm_quantize", "moe_rope", "moe_rope_turns", "ROPE_LINEAR", "ROPE_BANDS", "ROPE_RAMP",
     "moe_kv_fork", "moe_kv_reclaim", "moe_kv_reclaim_bytes", "moe_kv_copy",
+    "moe_kv_attend_shared", "moe_kv_shared_bytes", "MOE_KV_SHARED_HEADER",
     "MOE_KV_WORKSPACE_BYTES", "MOE_KV_WORKSPACE_HEADER", "MOE_KV_MAX_REQUESTS",
 ]
 
@@ -45,6 +46,7 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 MOE_KV_WORKSPACE_BYTES = 32 << 20  # workspace of moe_kv_attend
 MOE_KV_WORKSPACE_HEADER = 8192  # its bytes that must start as zero
 MOE_KV_MAX_REQUESTS = 1024
+MOE_KV_SHARED_HEADER = 65536  # moe_kv_attend_shared's scratch in front of the rows' outputs
 
 
 class MoeInfo(ctypes.Structure):
@@ -87,6 +89,10 @@ class _Rope(ctypes.Structure):
         for s, t in (("", _vp), ("_token_stride", _i64), ("_head_stride", _i64))] + [
         (n, _i32) for n in ("tokens", "q_heads", "k_heads", "head_dim", "rotary_dim", "interleaved")] + [
         ("amplitude", ctypes.c_float)]
+
+
+class _KvPrefixes(ctypes.Structure):
+    _fields_ = [("group_start", _vp), ("prefix_lens", _vp), ("groups", _i32)]
 
 
 class _KvFork(ctypes.Structure):
@@ -148,6 +154,9 @@ def _load():
         "moe_route": ([ctypes.POINTER(_Route), vp], i32),
         "moe_kv_plan": ([ctypes.POINTER(_KvPlan), vp], i32),
         "moe_kv_append": ([ctypes.POINTER(_KvCache), vp, _i64, _i64, vp, _i64, _i64, vp, i32, vp], i32),
+        "moe_kv_shared_bytes": ([i32, i32, i32], ctypes.c_size_t),
+        "moe_kv_attend_shared": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), ctypes.POINTER(_KvPrefixes), vp, _i64, _i64,
+                                  i32, ctypes.c_float, vp, vp, vp, vp, vp], i32),
         "moe_norm": ([ctypes.POINTER(_Norm), vp], i32),
         "moe_norm_quantize": ([vp, ctypes.POINTER(_Norm), vp], i32),
         "moe_rope": ([ctypes.POINTER(_Rope), vp], i32),
@@ -381,6 +390,7 @@ def _packed(name: str):
 _route, _plan, _append, _attend = (_packed(n) for n in ("moe_route", "moe_kv_plan", "moe_kv_append", "moe_kv_attend"))
 _norm, _norm_quantize, _rope = (_packed(n) for n in ("moe_norm", "moe_norm_quantize", "moe_rope"))
 _fork, _reclaim, _copy = (_packed(n) for n in ("moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy"))
+_attend_shared = _packed("moe_kv_attend_shared")
 _torch = None
 _LOGITS: dict = {}
 
@@ -507,30 +517,59 @@ def moe_kv_append(cache, k, v, slots, stream=None):
                           _dense(call, "slots", slots, _i64t, (tokens,), device), tokens, stream), call)
 
 
-def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, lse=None, scale=None, window: int = 0,
-                  stream=None):
-    """Causal attention of q (bfloat16 [T, q_heads, head_dim]) over the cache, into out and lse (float32 [T, q_heads]);
-    scale None: head_dim ** -0.5. `workspace`: MOE_KV_WORKSPACE_BYTES of zeroed uint8; see include/moe.h."""
-    call = "moe_kv_attend"
-    device, stream = _on(call, q, stream)
+def _attend_args(call: str, cache, q, block_table, query_start, seq_lens, workspace, device: int):
+    """(cache block, batch block, q's address and strides, tokens, heads, dim) of an attend call; the workspace checked."""
     block, _, dim = _cache_block(call, cache, device)
     requests = seq_lens.shape[0]
     table, table_stride, width = _table(call, block_table, requests, device)
     if q.dim() != 3:
         _refuse(call, "q must be [tokens, q_heads, head_dim]")
     tokens, heads, _ = q.shape
-    shape = (tokens, heads, dim)
     batch = _BATCH.pack(table, table_stride, _dense(call, "query_start", query_start, _i32t, (requests + 1,), device),
                         _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device), width, requests, tokens)
-    if not 0 <= window < 1 << 31:  # (ctypes would take it modulo 2^32)
-        _refuse(call, "window must be 0 or a number of tokens below 2^31")
     room = workspace.shape
     if len(room) != 1 or room[0] < MOE_KV_WORKSPACE_BYTES:
         _refuse(call, f"workspace must be {MOE_KV_WORKSPACE_BYTES} bytes of uint8")
-    return _check(_attend(block, batch, *_rows(call, "q", q, _bf16t, shape, device), heads,
-                          dim ** -0.5 if scale is None else scale, window, _dense(call, "out", out, _bf16t, shape, device),
+    return block, batch, _rows(call, "q", q, _bf16t, (tokens, heads, dim), device), tokens, heads, dim
+
+
+def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, lse=None, scale=None, window: int = 0,
+                  stream=None):
+    """Causal attention of q (bfloat16 [T, q_heads, head_dim]) over the cache, into out and lse (float32 [T, q_heads]);
+    scale None: head_dim ** -0.5. `workspace`: MOE_KV_WORKSPACE_BYTES of zeroed uint8; see include/moe.h."""
+    call = "moe_kv_attend"
+    device, stream = _on(call, q, stream)
+    if not 0 <= window < 1 << 31:  # (ctypes would take it modulo 2^32)
+        _refuse(call, "window must be 0 or a number of tokens below 2^31")
+    block, batch, rows, tokens, heads, dim = _attend_args(call, cache, q, block_table, query_start, seq_lens, workspace, device)
+    return _check(_attend(block, batch, *rows, heads, dim ** -0.5 if scale is None else scale, window,
+                          _dense(call, "out", out, _bf16t, q.shape, device),
                           None if lse is None else _dense(call, "lse", lse, _f32t, (tokens, heads), device),
-                          _dense(call, "workspace", workspace, _u8t, room, device), stream), call)
+                          _dense(call, "workspace", workspace, _u8t, workspace.shape, device), stream), call)
+
+
+def moe_kv_shared_bytes(tokens: int, q_heads: int, head_dim: int) -> int:
+    """Bytes of moe_kv_attend_shared's scratch."""
+    return _lib.moe_kv_shared_bytes(tokens, q_heads, head_dim)
+
+
+def moe_kv_attend_shared(cache, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, workspace, scratch,
+                         lse=None, scale=None, stream=None):
+    """moe_kv_attend for requests in groups that share a prefix, whose pages are read once: group_start (int32 [G + 1]),
+    prefix_lens (int32 [G]). `scratch`: uint8 of moe_kv_shared_bytes(T, q_heads, head_dim); see include/moe.h."""
+    call = "moe_kv_attend_shared"
+    device, stream = _on(call, q, stream)
+    block, batch, rows, tokens, heads, dim = _attend_args(call, cache, q, block_table, query_start, seq_lens, workspace, device)
+    groups, room = prefix_lens.shape[0], scratch.shape
+    if len(room) != 1 or room[0] < MOE_KV_SHARED_HEADER + 4 * tokens * heads * (dim + 1):
+        _refuse(call, f"scratch must be {moe_kv_shared_bytes(tokens, heads, dim)} bytes of uint8")
+    prefixes = _PREFIXES.pack(_dense(call, "group_start", group_start, _i32t, (groups + 1,), device),
+                              _dense(call, "prefix_lens", prefix_lens, _i32t, (groups,), device), groups)
+    return _check(_attend_shared(block, batch, prefixes, *rows, heads, dim ** -0.5 if scale is None else scale,
+                                 _dense(call, "out", out, _bf16t, q.shape, device),
+                                 None if lse is None else _dense(call, "lse", lse, _f32t, (tokens, heads), device),
+                                 _dense(call, "workspace", workspace, _u8t, workspace.shape, device),
+                                 _dense(call, "scratch", scratch, _u8t, room, device), stream), call)
 
 
 def moe_kv_sync_status(workspace, stream=None) -> int:
@@ -559,6 +598,7 @@ def _allocating_on(stream):
 _NORM = struct.Struct("PqPqPqPPqPP5i2f0P")
 _ROPE = struct.Struct("PP" + "PqqPqq" * 2 + "6if0P")
 _FORK = struct.Struct("PPqPPPPqPPP5i0P")
+_PREFIXES = struct.Struct("PPi0P")
 _RECLAIM = struct.Struct("PqPPPPqPP4i")
 
 
@@ -733,6 +773,7 @@ class KvCache:
     ``append(k, v, slots)`` writes a step's keys and values, ``attend(q,
     block_table, query_start, seq_lens)`` returns the BF16 [T, q_heads,
     head_dim] outputs (and the FP32 log-sum-exp with ``return_lse=True``),
+    ``attend_shared`` does it for groups of requests that share a prefix, and
     ``copy(moves)`` moves pages within it (moe_kv_fork, moe_kv_reclaim), all
     on the current torch stream or on ``stream``, which the outputs are then
     allocated for too (the inputs are the caller's to keep). Layers that run one after the other on one
@@ -771,6 +812,20 @@ class KvCache:
             lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
         moe_kv_attend(self.tensors, q, block_table, query_start, seq_lens, out, self.workspace, lse, scale, window,
                       stream)
+        return (out, lse) if return_lse else out
+
+    def attend_shared(self, q, block_table, query_start, seq_lens, group_start, prefix_lens, out=None, scale=None,
+                      return_lse: bool = False, scratch=None, stream=None):
+        import torch
+
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+            if scratch is None:
+                scratch = torch.empty(moe_kv_shared_bytes(*q.shape), dtype=torch.uint8, device=q.device)
+        moe_kv_attend_shared(self.tensors, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, self.workspace,
+                             scratch, lse, scale, stream)
         return (out, lse) if return_lse else out
 
     def copy(self, moves, count=None, stream=None):

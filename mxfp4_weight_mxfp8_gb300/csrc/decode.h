@@ -25,7 +25,15 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   uint8_t* workspace;
+  // Requests that share prefixes (kv_attend.cuh): the groups' rows of the block table, the pages that each request skips,
+  // and the rows' outputs and (base 2) log-sum-exps over the prefixes.
+  const int32_t* rows;
+  const int32_t* skipped;
+  float* partial;
+  float* partial_lse;
 };
+
+enum AttendMode : int { kWhole = 0, kPrefix = 1, kSuffix = 2 };
 
 struct AttendMaps {
   CUtensorMap k, v;          // [pages * kv_heads][page_tokens][head_dim]; a box is a page's span of a head
@@ -40,7 +48,14 @@ cudaError_t launch_kv_copy(const moe_kv_cache_t& c, const int32_t* moves, const 
 cudaError_t launch_kv_reclaim(const moe_kv_reclaim_t& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_attend_shared(const AttendArgs& a, const moe_kv_prefixes_t& p, void* scratch, cudaStream_t stream);
+// The forms of 8 * tile query rows and of 128, in each mode.
+cudaError_t launch_kv_attend_decode(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
+cudaError_t launch_kv_attend_decode_prefix(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
+cudaError_t launch_kv_attend_decode_suffix(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
 cudaError_t launch_kv_attend_rows(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
+cudaError_t launch_kv_attend_rows_prefix(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
+cudaError_t launch_kv_attend_rows_suffix(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
 
 // What moe_norm refuses (null: nothing); `plan`: its codes go to a layer's plan.
 const char* norm_fault(const moe_norm_t* n, bool plan);

@@ -48,6 +48,37 @@ bool strides_ok(int64_t token, int64_t head) {
   return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0;
 }
 
+// The arguments of an attend call (null: nothing to refuse).
+const char* attend_args(moe::AttendArgs* a, const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, int q_heads, float scale, int window, void* out, float* lse, void* workspace) {
+  if (const char* fault = cache_fault(cache)) return fault;
+  if (batch == nullptr) return "null argument";
+  if (batch->requests < 1 || batch->requests > MOE_KV_MAX_REQUESTS) return "requests out of range";
+  if (batch->tokens < 0 || batch->table_width < 1 || batch->table_stride < batch->table_width) return "tokens or table size out of range";
+  if (q_heads < 1 || q_heads > 1024 || q_heads % cache->kv_heads != 0) return "q_heads must be a multiple of kv_heads, at most 1024";
+  if (!strides_ok(q_token_stride, q_head_stride)) return "strides must be multiples of 8 elements, not negative";
+  if (window < 0) return "window < 0";
+  if (!std::isfinite(scale)) return "scale not finite";
+  if (batch->tokens == 0) return nullptr;
+  if (!batch->block_table || !batch->query_start || !batch->seq_lens || !q || !out || !workspace) return "null pointer";
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(batch->block_table, 4) ||
+      !aligned(batch->query_start, 4) || !aligned(batch->seq_lens, 4))
+    return "misaligned pointer";
+  a->c = *cache;
+  a->b = *batch;
+  a->q = static_cast<const uint16_t*>(q);
+  a->q_token_stride = q_token_stride;
+  a->q_head_stride = q_head_stride;
+  a->q_heads = q_heads;
+  a->group = q_heads / cache->kv_heads;
+  a->window = window;
+  a->scale = scale;
+  a->out = static_cast<uint16_t*>(out);
+  a->lse = lse;
+  a->workspace = static_cast<uint8_t*>(workspace);
+  return nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -239,39 +270,30 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, int64_t k_token_st
 int moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
                   int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
                   int window, void* out, float* lse, void* workspace, void* stream) {
-  if (const char* fault = cache_fault(cache)) return refuse(fault);
-  if (batch == nullptr) return refuse("null argument");
-  if (batch->requests < 1 || batch->requests > MOE_KV_MAX_REQUESTS)
-    return refuse("requests out of range");
-  if (batch->tokens < 0 || batch->table_width < 1 || batch->table_stride < batch->table_width)
-    return refuse("tokens or table size out of range");
-  if (q_heads < 1 || q_heads > 1024 || q_heads % cache->kv_heads != 0)
-    return refuse("q_heads must be a multiple of kv_heads, at most 1024");
-  if (!strides_ok(q_token_stride, q_head_stride))
-    return refuse("strides must be multiples of 8 elements, not negative");
-  if (window < 0) return refuse("window < 0");
-  if (!std::isfinite(scale)) return refuse("scale not finite");
-  if (batch->tokens == 0) return MOE_OK;
-  if (!batch->block_table || !batch->query_start || !batch->seq_lens || !q || !out || !workspace)
-    return refuse("null pointer");
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) ||
-      !aligned(batch->block_table, 4) || !aligned(batch->query_start, 4) ||
-      !aligned(batch->seq_lens, 4))
-    return refuse("misaligned pointer");
   moe::AttendArgs a{};
-  a.c = *cache;
-  a.b = *batch;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_token_stride = q_token_stride;
-  a.q_head_stride = q_head_stride;
-  a.q_heads = q_heads;
-  a.group = q_heads / cache->kv_heads;
-  a.window = window;
-  a.scale = scale;
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.workspace = static_cast<uint8_t*>(workspace);
+  if (const char* fault = attend_args(&a, cache, batch, q, q_token_stride, q_head_stride, q_heads, scale, window, out, lse, workspace))
+    return refuse(fault);
+  if (batch->tokens == 0) return MOE_OK;
   return launched(moe::launch_kv_attend(a, static_cast<cudaStream_t>(stream)), "moe_kv_attend");
+}
+
+size_t moe_kv_shared_bytes(int tokens, int q_heads, int head_dim) {
+  if (tokens < 0 || q_heads < 1 || q_heads > 1024 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
+  return MOE_KV_SHARED_HEADER + 4ull * tokens * q_heads * (head_dim + 1);
+}
+
+int moe_kv_attend_shared(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const moe_kv_prefixes_t* prefixes, const void* q,
+                         int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale, void* out, float* lse,
+                         void* workspace, void* scratch, void* stream) {
+  moe::AttendArgs a{};
+  if (const char* fault = attend_args(&a, cache, batch, q, q_token_stride, q_head_stride, q_heads, scale, 0, out, lse, workspace))
+    return refuse(fault);
+  if (prefixes == nullptr) return refuse("null argument");
+  if (prefixes->groups < 1 || prefixes->groups > batch->requests) return refuse("groups out of range");
+  if (batch->tokens == 0) return MOE_OK;
+  if (!prefixes->group_start || !prefixes->prefix_lens || !scratch) return refuse("null pointer");
+  if (!aligned(prefixes->group_start, 4) || !aligned(prefixes->prefix_lens, 4) || !aligned(scratch, 16)) return refuse("misaligned pointer");
+  return launched(moe::launch_kv_attend_shared(a, *prefixes, scratch, static_cast<cudaStream_t>(stream)), "moe_kv_attend_shared");
 }
 
 int moe_kv_sync_status(void* workspace, void* stream) {

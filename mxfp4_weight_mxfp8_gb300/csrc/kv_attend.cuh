@@ -1,5 +1,5 @@
 // Building blocks of the attention kernels over the paged 8-bit cache
-// (kv_attend.cu, kv_attend_rows.cu): the work split, the tile stream, the
+// (kv_attend_decode.cuh, kv_attend_rows.cuh): the work split, the tile stream, the
 // tensor-core and numeric primitives, the join of an item's pieces. Each
 // translation unit that includes it gets its own copy (internal linkage).
 //
@@ -8,6 +8,13 @@
 // of 128; all tiles in a row, [request][row tile][head][tile], are dealt to the
 // CTAs in equal runs, so a long context is split over many CTAs and short ones
 // share one. Results are sums over pieces in CTA order, whoever adds them.
+//
+// Every part comes in three modes. kWhole: a request's causal attention. For
+// requests that share a prefix, kPrefix: the "requests" are groups of them, the
+// rows those of all of a group's requests, the tokens the prefix, all of which
+// every row sees; the output stays in FP32, with its log-sum-exp. Then kSuffix:
+// a request's tokens from its prefix on (positions count from there), joined with
+// what kPrefix left as with another piece.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -183,8 +190,17 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
+// Where a request's pages are named: its row of the block table, the entry of its first page (kWhole: its own, the first).
+template <int kMode>
+struct Place {
+  int row, page0;
+};
+template <>
+struct Place<kWhole> {};
+
 // A request's share of the work.
-struct Request {
+template <int kMode>
+struct Request : Place<kMode> {
   int first, n, seq;       // first query row's token, query tokens, visible length
   int end;                 // tokens that the table has room for
   int tile0, tiles;        // first tile that some query sees, their number (one at least)
@@ -194,7 +210,18 @@ struct Request {
     first = min(max(a.b.query_start[r], 0), a.b.tokens);
     n = min(max(a.b.query_start[r + 1], first), a.b.tokens) - first;
     seq = a.b.seq_lens[r];
-    const long long room = static_cast<long long>(a.b.table_width) << shift;
+    long long room = static_cast<long long>(a.b.table_width) << shift;
+    if constexpr (kMode == kPrefix) {
+      this->row = a.rows[r];
+      this->page0 = 0;
+      if (seq <= 0) n = 0;
+    }
+    if constexpr (kMode == kSuffix) {
+      this->row = r;
+      this->page0 = a.skipped[r];
+      seq -= this->page0 << shift;
+      room -= static_cast<long long>(this->page0) << shift;
+    }
     end = static_cast<int>(min(static_cast<long long>(max(seq, 0)), room));
     tile0 = a.window > 0 ? static_cast<int>(min(max(0ll, static_cast<long long>(seq) - n - a.window + 1), static_cast<long long>(end))) / kTile : 0;
     tiles = max(1, (end + kTile - 1) / kTile - tile0);
@@ -205,13 +232,15 @@ struct Request {
 
 // The tiles that each row tile of a request sees. In the 128-row form, which prompts take, they are counted exactly: a
 // row tile's 128 rows advance the visible tokens by 128 / group, so row tile j sees the tiles from max(0, low + j) / group
-// to before (high + j) / group. In the decode form, whose row tiles differ by a few tokens, each counts them all.
-template <int kRows>
+// to before (high + j) / group. In the decode form, whose row tiles differ by a few tokens, each counts them all, as
+// each sees them all of a prefix.
+template <int kMode, int kRows>
 struct RowTiles {
+  static constexpr bool kAlike = kRows != kTile || kMode == kPrefix;
   long long low = 0, high = 0;
   int group;
-  __device__ __forceinline__ RowTiles(const AttendArgs& a, const Request& q) : group(a.group) {
-    if constexpr (kRows != kTile) return;
+  __device__ __forceinline__ RowTiles(const AttendArgs& a, const Request<kMode>& q) : group(a.group) {
+    if constexpr (kAlike) return;
     const long long before = max(0, q.seq - q.n);
     high = (before * group + kTile + kTile * group - 1) >> 7;
     low = a.window > 0 ? (before - a.window + 1) * group >> 7 : -(1ll << 40);
@@ -223,29 +252,29 @@ struct RowTiles {
     return n * (n - 1) / 2 * group + n * (x - n * group);
   }
   // The tiles of the row tiles before j (j < row_tiles).
-  __device__ __forceinline__ long long before(const Request& q, int j) const {
-    if constexpr (kRows != kTile) return static_cast<long long>(j) * q.tiles;
+  __device__ __forceinline__ long long before(const Request<kMode>& q, int j) const {
+    if constexpr (kAlike) return static_cast<long long>(j) * q.tiles;
     return sum(high + j) - sum(high) - (sum(low + j) - sum(low));
   }
-  __device__ __forceinline__ int first(const Request& q, int j) const {
-    if constexpr (kRows != kTile) return q.tile0;
+  __device__ __forceinline__ int first(const Request<kMode>& q, int j) const {
+    if constexpr (kAlike) return q.tile0;
     return static_cast<int>(divide(max(0ll, low + j), group));
   }
-  __device__ __forceinline__ int count(const Request& q, int j) const {
-    if constexpr (kRows != kTile) return q.tiles;
+  __device__ __forceinline__ int count(const Request<kMode>& q, int j) const {
+    if constexpr (kAlike) return q.tiles;
     const int from = first(q, j), to = static_cast<int>(divide(high + j, group));
     return max(1, (j + 1 == q.row_tiles ? min(to, q.tile0 + q.tiles) : to) - from);
   }
-  __device__ __forceinline__ long long all(const Request& q) const {
+  __device__ __forceinline__ long long all(const Request<kMode>& q) const {
     return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + count(q, q.row_tiles - 1);
   }
 };
 static_assert(kTile == 128, "RowTiles' shifts");
 
 // A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
-template <int kRows>
+template <int kMode, int kRows>
 struct Segment {
-  Request q;
+  Request<kMode> q;
   int r, head, row_tile;
   int token, within;       // the row tile's first query token, its first row among that token's
   int tile_first, units;   // the item's first tile, from q.tile0 on; its length in the units of the work
@@ -264,6 +293,10 @@ struct Segment {
     first = from == 0;
     begin = tile_first + max(0, from - weight);
     end = tile_first + max(0, to - weight);
+    if constexpr (kMode == kPrefix) {
+      if (begin >= end) begin = end = 0;
+      return;
+    }
     const int before = q.seq - q.n;  // position of the request's first query
     const int last = min(q.n - 1, static_cast<int>((static_cast<long long>(row_tile + 1) * kRows - 1) / a.group));
     end = min(end, (min(q.end, max(0, before + last + 1)) + kTile - 1) / kTile - q.tile0);
@@ -274,7 +307,7 @@ struct Segment {
     if (begin >= end) begin = end = 0;
   }
 
-  __device__ __forceinline__ void take(const RowTiles<kRows>& t) {
+  __device__ __forceinline__ void take(const RowTiles<kMode, kRows>& t) {
     const long long row0 = static_cast<long long>(row_tile) * kRows;
     token = static_cast<int>(divide(row0, t.group));
     within = static_cast<int>(row0 - static_cast<long long>(token) * t.group);
@@ -293,8 +326,8 @@ struct Segment {
       else hi = mid;
     }
     r = lo;
-    q = Request(a, shift, r, kRows);
-    const RowTiles<kRows> t(a, q);
+    q = Request<kMode>(a, shift, r, kRows);
+    const RowTiles<kMode, kRows> t(a, q);
     const long long local = x - prefix[lo];
     lo = 0;
     hi = q.row_tiles;
@@ -318,15 +351,16 @@ struct Segment {
         row_tile = 0;
         do ++r;
         while (prefix[r + 1] == x);  // requests without rows
-        q = Request(a, shift, r, kRows);
+        q = Request<kMode>(a, shift, r, kRows);
       }
-      take(RowTiles<kRows>(a, q));
+      take(RowTiles<kMode, kRows>(a, q));
     }
     cut(a, x, stop, 0);
   }
 };
 
 // What a row tile's rows see: the tokens that any of them sees and those that all see. Rows of later tokens see later ones.
+template <int kMode>
 struct Sight {
   int any_lo, any_hi, all_lo, all_hi;
   int rows;      // of the row tile
@@ -334,9 +368,15 @@ struct Sight {
   int within, window;
   uint32_t inverse;
   template <int kRows>
-  __device__ __forceinline__ Sight(const AttendArgs& a, const Segment<kRows>& s, uint32_t inverse)
+  __device__ __forceinline__ Sight(const AttendArgs& a, const Segment<kMode, kRows>& s, uint32_t inverse)
       : within(s.within), window(a.window), inverse(inverse) {
     rows = static_cast<int>(min(static_cast<long long>(s.q.n - s.token) * a.group - s.within, static_cast<long long>(kRows)));
+    if constexpr (kMode == kPrefix) {
+      any_lo = all_lo = 0;
+      any_hi = all_hi = s.q.seq - 1;
+      mixed = false;
+      return;
+    }
     all_hi = s.q.seq - s.q.n + s.token;
     any_hi = last(rows - 1);
     any_lo = first(all_hi);
@@ -344,7 +384,7 @@ struct Sight {
     mixed = any_lo != all_lo || any_hi != all_hi;
   }
   // The last token that row i sees, and the first that a row with this last one sees.
-  __device__ __forceinline__ int last(int i) const { return all_hi + per_group(within + i, inverse); }
+  __device__ __forceinline__ int last(int i) const { return kMode == kPrefix ? all_hi : all_hi + per_group(within + i, inverse); }
   __device__ __forceinline__ int first(int last) const {  // (in 64 bits: the window may be any, `last` below 0)
     return window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(last) - window + 1)) : 0;
   }
@@ -359,16 +399,16 @@ struct Sight {
 
 // Widens one token's value codes to BF16 rows of 64 dimensions. Values that no row sees are dropped, whatever they hold;
 // what is not finite and only some rows see is taken out and noted for those, in `nans` ([row][kWords]).
-template <int kWords>
+template <int kMode, int kWords>
 struct Widener {
-  const Sight& sight;
+  const Sight<kMode>& sight;
   uint32_t* nans;
   int* any_nans;
   int token;
   bool dropped, careful;
   uint32_t limit;
   __nv_bfloat162 factor;
-  __device__ __forceinline__ Widener(const Sight& sight, uint32_t entry, bool edge, int token, uint32_t* nans, int* any_nans)
+  __device__ __forceinline__ Widener(const Sight<kMode>& sight, uint32_t entry, bool edge, int token, uint32_t* nans, int* any_nans)
       : sight(sight), nans(nans), any_nans(any_nans), token(token) {
     uint32_t scale = (entry >> 8) & 0xFFu;
     limit = finite_limit(scale);
@@ -422,7 +462,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* st
 
 // Prefix sums of the requests' work, by the whole CTA of kThreads threads; returns what an item counts as: nothing
 // while there are no more tiles than CTAs, so that each gets one, else kItemTiles.
-template <int kThreads, int kRows, int kItemTiles>
+template <int kMode, int kThreads, int kRows, int kItemTiles>
 __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long long (*s_sum)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.b.requests + kThreads - 1) / kThreads;
@@ -430,9 +470,9 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r < a.b.requests) {
-      const Request q(a, shift, r, kRows);
+      const Request<kMode> q(a, shift, r, kRows);
       items += q.items(a.c.kv_heads);
-      tiles += RowTiles<kRows>(a, q).all(q) * a.c.kv_heads;
+      tiles += RowTiles<kMode, kRows>(a, q).all(q) * a.c.kv_heads;
     }
   }
   long long tiles_in = tiles, items_in = items;
@@ -463,8 +503,8 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
     const int r = tid * per + i;
     if (r < a.b.requests) {
       prefix[r] = at;
-      const Request q(a, shift, r, kRows);
-      at += (RowTiles<kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
+      const Request<kMode> q(a, shift, r, kRows);
+      at += (RowTiles<kMode, kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
       if (r == a.b.requests - 1) prefix[r + 1] = at;
     }
   }
@@ -475,7 +515,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
 // A producer warp: looks up the pages of the CTA's tiles and streams their keys (kWhich 1), values (2) or both (3)
 // through the ring. With the values go the pages' entries: key scale, value scale << 8, present << 16; and after a
 // tile's, whether every page is there.
-template <class X, int D, int kWhich>
+template <int kMode, class X, int D, int kWhich>
 __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int weight, int shift,
                         long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
   constexpr int kStages = kWhich == 1 ? X::kKeyStages : X::kStages;
@@ -485,10 +525,10 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
   int k = 0;
   bool alive = reinterpret_cast<const volatile Header*>(status)->withhold != static_cast<int>(blockIdx.x) + 1;
-  Segment<X::kRows> s;
+  Segment<kMode, X::kRows> s;
   s.find(a, prefix, weight, shift, start, stop);
   for (long long x = start; alive;) {
-    const Request& q = s.q;
+    const Request<kMode>& q = s.q;
     int page = -1;
     uint32_t entry = 0;
     bool fresh = false;  // a batch whose scales are not read yet
@@ -497,7 +537,10 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
       if (batch == 0) {
         const long long token = static_cast<long long>(q.tile0 + tile) * kTile + (lane << shift);
         page = -1;
-        if (token < q.end && tile + lane / per_tile < s.end) page = a.b.block_table[s.r * a.b.table_stride + (token >> shift)];
+        if (token < q.end && tile + lane / per_tile < s.end) {
+          if constexpr (kMode == kWhole) page = a.b.block_table[s.r * a.b.table_stride + (token >> shift)];
+          else page = a.b.block_table[q.row * a.b.table_stride + q.page0 + (token >> shift)];
+        }
         if (page >= a.c.pages) page = -1;
         fresh = true;
       }
@@ -546,10 +589,23 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   for (int i = max(0, k - kStages); i < k; ++i) wait(full + i % kStages, (i / kStages) & 1, status);
 }
 
+// A row's output and sum against the reference `m`, joined with a finished one: its normalized output and (base 2)
+// log-sum-exp.
+struct Joined {
+  float top, sum, own, other;
+  __device__ __forceinline__ Joined(float m, float l, float lse) : top(fmaxf(m, lse)) {
+    const float ref = top > -INFINITY ? top : 0.0f;
+    own = exp2_fast(m - ref);
+    other = exp2_fast(lse - ref);
+    sum = l * own + other;
+  }
+  __device__ __forceinline__ float operator()(float o, float finished) const { return o * own + finished * other; }
+};
+
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
 // is kBarrier. row_dst: the rows' places among the outputs' rows.
-template <int kRows, int D, int kThreads, int kBarrier>
-__device__ void join_item(const AttendArgs& a, const Segment<kRows>& s, const long long* row_dst, int rows, long long ctas, long long total,
+template <int kMode, int kRows, int D, int kThreads, int kBarrier>
+__device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, const long long* row_dst, int rows, long long ctas, long long total,
                           int tid, int* s_last) {
   constexpr int kPartialFloats = kRows * (D + 2);
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
@@ -645,8 +701,22 @@ __device__ void join_item(const AttendArgs& a, const Segment<kRows>& s, const lo
           continue;
         }
         if (i >= rows) continue;
-        const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
         const int64_t dst = row_dst[i];
+        if constexpr (kMode == kSuffix) {
+          if (s.q.page0 > 0) {
+            const Joined j(top[u], total_l[u], __ldcg(a.partial_lse + dst));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + dst * D + c4));
+            top[u] = j.top;
+            total_l[u] = j.sum;
+            o[u] = make_float4(j(o[u].x, v.x), j(o[u].y, v.y), j(o[u].z, v.z), j(o[u].w, v.w));
+          }
+        }
+        const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
+        if constexpr (kMode == kPrefix) {
+          *reinterpret_cast<float4*>(a.partial + dst * D + c4) = make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
+          if (c4 == 0) a.partial_lse[dst] = total_l[u] == 0.0f ? -INFINITY : top[u] + log2f(total_l[u]);
+          continue;
+        }
         __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv), __floats2bfloat162_rn(o[u].z * inv, o[u].w * inv)};
         *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
         if (a.lse != nullptr && c4 == 0) a.lse[dst] = total_l[u] == 0.0f ? -INFINITY : (top[u] + log2f(total_l[u])) * kLn2;

@@ -1,0 +1,10 @@
+// The decode form of attention over what follows a shared prefix (kv_attend_decode.cuh).
+#include "kv_attend_decode.cuh"
+
+namespace moe {
+
+cudaError_t launch_kv_attend_decode_suffix(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream) {
+  return launch_decode<kSuffix>(a, maps, tile, shift, sms, stream);
+}
+
+}  // namespace moe
