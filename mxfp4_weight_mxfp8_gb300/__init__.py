@@ -7,7 +7,8 @@ share (``moe_kv_fork``, ``moe_kv_reclaim``, ``moe_kv_copy``).
 
 A thin ctypes binding over the C ABI declared in ``include/moe.h``: every
 function here only marshals arguments (tensor or array -> pointer, torch
-stream -> cudaStream_t) and raises ``MoeError`` on a non-zero status. All of
+stream -> cudaStream_t; the smallest operators by ``csrc/tensors.cpp``) and
+raises ``MoeError`` on a non-zero status. All of
 the layer's work runs in the library's CUDA kernels; there is no other path.
 Importing fails loudly when the library has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``).
@@ -16,10 +17,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 
-from .build import LIBRARY
+from .build import LIBRARY, TENSORS
 
 __all__ = [
     "MoeError", "MoeInfo", "MoeLayer", "library", "moe_prepare", "moe_quantize", "moe_group",
@@ -391,21 +394,30 @@ _route, _plan, _append, _attend = (_packed(n) for n in ("moe_route", "moe_kv_pla
 _norm, _norm_quantize, _rope = (_packed(n) for n in ("moe_norm", "moe_norm_quantize", "moe_rope"))
 _fork, _reclaim, _copy = (_packed(n) for n in ("moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy"))
 _attend_shared = _packed("moe_kv_attend_shared")
-_torch = None
+_torch = _native = None
 _LOGITS: dict = {}
 
 
 def _use_torch():
     """torch and the lookups that need it, on the first call."""
-    global _torch, _i32t, _i64t, _f32t, _bf16t, _u8t, _raw_stream
+    global _torch, _i32t, _i64t, _f32t, _bf16t, _u8t, _raw_stream, _native
     import torch
 
+    if not os.path.exists(TENSORS):
+        raise ImportError(f"extension module not built ({TENSORS} missing): run "
+                          "`python -c \"import __graft_entry__ as g; g.build()\"`")
+    loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
+    native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
+    loader.exec_module(native)
+    native.bind(*(ctypes.cast(getattr(_lib, n), _vp).value for n in (
+        "moe_norm", "moe_rope", "moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy", "moe_kv_attend_shared")))
     _i32t, _i64t, _f32t, _bf16t, _u8t = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
     _LOGITS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     # The current stream's handle without building a stream object, where torch has it.
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
-    _torch = torch
+    _torch, _native = torch, native
+    return native
 
 
 def _refuse(call: str, what: str):
@@ -557,6 +569,11 @@ def moe_kv_attend_shared(cache, q, block_table, query_start, seq_lens, group_sta
                          lse=None, scale=None, stream=None):
     """moe_kv_attend for requests in groups that share a prefix, whose pages are read once: group_start (int32 [G + 1]),
     prefix_lens (int32 [G]). `scratch`: uint8 of moe_kv_shared_bytes(T, q_heads, head_dim); see include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).attend_shared(cache, q, block_table, query_start, seq_lens, group_start, prefix_lens,
+                                                       out, workspace, scratch, lse, scale)
+        if code is not None:
+            return _check(code, "moe_kv_attend_shared")
     call = "moe_kv_attend_shared"
     device, stream = _on(call, q, stream)
     block, batch, rows, tokens, heads, dim = _attend_args(call, cache, q, block_table, query_start, seq_lens, workspace, device)
@@ -595,6 +612,8 @@ def _allocating_on(stream):
 
 
 # --- norms, positions, shared pages ------------------------------------------
+# On the current stream these go by _native (csrc/tensors.cpp), which answers None for arguments that it does not take;
+# then, and on a given stream, by the checks here.
 _NORM = struct.Struct("PqPqPqPPqPP5i2f0P")
 _ROPE = struct.Struct("PP" + "PqqPqq" * 2 + "6if0P")
 _FORK = struct.Struct("PPqPPPPqPPP5i0P")
@@ -640,6 +659,10 @@ def moe_norm(x, weight, out=None, eps: float = 1e-6, residual=None, residual_out
              weight_offset: float = 0.0, stream=None):
     """Residual addition and root-mean-square norm of x [T, H] into out (x's type) and, in MXFP8, codes (uint8 [T, H])
     and scales (uint8 [T, H / 32]); x + residual into residual_out. See include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).norm(x, weight, out, eps, residual, residual_out, codes, scales, weight_offset)
+        if code is not None:
+            return _check(code, "moe_norm")
     call = "moe_norm"
     device, stream = _on(call, x, stream)
     return _check(_norm(_norm_block(call, x, weight, out, eps, residual, residual_out, codes, scales, weight_offset, device),
@@ -681,6 +704,10 @@ def _heads(call: str, name: str, t, device: int):
 def moe_rope(positions, turns, q, k=None, q_out=None, k_out=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
     """Rotates q and k (bfloat16 [T, heads, head_dim], any token and head strides) by `positions` into q_out and k_out,
     or in place; `turns`: moe_rope_turns on the device. See include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).rope(positions, turns, q, k, q_out, k_out, interleaved, amplitude)
+        if code is not None:
+            return _check(code, "moe_rope")
     call = "moe_rope"
     device, stream = _on(call, q, stream)
     *q_in, tokens, heads, dim = _heads(call, "q", q, device)
@@ -714,6 +741,10 @@ def _moves(call: str, t, least: int, device: int):
 def moe_kv_fork(parents, block_table, seq_lens, page_tokens: int, free_pages, free_head, out_table, out_lens, moves, counts,
                 stream=None):
     """Rows of requests that go on from others' caches, and the moves that moe_kv_copy makes; see include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).fork(parents, block_table, seq_lens, page_tokens, free_pages, free_head, out_table, out_lens, moves, counts)
+        if code is not None:
+            return _check(code, "moe_kv_fork")
     call = "moe_kv_fork"
     device, stream = _on(call, parents, stream)
     requests, rows, free = parents.shape[0], seq_lens.shape[0], free_pages.shape[0]
@@ -735,6 +766,10 @@ def moe_kv_reclaim(block_table, seq_lens, page_tokens: int, free_pages, counts, 
                    stream=None):
     """The free list of a pool of free_pages.shape[0] pages; with out_table and moves, the pool compacted. `workspace`:
     uint8 of moe_kv_reclaim_bytes(pages). See include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).reclaim(block_table, seq_lens, page_tokens, free_pages, counts, workspace, out_table, moves)
+        if code is not None:
+            return _check(code, "moe_kv_reclaim")
     call = "moe_kv_reclaim"
     device, stream = _on(call, block_table, stream)
     requests, pages = seq_lens.shape[0], free_pages.shape[0]
@@ -761,6 +796,10 @@ def moe_kv_reclaim_bytes(pages: int) -> int:
 def moe_kv_copy(cache, moves, count=None, stream=None):
     """Copies pages within a cache given as its uint8 tensors (k, v, k_scale, v_scale): moves (int32 [n, 3]: from, to,
     tokens), the first `count` (int32 [1]) of them or all; see include/moe.h."""
+    if stream is None:
+        code = (_native or _use_torch()).copy(cache, moves, count)
+        if code is not None:
+            return _check(code, "moe_kv_copy")
     call = "moe_kv_copy"
     device, stream = _on(call, moves, stream)
     return _check(_copy(_cache_block(call, cache, device)[0], _moves(call, moves, 0, device),

@@ -2,14 +2,18 @@
 
 Every translation unit is compiled in parallel with one -gencode
 (compute_103a / sm_103a) and linked into a shared library with the static
-CUDA runtime; nothing is installed outside this folder.
+CUDA runtime. csrc/tensors.cpp, the Python side's fast way from torch tensors
+to the library's calls, becomes an extension module beside it; nothing is
+installed outside this folder.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 # with -DMOE_TRACE); MOE_LIBRARY makes the binding load a given build.
 BUILD = os.environ.get("MOE_BUILD_DIR", os.path.join(HERE, "_build"))
 LIBRARY = os.environ.get("MOE_LIBRARY", os.path.join(BUILD, "libmoe_gb300.so"))
+TENSORS = os.path.join(os.path.dirname(LIBRARY), "_tensors.so")
 DEFINES = os.environ.get("MOE_NVCC_DEFINES", "").split()
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,14 +34,14 @@ def _sources():
 
 
 def _dependencies():
-    deps = _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    deps = _sources() + [os.path.join(CSRC, "tensors.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     return deps + [os.path.join(ROOT, "include", "moe.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not os.path.exists(LIBRARY) or not os.path.exists(TENSORS):
         return False
-    built = os.path.getmtime(LIBRARY)
+    built = min(os.path.getmtime(LIBRARY), os.path.getmtime(TENSORS))
     return all(os.path.getmtime(d) <= built for d in _dependencies())
 
 
@@ -56,8 +61,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources())) as pool:
+    def compile_tensors():
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        tmp = TENSORS + f".{os.getpid()}.tmp"
+        cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+        include = [os.path.join(ROOT, "include"), sysconfig.get_path("include"), os.path.join(torch, "include"),
+                   os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda]
+        lib = os.path.join(torch, "lib")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{i}" for i in include], os.path.join(CSRC, "tensors.cpp"),
+               "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed for tensors.cpp:\n{res.stderr}")
+        os.replace(tmp, TENSORS)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources()) + 1) as pool:
+        tensors = pool.submit(compile_tensors)
         objects = list(pool.map(compile_one, _sources()))
+        tensors.result()
     tmp = LIBRARY + f".{os.getpid()}.tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objects]
     res = subprocess.run(cmd, capture_output=True, text=True)
