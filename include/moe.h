@@ -810,7 +810,11 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
  *                first prefix_len / page_tokens entries, rounded down), as
  *                moe_kv_fork leaves them; the page where the prefix ends inside
  *                may be each request's own.
- * Both device memory. Shared are the whole pages that every query of the group
+ *   least_tiles  prefixes are shared only if that saves the call so many tiles of
+ *                work (128 tokens of a cache head for 8 query rows of a request);
+ *                0: the library's own number, below which two launches take
+ *                longer than one; 1: whatever it saves
+ * Both tensors are device memory. Shared are the whole pages that every query of the group
  * sees: prefix_len is held to the group's shortest cached context. Requests
  * without queries take no part (their rows may hold anything), a prefix that one
  * request reads, a length of 0 or below, and groups that do not cover the
@@ -826,7 +830,7 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
 typedef struct moe_kv_prefixes_t {
   const int32_t* group_start;
   const int32_t* prefix_lens;
-  int groups;
+  int groups, least_tiles;
 } moe_kv_prefixes_t;
 
 size_t moe_kv_shared_bytes(int tokens, int q_heads, int head_dim);

@@ -95,7 +95,7 @@ class _Rope(ctypes.Structure):
 
 
 class _KvPrefixes(ctypes.Structure):
-    _fields_ = [("group_start", _vp), ("prefix_lens", _vp), ("groups", _i32)]
+    _fields_ = [("group_start", _vp), ("prefix_lens", _vp), ("groups", _i32), ("least_tiles", _i32)]
 
 
 class _KvFork(ctypes.Structure):
@@ -566,12 +566,12 @@ def moe_kv_shared_bytes(tokens: int, q_heads: int, head_dim: int) -> int:
 
 
 def moe_kv_attend_shared(cache, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, workspace, scratch,
-                         lse=None, scale=None, stream=None):
+                         lse=None, scale=None, least_tiles: int = 0, stream=None):
     """moe_kv_attend for requests in groups that share a prefix, whose pages are read once: group_start (int32 [G + 1]),
     prefix_lens (int32 [G]). `scratch`: uint8 of moe_kv_shared_bytes(T, q_heads, head_dim); see include/moe.h."""
     if stream is None:
         code = (_native or _use_torch()).attend_shared(cache, q, block_table, query_start, seq_lens, group_start, prefix_lens,
-                                                       out, workspace, scratch, lse, scale)
+                                                       out, workspace, scratch, lse, scale, least_tiles)
         if code is not None:
             return _check(code, "moe_kv_attend_shared")
     call = "moe_kv_attend_shared"
@@ -581,7 +581,7 @@ def moe_kv_attend_shared(cache, q, block_table, query_start, seq_lens, group_sta
     if len(room) != 1 or room[0] < MOE_KV_SHARED_HEADER + 4 * tokens * heads * (dim + 1):
         _refuse(call, f"scratch must be {moe_kv_shared_bytes(tokens, heads, dim)} bytes of uint8")
     prefixes = _PREFIXES.pack(_dense(call, "group_start", group_start, _i32t, (groups + 1,), device),
-                              _dense(call, "prefix_lens", prefix_lens, _i32t, (groups,), device), groups)
+                              _dense(call, "prefix_lens", prefix_lens, _i32t, (groups,), device), groups, least_tiles)
     return _check(_attend_shared(block, batch, prefixes, *rows, heads, dim ** -0.5 if scale is None else scale,
                                  _dense(call, "out", out, _bf16t, q.shape, device),
                                  None if lse is None else _dense(call, "lse", lse, _f32t, (tokens, heads), device),
@@ -617,7 +617,7 @@ def _allocating_on(stream):
 _NORM = struct.Struct("PqPqPqPPqPP5i2f0P")
 _ROPE = struct.Struct("PP" + "PqqPqq" * 2 + "6if0P")
 _FORK = struct.Struct("PPqPPPPqPPP5i0P")
-_PREFIXES = struct.Struct("PPi0P")
+_PREFIXES = struct.Struct("PP2i")
 _RECLAIM = struct.Struct("PqPPPPqPP4i")
 
 
@@ -854,7 +854,7 @@ class KvCache:
         return (out, lse) if return_lse else out
 
     def attend_shared(self, q, block_table, query_start, seq_lens, group_start, prefix_lens, out=None, scale=None,
-                      return_lse: bool = False, scratch=None, stream=None):
+                      return_lse: bool = False, scratch=None, least_tiles: int = 0, stream=None):
         import torch
 
         with _allocating_on(stream):
@@ -864,7 +864,7 @@ class KvCache:
             if scratch is None:
                 scratch = torch.empty(moe_kv_shared_bytes(*q.shape), dtype=torch.uint8, device=q.device)
         moe_kv_attend_shared(self.tensors, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, self.workspace,
-                             scratch, lse, scale, stream)
+                             scratch, lse, scale, least_tiles, stream)
         return (out, lse) if return_lse else out
 
     def copy(self, moves, count=None, stream=None):

@@ -31,7 +31,31 @@ struct AttendArgs {
   const int32_t* skipped;
   float* partial;
   float* partial_lse;
+  // Of the requests' own part: its arrival counters (3 * kAttendMaxCtas, zero) and room for its pieces.
+  uint32_t* counters;
+  float* pieces;
+  // Where the prefixes' pieces are found: the groups' first units of the work, their sum and what an item counts as; their
+  // first query tokens, prefixes and first blocks of 8 rows.
+  long long* group_unit;
+  const int32_t* group_token;
+  const int32_t* group_prefix;
+  const int32_t* group_block;
+  int chained;  // whether the launch may start while the one before it runs
 };
+
+// Items of more units of work may be cut between CTAs in the 128-row form (the others' all may).
+constexpr int kAttendRowsLong = 16;
+// Pieces of an item are joined in runs of about the square root of their number; so many are merged as they are.
+constexpr int kAttendMerged = 32;
+__host__ __device__ inline int attend_join_width(int pieces) {
+  int width = 8;
+  while (width * width < pieces) ++width;
+  return width;
+}
+// Dimensions c4 .. c4 + 3 of row i in a piece of the prefixes' 128-row form.
+__host__ __device__ constexpr int attend_quad_at(int i, int c4) { return c4 * 128 + i * 4; }
+
+constexpr int kAttendMaxCtas = 512;
 
 enum AttendMode : int { kWhole = 0, kPrefix = 1, kSuffix = 2 };
 
@@ -53,6 +77,11 @@ cudaError_t launch_kv_attend_shared(const AttendArgs& a, const moe_kv_prefixes_t
 cudaError_t launch_kv_attend_decode(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
 cudaError_t launch_kv_attend_decode_prefix(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
 cudaError_t launch_kv_attend_decode_suffix(const AttendArgs& a, const AttendMaps& maps, int tile, int shift, int sms, cudaStream_t stream);
+// Their CTAs on so many SMs: each may leave two pieces of an item, of (head_dim + 2) floats a row.
+int kv_attend_decode_ctas(int head_dim, int tile, int sms);
+int kv_attend_rows_ctas(int sms);
+// Joins the pieces that the prefixes' launch (its rows of a row tile, CTAs) left with the requests' own parts.
+cudaError_t launch_kv_attend_merge(const AttendArgs& a, int rows, int ctas, cudaStream_t stream);
 cudaError_t launch_kv_attend_rows(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
 cudaError_t launch_kv_attend_rows_prefix(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
 cudaError_t launch_kv_attend_rows_suffix(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream);
@@ -61,6 +90,22 @@ cudaError_t launch_kv_attend_rows_suffix(const AttendArgs& a, const AttendMaps& 
 const char* norm_fault(const moe_norm_t* n, bool plan);
 
 const char* rope_fault(const moe_rope_t* r);
+
+// Launches a kernel; `chained`: by programmatic dependent launch, for kernels that wait for what they need themselves.
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, size_t smem, bool chained, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // Sets this thread's error detail (moe_last_error_detail) and returns `status`.
 int fail(int status, const char* format, ...);

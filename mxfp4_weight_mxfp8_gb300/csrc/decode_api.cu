@@ -290,6 +290,7 @@ int moe_kv_attend_shared(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
     return refuse(fault);
   if (prefixes == nullptr) return refuse("null argument");
   if (prefixes->groups < 1 || prefixes->groups > batch->requests) return refuse("groups out of range");
+  if (prefixes->least_tiles < 0) return refuse("least_tiles < 0");
   if (batch->tokens == 0) return MOE_OK;
   if (!prefixes->group_start || !prefixes->prefix_lens || !scratch) return refuse("null pointer");
   if (!aligned(prefixes->group_start, 4) || !aligned(prefixes->prefix_lens, 4) || !aligned(scratch, 16)) return refuse("misaligned pointer");

@@ -1,18 +1,21 @@
 // Attention over the paged 8-bit cache (moe_kv_attend, moe_kv_attend_shared in
 // include/moe.h): which form a call takes, and the plan of shared prefixes.
 //
-// Requests in groups that share a prefix take three launches: a small plan, the
-// prefix of every group for all of the group's rows at once (its keys and values
-// read once, not once for each request), and each request's own tokens, which
-// joins the two as it joins an item's pieces.
+// Requests in groups that share a prefix take four launches: a small plan, each
+// request's own tokens, the prefix of every group for all of the group's rows at
+// once (its keys and values read once, not once for each request), and the merging
+// of what the two left.
 #include <cudaTypedefs.h>
 
 #include <atomic>
 
 #include "decode.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
+
+using ptx::grid_launch_dependents;
 
 cudaError_t encode_map(CUtensorMap* map, const uint8_t* data, const moe_kv_cache_t& c) {
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> entry{nullptr};
@@ -68,30 +71,57 @@ int row_tile(const AttendArgs& a) {
 
 // ------------------------------------------------------------- shared prefixes
 constexpr int kPlanThreads = 1024;
+// Prefixes are shared from this much saved work on, in tiles of 8 rows: what two launches more cost. (One prefix of 8192
+// tokens, 64 query heads on 8 of 128: 8 requests, 3000 tiles, take 38.0 us with it and 41.1 without, 4 requests 37.6 and
+// 31.6, 16 requests 39.8 and 61.8; 64 requests on 1024 tokens, 3560 tiles, 55.1 and 49.5, on 2048 51.3 and 69.8. Heads of 64
+// and 256 turn at about the same number.)
+constexpr int kLeastTiles = 3500;
+// What a tile costs in row tiles of 8, 16, 24, 32 rows and (0) in the form of 128, in tenths of the first (from 64 ragged
+// requests with 8 to 32 rows, 62 to 96 us, and 1.95 us a tile and SM in the form of 128).
+constexpr int kTileCost[] = {21, 10, 12, 14, 15};
+
+// The plan's share of what the host knows.
+struct SharedWork {
+  int shift;
+  int group, kv_heads;        // query heads of one cache head; those
+  int own;                    // cost of a tile of the prefix to a request
+  int rows, cost;             // of the prefixes' launch: rows of a row tile, a tile's cost
+};
 static_assert(MOE_KV_MAX_REQUESTS <= kPlanThreads, "a thread to a request, and to a group");
 
 // Scratch: the groups' first query tokens, prefixes (tokens) and rows of the block table, the pages that each request skips;
-// then each row's log-sum-exp and output over its prefix.
+// the arrival counters of the requests' part, the groups' first blocks of 8 rows and units of work; then each row's log-sum-exp and output over its prefix.
 struct Scratch {
   int32_t *start, *prefix, *row, *skipped;
+  uint32_t* counters;
+  int32_t* block;
+  long long* unit;
   float *lse, *out;
   Scratch(void* p, const AttendArgs& a) {
     start = static_cast<int32_t*>(p);
     prefix = start + 2 * MOE_KV_MAX_REQUESTS;
     row = prefix + MOE_KV_MAX_REQUESTS;
     skipped = row + MOE_KV_MAX_REQUESTS;
+    counters = reinterpret_cast<uint32_t*>(skipped + MOE_KV_MAX_REQUESTS);
+    block = reinterpret_cast<int32_t*>(counters + 3 * kAttendMaxCtas);
+    unit = reinterpret_cast<long long*>(block + 2 * MOE_KV_MAX_REQUESTS);
     out = reinterpret_cast<float*>(static_cast<uint8_t*>(p) + MOE_KV_SHARED_HEADER);
     lse = out + static_cast<int64_t>(a.b.tokens) * a.q_heads * a.c.head_dim;
   }
 };
-static_assert(5 * MOE_KV_MAX_REQUESTS * 4 <= MOE_KV_SHARED_HEADER, "the plan's room");
+static_assert(7 * MOE_KV_MAX_REQUESTS * 4 + 3 * kAttendMaxCtas * 4 + (MOE_KV_MAX_REQUESTS + 2) * 8 <= MOE_KV_SHARED_HEADER, "the plan's room");
+static_assert((7 * MOE_KV_MAX_REQUESTS + 3 * kAttendMaxCtas) % 2 == 0, "alignment of the units");
 
 // What of a group's prefix its requests can share: whole pages that every query of theirs sees and the tables have. Of
 // requests without queries nothing is asked; a prefix that only one request reads is left to that. Groups that do not cover
-// the requests in order share nothing.
-__global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_batch_t b, const moe_kv_prefixes_t p, int shift, Scratch s) {
+// the requests in order share nothing; nor does a call in which that would save less than p.least_tiles tiles.
+__global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_batch_t b, const moe_kv_prefixes_t p, const SharedWork w, Scratch s) {
   __shared__ int s_least[kPlanThreads], s_row[kPlanThreads], s_count[kPlanThreads], s_start[kPlanThreads + 1];
+  __shared__ unsigned long long s_saved;
   const int tid = threadIdx.x;
+  grid_launch_dependents();  // (the next launch waits for this one's end before it reads what is written here)
+  for (int i = tid; i < 3 * kAttendMaxCtas; i += kPlanThreads) s.counters[i] = 0;
+  if (tid == 0) s_saved = 0;
   if (tid < p.groups) {
     s_least[tid] = 0x7FFFFFFF;
     s_row[tid] = 0x7FFFFFFF;
@@ -117,19 +147,44 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
     }
   }
   __syncthreads();
+  int tokens = 0;
+  long long rows = 0;  // of the group
   if (tid < p.groups) {
-    const long long room = static_cast<long long>(b.table_width) << shift;
-    int tokens = 0;
+    const long long room = static_cast<long long>(b.table_width) << w.shift;
     if (fine && s_count[tid] > 1) tokens = static_cast<int>(min(static_cast<long long>(min(p.prefix_lens[tid], s_least[tid])), room));
-    tokens = max(tokens, 0) >> shift << shift;
+    tokens = max(tokens, 0) >> w.shift << w.shift;
+    if (tokens) {
+      const int first = min(max(b.query_start[s_start[tid]], 0), b.tokens);
+      rows = static_cast<long long>(min(max(b.query_start[s_start[tid + 1]], first), b.tokens) - first) * w.group;
+      const long long saved = (static_cast<long long>(s_count[tid]) * w.own - (rows + w.rows - 1) / w.rows * w.cost) * w.kv_heads * ((tokens + 127) / 128) / 10;
+      atomicAdd(&s_saved, static_cast<unsigned long long>(max(saved, 1ll)));
+    }
+  }
+  __syncthreads();
+  if (s_saved < static_cast<unsigned long long>(p.least_tiles)) tokens = 0;
+  if (tid < p.groups) {
     s.start[tid] = b.query_start[fine ? s_start[tid] : 0];
     s.prefix[tid] = tokens;
     s.row[tid] = tokens ? s_row[tid] : 0;
-    s_least[tid] = tokens >> shift;
+    s_least[tid] = tokens >> w.shift;
   }
   if (tid == 0) s.start[p.groups] = b.query_start[fine ? b.requests : 0];
   __syncthreads();
   if (tid < b.requests) s.skipped[tid] = fine ? s_least[group] : 0;
+  // The blocks of 8 rows of the groups before this one, of those that share.
+  const int blocks = tokens ? static_cast<int>((rows + 7) / 8) : 0;
+  int sum = blocks;
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+    if (lane >= d) sum += u;
+  }
+  if (lane == 31) s_row[warp] = sum;
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) sum += s_row[k];
+  if (tid < p.groups) s.block[tid] = sum - blocks;
+  if (tid == p.groups - 1) s.block[p.groups] = sum;
 }
 
 }  // namespace
@@ -147,23 +202,44 @@ cudaError_t launch_kv_attend_shared(const AttendArgs& whole, const moe_kv_prefix
   cudaError_t e = c.open(whole.c);
   if (e != cudaSuccess) return e;
   const Scratch s(scratch, whole);
-  kv_shared_kernel<<<1, kPlanThreads, 0, stream>>>(whole.b, p, c.shift, s);
+  AttendArgs a = whole, b = whole;  // the requests' own part, their prefixes'
+  a.counters = s.counters;
+  a.skipped = s.skipped;
+  a.partial = b.partial = s.out;
+  a.partial_lse = b.partial_lse = s.lse;
+  a.chained = 1;
+  b.rows = s.row;
+  b.group_unit = s.unit;
+  b.group_token = s.start;
+  b.group_prefix = s.prefix;
+  b.group_block = s.block;
+  b.b.query_start = s.start;
+  b.b.seq_lens = s.prefix;
+  b.b.requests = p.groups;
+  const int own_tile = row_tile(whole), tile = row_tile(b), own_rows = own_tile ? 8 * own_tile : 128;
+  const long long rows = static_cast<long long>(whole.b.tokens) * whole.group, average = (rows + whole.b.requests - 1) / whole.b.requests;
+  const SharedWork work = {c.shift, a.group, a.c.kv_heads, static_cast<int>((average + own_rows - 1) / own_rows) * kTileCost[own_tile],
+                           tile ? 8 * tile : 128, kTileCost[tile]};
+  moe_kv_prefixes_t prefixes = p;
+  if (p.least_tiles == 0) prefixes.least_tiles = kLeastTiles;
+  kv_shared_kernel<<<1, kPlanThreads, 0, stream>>>(whole.b, prefixes, work, s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  AttendArgs a = whole;
-  a.rows = s.row;
-  a.skipped = s.skipped;
-  a.partial = s.out;
-  a.partial_lse = s.lse;
-  a.b.query_start = s.start;
-  a.b.seq_lens = s.prefix;
-  a.b.requests = p.groups;
-  int tile = row_tile(a);
-  e = tile ? launch_kv_attend_decode_prefix(a, c.maps, tile, c.shift, c.sms, stream) : launch_kv_attend_rows_prefix(a, c.maps, c.shift, c.sms, stream);
+  // The prefixes' part starts while the other's last CTAs run, if there is room for the pieces of both (not for twice the
+  // form of 128 rows, whose work is long).
+  const auto piece_bytes = [&](int t) {
+    return 8ull * (t ? 8 * t * kv_attend_decode_ctas(a.c.head_dim, t, c.sms) : 128 * kv_attend_rows_ctas(c.sms)) * (a.c.head_dim + 2);
+  };
+  const size_t theirs = (piece_bytes(tile) + 255) / 256 * 256, room = MOE_KV_WORKSPACE_BYTES - MOE_KV_WORKSPACE_HEADER;
+  b.chained = theirs + piece_bytes(own_tile) <= room;
+  a.pieces = reinterpret_cast<float*>(a.workspace + MOE_KV_WORKSPACE_HEADER + (b.chained ? theirs : 0));
+  e = own_tile ? launch_kv_attend_decode_suffix(a, c.maps, own_tile, c.shift, c.sms, stream)
+               : launch_kv_attend_rows_suffix(a, c.maps, c.shift, c.sms, stream);
   if (e != cudaSuccess) return e;
-  a.b = whole.b;
-  tile = row_tile(a);
-  return tile ? launch_kv_attend_decode_suffix(a, c.maps, tile, c.shift, c.sms, stream) : launch_kv_attend_rows_suffix(a, c.maps, c.shift, c.sms, stream);
+  e = tile ? launch_kv_attend_decode_prefix(b, c.maps, tile, c.shift, c.sms, stream)
+           : launch_kv_attend_rows_prefix(b, c.maps, c.shift, c.sms, stream);
+  if (e != cudaSuccess) return e;
+  return launch_kv_attend_merge(b, tile ? 8 * tile : 128, tile ? kv_attend_decode_ctas(a.c.head_dim, tile, c.sms) : kv_attend_rows_ctas(c.sms), stream);
 }
 
 }  // namespace moe

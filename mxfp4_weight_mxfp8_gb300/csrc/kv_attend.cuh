@@ -10,11 +10,15 @@
 // share one. Results are sums over pieces in CTA order, whoever adds them.
 //
 // Every part comes in three modes. kWhole: a request's causal attention. For
-// requests that share a prefix, kPrefix: the "requests" are groups of them, the
-// rows those of all of a group's requests, the tokens the prefix, all of which
-// every row sees; the output stays in FP32, with its log-sum-exp. Then kSuffix:
-// a request's tokens from its prefix on (positions count from there), joined with
-// what kPrefix left as with another piece.
+// requests that share a prefix, kSuffix: a request's tokens from its prefix on
+// (positions count from there), whose output stays in FP32, with its log-sum-exp;
+// then kPrefix: the "requests" are groups of them, the rows those of all of a
+// group's requests, the tokens the prefix, all of which every row sees. An item of
+// kPrefix that one CTA has to itself is joined with what kSuffix left there; the
+// pieces of the others, by a launch of their own (kv_attend_merge.cu): a CTA takes
+// 9 us for the half a megabyte of six pieces of 128 rows, all together 4. kSuffix
+// comes first because it is the shorter one: kPrefix's CTAs take its CTAs' places
+// as they leave.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -40,9 +44,21 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // Workspace: the status word, arrival counters (zero between calls: for the
 // runs of pieces that start with an item, for its other runs, for the item;
 // each under the CTA of the first piece), two partial results for each CTA.
+// kSuffix has its own counters and partial results, as kPrefix may start while it
+// runs.
 constexpr int kCounterOffset = 256;
 constexpr int kPartialOffset = MOE_KV_WORKSPACE_HEADER;
 static_assert(kCounterOffset + 3 * kMaxCtas * 4 <= kPartialOffset, "counters fit");
+static_assert(kMaxCtas == kAttendMaxCtas, "kSuffix's counters");
+
+template <int kMode>
+__device__ __forceinline__ uint32_t* counters_of(const AttendArgs& a) {
+  return kMode == kSuffix ? a.counters : reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
+}
+template <int kMode>
+__device__ __forceinline__ float* pieces_of(const AttendArgs& a) {
+  return kMode == kSuffix ? a.pieces : reinterpret_cast<float*>(a.workspace + kPartialOffset);
+}
 
 
 // ---------------------------------------------------------------- tensor core
@@ -207,12 +223,14 @@ struct Request : Place<kMode> {
   int row_tiles;
   Request() = default;
   __device__ Request(const AttendArgs& a, int shift, int r, int rows) {
-    first = min(max(a.b.query_start[r], 0), a.b.tokens);
-    n = min(max(a.b.query_start[r + 1], first), a.b.tokens) - first;
-    seq = a.b.seq_lens[r];
+    // (kPrefix's were written while its launch was on its way: from the second level.)
+    const auto read = [](const int32_t* p) { return kMode == kPrefix ? __ldcg(p) : *p; };
+    first = min(max(read(a.b.query_start + r), 0), a.b.tokens);
+    n = min(max(read(a.b.query_start + r + 1), first), a.b.tokens) - first;
+    seq = read(a.b.seq_lens + r);
     long long room = static_cast<long long>(a.b.table_width) << shift;
     if constexpr (kMode == kPrefix) {
-      this->row = a.rows[r];
+      this->row = __ldcg(a.rows + r);
       this->page0 = 0;
       if (seq <= 0) n = 0;
     }
@@ -283,6 +301,12 @@ struct Segment {
   int length;              // in the units that the work is dealt in: `weight` for the item, then its tiles
   bool first, whole;       // the item starts here; and ends here too
   long long item;          // the item's first unit among all
+
+  // kSuffix: its rows go on to their prefix.
+  __device__ __forceinline__ bool shared() const {
+    if constexpr (kMode == kSuffix) return q.page0 > 0;
+    return false;
+  }
 
   // The item's tiles from unit `from` on, as far as the run goes and this row tile's queries see.
   __device__ __forceinline__ void cut(const AttendArgs& a, long long x, long long stop, int from) {
@@ -509,6 +533,12 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
     }
   }
   __syncthreads();
+  if constexpr (kMode == kPrefix) {  // for the merging launch
+    if (blockIdx.x == 0) {
+      for (int r = tid; r <= a.b.requests; r += kThreads) a.group_unit[r] = prefix[r];
+      if (tid == 0) a.group_unit[a.b.requests + 1] = weight;
+    }
+  }
   return weight;
 }
 
@@ -602,26 +632,38 @@ struct Joined {
   __device__ __forceinline__ float operator()(float o, float finished) const { return o * own + finished * other; }
 };
 
+// Dimensions c4 .. c4 + 3 of row i in a piece: row by row, or in kPrefix's 128-row form, whose threads hold rows, quad by quad.
+template <int kMode, int kRows, int D>
+__device__ __forceinline__ int piece_at(int i, int c4) {
+  return kMode == kPrefix && kRows == 128 ? attend_quad_at(i, c4) : i * D + c4;
+}
+
+// Quad c of row i in a piece of kPrefix: row by row, or in the 128-row form, whose threads hold rows, quad by quad.
+template <int kRows, int D>
+__device__ __forceinline__ int quad_at(int i, int c) {
+  return kRows == 128 ? (c * kRows + i) * 4 : i * D + c * 4;
+}
+
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
 // is kBarrier. row_dst: the rows' places among the outputs' rows.
 template <int kMode, int kRows, int D, int kThreads, int kBarrier>
 __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, const long long* row_dst, int rows, long long ctas, long long total,
                           int tid, int* s_last) {
   constexpr int kPartialFloats = kRows * (D + 2);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace + kCounterOffset);
-  float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
+  uint32_t* counters = counters_of<kMode>(a);
+  float* partials = pieces_of<kMode>(a);
   auto sync = [] { asm volatile("bar.sync %0, %1;" ::"n"(kBarrier), "n"(kThreads) : "memory"); };
   // The CTAs of this item: c0 .. c1, by the bounds of their runs.
   const int c0 = static_cast<int>(divide((s.item + 1) * ctas - 1, total));
   const int c1 = static_cast<int>(divide((s.item + s.units) * ctas - 1, total));
   // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
-  // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces.
+  // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces. (kPrefix: the first
+  // step alone, where there are more than the merging launch takes.)
   float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * kPartialFloats;  // the first piece
   float* piece0 = partials + static_cast<int64_t>(c0 * 2) * kPartialFloats;      // piece i: 2 i slots on
   auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * kPartialFloats; };
-  const int pieces = c1 - c0 + 1;
-  int width = 8;
-  while (width * width < pieces) ++width;
+  const int pieces = c1 - c0 + 1, width = attend_join_width(pieces);
+  if (kMode == kPrefix && pieces <= kAttendMerged) return;
   int from = (static_cast<int>(blockIdx.x) - c0) / width * width, stride = 1, count = min(width, pieces - from);
   uint32_t* counter = from == 0 ? counters + c0 : counters + kMaxCtas + c0 + from;
   for (;;) {
@@ -634,10 +676,11 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
     }
     sync();
     if (!*s_last) break;
+    if (kMode == kPrefix && count == 1) break;
     // A thread joins four dimensions of some rows, several pieces' loads in flight together.
     constexpr int kQuads = D / 4, kAllUnits = kRows * kQuads / kThreads, kUnits = kAllUnits % 4 == 0 ? 4 : kAllUnits % 2 == 0 ? 2 : 1;
     constexpr int kBatch = 8 / kUnits;
-    const bool last = stride > 1 || count == pieces;
+    const bool last = kMode != kPrefix && (stride > 1 || count == pieces);
     for (int group = 0; group < kAllUnits; group += kUnits) {
       float4 o[kUnits];
       float top[kUnits], total_l[kUnits];
@@ -659,7 +702,7 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
             const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
             pm[e][u] = __ldcg(src + kRows * D + i);
             pl[e][u] = __ldcg(src + kRows * D + kRows + i);
-            pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + i * D + c4));
+            pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + piece_at<kMode, kRows, D>(i, c4)));
             if (!in) pm[e][u] = -INFINITY;
           }
         }
@@ -693,7 +736,7 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
         const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
         if (!last) {
           float* dst = piece(from);
-          *reinterpret_cast<float4*>(dst + i * D + c4) = o[u];
+          *reinterpret_cast<float4*>(dst + piece_at<kMode, kRows, D>(i, c4)) = o[u];
           if (c4 == 0) {
             dst[kRows * D + i] = top[u];
             dst[kRows * D + kRows + i] = total_l[u];
@@ -702,27 +745,20 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
         }
         if (i >= rows) continue;
         const int64_t dst = row_dst[i];
+        const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
         if constexpr (kMode == kSuffix) {
           if (s.q.page0 > 0) {
-            const Joined j(top[u], total_l[u], __ldcg(a.partial_lse + dst));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + dst * D + c4));
-            top[u] = j.top;
-            total_l[u] = j.sum;
-            o[u] = make_float4(j(o[u].x, v.x), j(o[u].y, v.y), j(o[u].z, v.z), j(o[u].w, v.w));
+            *reinterpret_cast<float4*>(a.partial + dst * D + c4) = make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
+            if (c4 == 0) a.partial_lse[dst] = total_l[u] == 0.0f ? -INFINITY : top[u] + log2f(total_l[u]);
+            continue;
           }
-        }
-        const float inv = total_l[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, total_l[u]);
-        if constexpr (kMode == kPrefix) {
-          *reinterpret_cast<float4*>(a.partial + dst * D + c4) = make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
-          if (c4 == 0) a.partial_lse[dst] = total_l[u] == 0.0f ? -INFINITY : top[u] + log2f(total_l[u]);
-          continue;
         }
         __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv), __floats2bfloat162_rn(o[u].z * inv, o[u].w * inv)};
         *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
         if (a.lse != nullptr && c4 == 0) a.lse[dst] = total_l[u] == 0.0f ? -INFINITY : (top[u] + log2f(total_l[u])) * kLn2;
       }
     }
-    if (last) break;
+    if (last || kMode == kPrefix) break;
     from = 0;
     stride = width;
     count = (pieces + width - 1) / width;

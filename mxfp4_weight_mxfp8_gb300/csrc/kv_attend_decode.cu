@@ -7,4 +7,6 @@ cudaError_t launch_kv_attend_decode(const AttendArgs& a, const AttendMaps& maps,
   return launch_decode<kWhole>(a, maps, tile, shift, sms, stream);
 }
 
+int kv_attend_decode_ctas(int head_dim, int tile, int sms) { return decode_ctas(head_dim, tile, sms); }
+
 }  // namespace moe

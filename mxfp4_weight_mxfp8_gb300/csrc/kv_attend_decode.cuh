@@ -201,8 +201,14 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   __shared__ long long s_unit;
   __shared__ int32_t s_status;   // the workspace's when the CTA started
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
-  float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
+  float* partials = pieces_of<kMode>(a);
 
+  if constexpr (kMode == kPrefix) {
+    if (__ldcg(a.group_block + a.b.requests) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
+      if (blockIdx.x == 0) grid_dependency_wait();
+      return;
+    }
+  }
   const int32_t found = tid == 0 ? *static_cast<const volatile int32_t*>(status) : 0;  // (on its way while the work is summed)
   if (tid == 0) {
     for (int i = 0; i < X::kStages; ++i) {
@@ -219,9 +225,12 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
     mbar_init(v_ready + 1, kCompute);
     fence_mbar_init();
   }
+  if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
   const int weight = sum_work<kMode, X::kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
+  // (Whatever it does, kPrefix's launch ends after kSuffix's.)
+  if (kMode == kPrefix && blockIdx.x == 0 && ctas == 0) grid_dependency_wait();
   if (blockIdx.x >= ctas) return;
   const long long start = total * blockIdx.x / ctas, stop = total * (blockIdx.x + 1) / ctas;
   if (warp == kIssueWarp) {
@@ -232,6 +241,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // The next launch may start, now that this CTA has its TMEM: that one holds TMEM too while it waits for this one's end.
+  if constexpr (kMode != kWhole) grid_launch_dependents();
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * X::kCols;
 
   if (s_status != MOE_OK) {
@@ -573,7 +584,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
       const bool holds = D >= 128 || tid < D;  // this thread's dimension (D = 64: the upper lanes repeat the lower)
       auto store_row = [&](int i, float v0, float v1, float inv, float lse) {
         const int64_t dst = row_dst[i];
-        if constexpr (kMode == kPrefix) {
+        if (kMode == kSuffix && s.shared()) {
           if (holds) {
             a.partial[dst * D + tid] = v0 * inv;
             if (X::kHalves == 2) a.partial[dst * D + 128 + tid] = v1 * inv;
@@ -588,23 +599,22 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
         if (a.lse != nullptr && tid == 0) a.lse[dst] = lse;
       };
       if (s.whole) {
-        if constexpr (kMode == kSuffix) {
-          if (rq.page0 > 0) {
-            const Joined j(m, sum, lane < rows ? __ldcg(a.partial_lse + row_dst[lane]) : -INFINITY);
-            m = j.top;
-            sum = j.sum;
+        if constexpr (kMode == kPrefix) {
+          grid_dependency_wait();  // the requests' own parts are done
+          const Joined j(m, sum, lane < rows ? __ldcg(a.partial_lse + row_dst[lane]) : -INFINITY);
+          m = j.top;
+          sum = j.sum;
 #pragma unroll
-            for (int i = 0; i < X::kRows; ++i) {
-              const float own = __shfl_sync(kAll, j.own, i), other = __shfl_sync(kAll, j.other, i);
-              if (i >= rows) continue;
+          for (int i = 0; i < X::kRows; ++i) {
+            const float own = __shfl_sync(kAll, j.own, i), other = __shfl_sync(kAll, j.other, i);
+            if (i >= rows) continue;
 #pragma unroll
-              for (int h = 0; h < X::kHalves; ++h)
-                acc[h][i] = acc[h][i] * own + (holds ? __ldcg(a.partial + row_dst[i] * D + h * 128 + tid) : 0.0f) * other;
-            }
+            for (int h = 0; h < X::kHalves; ++h)
+              acc[h][i] = acc[h][i] * own + (holds ? __ldcg(a.partial + row_dst[i] * D + h * 128 + tid) : 0.0f) * other;
           }
         }
         const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-        const float lse = sum == 0.0f ? -INFINITY : kMode == kPrefix ? m + log2f(sum) : (m + log2f(sum)) * kLn2;
+        const float lse = sum == 0.0f ? -INFINITY : kMode == kSuffix && s.shared() ? m + log2f(sum) : (m + log2f(sum)) * kLn2;
 #pragma unroll
         for (int i = 0; i < X::kRows; ++i) {
           const float f = __shfl_sync(kAll, inv, i), e = __shfl_sync(kAll, lse, i);
@@ -640,7 +650,26 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
     tc_fence_after_sync();
     tmem_dealloc(tmem, X::kTmem);
   }
+  if (kMode == kPrefix && blockIdx.x == 0) grid_dependency_wait();
 }
+
+// CTAs of a call in row tiles of 8 * tile rows: as many as are resident together.
+inline int decode_ctas(int head_dim, int tile, int sms) {
+  int per_sm = 0;
+  switch (head_dim * 8 + tile) {
+    case 64 * 8 + 1: per_sm = Shape<64, 1>::kCtasPerSm; break;
+    case 64 * 8 + 2: per_sm = Shape<64, 2>::kCtasPerSm; break;
+    case 64 * 8 + 3: per_sm = Shape<64, 3>::kCtasPerSm; break;
+    case 64 * 8 + 4: per_sm = Shape<64, 4>::kCtasPerSm; break;
+    case 128 * 8 + 1: per_sm = Shape<128, 1>::kCtasPerSm; break;
+    case 128 * 8 + 2: per_sm = Shape<128, 2>::kCtasPerSm; break;
+    case 128 * 8 + 3: per_sm = Shape<128, 3>::kCtasPerSm; break;
+    case 128 * 8 + 4: per_sm = Shape<128, 4>::kCtasPerSm; break;
+    default: per_sm = 1;
+  }
+  return sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+}
+static_assert(Shape<256, 1>::kCtasPerSm == 1 && Shape<256, 2>::kCtasPerSm == 1, "heads of 256");
 
 template <int kMode, int D, int RT>
 cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
@@ -649,9 +678,8 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
       cudaFuncSetAttribute(kv_attend_kernel<kMode, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Shape<D, RT>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
-  const int resident = sms * Shape<D, RT>::kCtasPerSm, grid = resident < kMaxCtas ? resident : kMaxCtas;
-  kv_attend_kernel<kMode, D, RT><<<grid, Shape<D, RT>::kThreads, smem, stream>>>(a, maps, shift);
-  return cudaGetLastError();
+  return launch_chained(kv_attend_kernel<kMode, D, RT>, decode_ctas(D, RT, sms), Shape<D, RT>::kThreads, smem,
+                        kMode != kWhole && a.chained, stream, a, maps, shift);
 }
 
 // The form of row tiles of 8 * tile rows (heads of 256: of 16 at most).

@@ -7,4 +7,6 @@ cudaError_t launch_kv_attend_rows(const AttendArgs& a, const AttendMaps& maps, i
   return launch_rows<kWhole>(a, maps, shift, sms, stream);
 }
 
+int kv_attend_rows_ctas(int sms) { return rows_ctas(sms); }
+
 }  // namespace moe

@@ -78,7 +78,7 @@ struct RowsShape {
 // What starting and joining an item costs, in tiles (prompts without earlier tokens: 139 us with 4 and 5, 146 with 6, 153
 // with 8; one of 900 tokens with a window of 100: 104 with 4, 100 with 5; the chunks: 313 with any).
 constexpr int kItemTiles = 5;
-constexpr int kLongUnits = 16;       // longer items may be cut anywhere (one head to a group, 900 tokens: 46 -> 34.6 us)
+constexpr int kLongUnits = kAttendRowsLong;       // longer items may be cut anywhere (one head to a group, 900 tokens: 46 -> 34.6 us)
 constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
 
@@ -223,8 +223,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int32_t s_status;   // the workspace's when the CTA started
   __shared__ long long s_run[2];  // the CTA's units
   int32_t* status = reinterpret_cast<int32_t*>(a.workspace);
-  float* partials = reinterpret_cast<float*>(a.workspace + kPartialOffset);
+  float* partials = pieces_of<kMode>(a);
 
+  if constexpr (kMode == kPrefix) {
+    if (__ldcg(a.group_block + a.b.requests) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
+      if (blockIdx.x == 0) grid_dependency_wait();
+      return;
+    }
+  }
   const int32_t found = tid == 0 ? *static_cast<const volatile int32_t*>(status) : 0;  // (on its way while the work is summed)
   if (tid == 0) {
     for (int i = 0; i < X::kKeyStages; ++i) {
@@ -244,9 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_ready, kAllCompute);
     fence_mbar_init();
   }
+  if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
   const int weight = sum_work<kMode, kThreads, kRows, kItemTiles>(a, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
+  // (Whatever it does, kPrefix's launch ends after kSuffix's.)
+  if (kMode == kPrefix && blockIdx.x == 0 && ctas == 0) grid_dependency_wait();
   if (blockIdx.x >= ctas) return;
   if (tid == 0 || tid == 32) {
     const int i = tid == 0 ? 0 : 1;
@@ -255,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) s_status = found;
   __syncthreads();
   const long long start = s_run[0], stop = s_run[1];
+  if (kMode == kPrefix && blockIdx.x == 0 && (start >= stop || s_status != MOE_OK)) grid_dependency_wait();
   if (start >= stop || s_status != MOE_OK) return;  // (an error that nobody has read yet: the arrival counters are anyhow)
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, kGroups * X::kGroupTmem);
@@ -263,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // The next launch may start, now that this CTA has its TMEM: that one holds TMEM too while it waits for this one's end.
+  if constexpr (kMode != kWhole) grid_launch_dependents();
   const uint32_t tmem = s_tmem;  // group g: scores at 256 g, then weights in their place; output at 256 g + 128
 
   if (warp == kProducerWarp) {
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (bad & 1u << i) own[i] = __uint_as_float(0x7FC00000u);
         }
       }
-      if (kMode == kPrefix && s.whole) {
+      if (kMode == kSuffix && s.whole && s.shared()) {
         const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
         if (tid < rows) a.partial_lse[row_dst[tid]] = l == 0.0f ? -INFINITY : m + log2f(l);
         if (row < rows) {
@@ -566,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float4*>(dst + c) = make_float4(own[c] * inv, own[c + 1] * inv, own[c + 2] * inv, own[c + 3] * inv);
         }
       } else if (s.whole) {
-        if constexpr (kMode == kSuffix) {
-          if (s.q.page0 > 0 && row < rows) {
+        if constexpr (kMode == kPrefix) {
+          grid_dependency_wait();  // the requests' own parts are done
+          if (row < rows) {
             const Joined j(m, l, __ldcg(a.partial_lse + row_dst[row]));
             const float4* src = reinterpret_cast<const float4*>(a.partial + row_dst[row] * D + column);
             m = j.top;
@@ -608,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < kOwn; c += 4)
-          *reinterpret_cast<float4*>(piece + row * D + column + c) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
+          *reinterpret_cast<float4*>(piece + piece_at<kMode, kRows, D>(row, column + c)) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
       }
       if (!s.whole) join_item<kMode, kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       all_sync();  // the output's room, the rows' factors and the join word are free again, the segment is done with
@@ -626,16 +639,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, kGroups * X::kGroupTmem);
   }
+  if (kMode == kPrefix && blockIdx.x == 0) grid_dependency_wait();
 }
+
+inline int rows_ctas(int sms) { return sms < kMaxRowsCtas ? sms : kMaxRowsCtas; }
 
 template <int kMode, int D>
 cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, int sms, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(kv_attend_rows_kernel<kMode, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              RowsShape<D>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
-  const int grid = sms < kMaxRowsCtas ? sms : kMaxRowsCtas;
-  kv_attend_rows_kernel<kMode, D><<<grid, kThreads, RowsShape<D>::smem(a.b.requests), stream>>>(a, maps, shift);
-  return cudaGetLastError();
+  return launch_chained(kv_attend_rows_kernel<kMode, D>, rows_ctas(sms), kThreads, RowsShape<D>::smem(a.b.requests),
+                        kMode != kWhole && a.chained, stream, a, maps, shift);
 }
 
 // Heads of 64 or 128.

@@ -308,9 +308,9 @@ PyObject* copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// cache, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, workspace, scratch, lse, scale
+// cache, q, block_table, query_start, seq_lens, group_start, prefix_lens, out, workspace, scratch, lse, scale, least_tiles
 PyObject* attend_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return call<12>(args, n, [](PyObject* const* a, Device& d) {
+  return call<13>(args, n, [](PyObject* const* a, Device& d) {
     const Heads q(d, a[1]);
     if (!q.at) throw Unfit();
     const moe_kv_cache_t cache = cache_of(d, a[0]);
@@ -329,6 +329,7 @@ PyObject* attend_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
     p.group_start = d.dense<int32_t>(a[5], kInt, groups + 1);
     p.prefix_lens = d.dense<int32_t>(a[6], kInt, groups);
     p.groups = narrow(groups);
+    p.least_tiles = integer(a[12]);
     const int64_t rows[3] = {q.tokens, q.heads, q.dim}, sums[2] = {q.tokens, q.heads};
     void* out = d.dense<void>(a[7], at::kBFloat16, rows);
     float* lse = a[10] == Py_None ? nullptr : d.dense<float>(a[10], at::kFloat, sums);

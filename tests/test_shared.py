@@ -47,7 +47,7 @@ def call(moe, cache=None, batch=None, prefixes=None, **changes):
     dict(batch=dict(table_stride=7)), dict(batch=dict(block_table=0)), dict(batch=dict(query_start=0x60002)), dict(q_heads=3), dict(q_heads=0),
     dict(token=4), dict(head=-8), dict(scale=math.inf), dict(q=0), dict(q=0xA0008), dict(out=0), dict(workspace=0), dict(workspace=0xC0008),
     dict(lse=0xE0002), dict(no_prefixes=True), dict(prefixes=dict(groups=0)), dict(prefixes=dict(groups=5)), dict(prefixes=dict(group_start=0)),
-    dict(prefixes=dict(prefix_lens=0)), dict(prefixes=dict(prefix_lens=0x90001)), dict(scratch=0), dict(scratch=0xD0004)])
+    dict(prefixes=dict(prefix_lens=0)), dict(prefixes=dict(least_tiles=-1)), dict(prefixes=dict(prefix_lens=0x90001)), dict(scratch=0), dict(scratch=0xD0004)])
 def test_shared_refusals(moe, changes):
     assert call(moe, **changes) == moe.MOE_ERR_ARG
     assert moe.moe_last_error_detail()
@@ -110,13 +110,13 @@ class Batch:
         self.q = (torch.randn(sum(self.new) + pad, q_heads, dim, generator=g, device="cuda") * 1.3).to(torch.bfloat16)
         self.workspace = torch.zeros(moe.MOE_KV_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
 
-    def run(self, scratch=None, scale=None, stream=None):
+    def run(self, scratch=None, scale=None, stream=None, least=1):  # least 1: shared whatever that saves
         out = torch.full(self.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
         lse = torch.full(self.q.shape[:2], 7.0, device="cuda")
         if scratch is None:  # NaN where nothing has been written
             scratch = torch.full((self.moe.moe_kv_shared_bytes(*self.q.shape),), 0xFF, dtype=torch.uint8, device="cuda")
         self.moe.moe_kv_attend_shared(self.cache, self.q, self.table, self.start, self.lens, self.group_start, self.prefix_lens, out,
-                                      self.workspace, scratch, lse=lse, scale=scale, stream=stream)
+                                      self.workspace, scratch, lse=lse, scale=scale, least_tiles=least, stream=stream)
         return out, lse
 
     def reference(self, scale=None):
@@ -210,6 +210,10 @@ def test_shared_matches_64_bits(moe, page, dim, heads, q_heads, groups):
     for _ in range(3):
         again = b.run()
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    # By the library's own rule, and nothing shared: moe_kv_attend's results, bit for bit.
+    b.check(b.run(least=0))
+    alone = b.run(least=2 ** 31 - 1)
+    assert torch.equal(alone[0], out) and torch.equal(alone[1], lse)
     assert not b.workspace[:moe.MOE_KV_WORKSPACE_HEADER].any()
 
 
@@ -341,7 +345,7 @@ def test_shared_prefix_after_forks(moe):
         head = counts[1:2]
         cache.append(rows(samples, heads), rows(samples, heads), slots)
         q = rows(samples, q_heads)
-        got, got_lse = cache.attend_shared(q, table, q_start, lens, ints([0, samples]), ints([prompt]), return_lse=True)
+        got, got_lse = cache.attend_shared(q, table, q_start, lens, ints([0, samples]), ints([prompt]), return_lse=True, least_tiles=1)
         want, want_lse = cache.attend(q, table, q_start, lens, return_lse=True)
         # Both are held to the tolerances of this file's head; between two of them twice that.
         assert (got.double() - want.double()).abs().max() <= 2 * (2.0 ** -8 * want.abs().max() + 2.0 ** -12 * 4)
@@ -357,7 +361,7 @@ def test_shared_in_a_graph_with_new_lengths_and_on_a_stream(moe):
     full = b.lens.clone()
     out, lse = torch.zeros_like(b.q), torch.zeros(b.q.shape[:2], device="cuda")
     scratch = torch.zeros(moe.moe_kv_shared_bytes(*b.q.shape), dtype=torch.uint8, device="cuda")
-    args = (b.cache, b.q, b.table, b.start, b.lens, b.group_start, b.prefix_lens, out, b.workspace, scratch, lse)
+    args = (b.cache, b.q, b.table, b.start, b.lens, b.group_start, b.prefix_lens, out, b.workspace, scratch, lse, None, 1)
     moe.moe_kv_attend_shared(*args)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -375,7 +379,7 @@ def test_shared_in_a_graph_with_new_lengths_and_on_a_stream(moe):
     b.check(got)
     c = moe.KvCache(1, 2, 64, 128)
     c.k, c.v, c.k_scale, c.v_scale = b.cache
-    again, again_lse = c.attend_shared(b.q, b.table, b.start, b.lens, b.group_start, b.prefix_lens, return_lse=True, stream=side)
+    again, again_lse = c.attend_shared(b.q, b.table, b.start, b.lens, b.group_start, b.prefix_lens, return_lse=True, least_tiles=1, stream=side)
     side.synchronize()
     assert torch.equal(again, got[0]) and torch.equal(again_lse, got[1])
 
