@@ -93,9 +93,9 @@ const char* rope_fault(const moe_rope_t* r);
 
 // Launches a kernel; `chained`: by programmatic dependent launch, for kernels that wait for what they need themselves.
 template <class... Params, class... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), int grid, int threads, size_t smem, bool chained, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, bool chained, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

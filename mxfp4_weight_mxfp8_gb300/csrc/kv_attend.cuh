@@ -236,7 +236,7 @@ struct Request : Place<kMode> {
     }
     if constexpr (kMode == kSuffix) {
       this->row = r;
-      this->page0 = a.skipped[r];
+      this->page0 = __ldcg(a.skipped + r);
       seq -= this->page0 << shift;
       room -= static_cast<long long>(this->page0) << shift;
     }

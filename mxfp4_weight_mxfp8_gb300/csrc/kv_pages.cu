@@ -6,6 +6,7 @@
 // some row holds are bits of a map; a page's place among the free ones is a
 // count of the bits before it. Copy: bytes.
 #include "decode.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -135,9 +136,13 @@ struct Map {
 
 constexpr int kReclaimThreads = 256;
 
+// The launches of a call are chained: each starts while the one before it runs, and waits for its end where it needs it (what
+// that one wrote it reads from the second level).
 __global__ void __launch_bounds__(kReclaimThreads) kv_clear_kernel(const moe_kv_reclaim_t a) {
   const Map m(a);
-  for (int i = blockIdx.x * kReclaimThreads + threadIdx.x; i < m.words; i += gridDim.x * kReclaimThreads) m.bits[i] = 0;
+  ptx::grid_launch_dependents();
+  for (int i = blockIdx.x * kReclaimThreads + threadIdx.x; i < (m.words + 3) / 4; i += gridDim.x * kReclaimThreads)
+    reinterpret_cast<uint4*>(m.bits)[i] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x == 0 && threadIdx.x == 0) *m.errors = 0;
 }
 
@@ -155,14 +160,15 @@ __global__ void __launch_bounds__(kReclaimThreads) kv_mark_kernel(const moe_kv_r
   uint32_t errors = 0;
   const int r = blockIdx.y, n = held_entries(a, r, shift, errors);
   const int32_t* row = a.block_table + r * a.table_stride;
-  for (int j = blockIdx.x * kReclaimThreads + threadIdx.x; j < n; j += gridDim.x * kReclaimThreads) {
-    const int page = row[j];
-    if (page < 0 || page >= a.pages) {
-      errors |= 2;
-      continue;
-    }
-    const uint32_t bit = 1u << (page & 31);
-    if (!(*static_cast<const volatile uint32_t*>(m.bits + (page >> 5)) & bit)) atomicOr(m.bits + (page >> 5), bit);
+  const int stride = gridDim.x * kReclaimThreads;
+  int j = blockIdx.x * kReclaimThreads + threadIdx.x, page = j < n ? row[j] : -1;
+  ptx::grid_dependency_wait();  // the map is clear
+  ptx::grid_launch_dependents();
+  while (j < n) {
+    if (page < 0 || page >= a.pages) errors |= 2;
+    else atomicOr(m.bits + (page >> 5), 1u << (page & 31));
+    j += stride;
+    if (j < n) page = row[j];
   }
   errors = __reduce_or_sync(kAll, errors);
   if (errors && (threadIdx.x & 31) == 0) atomicOr(m.errors, errors);
@@ -183,32 +189,38 @@ __device__ __forceinline__ long long block_sum(int x, int* s_part) {
 // Each CTA lists the pages of a run of words: free ones, or what leaves and where it goes.
 template <bool kCompact>
 __global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_reclaim_t a, int shift, int words_per) {
-  __shared__ int s_part[kReclaimThreads / 32], s_scan[kReclaimThreads / 32];
+  __shared__ int s_part[kReclaimThreads / 32], s_scan[kReclaimThreads / 32], s_first[kReclaimThreads];
+  __shared__ uint32_t s_word[kReclaimThreads];
   const Map m(a);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int begin = blockIdx.x * words_per, end = min(begin + words_per, m.words);
+  const int begin = blockIdx.x * words_per, end = min(begin + words_per, m.words);  // (begin is a multiple of 4)
+  ptx::grid_dependency_wait();  // the marks are made
+  ptx::grid_launch_dependents();
   int held = 0, before = 0;
-  for (int i = tid; i < m.words; i += kReclaimThreads) {
-    const int c = __popc(m.bits[i]);
+  const uint4* quads = reinterpret_cast<const uint4*>(m.bits);
+#pragma unroll 4
+  for (int i = tid; i < (m.words + 3) / 4; i += kReclaimThreads) {
+    const uint4 w = __ldcg(quads + i);  // (what is past the last word is clear)
+    const int c = __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w);
     held += c;
-    before += i < begin ? c : 0;
+    before += 4 * i < begin ? c : 0;
   }
   const int n = static_cast<int>(block_sum(held, s_part));
   int at = static_cast<int>(block_sum(before, s_part));  // pages held before the CTA's first word
   int kept = 0;                                          // held pages before page n, which stay
   if (kCompact) {
     for (int i = tid; i <= n >> 5 && i < m.words; i += kReclaimThreads)
-      kept += __popc(i < n >> 5 ? m.bits[i] : m.bits[i] & ((1u << (n & 31)) - 1));
+      kept += __popc(i < n >> 5 ? __ldcg(m.bits + i) : __ldcg(m.bits + i) & ((1u << (n & 31)) - 1));
     kept = static_cast<int>(block_sum(kept, s_part));
   }
   if (blockIdx.x == 0 && tid == 0) {
     a.counts[0] = a.counts[1] = n;
     a.counts[2] = kCompact ? n - kept : 0;
-    a.counts[3] = static_cast<int>(*m.errors);
+    a.counts[3] = static_cast<int>(__ldcg(m.errors));
   }
   // Words, a lane to a page.
   for (int base = begin; base < end; base += kReclaimThreads) {
-    const uint32_t word = base + tid < end ? m.bits[base + tid] : 0;
+    const uint32_t word = base + tid < end ? __ldcg(m.bits + base + tid) : 0;
     const int own = __popc(word);
     int in = own;
 #pragma unroll
@@ -227,11 +239,12 @@ __global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_r
     }
     first += in - own;  // held before this thread's word
     at += total;
-    for (int k = 0; k < 32; ++k) {
-      const int index = base + warp * 32 + k;
-      if (index >= end) break;
-      const uint32_t bits = __shfl_sync(kAll, word, k);
-      const int page = index * 32 + lane, rank = __shfl_sync(kAll, first, k) + __popc(bits & ((1u << lane) - 1));  // held before it
+    s_word[tid] = word;
+    s_first[tid] = first;
+    __syncthreads();
+    for (int k = warp; k < kReclaimThreads && base + k < end; k += kReclaimThreads / 32) {
+      const uint32_t bits = s_word[k];
+      const int page = (base + k) * 32 + lane, rank = s_first[k] + __popc(bits & ((1u << lane) - 1));  // held before it
       const bool mine = bits >> lane & 1;
       if (page >= a.pages) continue;
       if (!kCompact) {
@@ -255,40 +268,55 @@ __global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_r
 __global__ void __launch_bounds__(kReclaimThreads) kv_rename_kernel(const moe_kv_reclaim_t a, int shift) {
   const Map m(a);
   uint32_t errors = 0;
-  const int r = blockIdx.y, used = held_entries(a, r, shift, errors), n = a.counts[0];
+  const int r = blockIdx.y, used = held_entries(a, r, shift, errors);
+  ptx::grid_dependency_wait();  // the moves are listed
+  const int n = __ldcg(a.counts);
   const int32_t* row = a.block_table + r * a.table_stride;
   int32_t* out = a.out_table + r * a.out_stride;
   for (int j = blockIdx.x * kReclaimThreads + threadIdx.x; j < a.table_width; j += gridDim.x * kReclaimThreads) {
     int page = j < used ? row[j] : -1;
     if (page >= a.pages) page = -1;
-    if (page >= n) page = a.moves[3ll * m.leaver[page] + 1];
+    if (page >= n) page = __ldcg(a.moves + 3ll * __ldcg(m.leaver + page) + 1);
     out[j] = max(page, -1);
   }
 }
 
 // ------------------------------------------------------------------------ copy
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 128;
 
-// A unit is a move's keys or values of one head; a CTA takes them in turn.
-__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const moe_kv_cache_t c, const int32_t* moves, const int32_t* count, int capacity) {
-  const int n = count ? min(max(*count, 0), capacity) : capacity;
-  const long long page_bytes = static_cast<long long>(c.kv_heads) * c.page_tokens * c.head_dim;
-  const int head_bytes = c.page_tokens * c.head_dim;
-  for (long long u = blockIdx.x; u < 2ll * n; u += gridDim.x) {
-    const int32_t* move = moves + 3 * (u >> 1);
-    const int from = move[0], to = move[1], tokens = min(move[2], c.page_tokens);
+// A unit is a move's keys or values of some heads, of a few thousand bytes; a CTA takes units in turn, eight words of a thread
+// on their way together.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const moe_kv_cache_t c, const int32_t* moves, const int32_t* count, int capacity, int heads_per) {
+  ptx::grid_dependency_wait();
+  const int n = count ? min(max(__ldcg(count), 0), capacity) : capacity;
+  const int head_words = c.page_tokens * c.head_dim / 16, parts = (c.kv_heads + heads_per - 1) / heads_per;
+  const long long page_words = static_cast<long long>(c.kv_heads) * head_words;
+  for (long long u = blockIdx.x; u < 2ll * n * parts; u += gridDim.x) {
+    const long long which = u / parts;
+    const int h0 = static_cast<int>(u - which * parts) * heads_per, heads = min(heads_per, c.kv_heads - h0);
+    const int32_t* move = moves + 3 * (which >> 1);
+    const int from = __ldcg(move), to = __ldcg(move + 1), tokens = min(__ldcg(move + 2), c.page_tokens);
     if (from < 0 || to < 0 || from >= c.pages || to >= c.pages || from == to || tokens <= 0) continue;
-    uint8_t* data = u & 1 ? c.v : c.k;
-    uint8_t* scales = u & 1 ? c.v_scale : c.k_scale;
-    const uint4* src = reinterpret_cast<const uint4*>(data + from * page_bytes);
-    uint4* dst = reinterpret_cast<uint4*>(data + to * page_bytes);
-    const int words = tokens * c.head_dim / 16, stride = head_bytes / 16, all = words * c.kv_heads;
-    for (int i = threadIdx.x; i < all; i += kCopyThreads) {
-      const int h = i / words, w = h * stride + i - h * words;
-      dst[w] = src[w];
+    uint8_t* scales = which & 1 ? c.v_scale : c.k_scale;
+    uint4* data = reinterpret_cast<uint4*>(which & 1 ? c.v : c.k) + h0 * head_words;
+    const uint4* src = data + from * page_words;
+    uint4* dst = data + to * page_words;
+    const int words = tokens * c.head_dim / 16, all = words * heads;
+    for (int base = threadIdx.x; base < all; base += 8 * kCopyThreads) {
+      uint4 v[8];
+      int at[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = base + e * kCopyThreads, h = i / words;
+        at[e] = h * head_words + i - h * words;
+        if (i < all) v[e] = src[at[e]];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (base + e * kCopyThreads < all) dst[at[e]] = v[e];
     }
-    for (int h = threadIdx.x; h < c.kv_heads; h += kCopyThreads)
-      scales[static_cast<long long>(to) * c.kv_heads + h] = scales[static_cast<long long>(from) * c.kv_heads + h];
+    if (threadIdx.x < heads)
+      scales[static_cast<long long>(to) * c.kv_heads + h0 + threadIdx.x] = scales[static_cast<long long>(from) * c.kv_heads + h0 + threadIdx.x];
   }
 }
 
@@ -311,25 +339,26 @@ cudaError_t launch_kv_fork(const moe_kv_fork_t& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_copy(const moe_kv_cache_t& c, const int32_t* moves, const int32_t* count, int capacity, cudaStream_t stream) {
-  const long long units = 2ll * capacity;
-  kv_copy_kernel<<<static_cast<int>(units < 152 * 8 ? units : 152 * 8), kCopyThreads, 0, stream>>>(c, moves, count, capacity);
-  return cudaGetLastError();
+  // Heads of about 16 KB to a unit: a page of 64 tokens and 8 heads of 128 is four (CTAs of a whole page's keys take 10 us for
+  // 56 moves, units of a head 7.5).
+  int heads_per = 16384 / (c.page_tokens * c.head_dim);
+  heads_per = heads_per < 1 ? 1 : heads_per > c.kv_heads ? c.kv_heads : heads_per;
+  const long long units = 2ll * capacity * ((c.kv_heads + heads_per - 1) / heads_per);
+  return launch_chained(kv_copy_kernel, static_cast<int>(units < 152 * 16 ? units : 152 * 16), kCopyThreads, 0, true, stream, c, moves, count, capacity, heads_per);
 }
 
 cudaError_t launch_kv_reclaim(const moe_kv_reclaim_t& a, cudaStream_t stream) {
   const int shift = shift_of(a.page_tokens), words = (a.pages + 31) / 32;
   const auto least = [](int x, int y) { return x < y ? x : y; };
-  kv_clear_kernel<<<least((words + kReclaimThreads - 1) / kReclaimThreads, 152), kReclaimThreads, 0, stream>>>(a);
+  kv_clear_kernel<<<least((words + 4 * kReclaimThreads - 1) / (4 * kReclaimThreads), 152), kReclaimThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
   const dim3 rows(least((a.table_width + kReclaimThreads - 1) / kReclaimThreads, 8), a.requests);
-  kv_mark_kernel<<<rows, kReclaimThreads, 0, stream>>>(a, shift);
-  const int ctas = least((words + 31) / 32, 152), words_per = (words + ctas - 1) / ctas, grid = (words + words_per - 1) / words_per;
-  if (a.out_table == nullptr) {
-    kv_list_kernel<false><<<grid, kReclaimThreads, 0, stream>>>(a, shift, words_per);
-    return cudaGetLastError();
-  }
-  kv_list_kernel<true><<<grid, kReclaimThreads, 0, stream>>>(a, shift, words_per);
-  kv_rename_kernel<<<rows, kReclaimThreads, 0, stream>>>(a, shift);
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = launch_chained(kv_mark_kernel, rows, kReclaimThreads, 0, true, stream, a, shift);
+  const int ctas = least((words + 7) / 8, 152), words_per = ((words + ctas - 1) / ctas + 3) / 4 * 4, grid = (words + words_per - 1) / words_per;
+  const bool compact = a.out_table != nullptr;
+  if (e == cudaSuccess) e = launch_chained(compact ? kv_list_kernel<true> : kv_list_kernel<false>, grid, kReclaimThreads, 0, true, stream, a, shift, words_per);
+  if (e == cudaSuccess && compact) e = launch_chained(kv_rename_kernel, rows, kReclaimThreads, 0, true, stream, a, shift);
+  return e;
 }
 
 }  // namespace moe

@@ -2,10 +2,9 @@
 //
 // The angle of a pair is position * turns, a whole number of 2^-64 turns: the
 // product modulo 2^64 drops whole turns exactly, and its upper half is the angle
-// to 2^-32 of a turn, whatever the position. A lane keeps the sines of its
-// eight pairs and takes the same dimensions of one head after the other, so
-// they are computed once for several heads; every element is read and written
-// once and the bytes bound it.
+// to 2^-32 of a turn, whatever the position. A CTA takes a token's heads, so the
+// sines are computed once for all of them; every element is read and written once
+// and the bytes bound it.
 #include "decode.h"
 
 namespace moe {
@@ -40,56 +39,84 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 __device__ __forceinline__ float first_of(float a, float b, float sin, float cos) { return __fmaf_rn(a, cos, -__fmul_rn(b, sin)); }
 __device__ __forceinline__ float second_of(float a, float b, float sin, float cos) { return __fmaf_rn(b, cos, __fmul_rn(a, sin)); }
 
-// A head's row is `units` units: rotated ones (8 pairs: two 16-byte words), then copied ones (a word each, where the output
-// is another tensor). `slots` lanes, a power of two, share the units of a head; the heads of a token go by in turn, `heads`
-// of them to a CTA's y.
+// A head's row is a number of units of two 16-byte words each: rotated ones (8 pairs), then copied ones, where the output is
+// another tensor. `slots` lanes, a power of two, share the units of a head, so a warp takes whole rows; the heads of a token
+// go by in turn, `heads_per` of them to a CTA's y.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const moe_rope_t a, int slots, int heads_per) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const moe_rope_t a, int slots, int heads_per, int units) {
+  __shared__ __align__(16) float s_sin[MOE_ROPE_MAX_DIM / 2], s_cos[MOE_ROPE_MAX_DIM / 2];
   const int pairs = a.rotary_dim / 2, rotated = pairs / 8, all_heads = a.q_heads + a.k_heads;
-  const int copied = (a.head_dim - a.rotary_dim) / 8;
   const int slot = threadIdx.x & (slots - 1), groups = kRopeThreads / slots, first = blockIdx.y * heads_per;
-  const int last = min(first + heads_per, all_heads);
-  const int t = blockIdx.x;
-  const int position = a.positions[t];
+  const int last = min(first + heads_per, all_heads), t = blockIdx.x;
   const Rows q{static_cast<const uint16_t*>(a.q) + t * a.q_token_stride, static_cast<uint16_t*>(a.q_out) + t * a.q_out_token_stride,
                0, a.q_head_stride, 0, a.q_out_head_stride};
   const Rows k{static_cast<const uint16_t*>(a.k) + t * a.k_token_stride, static_cast<uint16_t*>(a.k_out) + t * a.k_out_token_stride,
                0, a.k_head_stride, 0, a.k_out_head_stride};
-  for (int u = slot; u < rotated; u += slots) {
-    float sin[8], cos[8];
+  const auto from_of = [&](int h) { return h >= a.q_heads ? k.from + (h - a.q_heads) * k.head : q.from + h * q.head; };
+  const auto to_of = [&](int h) { return h >= a.q_heads ? k.to + (h - a.q_heads) * k.to_head : q.to + h * q.to_head; };
+  const int rounds = (units + slots - 1) / slots;
+  for (int round = 0; round < rounds; ++round) {
+    const int u = slot + round * slots;
+    const bool turned = u < rotated;
+    const int at0 = !turned ? a.rotary_dim + (u - rotated) * 16 : kInterleaved ? u * 16 : u * 8;
+    const int at1 = !turned || kInterleaved ? at0 + 8 : at0 + pairs;
+    const bool has0 = u < units, has1 = has0 && at1 < a.head_dim;  // (a copied unit may be one word)
+    // Two heads' elements are on their way while the sines are computed; then always the next two.
+    int h = first + threadIdx.x / slots;
+    uint4 x[2], y[2];
+    const auto load = [&](int from) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sin_cos(a.turns[u * 8 + j], position, a.amplitude, sin[j], cos[j]);
-    const int at0 = kInterleaved ? u * 16 : u * 8, at1 = kInterleaved ? at0 + 8 : at0 + pairs;
-#pragma unroll 2
-    for (int h = first + threadIdx.x / slots; h < last; h += groups) {
-      const bool key = h >= a.q_heads;
-      const uint16_t* from = key ? k.from + (h - a.q_heads) * k.head : q.from + h * q.head;
-      uint16_t* to = key ? k.to + (h - a.q_heads) * k.to_head : q.to + h * q.to_head;
-      const uint4 x = *reinterpret_cast<const uint4*>(from + at0), y = *reinterpret_cast<const uint4*>(from + at1);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-      uint32_t xo[4], yo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kInterleaved) {
-          const float a0 = low(xs[j]), b0 = high(xs[j]), a1 = low(ys[j]), b1 = high(ys[j]);
-          xo[j] = pack(first_of(a0, b0, sin[j], cos[j]), second_of(a0, b0, sin[j], cos[j]));
-          yo[j] = pack(first_of(a1, b1, sin[4 + j], cos[4 + j]), second_of(a1, b1, sin[4 + j], cos[4 + j]));
-        } else {
-          const float a0 = low(xs[j]), a1 = high(xs[j]), b0 = low(ys[j]), b1 = high(ys[j]);
-          xo[j] = pack(first_of(a0, b0, sin[2 * j], cos[2 * j]), first_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
-          yo[j] = pack(second_of(a0, b0, sin[2 * j], cos[2 * j]), second_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
+      for (int e = 0; e < 2; ++e)
+        if (from + e * groups < last) {
+          const uint16_t* p = from_of(from + e * groups);
+          if (has0) x[e] = *reinterpret_cast<const uint4*>(p + at0);
+          if (has1) y[e] = *reinterpret_cast<const uint4*>(p + at1);
         }
-      }
-      *reinterpret_cast<uint4*>(to + at0) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-      *reinterpret_cast<uint4*>(to + at1) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+    };
+    load(h);
+    if (round == 0) {
+      const int position = a.positions[t];
+      for (int i = threadIdx.x; i < pairs; i += kRopeThreads) sin_cos(a.turns[i], position, a.amplitude, s_sin[i], s_cos[i]);
+      __syncthreads();
     }
-  }
-  for (int i = threadIdx.x; i < copied * (last - first); i += kRopeThreads) {
-    const int h = first + i / copied, at = a.rotary_dim + i % copied * 8;
-    const bool key = h >= a.q_heads;
-    const uint16_t* from = key ? k.from + (h - a.q_heads) * k.head : q.from + h * q.head;
-    uint16_t* to = key ? k.to + (h - a.q_heads) * k.to_head : q.to + h * q.to_head;
-    if (from != to) *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+    float sin[8], cos[8];
+    if (turned) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<float4*>(sin + j) = *reinterpret_cast<const float4*>(s_sin + u * 8 + j);
+        *reinterpret_cast<float4*>(cos + j) = *reinterpret_cast<const float4*>(s_cos + u * 8 + j);
+      }
+    }
+    for (; h < last; h += 2 * groups) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (h + e * groups >= last) continue;
+        uint4 xo = x[e], yo = y[e];
+        if (turned) {
+          const uint32_t xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+          uint32_t p[4], r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (kInterleaved) {
+              const float a0 = low(xs[j]), b0 = high(xs[j]), a1 = low(ys[j]), b1 = high(ys[j]);
+              p[j] = pack(first_of(a0, b0, sin[j], cos[j]), second_of(a0, b0, sin[j], cos[j]));
+              r[j] = pack(first_of(a1, b1, sin[4 + j], cos[4 + j]), second_of(a1, b1, sin[4 + j], cos[4 + j]));
+            } else {
+              const float a0 = low(xs[j]), a1 = high(xs[j]), b0 = low(ys[j]), b1 = high(ys[j]);
+              p[j] = pack(first_of(a0, b0, sin[2 * j], cos[2 * j]), first_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
+              r[j] = pack(second_of(a0, b0, sin[2 * j], cos[2 * j]), second_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
+            }
+          }
+          xo = make_uint4(p[0], p[1], p[2], p[3]);
+          yo = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+        uint16_t* to = to_of(h + e * groups);
+        if (!turned && to == from_of(h + e * groups)) continue;  // in place: as it is
+        if (has0) *reinterpret_cast<uint4*>(to + at0) = xo;
+        if (has1) *reinterpret_cast<uint4*>(to + at1) = yo;
+      }
+      load(h + 2 * groups);
+    }
   }
 }
 
@@ -208,12 +235,15 @@ cudaError_t launch_rope(const moe_rope_t& a, cudaStream_t stream) {
     rope_elements_kernel<<<dim3(a.tokens, parts(1)), kRopeThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
+  // Nothing is copied in place.
+  const bool copies = a.q != a.q_out || (a.k_heads && a.k != a.k_out);
+  const int units = a.rotary_dim / 16 + (copies ? (a.head_dim - a.rotary_dim + 15) / 16 : 0);
   int slots = 1;
-  while (slots < a.rotary_dim / 16 && slots < 32) slots *= 2;
+  while (slots < units && slots < 32) slots *= 2;
   const int groups = kRopeThreads / slots, n = parts(groups), per = (heads + n - 1) / n;
   const dim3 grid(a.tokens, (heads + per - 1) / per);
-  if (a.interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, slots, per);
-  else rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a, slots, per);
+  if (a.interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, slots, per, units);
+  else rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a, slots, per, units);
   return cudaGetLastError();
 }
 
