@@ -817,8 +817,9 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
  * Both tensors are device memory. Shared are the whole pages that every query of the group
  * sees: prefix_len is held to the group's shortest cached context. Requests
  * without queries take no part (their rows may hold anything), a prefix that one
- * request reads, a length of 0 or below, and groups that do not cover the
- * requests in order share nothing, and the call is moe_kv_attend's then.
+ * request reads, a length of 0 or below, groups that do not cover the requests in
+ * order and query_start that falls anywhere share nothing, and the call is
+ * moe_kv_attend's then.
  *   scratch  device, moe_kv_shared_bytes(tokens, q_heads, head_dim) bytes, 16-byte
  *            aligned, whatever they hold; the call's own while it runs
  * Everything else as for moe_kv_attend, the workspace and its status too.

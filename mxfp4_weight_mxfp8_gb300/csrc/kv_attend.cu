@@ -114,7 +114,8 @@ static_assert((7 * MOE_KV_MAX_REQUESTS + 3 * kAttendMaxCtas) % 2 == 0, "alignmen
 
 // What of a group's prefix its requests can share: whole pages that every query of theirs sees and the tables have. Of
 // requests without queries nothing is asked; a prefix that only one request reads is left to that. Groups that do not cover
-// the requests in order share nothing; nor does a call in which that would save less than p.least_tiles tiles.
+// the requests in order share nothing, nor do requests whose query rows do not follow each other (a group's rows would not be
+// theirs), nor does a call in which that would save less than p.least_tiles tiles.
 __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_batch_t b, const moe_kv_prefixes_t p, const SharedWork w, Scratch s) {
   __shared__ int s_least[kPlanThreads], s_row[kPlanThreads], s_count[kPlanThreads], s_start[kPlanThreads + 1];
   __shared__ unsigned long long s_saved;
@@ -127,10 +128,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
     s_row[tid] = 0x7FFFFFFF;
     s_count[tid] = 0;
   }
+  int first = 0, n = 0, behind = 0;  // a request's rows; the tokens before them
+  bool falls = false;
+  if (tid < b.requests) {
+    const int from = b.query_start[tid], to = b.query_start[tid + 1];
+    falls = from > to;
+    first = min(max(from, 0), b.tokens);
+    n = min(max(to, first), b.tokens) - first;
+    behind = b.seq_lens[tid];
+  }
   if (tid < p.groups) s_start[tid] = p.group_start[tid];
   if (tid == 0) s_start[p.groups] = p.group_start[p.groups];
   __syncthreads();
-  const bool fine = !__syncthreads_or((tid < p.groups && s_start[tid] > s_start[tid + 1]) || s_start[0] != 0 || s_start[p.groups] != b.requests);
+  const bool fine = !__syncthreads_or(falls || (tid < p.groups && s_start[tid] > s_start[tid + 1]) || s_start[0] != 0 || s_start[p.groups] != b.requests);
   int group = 0;
   if (tid < b.requests && fine) {
     int hi = p.groups;  // s_start[group] <= tid < s_start[hi]
@@ -139,9 +149,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
       if (s_start[mid] <= tid) group = mid;
       else hi = mid;
     }
-    const int first = min(max(b.query_start[tid], 0), b.tokens), n = min(max(b.query_start[tid + 1], first), b.tokens) - first;
     if (n > 0) {
-      atomicMin(s_least + group, b.seq_lens[tid] - n);
+      atomicMin(s_least + group, behind - n);
       atomicMin(s_row + group, tid);
       atomicAdd(s_count + group, 1);
     }
@@ -163,12 +172,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
   __syncthreads();
   if (s_saved < static_cast<unsigned long long>(p.least_tiles)) tokens = 0;
   if (tid < p.groups) {
-    s.start[tid] = b.query_start[fine ? s_start[tid] : 0];
+    s.start[tid] = min(max(b.query_start[fine ? s_start[tid] : 0], 0), b.tokens);  // (the merging launch takes it as it is)
     s.prefix[tid] = tokens;
     s.row[tid] = tokens ? s_row[tid] : 0;
     s_least[tid] = tokens >> w.shift;
   }
-  if (tid == 0) s.start[p.groups] = b.query_start[fine ? b.requests : 0];
+  if (tid == 0) s.start[p.groups] = min(max(b.query_start[fine ? b.requests : 0], 0), b.tokens);
   __syncthreads();
   if (tid < b.requests) s.skipped[tid] = fine ? s_least[group] : 0;
   // The blocks of 8 rows of the groups before this one, of those that share.

@@ -252,6 +252,23 @@ def test_shared_groups_that_do_not_cover_the_requests_share_nothing(moe, starts)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("change", [{0: -5}, {0: -2 ** 31}, {-1: 2 ** 31 - 1}, {0: -3, -1: 10 ** 6}, {-1: 0}, {-1: -7}, {-2: 10 ** 6}])
+def test_shared_query_starts_out_of_range_are_what_they_are_to_attend(moe, change, rows):
+    """Starts below 0 and past the tokens count as those; one that falls leaves its request no rows."""
+    b = Batch(moe, [(160, [(9, rows)] * 2), (96, [(rows, rows), (70, rows), (80, rows)])], 16, 2, 64, 4, seed=21)
+    for at, value in change.items():
+        b.start[at] = value
+    out, lse = b.run()
+    want, want_lse = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    moe.moe_kv_attend(b.cache, b.q, b.table, b.start, b.lens, want, b.workspace, lse=want_lse)
+    assert torch.equal((lse == 7.0), (want_lse == 7.0)) and torch.equal((out == 7.0).all(2), (want_lse == 7.0))
+    # Each is half a step of BF16 and 2^-12 of sum_j w_j |v_j| <= 448 / 16 off, its log-sum-exp 1.6e-4.
+    assert ((out.double() - want.double()).abs() <= 1.01 * (2.0 ** -7 * want.double().abs() + 2.0 ** -11 * 28)).all()
+    assert ((lse - want_lse).abs()[want_lse != 7.0] <= 3.2e-4).all()
+
+
+@pytest.mark.gpu
 def test_shared_empty_groups_and_tables_with_holes(moe):
     b = Batch(moe, [(100, same(2, 10)), (200, same(3, 20))], 16, 1, 64, 4, seed=6)
     b.group_start = torch.tensor([0, 0, 2, 2, 5], dtype=torch.int32, device="cuda")
