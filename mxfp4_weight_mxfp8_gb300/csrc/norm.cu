@@ -252,7 +252,7 @@ cudaError_t launch_row(const moe_norm_t& a, cudaStream_t stream) {
   const int chunks = (a.hidden + kChunk - 1) / kChunk;
   if (chunks <= 128) {
     // A warp to a row, four rows to a CTA.
-    const int grid = (a.tokens + 3) / 4;
+    const int grid = a.tokens / 4 + (a.tokens % 4 != 0);
     if (!kVector || chunks > 64) norm_kernel<XW, RW, 4, kVector, true><<<grid, 128, 0, stream>>>(a);
     else if (chunks > 32) norm_kernel<XW, RW, 2, true, true><<<grid, 128, 0, stream>>>(a);
     else norm_kernel<XW, RW, 1, true, true><<<grid, 128, 0, stream>>>(a);

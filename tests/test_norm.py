@@ -210,6 +210,15 @@ def test_norm_magnitudes_from_the_smallest_to_the_largest(moe, hidden, dtype):
 
 
 @pytest.mark.gpu
+def test_norm_of_as_many_rows_as_there_can_be(moe):
+    """2^31 - 1 rows of one element (4 GB), from an input that is broadcast."""
+    x = torch.full((1, 1), 3.0, dtype=torch.bfloat16, device="cuda").expand(2 ** 31 - 1, 1)
+    out = torch.zeros(2 ** 31 - 1, 1, dtype=torch.bfloat16, device="cuda")
+    moe.moe_norm(x, torch.full((1,), 0.5, device="cuda"), out, 1e-6)  # 3 * 0.5 / sqrt(9 + 1e-6): 0.5 in BF16
+    assert (out == 0.5).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("hidden", [64, 1000, 3584])
 def test_norm_zeros_infinities_and_nan(moe, hidden):
     x = torch.ones(5, hidden, dtype=torch.bfloat16, device="cuda")
