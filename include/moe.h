@@ -724,7 +724,8 @@ int moe_rope_turns(int rotary_dim, double base, int scaling, double factor, doub
  *                longer than its row (what is past it has no page), 8 free pages
  *                exhausted (the entries concerned are -1, with no move)
  * All device memory. No output overlaps an input or another output. requests
- * and rows <= MOE_KV_MAX_REQUESTS. The same inputs give the same outputs.
+ * and rows <= MOE_KV_MAX_REQUESTS, table_width <= 2^30. The same inputs give the
+ * same outputs.
  */
 typedef struct moe_kv_fork_t {
   const int32_t* parents;
@@ -767,7 +768,9 @@ int moe_kv_copy(const moe_kv_cache_t* cache, const int32_t* moves, const int32_t
  *                moves, and error bits: 1 a negative length (counted as 0), 2 an
  *                entry held outside the pool (left out), 4 a length longer than
  *                its row (the row's entries count)
- *   workspace    MOE_KV_RECLAIM_BYTES(pages), 16-byte aligned, whatever it holds
+ *   workspace    MOE_KV_RECLAIM_BYTES(pages), 16-byte aligned, whatever it holds;
+ *                the call's own while it runs (of two at once the outputs are
+ *                undefined)
  * Compaction (both or neither null): the held pages from n on go to the free ones
  * before n, both in rising order, so that the pool's first n pages are held.
  *   out_table    int32 [requests, table_width], rows out_stride apart: the rows
@@ -777,8 +780,8 @@ int moe_kv_copy(const moe_kv_cache_t* cache, const int32_t* moves, const int32_t
  *                of them, for moe_kv_copy with count = &counts[2]; the rest is
  *                not written
  * All device memory. Otherwise no output overlaps an input or another output.
- * requests <= MOE_KV_MAX_REQUESTS, pages <= 2^30. The same inputs give the same
- * outputs.
+ * requests <= MOE_KV_MAX_REQUESTS, pages and table_width <= 2^30. The same inputs
+ * give the same outputs.
  */
 #define MOE_KV_RECLAIM_BYTES(pages) (1024 + 8 * (size_t)(pages))
 

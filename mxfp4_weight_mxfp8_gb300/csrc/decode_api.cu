@@ -184,7 +184,7 @@ int moe_kv_fork(const moe_kv_fork_t* f, void* stream) {
   if (f->requests < 1 || f->requests > MOE_KV_MAX_REQUESTS || f->rows < 1 || f->rows > MOE_KV_MAX_REQUESTS)
     return refuse("requests or rows out of range");
   if (!page_size_ok(f->page_tokens)) return refuse("page_tokens must be 16, 32, 64 or 128");
-  if (f->free_count < 0 || f->table_width < 1 || f->table_stride < f->table_width || f->out_stride < f->table_width)
+  if (f->free_count < 0 || f->table_width < 1 || f->table_width > 1 << 30 || f->table_stride < f->table_width || f->out_stride < f->table_width)
     return refuse("free_count or table size out of range");
   if (!f->parents || !f->block_table || !f->seq_lens || !f->free_head || !f->out_table || !f->out_lens || !f->moves || !f->counts ||
       (f->free_count && !f->free_pages))
@@ -219,7 +219,7 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* r, void* stream) {
   if (r->requests < 1 || r->requests > MOE_KV_MAX_REQUESTS) return refuse("requests out of range");
   if (!page_size_ok(r->page_tokens)) return refuse("page_tokens must be 16, 32, 64 or 128");
   if (r->pages < 1 || r->pages > 1 << 30) return refuse("pages out of range");
-  if (r->table_width < 1 || r->table_stride < r->table_width) return refuse("table size out of range");
+  if (r->table_width < 1 || r->table_width > 1 << 30 || r->table_stride < r->table_width) return refuse("table size out of range");
   if ((r->out_table == nullptr) != (r->moves == nullptr)) return refuse("out_table and moves come together");
   if (r->out_table && r->out_stride < r->table_width) return refuse("table size out of range");
   if (!r->block_table || !r->seq_lens || !r->free_pages || !r->counts || !r->workspace) return refuse("null pointer");

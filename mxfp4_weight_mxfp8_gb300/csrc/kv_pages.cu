@@ -186,6 +186,12 @@ __device__ __forceinline__ long long block_sum(int x, int* s_part) {
   return sum;
 }
 
+// Where the k-th move is listed: below the room that moves have, whatever another call with the same workspace makes of the
+// map meanwhile (its counts are wrong then, but nothing is written or read outside).
+__device__ __forceinline__ int32_t* move_at(const moe_kv_reclaim_t& a, int k) {
+  return a.moves + 3ll * min(static_cast<uint32_t>(k), static_cast<uint32_t>(max(a.pages / 2, 1) - 1));
+}
+
 // Each CTA lists the pages of a run of words: free ones, or what leaves and where it goes.
 template <bool kCompact>
 __global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_reclaim_t a, int shift, int words_per) {
@@ -248,17 +254,18 @@ __global__ void __launch_bounds__(kReclaimThreads) kv_list_kernel(const moe_kv_r
       const bool mine = bits >> lane & 1;
       if (page >= a.pages) continue;
       if (!kCompact) {
-        if (!mine) a.free_pages[n + (page - rank)] = page;
+        if (!mine) a.free_pages[min(static_cast<uint32_t>(n + (page - rank)), static_cast<uint32_t>(a.pages - 1))] = page;
       } else {
         if (page >= n) {
           a.free_pages[page] = page;
           if (mine) {
             m.leaver[page] = rank - kept;
-            a.moves[3ll * (rank - kept)] = page;
+            move_at(a, rank - kept)[0] = page;
           }
         } else if (!mine) {
-          a.moves[3ll * (page - rank) + 1] = page;
-          a.moves[3ll * (page - rank) + 2] = 1 << shift;
+          int32_t* move = move_at(a, page - rank);
+          move[1] = page;
+          move[2] = 1 << shift;
         }
       }
     }
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kReclaimThreads) kv_rename_kernel(const moe_kv
   for (int j = blockIdx.x * kReclaimThreads + threadIdx.x; j < a.table_width; j += gridDim.x * kReclaimThreads) {
     int page = j < used ? row[j] : -1;
     if (page >= a.pages) page = -1;
-    if (page >= n) page = __ldcg(a.moves + 3ll * __ldcg(m.leaver + page) + 1);
+    if (page >= n) page = __ldcg(move_at(a, __ldcg(m.leaver + page)) + 1);
     out[j] = max(page, -1);
   }
 }

@@ -129,6 +129,7 @@ def fork_block(moe, **changes):
 
 @pytest.mark.parametrize("changes", [
     dict(requests=0), dict(requests=1025), dict(rows=0), dict(rows=1025), dict(page_tokens=17), dict(free_count=-1), dict(table_width=0),
+    dict(table_width=2 ** 31 - 1, table_stride=2 ** 31, out_stride=2 ** 31),
     dict(table_stride=7), dict(out_stride=7), dict(parents=0), dict(block_table=0), dict(seq_lens=0), dict(free_pages=0), dict(free_head=0),
     dict(out_table=0), dict(out_lens=0), dict(moves=0), dict(counts=0), dict(parents=0x1002), dict(out_table=0x20001),
     dict(out_table=0x10000), dict(out_table=0x10020), dict(out_lens=0x2008), dict(counts=0x4000 - 12), dict(moves=0x5004), dict(counts=0x6010)])
@@ -147,6 +148,7 @@ def reclaim_block(moe, **changes):
 
 @pytest.mark.parametrize("changes", [
     dict(requests=0), dict(requests=1025), dict(page_tokens=8), dict(pages=0), dict(pages=(1 << 30) + 1), dict(table_width=0), dict(table_stride=4),
+    dict(table_width=2 ** 31 - 1, table_stride=2 ** 31, out_table=0, moves=0, block_table=0x100000, free_pages=0x1000, seq_lens=0x900),
     dict(out_stride=7), dict(out_table=0), dict(moves=0), dict(block_table=0), dict(seq_lens=0), dict(free_pages=0), dict(counts=0),
     dict(workspace=0), dict(workspace=0x40008), dict(counts=0x4002), dict(free_pages=0x2000), dict(out_table=0x10004), dict(counts=0x3004),
     dict(out_table=0x10000, out_stride=9), dict(moves=0x10010), dict(workspace=0x30100)])
