@@ -683,8 +683,9 @@ int moe_rope(const moe_rope_t* rope, void* stream);
  *     positions stay, those that turn at most `low` times take f_i / factor,
  *     those between f_i (s + (1 - s) / factor), s = (turns - low) / (high - low)
  *   MOE_ROPE_RAMP:   the same, s linear in the pair's index i instead, between the
- *     indices (rounded up and down to whole ones) of the pairs that turn `low`
- *     and `high` times
+ *     indices of the pairs that turn `high` times (rounded down, 0 at least) and
+ *     `low` times (rounded up, rotary_dim - 1 at most: the last pair may be in the
+ *     middle of the ramp)
  *   turns[i] = f_i / (2 pi) * 2^64, rounded, modulo 2^64.
  * base > 1; factor, trained > 0; 0 < low < high (not looked at by LINEAR).
  * Writes turns[rotary_dim / 2], host memory.

@@ -134,7 +134,7 @@ int moe_rope_turns(int rotary_dim, double base, int scaling, double factor, doub
   double from = 0.0, to = 1.0;
   if (scaling == MOE_ROPE_RAMP) {
     from = std::fmax(std::floor(index(high)), 0.0);
-    to = std::fmin(std::ceil(index(low)), rotary_dim / 2 - 1.0);
+    to = std::fmin(std::ceil(index(low)), rotary_dim - 1.0);
     if (to <= from) to = from + 0.001;  // a step
   }
   for (int i = 0; i < rotary_dim / 2; ++i) {
