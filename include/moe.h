@@ -817,7 +817,8 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
  *   least_tiles  prefixes are shared only if that saves the call so many tiles of
  *                work (128 tokens of a cache head for 8 query rows of a request);
  *                0: the library's own number, below which two launches take
- *                longer than one; 1: whatever it saves
+ *                longer than one; 1: whatever it saves. From 2 on (and for 0)
+ *                a group counts only if it saves a quarter of its prefix's work
  * Both tensors are device memory. Shared are the whole pages that every query of the group
  * sees: prefix_len is held to the group's shortest cached context. Requests
  * without queries take no part (their rows may hold anything), a prefix that one

@@ -40,12 +40,15 @@ struct AttendArgs {
   const int32_t* group_token;
   const int32_t* group_prefix;
   const int32_t* group_block;
-  int chained;  // whether the launch may start while the one before it runs
+  const int32_t* shared;  // blocks of rows in all; 0: nothing is shared
+  int early;  // kPrefix: whether it may work while the launch before it runs
 };
 
 // Items of more units of work may be cut between CTAs in the 128-row form (the others' all may).
 constexpr int kAttendRowsLong = 16;
-// Pieces of an item are joined in runs of about the square root of their number; so many are merged as they are.
+constexpr int kAttendRowsCtas = 240;
+// Pieces of an item are joined in runs of about the square root of their number; so many are merged as they are. (Those of
+// the 128-row form always are.)
 constexpr int kAttendMerged = 32;
 __host__ __device__ inline int attend_join_width(int pieces) {
   int width = 8;

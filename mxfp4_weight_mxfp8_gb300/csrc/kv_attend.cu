@@ -70,12 +70,15 @@ int row_tile(const AttendArgs& a) {
 }
 
 // ------------------------------------------------------------- shared prefixes
-constexpr int kPlanThreads = 1024;
-// Prefixes are shared from this much saved work on, in tiles of 8 rows: what two launches more cost. (One prefix of 8192
-// tokens, 64 query heads on 8 of 128: 8 requests, 3000 tiles, take 38.0 us with it and 41.1 without, 4 requests 37.6 and
-// 31.6, 16 requests 39.8 and 61.8; 64 requests on 1024 tokens, 3560 tiles, 55.1 and 49.5, on 2048 51.3 and 69.8. Heads of 64
-// and 256 turn at about the same number.)
-constexpr int kLeastTiles = 3500;
+// Prefixes are shared from this much saved work on, in tiles of 8 rows: what two launches, their starts and the merging cost.
+// One prefix of 8192 tokens, 64 query heads on 8 of 128: 8 requests, 3020 tiles, take 37.9 us with it and 36.9 without, 4
+// requests 36.8 and 27.0, 16 requests 39.1 and 57.6; 64 requests on 1024 tokens, 3558 tiles, 54.2 and 43.7, on 2048 50.6 and
+// 63.4 (and 4 to 7 us go to looking where nothing is shared in the end). Heads of 64 turn at the same number. A tile of 256
+// takes twice as long: 8 requests on 8192 tokens, 1638 tiles, 54.3 and 63.1, 64 on 2048, 3276 tiles, 109 and 125.
+constexpr int least_tiles(int head_dim) { return head_dim == 256 ? 1600 : 3700; }
+// And of those only groups for whom it saves a share of their prefix's work: what rows fill already many row tiles of their
+// own reads a prefix as often either way (16 requests with up to 300 rows of 256 each: 506 us with it, 460 without).
+constexpr int kLeastShare = 4;
 // What a tile costs in row tiles of 8, 16, 24, 32 rows and (0) in the form of 128, in tenths of the first (from 64 ragged
 // requests with 8 to 32 rows, 62 to 96 us, and 1.95 us a tile and SM in the form of 128).
 constexpr int kTileCost[] = {21, 10, 12, 14, 15};
@@ -87,7 +90,6 @@ struct SharedWork {
   int own;                    // cost of a tile of the prefix to a request
   int rows, cost;             // of the prefixes' launch: rows of a row tile, a tile's cost
 };
-static_assert(MOE_KV_MAX_REQUESTS <= kPlanThreads, "a thread to a request, and to a group");
 
 // Scratch: the groups' first query tokens, prefixes (tokens) and rows of the block table, the pages that each request skips;
 // the arrival counters of the requests' part, the groups' first blocks of 8 rows and units of work; then each row's log-sum-exp and output over its prefix.
@@ -116,31 +118,36 @@ static_assert((7 * MOE_KV_MAX_REQUESTS + 3 * kAttendMaxCtas) % 2 == 0, "alignmen
 // requests without queries nothing is asked; a prefix that only one request reads is left to that. Groups that do not cover
 // the requests in order share nothing, nor do requests whose query rows do not follow each other (a group's rows would not be
 // theirs), nor does a call in which that would save less than p.least_tiles tiles.
-__global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_batch_t b, const moe_kv_prefixes_t p, const SharedWork w, Scratch s) {
-  __shared__ int s_least[kPlanThreads], s_row[kPlanThreads], s_count[kPlanThreads], s_start[kPlanThreads + 1];
+// A thread to a request, and to a group; everything that is read is on its way at once.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) kv_shared_kernel(const moe_kv_batch_t b, const moe_kv_prefixes_t p, const SharedWork w, Scratch s) {
+  __shared__ int s_least[kThreads], s_row[kThreads], s_count[kThreads], s_start[kThreads + 1], s_first[kThreads + 1], s_warp[kThreads / 32];
   __shared__ unsigned long long s_saved;
   const int tid = threadIdx.x;
   grid_launch_dependents();  // (the next launch waits for this one's end before it reads what is written here)
-  for (int i = tid; i < 3 * kAttendMaxCtas; i += kPlanThreads) s.counters[i] = 0;
-  if (tid == 0) s_saved = 0;
-  if (tid < p.groups) {
-    s_least[tid] = 0x7FFFFFFF;
-    s_row[tid] = 0x7FFFFFFF;
-    s_count[tid] = 0;
-  }
-  int first = 0, n = 0, behind = 0;  // a request's rows; the tokens before them
-  bool falls = false;
+  const auto token = [&](int at) { return min(max(at, 0), b.tokens); };
+  int from = 0, to = 0, behind = 0, start = 0, prefix = 0;  // a request's query rows, its tokens; a group's
   if (tid < b.requests) {
-    const int from = b.query_start[tid], to = b.query_start[tid + 1];
-    falls = from > to;
-    first = min(max(from, 0), b.tokens);
-    n = min(max(to, first), b.tokens) - first;
+    from = b.query_start[tid];
+    to = b.query_start[tid + 1];
     behind = b.seq_lens[tid];
   }
-  if (tid < p.groups) s_start[tid] = p.group_start[tid];
+  if (tid < p.groups) {
+    start = p.group_start[tid];
+    prefix = p.prefix_lens[tid];
+  }
   if (tid == 0) s_start[p.groups] = p.group_start[p.groups];
+  for (int i = tid; i < 3 * kAttendMaxCtas; i += kThreads) s.counters[i] = 0;
+  if (tid == 0) s_saved = 0;
+  s_least[tid] = s_row[tid] = 0x7FFFFFFF;
+  s_count[tid] = 0;
+  if (tid < p.groups) s_start[tid] = start;
+  if (tid < b.requests) s_first[tid] = token(from);
+  if (tid == b.requests - 1) s_first[b.requests] = token(to);
   __syncthreads();
-  const bool fine = !__syncthreads_or(falls || (tid < p.groups && s_start[tid] > s_start[tid + 1]) || s_start[0] != 0 || s_start[p.groups] != b.requests);
+  bool fine = from <= to;
+  if (tid < p.groups) fine = fine && start <= s_start[tid + 1];
+  fine = __syncthreads_and(fine) && s_start[0] == 0 && s_start[p.groups] == b.requests;
   int group = 0;
   if (tid < b.requests && fine) {
     int hi = p.groups;  // s_start[group] <= tid < s_start[hi]
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
       if (s_start[mid] <= tid) group = mid;
       else hi = mid;
     }
+    const int n = token(to) - token(from);
     if (n > 0) {
       atomicMin(s_least + group, behind - n);
       atomicMin(s_row + group, tid);
@@ -156,32 +164,26 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
     }
   }
   __syncthreads();
-  int tokens = 0;
-  long long rows = 0;  // of the group
-  if (tid < p.groups) {
+  int tokens = 0, blocks = 0;
+  if (tid < p.groups && fine && s_count[tid] > 1) {
     const long long room = static_cast<long long>(b.table_width) << w.shift;
-    if (fine && s_count[tid] > 1) tokens = static_cast<int>(min(static_cast<long long>(min(p.prefix_lens[tid], s_least[tid])), room));
+    tokens = static_cast<int>(min(static_cast<long long>(min(prefix, s_least[tid])), room));
     tokens = max(tokens, 0) >> w.shift << w.shift;
     if (tokens) {
-      const int first = min(max(b.query_start[s_start[tid]], 0), b.tokens);
-      rows = static_cast<long long>(min(max(b.query_start[s_start[tid + 1]], first), b.tokens) - first) * w.group;
-      const long long saved = (static_cast<long long>(s_count[tid]) * w.own - (rows + w.rows - 1) / w.rows * w.cost) * w.kv_heads * ((tokens + 127) / 128) / 10;
-      atomicAdd(&s_saved, static_cast<unsigned long long>(max(saved, 1ll)));
+      const long long rows = static_cast<long long>(s_first[s_start[tid + 1]] - s_first[start]) * w.group;  // of the group
+      const long long own = static_cast<long long>(s_count[tid]) * w.own, less = own - (rows + w.rows - 1) / w.rows * w.cost;
+      const long long saved = less * w.kv_heads * ((tokens + 127) / 128) / 10;
+      if (p.least_tiles > 1 && kLeastShare * less < own) {
+        tokens = 0;
+      } else {
+        atomicAdd(&s_saved, static_cast<unsigned long long>(max(saved, 1ll)));
+        blocks = static_cast<int>((rows + 7) / 8);
+      }
     }
   }
   __syncthreads();
-  if (s_saved < static_cast<unsigned long long>(p.least_tiles)) tokens = 0;
-  if (tid < p.groups) {
-    s.start[tid] = min(max(b.query_start[fine ? s_start[tid] : 0], 0), b.tokens);  // (the merging launch takes it as it is)
-    s.prefix[tid] = tokens;
-    s.row[tid] = tokens ? s_row[tid] : 0;
-    s_least[tid] = tokens >> w.shift;
-  }
-  if (tid == 0) s.start[p.groups] = min(max(b.query_start[fine ? b.requests : 0], 0), b.tokens);
-  __syncthreads();
-  if (tid < b.requests) s.skipped[tid] = fine ? s_least[group] : 0;
+  if (s_saved < static_cast<unsigned long long>(p.least_tiles)) tokens = blocks = 0;
   // The blocks of 8 rows of the groups before this one, of those that share.
-  const int blocks = tokens ? static_cast<int>((rows + 7) / 8) : 0;
   int sum = blocks;
   const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -189,11 +191,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv_shared_kernel(const moe_kv_ba
     const int u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
     if (lane >= d) sum += u;
   }
-  if (lane == 31) s_row[warp] = sum;
+  if (lane == 31) s_warp[warp] = sum;
+  const int row = s_row[tid];
+  s_least[tid] = tokens >> w.shift;
   __syncthreads();
-  for (int k = 0; k < warp; ++k) sum += s_row[k];
-  if (tid < p.groups) s.block[tid] = sum - blocks;
-  if (tid == p.groups - 1) s.block[p.groups] = sum;
+  if (tid < b.requests) s.skipped[tid] = s_least[group];  // (0 everywhere where nothing is fine)
+  for (int k = 0; k < warp; ++k) sum += s_warp[k];
+  if (tid < p.groups) {
+    s.start[tid] = s_first[fine ? start : 0];  // (the merging launch takes it as it is)
+    s.prefix[tid] = tokens;
+    s.row[tid] = tokens ? row : 0;
+    s.block[tid] = sum - blocks;
+  }
+  if (tid == p.groups - 1) {
+    s.block[p.groups] = sum;
+    s.start[p.groups] = s_first[fine ? b.requests : 0];
+  }
 }
 
 }  // namespace
@@ -214,9 +227,9 @@ cudaError_t launch_kv_attend_shared(const AttendArgs& whole, const moe_kv_prefix
   AttendArgs a = whole, b = whole;  // the requests' own part, their prefixes'
   a.counters = s.counters;
   a.skipped = s.skipped;
+  a.shared = b.shared = s.block + p.groups;
   a.partial = b.partial = s.out;
   a.partial_lse = b.partial_lse = s.lse;
-  a.chained = 1;
   b.rows = s.row;
   b.group_unit = s.unit;
   b.group_token = s.start;
@@ -230,18 +243,20 @@ cudaError_t launch_kv_attend_shared(const AttendArgs& whole, const moe_kv_prefix
   const SharedWork work = {c.shift, a.group, a.c.kv_heads, static_cast<int>((average + own_rows - 1) / own_rows) * kTileCost[own_tile],
                            tile ? 8 * tile : 128, kTileCost[tile]};
   moe_kv_prefixes_t prefixes = p;
-  if (p.least_tiles == 0) prefixes.least_tiles = kLeastTiles;
-  kv_shared_kernel<<<1, kPlanThreads, 0, stream>>>(whole.b, prefixes, work, s);
+  if (p.least_tiles == 0) prefixes.least_tiles = least_tiles(whole.c.head_dim);
+  // (A small batch's few warps are through their barriers sooner.)
+  if (whole.b.requests <= 128) kv_shared_kernel<128><<<1, 128, 0, stream>>>(whole.b, prefixes, work, s);
+  else kv_shared_kernel<1024><<<1, 1024, 0, stream>>>(whole.b, prefixes, work, s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // The prefixes' part starts while the other's last CTAs run, if there is room for the pieces of both (not for twice the
-  // form of 128 rows, whose work is long).
+  // The prefixes' part works while the other's last CTAs run, if there is room for the pieces of both (not for twice the form
+  // of 128 rows, whose work is long).
   const auto piece_bytes = [&](int t) {
     return 8ull * (t ? 8 * t * kv_attend_decode_ctas(a.c.head_dim, t, c.sms) : 128 * kv_attend_rows_ctas(c.sms)) * (a.c.head_dim + 2);
   };
   const size_t theirs = (piece_bytes(tile) + 255) / 256 * 256, room = MOE_KV_WORKSPACE_BYTES - MOE_KV_WORKSPACE_HEADER;
-  b.chained = theirs + piece_bytes(own_tile) <= room;
-  a.pieces = reinterpret_cast<float*>(a.workspace + MOE_KV_WORKSPACE_HEADER + (b.chained ? theirs : 0));
+  b.early = theirs + piece_bytes(own_tile) <= room;
+  a.pieces = reinterpret_cast<float*>(a.workspace + MOE_KV_WORKSPACE_HEADER + (b.early ? theirs : 0));
   e = own_tile ? launch_kv_attend_decode_suffix(a, c.maps, own_tile, c.shift, c.sms, stream)
                : launch_kv_attend_rows_suffix(a, c.maps, c.shift, c.sms, stream);
   if (e != cudaSuccess) return e;

@@ -236,7 +236,7 @@ struct Request : Place<kMode> {
     }
     if constexpr (kMode == kSuffix) {
       this->row = r;
-      this->page0 = __ldcg(a.skipped + r);
+      this->page0 = a.skipped[r];
       seq -= this->page0 << shift;
       room -= static_cast<long long>(this->page0) << shift;
     }
@@ -485,9 +485,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* st
 }
 
 // Prefix sums of the requests' work, by the whole CTA of kThreads threads; returns what an item counts as: nothing
-// while there are no more tiles than CTAs, so that each gets one, else kItemTiles.
-template <int kMode, int kThreads, int kRows, int kItemTiles>
-__device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long long (*s_sum)[2]) {
+// while there are no more tiles than CTAs, so that each gets one, else item_tiles.
+template <int kMode, int kThreads, int kRows>
+__device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long long* prefix, long long (*s_sum)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.b.requests + kThreads - 1) / kThreads;
   long long tiles = 0, items = 0;
@@ -521,7 +521,7 @@ __device__ int sum_work(const AttendArgs& a, int shift, long long* prefix, long 
       items_at += s_sum[w][1];
     }
   }
-  const int weight = all > gridDim.x ? kItemTiles : 0;
+  const int weight = all > gridDim.x ? item_tiles : 0;
   long long at = tiles_at + items_at * weight;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
@@ -638,12 +638,6 @@ __device__ __forceinline__ int piece_at(int i, int c4) {
   return kMode == kPrefix && kRows == 128 ? attend_quad_at(i, c4) : i * D + c4;
 }
 
-// Quad c of row i in a piece of kPrefix: row by row, or in the 128-row form, whose threads hold rows, quad by quad.
-template <int kRows, int D>
-__device__ __forceinline__ int quad_at(int i, int c) {
-  return kRows == 128 ? (c * kRows + i) * 4 : i * D + c * 4;
-}
-
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
 // is kBarrier. row_dst: the rows' places among the outputs' rows.
 template <int kMode, int kRows, int D, int kThreads, int kBarrier>
@@ -658,7 +652,7 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
   const int c1 = static_cast<int>(divide((s.item + s.units) * ctas - 1, total));
   // The pieces are joined in two steps, by about the square root of their number at a time: by the last CTA of
   // each run of `width` pieces, then by the last of those, so no CTA reads more than a few dozen pieces. (kPrefix: the first
-  // step alone, where there are more than the merging launch takes.)
+  // step alone, where there are many; the merging launch takes the runs'.)
   float* piece1 = partials + static_cast<int64_t>(c0 * 2 + 1) * kPartialFloats;  // the first piece
   float* piece0 = partials + static_cast<int64_t>(c0 * 2) * kPartialFloats;      // piece i: 2 i slots on
   auto piece = [&](int i) { return i == 0 ? piece1 : piece0 + static_cast<int64_t>(i) * 2 * kPartialFloats; };

@@ -67,6 +67,9 @@ struct Shape {
   // (64 ragged requests of 128: 8 rows take 102 us with 2, 106 with 1 or 5; 24 rows 84 with 4, 88 with 7; of 64: 8 rows 54
   // with 3 to 5, 61 with 1).
   static constexpr int kItemTiles = RT + (D == 64 ? 3 : 1);
+  // The same for short items, the requests' own behind a shared prefix (36 requests with 32 rows of 64 and up to 1500 tokens
+  // behind prefixes of up to 5000, 12 alone: 81 us with 3, 84 with 7; the other shapes turn where they do above).
+  static constexpr int kOwnItemTiles = D == 64 ? 3 : kItemTiles;
   static constexpr int kPartialFloats = kRows * (D + 2);  // rows, then maxima, then sums
   static constexpr int kTmem = 2 * kCols + kHalves * kCols <= 64 ? 64 : 2 * kCols + kHalves * kCols <= 128 ? 128 : 256;
   static constexpr int kRing = 0;
@@ -204,7 +207,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   float* partials = pieces_of<kMode>(a);
 
   if constexpr (kMode == kPrefix) {
-    if (__ldcg(a.group_block + a.b.requests) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
+    if (!a.early) grid_dependency_wait();
+    if (__ldcg(a.shared) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
       if (blockIdx.x == 0) grid_dependency_wait();
       return;
     }
@@ -226,7 +230,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
     fence_mbar_init();
   }
   if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
-  const int weight = sum_work<kMode, X::kThreads, X::kRows, X::kItemTiles>(a, shift, prefix, s_sum);
+  const int item_tiles = kMode == kSuffix && *a.shared > 0 ? X::kOwnItemTiles : X::kItemTiles;
+  const int weight = sum_work<kMode, X::kThreads, X::kRows>(a, item_tiles, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   // (Whatever it does, kPrefix's launch ends after kSuffix's.)
@@ -679,7 +684,7 @@ cudaError_t launch_shape(const AttendArgs& a, const AttendMaps& maps, int shift,
                              Shape<D, RT>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
   return launch_chained(kv_attend_kernel<kMode, D, RT>, decode_ctas(D, RT, sms), Shape<D, RT>::kThreads, smem,
-                        kMode != kWhole && a.chained, stream, a, maps, shift);
+                        kMode != kWhole, stream, a, maps, shift);
 }
 
 // The form of row tiles of 8 * tile rows (heads of 256: of 16 at most).

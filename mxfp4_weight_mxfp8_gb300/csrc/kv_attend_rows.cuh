@@ -79,7 +79,7 @@ struct RowsShape {
 // with 8; one of 900 tokens with a window of 100: 104 with 4, 100 with 5; the chunks: 313 with any).
 constexpr int kItemTiles = 5;
 constexpr int kLongUnits = kAttendRowsLong;       // longer items may be cut anywhere (one head to a group, 900 tokens: 46 -> 34.6 us)
-constexpr int kMaxRowsCtas = 240;  // two pieces each fit the workspace
+constexpr int kMaxRowsCtas = kAttendRowsCtas;  // two pieces each fit the workspace
 static_assert(kPartialOffset + 2ll * kMaxRowsCtas * kRows * (128 + 2) * 4 <= MOE_KV_WORKSPACE_BYTES, "workspace");
 
 // Sixteen consecutive TMEM columns of this thread's lane, without the wait.
@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* partials = pieces_of<kMode>(a);
 
   if constexpr (kMode == kPrefix) {
-    if (__ldcg(a.group_block + a.b.requests) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
+    if (!a.early) grid_dependency_wait();
+    if (__ldcg(a.shared) == 0) {  // nothing is shared (this launch ends after kSuffix's all the same)
       if (blockIdx.x == 0) grid_dependency_wait();
       return;
     }
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
-  const int weight = sum_work<kMode, kThreads, kRows, kItemTiles>(a, shift, prefix, s_sum);
+  const int weight = sum_work<kMode, kThreads, kRows>(a, kItemTiles, shift, prefix, s_sum);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   // (Whatever it does, kPrefix's launch ends after kSuffix's.)
@@ -623,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kOwn; c += 4)
           *reinterpret_cast<float4*>(piece + piece_at<kMode, kRows, D>(row, column + c)) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
       }
-      if (!s.whole) join_item<kMode, kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
+      // (kPrefix's pieces all wait for the merging launch: runs of eight, joined by one CTA each, took 30 us of 4 requests' 72
+      // on 8192 tokens of 4 heads, 38 pieces an item.)
+      if (kMode != kPrefix && !s.whole) join_item<kMode, kRows, D, kAllCompute, 3>(a, s, row_dst, rows, ctas, total, tid, &s_last);
       all_sync();  // the output's room, the rows' factors and the join word are free again, the segment is done with
       if (tid == 0) {
         s_unit += s_segment.length;
@@ -650,7 +653,7 @@ cudaError_t launch_dim(const AttendArgs& a, const AttendMaps& maps, int shift, i
                                              RowsShape<D>::smem(MOE_KV_MAX_REQUESTS));
   if (e != cudaSuccess) return e;
   return launch_chained(kv_attend_rows_kernel<kMode, D>, rows_ctas(sms), kThreads, RowsShape<D>::smem(a.b.requests),
-                        kMode != kWhole && a.chained, stream, a, maps, shift);
+                        kMode != kWhole, stream, a, maps, shift);
 }
 
 // Heads of 64 or 128.
