@@ -69,6 +69,10 @@ int row_tile(const AttendArgs& a) {
   return rows <= 24ll * a.b.requests ? 3 : 4;
 }
 
+cudaError_t launch_whole(const AttendArgs& a, const Call& c, int tile, cudaStream_t stream) {
+  return tile ? launch_kv_attend_decode(a, c.maps, tile, c.shift, c.sms, stream) : launch_kv_attend_rows(a, c.maps, c.shift, c.sms, stream);
+}
+
 // ------------------------------------------------------------- shared prefixes
 // Prefixes are shared from this much saved work on, in tiles of 8 rows: what two launches, their starts and the merging cost.
 // One prefix of 8192 tokens, 64 query heads on 8 of 128: 8 requests, 3020 tiles, take 37.9 us with it and 36.9 without, 4
@@ -215,8 +219,7 @@ cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t stream) {
   Call c;
   const cudaError_t e = c.open(a.c);
   if (e != cudaSuccess) return e;
-  const int tile = row_tile(a);
-  return tile ? launch_kv_attend_decode(a, c.maps, tile, c.shift, c.sms, stream) : launch_kv_attend_rows(a, c.maps, c.shift, c.sms, stream);
+  return launch_whole(a, c, row_tile(a), stream);
 }
 
 cudaError_t launch_kv_attend_shared(const AttendArgs& whole, const moe_kv_prefixes_t& p, void* scratch, cudaStream_t stream) {
@@ -244,6 +247,11 @@ cudaError_t launch_kv_attend_shared(const AttendArgs& whole, const moe_kv_prefix
                            tile ? 8 * tile : 128, kTileCost[tile]};
   moe_kv_prefixes_t prefixes = p;
   if (p.least_tiles == 0) prefixes.least_tiles = least_tiles(whole.c.head_dim);
+  // What the call can save at most, were its whole table one prefix: less than that, and no plan is asked (4 requests on 777
+  // tokens: 11.2 us, 15.6 with it).
+  const long long table_tiles = ((static_cast<long long>(whole.b.table_width) << c.shift) + 127) / 128;
+  if (static_cast<double>(whole.b.requests) * work.own * work.kv_heads * static_cast<double>(table_tiles) / 10 < prefixes.least_tiles)
+    return launch_whole(whole, c, own_tile, stream);
   // (A small batch's few warps are through their barriers sooner.)
   if (whole.b.requests <= 128) kv_shared_kernel<128><<<1, 128, 0, stream>>>(whole.b, prefixes, work, s);
   else kv_shared_kernel<1024><<<1, 1024, 0, stream>>>(whole.b, prefixes, work, s);
