@@ -4,7 +4,13 @@
 // Fork: who takes a page is a prefix sum over the requests, which every CTA
 // takes for itself; the rows are copied a warp to a row. Reclaim: the pages that
 // some row holds are bits of a map; a page's place among the free ones is a
-// count of the bits before it. Copy: bytes.
+// count of the bits before it (one CTA with the map in its shared memory, without
+// launches in between, is 2 us quicker up to some 2000 entries, and three times
+// slower at 16 thousand: not kept). Copy: bytes.
+//
+// Latency bounds the tables: a fork of 1000 requests with its copies takes 7.9 us, a
+// free list from 1000 requests 6.2 us, against 2.5 for any launch. The bytes bound a
+// pool's compaction: 64 requests, 198 MB moved, 41 us in all, 34 of them the copy's.
 #include "decode.h"
 #include "ptx.cuh"
 
@@ -346,8 +352,9 @@ cudaError_t launch_kv_fork(const moe_kv_fork_t& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_copy(const moe_kv_cache_t& c, const int32_t* moves, const int32_t* count, int capacity, cudaStream_t stream) {
-  // Heads of about 16 KB to a unit: a page of 64 tokens and 8 heads of 128 is four (CTAs of a whole page's keys take 10 us for
-  // 56 moves, units of a head 7.5).
+  // Heads of about 16 KB to a unit, of a page of 64 tokens two heads of 128 (a fork with 56 moves of up to 64 tokens of 8 heads
+  // takes 6.2 us so, 6.6 with a page's keys to a unit, 7.1 with a head; one of 1000 requests with few moves 7.9, 7.9 and 12.1;
+  // a compaction 41, 42 and 50). The most CTAs, from 12 to 64 an SM, make no difference.
   int heads_per = 16384 / (c.page_tokens * c.head_dim);
   heads_per = heads_per < 1 ? 1 : heads_per > c.kv_heads ? c.kv_heads : heads_per;
   const long long units = 2ll * capacity * ((c.kv_heads + heads_per - 1) / heads_per);
