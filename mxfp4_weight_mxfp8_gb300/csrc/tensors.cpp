@@ -164,7 +164,8 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, F&& body) {
     try {
       Device d;
       return PyLong_FromLong(body(a, d));
-    } catch (...) {  // Unfit, or torch's own
+    } catch (...) {  // Unfit, or torch's own, with or without a Python error
+      PyErr_Clear();
     }
   }
   Py_RETURN_NONE;
