@@ -527,8 +527,12 @@ __device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long lon
     const int r = tid * per + i;
     if (r < a.b.requests) {
       prefix[r] = at;
-      const Request<kMode> q(a, shift, r, kRows);
-      at += (RowTiles<kMode, kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
+      if (per == 1) {  // (no other look at the request)
+        at += tiles + items * weight;
+      } else {
+        const Request<kMode> q(a, shift, r, kRows);
+        at += (RowTiles<kMode, kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
+      }
       if (r == a.b.requests - 1) prefix[r + 1] = at;
     }
   }
