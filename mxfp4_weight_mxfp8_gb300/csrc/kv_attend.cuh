@@ -342,19 +342,24 @@ struct Segment {
   // The segment at unit x of a run that ends at `stop`.
   __device__ void find(const AttendArgs& a, const long long* prefix, int item_weight, int shift, long long x,
                        long long stop) {
-    weight = item_weight;
     int lo = 0, hi = a.b.requests;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (prefix[mid] <= x) lo = mid;
       else hi = mid;
     }
-    r = lo;
-    q = Request<kMode>(a, shift, r, kRows);
+    place(a, lo, Request<kMode>(a, shift, lo, kRows), prefix[lo], item_weight, x, stop);
+  }
+
+  // The same, of the request that x is known to lie in; its units start at `base`.
+  __device__ void place(const AttendArgs& a, int request, const Request<kMode>& its, long long base, int item_weight, long long x,
+                        long long stop) {
+    weight = item_weight;
+    r = request;
+    q = its;
     const RowTiles<kMode, kRows> t(a, q);
-    const long long local = x - prefix[lo];
-    lo = 0;
-    hi = q.row_tiles;
+    const long long local = x - base;
+    int lo = 0, hi = q.row_tiles;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if ((t.before(q, mid) + static_cast<long long>(mid) * weight) * a.c.kv_heads <= local) lo = mid;
@@ -484,19 +489,28 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* st
   return mbar_test(bar, parity) || wait_more(bar, parity, status);
 }
 
+// The request that a thread has looked at, where there is one to a thread, and its units: who has the one in which a CTA's
+// run starts says so, as another look at memory, with nothing else on its way, takes most of a microsecond.
+template <int kMode>
+struct Own {
+  Request<kMode> q;
+  long long from = 0, to = 0;
+  __device__ __forceinline__ bool holds(long long x) const { return from <= x && x < to; }
+};
+
 // Prefix sums of the requests' work, by the whole CTA of kThreads threads; returns what an item counts as: nothing
 // while there are no more tiles than CTAs, so that each gets one, else item_tiles.
 template <int kMode, int kThreads, int kRows>
-__device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long long* prefix, long long (*s_sum)[2]) {
+__device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long long* prefix, long long (*s_sum)[2], Own<kMode>& own) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.b.requests + kThreads - 1) / kThreads;
   long long tiles = 0, items = 0;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r < a.b.requests) {
-      const Request<kMode> q(a, shift, r, kRows);
-      items += q.items(a.c.kv_heads);
-      tiles += RowTiles<kMode, kRows>(a, q).all(q) * a.c.kv_heads;
+      own.q = Request<kMode>(a, shift, r, kRows);
+      items += own.q.items(a.c.kv_heads);
+      tiles += RowTiles<kMode, kRows>(a, own.q).all(own.q) * a.c.kv_heads;
     }
   }
   long long tiles_in = tiles, items_in = items;
@@ -527,8 +541,9 @@ __device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long lon
     const int r = tid * per + i;
     if (r < a.b.requests) {
       prefix[r] = at;
-      if (per == 1) {  // (no other look at the request)
-        at += tiles + items * weight;
+      if (per == 1) {
+        own.from = at;
+        own.to = at += tiles + items * weight;
       } else {
         const Request<kMode> q(a, shift, r, kRows);
         at += (RowTiles<kMode, kRows>(a, q).all(q) + static_cast<long long>(q.row_tiles) * weight) * a.c.kv_heads;
@@ -550,8 +565,8 @@ __device__ int sum_work(const AttendArgs& a, int item_tiles, int shift, long lon
 // through the ring. With the values go the pages' entries: key scale, value scale << 8, present << 16; and after a
 // tile's, whether every page is there.
 template <int kMode, class X, int D, int kWhich>
-__device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int weight, int shift,
-                        long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
+__device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long long* prefix, int shift,
+                        const Segment<kMode, X::kRows>& first, long long start, long long stop, uint8_t* sm, uint32_t* meta, uint64_t* full, uint64_t* empty, int32_t* status) {
   constexpr int kStages = kWhich == 1 ? X::kKeyStages : X::kStages;
   const int lane = threadIdx.x & 31;
   const uint64_t policy = policy_evict_first();
@@ -559,8 +574,7 @@ __device__ void produce(const AttendArgs& a, const AttendMaps& maps, const long 
   const int batch_tiles = 32 / per_tile;                                 // tiles looked up at once
   int k = 0;
   bool alive = reinterpret_cast<const volatile Header*>(status)->withhold != static_cast<int>(blockIdx.x) + 1;
-  Segment<kMode, X::kRows> s;
-  s.find(a, prefix, weight, shift, start, stop);
+  Segment<kMode, X::kRows> s = first;
   for (long long x = start; alive;) {
     const Request<kMode>& q = s.q;
     int page = -1;

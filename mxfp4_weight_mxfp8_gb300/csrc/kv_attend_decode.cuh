@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ int s_nans;         // the item has outputs noted in `nans`
+  __shared__ Segment<kMode, X::kRows> s_first;    // the CTA's first
   __shared__ Segment<kMode, X::kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   __shared__ int32_t s_status;   // the workspace's when the CTA started
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   }
   if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
   const int item_tiles = kMode == kSuffix && *a.shared > 0 ? X::kOwnItemTiles : X::kItemTiles;
-  const int weight = sum_work<kMode, X::kThreads, X::kRows>(a, item_tiles, shift, prefix, s_sum);
+  Own<kMode> own;
+  const int weight = sum_work<kMode, X::kThreads, X::kRows>(a, item_tiles, shift, prefix, s_sum, own);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   // (Whatever it does, kPrefix's launch ends after kSuffix's.)
@@ -241,6 +243,10 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, X::kTmem);
     tmem_relinquish();  // the SM's other CTA allocates its own
+  }
+  if (a.b.requests > X::kThreads ? tid == 0 : own.holds(start)) {
+    if (a.b.requests > X::kThreads) s_first.find(a, prefix, weight, shift, start, stop);
+    else s_first.place(a, tid, own.q, own.from, weight, start, stop);
   }
   if (tid == 0) s_status = found;
   tc_fence_before_sync();
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
   if (s_status != MOE_OK) {
     // An error that nobody has read yet: its call has left the arrival counters anyhow.
   } else if (warp == kProducerWarp) {
-    produce<kMode, X, D, 3>(a, maps, prefix, weight, shift, start, stop, sm, meta, full, empty, status);
+    produce<kMode, X, D, 3>(a, maps, prefix, shift, s_first, start, stop, sm, meta, full, empty, status);
   } else if (warp == kIssueWarp) {
     // Operand descriptors: keys and queries in the 128-byte (64-byte) swizzle, 8-row groups 1024 (512) bytes apart; values
     // M-major, 64 dimensions wide (D = 64: both 64-row halves of the operand read the same 64).
@@ -278,8 +284,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
       }
       __syncwarp();
     };
-    Segment<kMode, X::kRows> s;
-    s.find(a, prefix, weight, shift, start, stop);
+    Segment<kMode, X::kRows> s = s_first;
     for (long long x = start; alive;) {
       if (s.begin < s.end) {
         alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -323,8 +328,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
     const uint32_t inverse = inverse_of(a.group);
     int k = 0, segments = 0;
     bool alive = true;
-    Segment<kMode, X::kRows> s;
-    s.find(a, prefix, weight, shift, start, stop);
+    Segment<kMode, X::kRows> s = s_first;
     for (long long x = start; alive;) {
       const Sight<kMode> sight(a, s, inverse);
       if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
     bool failed = false, dead = false;  // a wait of this thread's ran out; one of any thread's did, all agreed
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, weight, shift, start, stop);
+      s_segment = s_first;
     }
     compute_sync();
     const Segment<kMode, X::kRows>& s = s_segment;

@@ -188,10 +188,7 @@ __device__ __forceinline__ void scale_output(uint32_t taddr, float factor) {
 // Where a CTA's run of units ends and the next one's starts: inside an item only if the item is long, else at its nearer
 // end (a piece costs an item's start and the join, some kItemTiles tiles).
 template <int kMode>
-__device__ long long snap(const AttendArgs& a, const long long* prefix, int weight, int shift, long long x, long long total) {
-  if (weight == 0 || x <= 0 || x >= total) return x;
-  Segment<kMode, kRows> s;
-  s.find(a, prefix, weight, shift, x, x + 1);
+__device__ long long snap(const Segment<kMode, kRows>& s, long long x) {
   if (s.units > kLongUnits) return x;
   return 2 * (x - s.item) >= s.units ? s.item + s.units : s.item;
 }
@@ -218,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ int s_nans;         // the item has outputs noted in `nans`
+  __shared__ Segment<kMode, kRows> s_first;    // the CTA's first
   __shared__ Segment<kMode, kRows> s_segment;  // the compute warps', kept by one of their threads
   __shared__ long long s_unit;
   __shared__ int32_t s_status;   // the workspace's when the CTA started
@@ -252,21 +250,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if constexpr (kMode == kSuffix) grid_dependency_wait();  // the plan
-  const int weight = sum_work<kMode, kThreads, kRows>(a, kItemTiles, shift, prefix, s_sum);
+  Own<kMode> own;
+  const int weight = sum_work<kMode, kThreads, kRows>(a, kItemTiles, shift, prefix, s_sum, own);
   const long long total = prefix[a.b.requests];
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   // (Whatever it does, kPrefix's launch ends after kSuffix's.)
   if (kMode == kPrefix && blockIdx.x == 0 && ctas == 0) grid_dependency_wait();
   if (blockIdx.x >= ctas) return;
-  if (tid == 0 || tid == 32) {
-    const int i = tid == 0 ? 0 : 1;
-    s_run[i] = snap<kMode>(a, prefix, weight, shift, total * (blockIdx.x + i) / ctas, total);
+  const bool many = a.b.requests > kThreads;
+  for (int i = 0; i < 2; ++i) {
+    const long long x = total * (blockIdx.x + i) / ctas;
+    const bool inside = weight > 0 && x > 0 && x < total;
+    if (inside ? many ? tid == 32 * i : own.holds(x) : tid == 32 * i) {
+      long long at = x;
+      if (inside) {
+        Segment<kMode, kRows> s;
+        if (many) s.find(a, prefix, weight, shift, x, x + 1);
+        else s.place(a, tid, own.q, own.from, weight, x, x + 1);
+        at = snap(s, x);
+      }
+      s_run[i] = at;
+    }
   }
   if (tid == 0) s_status = found;
   __syncthreads();
   const long long start = s_run[0], stop = s_run[1];
   if (kMode == kPrefix && blockIdx.x == 0 && (start >= stop || s_status != MOE_OK)) grid_dependency_wait();
   if (start >= stop || s_status != MOE_OK) return;  // (an error that nobody has read yet: the arrival counters are anyhow)
+  if (many ? tid == 0 : own.holds(start)) {
+    if (many) s_first.find(a, prefix, weight, shift, start, stop);
+    else s_first.place(a, tid, own.q, own.from, weight, start, stop);
+  }
   if (warp == kIssueWarp) {
     tmem_alloc(&s_tmem, kGroups * X::kGroupTmem);
     tmem_relinquish();
@@ -279,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;  // group g: scores at 256 g, then weights in their place; output at 256 g + 128
 
   if (warp == kProducerWarp) {
-    produce<kMode, X, D, 1>(a, maps, prefix, weight, shift, start, stop, sm, meta, k_full, k_empty, status);
+    produce<kMode, X, D, 1>(a, maps, prefix, shift, s_first, start, stop, sm, meta, k_full, k_empty, status);
   } else if (warp == kProducerWarp + 1) {
-    produce<kMode, X, D, 2>(a, maps, prefix, weight, shift, start, stop, sm, meta, v_full, v_empty, status);
+    produce<kMode, X, D, 2>(a, maps, prefix, shift, s_first, start, stop, sm, meta, v_full, v_empty, status);
   } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
     constexpr uint32_t kSwizzle = X::kSpan == 128 ? 2 : 4, kGroup = 8 * X::kSpan;
     const uint32_t q_at = smem_addr(sm + X::kQ), wide = smem_addr(sm + X::kWide), ring = smem_addr(sm + X::kRing);
@@ -306,8 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    Segment<kMode, kRows> s;
-    s.find(a, prefix, weight, shift, start, stop);
+    Segment<kMode, kRows> s = s_first;
     for (long long x = start; alive;) {
       const int last = k + s.end - s.begin;
       if (s.begin < s.end) alive = __all_sync(kAll, wait(q_ready, segments++ & 1, status));
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool failed = false;   // a wait ran out: no more waits; agreed on at the barriers
     if (tid == 0) {
       s_unit = start;
-      s_segment.find(a, prefix, weight, shift, start, stop);
+      s_segment = s_first;
     }
     all_sync();
     const Segment<kMode, kRows>& s = s_segment;
