@@ -26,12 +26,12 @@
 // token) and read the output at the end (thread = dimension).
 //
 // The cache's bytes bound large decode steps: 64 requests of up to 8192 tokens
-// (64 query heads on 8 of 128) take 102 us for 532 MB, 5.2 TB/s, 77 % of a
+// (64 query heads on 8 of 128) take 100 us for 532 MB, 5.3 TB/s, 78 % of a
 // copy's rate, with the schedulers issuing in 57 % of the cycles: the widening's
 // instructions (the loop without them takes 93 us). Two requests of 100 to 131
-// thousand tokens take 55 us for 244 MB: the same, with longer joins. One request
-// of 777 tokens takes 11 us, all latency. With several rows a request and a
-// window (40 requests, up to 24 rows, 1024 tokens of 64: 43 us for 35 MB) an
+// thousand tokens take 53 us for 244 MB: the same, with longer joins. One request
+// of 777 tokens takes 10.3 us, all latency. With several rows a request and a
+// window (40 requests, up to 24 rows, 1024 tokens of 64: 42 us for 35 MB) an
 // item's start and end bound it, twice as long as a tile.
 #pragma once
 
