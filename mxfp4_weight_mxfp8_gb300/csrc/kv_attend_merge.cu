@@ -27,7 +27,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <int D>
 __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs a, int tile_rows, int grid) {
   constexpr int kWarps = D / 16;
-  __shared__ float s_factor[kAttendRowsCtas][8], s_sum[kAttendRowsCtas][8], s_other[8];
+  __shared__ float s_factor[kAttendRowsCtas][8], s_sum[kAttendRowsCtas][8], s_other[8], s_lse[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = a.b.requests, heads = a.c.kv_heads;
   // The plan is there since before the launch before this one started; that one's units and pieces when it has ended.
@@ -43,12 +43,21 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
     }
     const int first = __ldcg(a.group_block + g), token0 = __ldcg(a.group_token + g), prefix = __ldcg(a.group_prefix + g);
     const int token1 = min(__ldcg(a.group_token + g + 1), a.b.tokens);
-    ptx::grid_dependency_wait();
-    if (__ldcg(reinterpret_cast<const int32_t*>(a.workspace)) != MOE_OK) return;  // (after an error nothing is to be used)
     const int row0 = (block - first) * 8, tile = row0 / tile_rows, i0 = row0 - tile * tile_rows;
-    const long long total = __ldcg(a.group_unit + groups), ctas = min(static_cast<long long>(grid), total);
-    const int weight = static_cast<int>(__ldcg(a.group_unit + groups + 1)), units = (prefix + kTile - 1) / kTile + weight;
-    const long long item = __ldcg(a.group_unit + g) + (static_cast<long long>(tile) * heads + head) * units;
+    // This thread's row, its quad, and its place among the outputs' rows.
+    const int i = lane & 7, c4 = (warp * 4 + (lane >> 3)) * 4, row = row0 + i, token = token0 + row / a.group;
+    const bool used = token < token1;
+    const int64_t dst = static_cast<int64_t>(used ? token : token0) * a.q_heads + head * a.group + row % a.group;
+    ptx::grid_dependency_wait();
+    // What is needed first is on its way together.
+    const int32_t status = __ldcg(reinterpret_cast<const int32_t*>(a.workspace));
+    const long long total = __ldcg(a.group_unit + groups), units_before = __ldcg(a.group_unit + g);
+    const int weight = static_cast<int>(__ldcg(a.group_unit + groups + 1));
+    const float4 own = __ldcg(reinterpret_cast<const float4*>(a.partial + dst * D + c4));
+    const float lse_of_row = __ldcg(a.partial_lse + dst);
+    if (status != MOE_OK) return;  // (after an error nothing is to be used)
+    const int units = (prefix + kTile - 1) / kTile + weight;
+    const long long ctas = min(static_cast<long long>(grid), total), item = units_before + (static_cast<long long>(tile) * heads + head) * units;
     const int c0 = static_cast<int>(((item + 1) * ctas - 1) / total), c1 = static_cast<int>(((item + units) * ctas - 1) / total);
     if (c0 == c1 || (tile_rows == 128 && weight > 0 && units <= kAttendRowsLong)) continue;  // one CTA's, which has joined it
     const int pieces = c1 - c0 + 1, width = tile_rows != 128 && pieces > kAttendMerged ? attend_join_width(pieces) : 1, count = (pieces + width - 1) / width;
@@ -56,11 +65,6 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
     const float* base = reinterpret_cast<const float*>(a.workspace + MOE_KV_WORKSPACE_HEADER) + c0 * 2 * floats;
     const auto piece = [&](int e) { return base + (e == 0 ? 1 : static_cast<int64_t>(e) * 2 * width) * floats; };
 
-    // This thread's row, its quad, and its place among the outputs' rows.
-    const int i = lane & 7, c4 = (warp * 4 + (lane >> 3)) * 4, row = row0 + i, token = token0 + row / a.group;
-    const bool used = token < token1;
-    const int64_t dst = static_cast<int64_t>(used ? token : token0) * a.q_heads + head * a.group + row % a.group;
-    const float4 own = __ldcg(reinterpret_cast<const float4*>(a.partial + dst * D + c4));
     for (int k = tid; k < count * 8; k += 2 * D) {
       const float* p = piece(k >> 3) + static_cast<int64_t>(tile_rows) * D + i0 + (k & 7);
       s_factor[k >> 3][k & 7] = __ldcg(p);
@@ -68,9 +72,7 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
     }
     __syncthreads();
     for (int r = warp; r < 8; r += kWarps) {  // a row to a warp, pieces to a lane
-      const int t = token0 + (row0 + r) / a.group;
-      const int64_t to = static_cast<int64_t>(t < token1 ? t : token0) * a.q_heads + head * a.group + (row0 + r) % a.group;
-      const float lse = __ldcg(a.partial_lse + to);
+      const float lse = __shfl_sync(kAll, lse_of_row, r);
       float top = lse;
       for (int e = lane; e < count; e += 32) top = fmaxf(top, s_factor[e][r]);
 #pragma unroll
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
       for (int e = lane; e < count; e += 32) s_factor[e][r] *= inv;
       if (lane == 0) {
         s_other[r] = other * inv;
-        if (a.lse != nullptr && t < token1) a.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        s_lse[r] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
     }
     __syncthreads();
@@ -109,6 +111,7 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
     }
     __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
     if (used) *reinterpret_cast<uint2*>(a.out + dst * D + c4) = *reinterpret_cast<uint2*>(w);
+    if (used && a.lse != nullptr && tid < 8) a.lse[dst] = s_lse[i];
     __syncthreads();  // the factors' room is free again
   }
 }

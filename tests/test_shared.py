@@ -252,6 +252,20 @@ def test_shared_groups_that_do_not_cover_the_requests_share_nothing(moe, starts)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,q_heads", [(1, 4), (4, 8), (50, 4)])
+def test_shared_plan_that_shares_nothing_leaves_attends_bits(moe, dim, n, q_heads):
+    """A table so wide that the call might save much, prefixes so short that it would not: decided on the device."""
+    b = Batch(moe, [(200, [(5 + 61 * i % 90 + n, n) for i in range(12)]), (70, [(3 + n, n)] * 12)], 16, 2, dim, q_heads, seed=dim + n)
+    b.table = torch.cat([b.table, torch.full((len(b.seq), 8000), -1, dtype=torch.int32, device="cuda")], 1)
+    got = b.run(least=0)
+    out, lse = torch.full_like(got[0], 7), torch.full_like(got[1], 7)
+    moe.moe_kv_attend(b.cache, b.q, b.table, b.start, b.lens, out, b.workspace, lse=lse)
+    assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
+    b.check(b.run())  # and shared, in spite of that
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", [2, 40])
 @pytest.mark.parametrize("change", [{0: -5}, {0: -2 ** 31}, {-1: 2 ** 31 - 1}, {0: -3, -1: 10 ** 6}, {-1: 0}, {-1: -7}, {-2: 10 ** 6}])
 def test_shared_query_starts_out_of_range_are_what_they_are_to_attend(moe, change, rows):
