@@ -5,7 +5,7 @@
 // pieces' rows first, in shared memory, then a thread its four dimensions of one row
 // over the pieces, eight loads in flight, a warp 8 rows by 4 quads: whole sectors in
 // either layout of a piece. Everything lies in L2. The launch takes some 4 us of 512
-// rows' 81 (64 requests on a prefix of 8192 tokens, 64 query heads on 8 of 128, 10 MB
+// rows' 80 (64 requests on a prefix of 8192 tokens, 64 query heads on 8 of 128, 10 MB
 // of pieces); four CTAs of 32 dimensions each in the place of one of 128 make it 2 to 4
 // us more, even where there are few rows.
 #include "decode.h"
