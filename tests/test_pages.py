@@ -430,3 +430,35 @@ def test_pages_python_refusals(moe):
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.code == moe.MOE_ERR_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("before", ["nothing", "memcpy", "memset", "join"])
+def test_copy_in_a_graph_behind_what_is_no_kernel(moe, before):
+    """Its launch is a chained one; the moves come by a memcpy, or from another stream."""
+    cache = [torch.randint(0, 255, s, dtype=torch.uint8, device="cuda") for s in ((9, 2, 16, 64), (9, 2, 16, 64), (9, 2), (9, 2))]
+    source = torch.tensor([[0, 4, 16], [1, 5, 7], [-1, -1, 0]], dtype=torch.int32, device="cuda")
+    moves = source.clone() if before in ("nothing", "memset") else torch.zeros_like(source)
+    junk, other, graph = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    want = [c.clone() for c in cache]
+    for c, w in zip(cache, want):
+        w[4], w[5] = c[0], c[1]
+        if c.dim() == 4:
+            w[5][:, 7:] = c[5][:, 7:]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        if before == "memcpy":
+            moves.copy_(source)
+        elif before == "memset":
+            junk.zero_()
+        elif before == "join":
+            other.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(other):
+                moves.copy_(source)
+            junk.fill_(3)
+            torch.cuda.current_stream().wait_stream(other)
+        moe.moe_kv_copy(tuple(cache), moves)
+    graph.replay()
+    torch.cuda.synchronize()
+    for c, w in zip(cache, want):
+        assert torch.equal(c, w)

@@ -416,6 +416,29 @@ def test_shared_in_a_graph_with_new_lengths_and_on_a_stream(moe):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,n,other", [(64, 1, 40), (128, 1, 40), (64, 40, 2), (256, 2, 6), (128, 2, 1)])
+def test_shared_two_calls_at_once(moe, dim, n, other):
+    """On two streams, each with its own workspace and scratch: the bits of each alone."""
+    batches = [Batch(moe, [(3000, [(20 + 70 * i % 300 + r, r) for i in range(14)]), (500, [(9 + r, r)] * 9)], 16, 2, dim, 8, seed=r)
+               for r in (n, other)]
+    alone = [b.run() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    room = [[torch.empty(moe.moe_kv_shared_bytes(*b.q.shape), dtype=torch.uint8, device="cuda"), *(torch.empty_like(x) for x in a)]
+            for b, a in zip(batches, alone)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, s, (scratch, out, lse) in zip(batches, streams, room):
+            with torch.cuda.stream(s):
+                out.fill_(7.0), lse.fill_(7.0)
+                moe.moe_kv_attend_shared(b.cache, b.q, b.table, b.start, b.lens, b.group_start, b.prefix_lens, out, b.workspace, scratch,
+                                         lse=lse, least_tiles=1)
+    torch.cuda.synchronize()
+    for b, (want, want_lse), (_, out, lse) in zip(batches, alone, room):
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert not b.workspace[:moe.MOE_KV_WORKSPACE_HEADER].any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dim,n,rows", [(64, 4, 1), (128, 4, 1), (256, 4, 1), (128, 40, 1), (64, 40, 1), (128, 3, 50)])
 @pytest.mark.parametrize("cta", [1, 5])
 def test_shared_waits_that_run_out(moe, dim, n, rows, cta):
