@@ -55,7 +55,8 @@ __host__ __device__ inline int attend_join_width(int pieces) {
   while (width * width < pieces) ++width;
   return width;
 }
-// Dimensions c4 .. c4 + 3 of row i in a piece of the prefixes' 128-row form.
+// Dimensions c4 .. c4 + 3 of row i in a piece of the prefixes' 128-row form, whose threads hold rows: quad by quad (other
+// pieces are row by row).
 __host__ __device__ constexpr int attend_quad_at(int i, int c4) { return c4 * 128 + i * 4; }
 
 constexpr int kAttendMaxCtas = 512;

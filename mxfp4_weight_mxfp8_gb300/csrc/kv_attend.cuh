@@ -60,7 +60,6 @@ __device__ __forceinline__ float* pieces_of(const AttendArgs& a) {
   return kMode == kSuffix ? a.pieces : reinterpret_cast<float*>(a.workspace + kPartialOffset);
 }
 
-
 // ---------------------------------------------------------------- tensor core
 // D[tmem] (+)= A[smem] x B[smem], e4m3 operands, FP32 accumulation; K = 32.
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -650,12 +649,6 @@ struct Joined {
   __device__ __forceinline__ float operator()(float o, float finished) const { return o * own + finished * other; }
 };
 
-// Dimensions c4 .. c4 + 3 of row i in a piece: row by row, or in kPrefix's 128-row form, whose threads hold rows, quad by quad.
-template <int kMode, int kRows, int D>
-__device__ __forceinline__ int piece_at(int i, int c4) {
-  return kMode == kPrefix && kRows == 128 ? attend_quad_at(i, c4) : i * D + c4;
-}
-
 // A piece of an item has been stored: joins the item's pieces once they are all there. By kThreads threads, whose barrier
 // is kBarrier. row_dst: the rows' places among the outputs' rows.
 template <int kMode, int kRows, int D, int kThreads, int kBarrier>
@@ -714,7 +707,7 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
             const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
             pm[e][u] = __ldcg(src + kRows * D + i);
             pl[e][u] = __ldcg(src + kRows * D + kRows + i);
-            pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + piece_at<kMode, kRows, D>(i, c4)));
+            pv[e][u] = __ldcg(reinterpret_cast<const float4*>(src + i * D + c4));
             if (!in) pm[e][u] = -INFINITY;
           }
         }
@@ -748,7 +741,7 @@ __device__ void join_item(const AttendArgs& a, const Segment<kMode, kRows>& s, c
         const int i = ((group + u) * kThreads + tid) / kQuads, c4 = ((group + u) * kThreads + tid) % kQuads * 4;
         if (!last) {
           float* dst = piece(from);
-          *reinterpret_cast<float4*>(dst + piece_at<kMode, kRows, D>(i, c4)) = o[u];
+          *reinterpret_cast<float4*>(dst + i * D + c4) = o[u];
           if (c4 == 0) {
             dst[kRows * D + i] = top[u];
             dst[kRows * D + kRows + i] = total_l[u];

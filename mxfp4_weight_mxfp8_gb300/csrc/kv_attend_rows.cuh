@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < kOwn; c += 4)
-          *reinterpret_cast<float4*>(piece + piece_at<kMode, kRows, D>(row, column + c)) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
+          *reinterpret_cast<float4*>(piece + (kMode == kPrefix ? attend_quad_at(row, column + c) : row * D + column + c)) = make_float4(own[c], own[c + 1], own[c + 2], own[c + 3]);
       }
       // (kPrefix's pieces all wait for the merging launch: runs of eight, joined by one CTA each, took 30 us of 4 requests' 72
       // on 8192 tokens of 4 heads, 38 pieces an item.)
