@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv_shared_kernel(const moe_kv_batch_
   if (tid < b.requests) {
     from = b.query_start[tid];
     to = b.query_start[tid + 1];
-    behind = b.seq_lens[tid];
+    behind = max(b.seq_lens[tid], 0);
   }
   if (tid < p.groups) {
     start = p.group_start[tid];

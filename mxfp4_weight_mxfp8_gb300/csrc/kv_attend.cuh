@@ -226,7 +226,7 @@ struct Request : Place<kMode> {
     const auto read = [](const int32_t* p) { return kMode == kPrefix ? __ldcg(p) : *p; };
     first = min(max(read(a.b.query_start + r), 0), a.b.tokens);
     n = min(max(read(a.b.query_start + r + 1), first), a.b.tokens) - first;
-    seq = read(a.b.seq_lens + r);
+    seq = max(read(a.b.seq_lens + r), 0);  // (below 0 as at 0: its queries stand before the sequence)
     long long room = static_cast<long long>(a.b.table_width) << shift;
     if constexpr (kMode == kPrefix) {
       this->row = __ldcg(a.rows + r);
