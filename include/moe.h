@@ -654,6 +654,9 @@ int moe_norm_quantize(moe_handle h, const moe_norm_t* norm, void* stream);
  *               strides) for rotating in place, where only the rotated
  *               dimensions are touched. Otherwise no output overlaps an input
  *               or the other output, and no output's rows overlap each other.
+ *               (Rows may lie between another tensor's, as those of a fused
+ *               projection do; tensors whose tokens are not equally far apart
+ *               are taken to overlap where their ranges of memory do.)
  * head_dim up to MOE_ROPE_MAX_DIM, rotary_dim even, 2 .. head_dim; q_heads 1 .. 1024, k_heads
  * 0 .. 1024. Rows not on 16-byte boundaries, and rotary_dim / 2 not a multiple of
  * 8, are served element by element.

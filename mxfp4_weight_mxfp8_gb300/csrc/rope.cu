@@ -154,32 +154,62 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements_kernel(const moe_r
   }
 }
 
-// A tensor's rows as an outer run of equally spaced blocks of bytes.
-struct Blocks {
-  int64_t at, stride, bytes, count;
+// A tensor's rows: blocks of bytes, one to a token and head, in bytes from each other. (A table is one block.)
+struct Spread {
+  int64_t at, token, head, tokens, heads, bytes;
 };
 
-Blocks blocks_of(const void* p, int64_t token, int64_t head, int tokens, int heads, int dim) {
-  const int64_t x = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p));
-  if (tokens == 1) token = (heads - 1) * head + dim;  // (any)
-  if (heads == 1) head = dim;
-  if (token >= head) return {x, 2 * token, 2 * ((heads - 1) * head + dim), tokens};
-  return {x, 2 * head, 2 * ((tokens - 1) * token + dim), heads};
+Spread table_of(const void* p, int64_t bytes) { return {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), 0, 0, 1, 1, bytes}; }
+
+Spread rows_of(const void* p, int64_t token, int64_t head, int64_t tokens, int64_t heads, int64_t dim) {
+  Spread r{static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), 2 * token, 2 * head, tokens, heads, 2 * dim};
+  if (r.heads > 1 && r.head == r.bytes) {  // one block
+    r.bytes *= r.heads;
+    r.heads = 1;
+  }
+  if (r.tokens == 1) r.token = 0;
+  if (r.heads == 1) r.head = 0;
+  return r;
 }
 
-// Whether two tensors share bytes: blocks equally far apart may lie side by side, others only in separate ranges.
-bool meet(const Blocks& a, const Blocks& b) {
-  if (a.at >= b.at + (b.count - 1) * b.stride + b.bytes || b.at >= a.at + (a.count - 1) * a.stride + a.bytes) return false;
-  if (a.stride != b.stride || a.stride == 0) return true;
-  const int64_t off = ((b.at - a.at) % a.stride + a.stride) % a.stride;
-  return off < a.bytes || a.stride - off < b.bytes;
+// Whether a run of blocks of a_bytes meets one of b_bytes, `off` bytes further, by a difference of `low` .. `high` strides.
+bool runs_meet(int64_t off, int64_t stride, int64_t low, int64_t high, int64_t a_bytes, int64_t b_bytes) {
+  // The least d from `low` on that brings b's block past the end of what lies before a's.
+  int64_t d = low;
+  if (stride > 0) {
+    const int64_t x = -b_bytes - off;  // off + d * stride > -b_bytes
+    const int64_t least = (x >= 0 ? x / stride : -((-x + stride - 1) / stride)) + 1;
+    if (least > d) d = least;
+  }
+  return d <= high && off + d * stride > -b_bytes && off + d * stride < a_bytes;
+}
+
+int64_t end_of(const Spread& r) { return r.at + (r.tokens - 1) * r.token + (r.heads - 1) * r.head + r.bytes; }
+
+// Whether two tensors share bytes. Of rows whose tokens are equally far apart (heads side by side in a fused projection,
+// in any order) exactly; of others only those in separate ranges are known not to.
+bool meet(const Spread& a, const Spread& b) {
+  if (a.at >= end_of(b) || b.at >= end_of(a)) return false;
+  if (a.tokens > 1 && b.tokens > 1 && a.token != b.token) return true;
+  const int64_t stride = a.tokens > 1 ? a.token : b.token, low = 1 - a.tokens, high = b.tokens - 1;
+  if (a.head == b.head || a.heads == 1 || b.heads == 1) {
+    const int64_t head = a.heads > 1 ? a.head : b.head;
+    for (int64_t d = 1 - a.heads; d < b.heads; ++d)
+      if (runs_meet(b.at - a.at + d * head, stride, low, high, a.bytes, b.bytes)) return true;
+    return false;
+  }
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t j = 0; j < b.heads; ++j)
+      if (runs_meet(b.at + j * b.head - a.at - i * a.head, stride, low, high, a.bytes, b.bytes)) return true;
+  return false;
 }
 
 // Whether a tensor's rows share bytes with each other.
-bool folded(int64_t token, int64_t head, int tokens, int heads, int dim) {
-  if (tokens == 1) return heads > 1 && head < dim;
-  if (heads == 1) return token < dim;
-  return token >= head ? head < dim || token < (heads - 1) * head + dim : token < dim || head < (tokens - 1) * token + dim;
+bool folded(const Spread& r) {
+  if (r.tokens > 1 && r.token < r.bytes) return true;
+  for (int64_t d = 1; d < r.heads; ++d)
+    if (runs_meet(d * r.head, r.token, 1 - r.tokens, r.tokens - 1, r.bytes, r.bytes)) return true;
+  return false;
 }
 
 }  // namespace
@@ -200,19 +230,17 @@ const char* rope_fault(const moe_rope_t* r) {
   if (off(r->positions, 4) || off(r->turns, 8) || off(r->q, 2) || off(r->k, 2) || off(r->q_out, 2) || off(r->k_out, 2))
     return "misaligned pointer";
   const int T = r->tokens, D = r->head_dim;
-  if (folded(r->q_out_token_stride, r->q_out_head_stride, T, r->q_heads, D) ||
-      (r->k_heads && folded(r->k_out_token_stride, r->k_out_head_stride, T, r->k_heads, D)))
-    return "an output's rows overlap";
+  const Spread q = rows_of(r->q, r->q_token_stride, r->q_head_stride, T, r->q_heads, D);
+  const Spread qo = rows_of(r->q_out, r->q_out_token_stride, r->q_out_head_stride, T, r->q_heads, D);
+  const Spread at = table_of(r->positions, 4ll * T), table = table_of(r->turns, 4ll * r->rotary_dim);
   const bool q_same = r->q == r->q_out && r->q_token_stride == r->q_out_token_stride && r->q_head_stride == r->q_out_head_stride;
-  const bool k_same = r->k == r->k_out && r->k_token_stride == r->k_out_token_stride && r->k_head_stride == r->k_out_head_stride;
-  const Blocks q = blocks_of(r->q, r->q_token_stride, r->q_head_stride, T, r->q_heads, D);
-  const Blocks qo = blocks_of(r->q_out, r->q_out_token_stride, r->q_out_head_stride, T, r->q_heads, D);
-  const Blocks at = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(r->positions)), 0, 4ll * T, 1};
-  const Blocks table = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(r->turns)), 0, 4ll * r->rotary_dim, 1};
+  if (folded(qo)) return "an output's rows overlap";
   if ((!q_same && meet(q, qo)) || meet(at, qo) || meet(table, qo)) return "an output overlaps an input (only q_out may be q, k_out k)";
   if (r->k_heads) {
-    const Blocks k = blocks_of(r->k, r->k_token_stride, r->k_head_stride, T, r->k_heads, D);
-    const Blocks ko = blocks_of(r->k_out, r->k_out_token_stride, r->k_out_head_stride, T, r->k_heads, D);
+    const Spread k = rows_of(r->k, r->k_token_stride, r->k_head_stride, T, r->k_heads, D);
+    const Spread ko = rows_of(r->k_out, r->k_out_token_stride, r->k_out_head_stride, T, r->k_heads, D);
+    const bool k_same = r->k == r->k_out && r->k_token_stride == r->k_out_token_stride && r->k_head_stride == r->k_out_head_stride;
+    if (folded(ko)) return "an output's rows overlap";
     if ((!k_same && meet(k, ko)) || meet(q, ko) || meet(k, qo) || meet(at, ko) || meet(table, ko))
       return "an output overlaps an input (only q_out may be q, k_out k)";
     if (meet(qo, ko)) return "the outputs overlap";
