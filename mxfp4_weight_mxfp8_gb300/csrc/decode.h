@@ -61,6 +61,9 @@ __host__ __device__ constexpr int attend_quad_at(int i, int c4) { return c4 * 12
 
 constexpr int kAttendMaxCtas = 512;
 
+// Tiles of 128 that so many cache tokens take (any number up to 2^31 - 1).
+__host__ __device__ inline int attend_tiles(int tokens) { return static_cast<int>((static_cast<uint32_t>(tokens) + 127u) / 128u); }
+
 enum AttendMode : int { kWhole = 0, kPrefix = 1, kSuffix = 2 };
 
 struct AttendMaps {

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) kv_shared_kernel(const moe_kv_batch_
     if (tokens) {
       const long long rows = static_cast<long long>(s_first[s_start[tid + 1]] - s_first[start]) * w.group;  // of the group
       const long long own = static_cast<long long>(s_count[tid]) * w.own, less = own - (rows + w.rows - 1) / w.rows * w.cost;
-      const long long saved = less * w.kv_heads * ((tokens + 127) / 128) / 10;
+      const long long saved = less * w.kv_heads * attend_tiles(tokens) / 10;
       if (p.least_tiles > 1 && kLeastShare * less < own) {
         tokens = 0;
       } else {

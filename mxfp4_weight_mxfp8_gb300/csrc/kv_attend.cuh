@@ -241,7 +241,7 @@ struct Request : Place<kMode> {
     }
     end = static_cast<int>(min(static_cast<long long>(max(seq, 0)), room));
     tile0 = a.window > 0 ? static_cast<int>(min(max(0ll, static_cast<long long>(seq) - n - a.window + 1), static_cast<long long>(end))) / kTile : 0;
-    tiles = max(1, (end + kTile - 1) / kTile - tile0);
+    tiles = max(1, attend_tiles(end) - tile0);
     row_tiles = static_cast<int>((static_cast<long long>(n) * a.group + rows - 1) / rows);
   }
   __device__ long long items(int heads) const { return static_cast<long long>(heads) * row_tiles; }
@@ -286,7 +286,7 @@ struct RowTiles {
     return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + count(q, q.row_tiles - 1);
   }
 };
-static_assert(kTile == 128, "RowTiles' shifts");
+static_assert(kTile == 128, "RowTiles' shifts, attend_tiles");
 
 // A run of one item's tiles in this CTA (none, where the run covers only what the item's start counts).
 template <int kMode, int kRows>
@@ -322,7 +322,7 @@ struct Segment {
     }
     const int before = q.seq - q.n;  // position of the request's first query
     const int last = min(q.n - 1, static_cast<int>((static_cast<long long>(row_tile + 1) * kRows - 1) / a.group));
-    end = min(end, (min(q.end, max(0, before + last + 1)) + kTile - 1) / kTile - q.tile0);
+    end = min(end, attend_tiles(min(q.end, max(0, before + last + 1))) - q.tile0);
     if (a.window > 0) {
       const long long from_token = static_cast<long long>(before) + static_cast<long long>(row_tile) * kRows / a.group - a.window + 1;
       begin = max(begin, static_cast<int>(max(from_token, 0ll) / kTile) - q.tile0);

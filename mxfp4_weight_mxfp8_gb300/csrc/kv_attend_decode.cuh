@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtasPer
         bool find = tile == s.begin;
         if (edge || blank)  // a row's first token
           find |= __any_sync(kAll, lane < X::kRows && m == -INFINITY && row_hi[min(lane, X::kRows - 1)] >= base &&
-                                       row_lo[min(lane, X::kRows - 1)] < base + kTile);
+                                       row_lo[min(lane, X::kRows - 1)] - base < kTile);
         for (int tries = 0;; ++tries) {
           // Scores of this token, times log2 e.
           float sc[X::kRows];

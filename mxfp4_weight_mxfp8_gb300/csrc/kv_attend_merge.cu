@@ -15,7 +15,6 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kTile = 128;  // cache tokens of a tile
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(2 * D) kv_attend_merge_kernel(const AttendArgs
     const float4 own = __ldcg(reinterpret_cast<const float4*>(a.partial + dst * D + c4));
     const float lse_of_row = __ldcg(a.partial_lse + dst);
     if (status != MOE_OK) return;  // (after an error nothing is to be used)
-    const int units = (prefix + kTile - 1) / kTile + weight;
+    const int units = attend_tiles(prefix) + weight;
     const long long ctas = min(static_cast<long long>(grid), total), item = units_before + (static_cast<long long>(tile) * heads + head) * units;
     const int c0 = static_cast<int>(((item + 1) * ctas - 1) / total), c1 = static_cast<int>(((item + units) * ctas - 1) / total);
     if (c0 == c1 || (tile_rows == 128 && weight > 0 && units <= kAttendRowsLong)) continue;  // one CTA's, which has joined it

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return 0xFFFFu >> (15 - to) & 0xFFFFu << from;
         };
         // Some row's first token may come with any of the group's tiles. (Both warps of the pair hold the same rows.)
-        const bool find = !written || __any_sync(kAll, m == -INFINITY && hi >= base && lo < base + kTile);
+        const bool find = !written || __any_sync(kAll, m == -INFINITY && hi >= base && lo - base < kTile);
         if (!failed) failed = !wait(s_full + group, turn & 1, status);
         __syncwarp();
         tc_fence_after_sync();
