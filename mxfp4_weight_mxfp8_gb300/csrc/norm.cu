@@ -26,14 +26,15 @@ struct Raw {
   uint4 w[kWords > 0 ? kWords : 1];
 };
 
-// Elements i .. i + 7 of a row of n; those from n on are zero.
-template <int kWords, bool kVector>
+// Elements i .. i + 7 of a row of n; those from n on are zero. kReadOnly: of memory that the kernel does not write (x and the
+// residual may be outputs too).
+template <int kWords, bool kVector, bool kReadOnly = false>
 __device__ __forceinline__ Raw<kWords> load(const void* row, int i, int n) {
   Raw<kWords> r;
   if constexpr (kVector) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(i) * 2 * kWords);
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) r.w[j] = i < n ? __ldg(p + j) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kWords; ++j) r.w[j] = i >= n ? make_uint4(0, 0, 0, 0) : kReadOnly ? __ldg(p + j) : p[j];
   } else if constexpr (kWords == 1) {
     const uint16_t* p = static_cast<const uint16_t*>(row) + i;
     uint32_t v[4];
@@ -110,9 +111,9 @@ __device__ __forceinline__ void store(void* row, int i, int n, bool half, const 
 template <bool kVector>
 __device__ __forceinline__ void load_weight(const moe_norm_t& a, int i, float (&v)[8]) {
   if (a.weight_dtype == MOE_F32)
-    unpack(load<2, kVector>(a.weight, i, a.hidden), false, v);
+    unpack(load<2, kVector, true>(a.weight, i, a.hidden), false, v);
   else
-    unpack(load<1, kVector>(a.weight, i, a.hidden), a.weight_dtype == MOE_F16, v);
+    unpack(load<1, kVector, true>(a.weight, i, a.hidden), a.weight_dtype == MOE_F16, v);
 }
 
 // The sum over a row's threads: a warp's, or the CTA's through `red`.
