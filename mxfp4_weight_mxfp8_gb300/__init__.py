@@ -398,19 +398,25 @@ _torch = _native = None
 _LOGITS: dict = {}
 
 
+class _Declines:
+    """In the place of csrc/tensors.cpp where that is not built: it takes no call, so the checks here do."""
+
+    def __getattr__(self, name):
+        return lambda *_: None
+
+
 def _use_torch():
     """torch and the lookups that need it, on the first call."""
     global _torch, _i32t, _i64t, _f32t, _bf16t, _u8t, _raw_stream, _native
     import torch
 
-    if not os.path.exists(TENSORS):
-        raise ImportError(f"extension module not built ({TENSORS} missing): run "
-                          "`python -c \"import __graft_entry__ as g; g.build()\"`")
-    loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
-    native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
-    loader.exec_module(native)
-    native.bind(*(ctypes.cast(getattr(_lib, n), _vp).value for n in (
-        "moe_norm", "moe_rope", "moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy", "moe_kv_attend_shared")))
+    native = _Declines()
+    if os.path.exists(TENSORS):
+        loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
+        loader.exec_module(native)
+        native.bind(*(ctypes.cast(getattr(_lib, n), _vp).value for n in (
+            "moe_norm", "moe_rope", "moe_kv_fork", "moe_kv_reclaim", "moe_kv_copy", "moe_kv_attend_shared")))
     _i32t, _i64t, _f32t, _bf16t, _u8t = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
     _LOGITS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     # The current stream's handle without building a stream object, where torch has it.

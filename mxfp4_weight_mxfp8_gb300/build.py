@@ -3,7 +3,8 @@
 Every translation unit is compiled in parallel with one -gencode
 (compute_103a / sm_103a) and linked into a shared library with the static
 CUDA runtime. csrc/tensors.cpp, the Python side's fast way from torch tensors
-to the library's calls, becomes an extension module beside it; nothing is
+to the library's calls, becomes an extension module beside it where torch is
+installed (the library needs none, and the package does without); nothing is
 installed outside this folder.
 """
 from __future__ import annotations
@@ -38,10 +39,18 @@ def _dependencies():
     return deps + [os.path.join(ROOT, "include", "moe.h")]
 
 
+def _torch_folder():
+    """The folder of the installed torch (found, not imported), None without one or with one for CPUs only."""
+    spec = importlib.util.find_spec("torch")
+    folder = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+    return folder if folder and os.path.exists(os.path.join(folder, "lib", "libc10_cuda.so")) else None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY) or not os.path.exists(TENSORS):
+    made = [LIBRARY] if _torch_folder() is None else [LIBRARY, TENSORS]
+    if not all(os.path.exists(m) for m in made):
         return False
-    built = min(os.path.getmtime(LIBRARY), os.path.getmtime(TENSORS))
+    built = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= built for d in _dependencies())
 
 
@@ -62,7 +71,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     def compile_tensors():
-        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        torch = _torch_folder()
+        if torch is None:
+            return
         tmp = TENSORS + f".{os.getpid()}.tmp"
         cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
         include = [os.path.join(ROOT, "include"), sysconfig.get_path("include"), os.path.join(torch, "include"),
