@@ -399,7 +399,7 @@ _LOGITS: dict = {}
 
 
 class _Declines:
-    """In the place of csrc/tensors.cpp where that is not built: it takes no call, so the checks here do."""
+    """In the place of csrc/tensors.cpp where that is not built, or not for this torch: it takes no call, so the checks here do."""
 
     def __getattr__(self, name):
         return lambda *_: None
@@ -411,7 +411,7 @@ def _use_torch():
     import torch
 
     native = _Declines()
-    if os.path.exists(TENSORS):
+    if TENSORS is not None and os.path.exists(TENSORS):
         loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
         native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
         loader.exec_module(native)

@@ -13,6 +13,7 @@ import concurrent.futures
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sysconfig
 
@@ -23,11 +24,31 @@ CSRC = os.path.join(HERE, "csrc")
 # with -DMOE_TRACE); MOE_LIBRARY makes the binding load a given build.
 BUILD = os.environ.get("MOE_BUILD_DIR", os.path.join(HERE, "_build"))
 LIBRARY = os.environ.get("MOE_LIBRARY", os.path.join(BUILD, "libmoe_gb300.so"))
-TENSORS = os.path.join(os.path.dirname(LIBRARY), "_tensors.so")
 DEFINES = os.environ.get("MOE_NVCC_DEFINES", "").split()
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
+
+
+def _torch_folder():
+    """The folder of the installed torch (found, not imported), None without one or with one for CPUs only."""
+    spec = importlib.util.find_spec("torch")
+    folder = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+    return folder if folder and os.path.exists(os.path.join(folder, "lib", "libc10_cuda.so")) else None
+
+
+def _tensors_path():
+    """The extension module's file, named by the torch and the Python that it is bound to: another's is not taken for it."""
+    torch = _torch_folder()
+    if torch is None:
+        return None
+    with open(os.path.join(torch, "version.py"), encoding="utf-8") as f:
+        version = re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read())
+    name = f"_tensors.{sysconfig.get_config_var('SOABI')}.torch-{version.group(1) if version else 'unknown'}"
+    return os.path.join(os.path.dirname(LIBRARY), re.sub(r"[^\w.-]", "-", name) + ".so")
+
+
+TENSORS = _tensors_path()
 
 
 def _sources():
@@ -39,15 +60,8 @@ def _dependencies():
     return deps + [os.path.join(ROOT, "include", "moe.h")]
 
 
-def _torch_folder():
-    """The folder of the installed torch (found, not imported), None without one or with one for CPUs only."""
-    spec = importlib.util.find_spec("torch")
-    folder = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
-    return folder if folder and os.path.exists(os.path.join(folder, "lib", "libc10_cuda.so")) else None
-
-
 def up_to_date() -> bool:
-    made = [LIBRARY] if _torch_folder() is None else [LIBRARY, TENSORS]
+    made = [LIBRARY] if TENSORS is None else [LIBRARY, TENSORS]
     if not all(os.path.exists(m) for m in made):
         return False
     built = min(os.path.getmtime(m) for m in made)
@@ -71,9 +85,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     def compile_tensors():
-        torch = _torch_folder()
-        if torch is None:
+        if TENSORS is None:
             return
+        torch = _torch_folder()
         tmp = TENSORS + f".{os.getpid()}.tmp"
         cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
         include = [os.path.join(ROOT, "include"), sysconfig.get_path("include"), os.path.join(torch, "include"),

@@ -29,6 +29,7 @@ def compiler(tmp_path):
     nvcc.parent.mkdir()
     nvcc.write_text('#!/bin/sh\nwhile [ "$1" != "-o" ]; do shift; done\n: > "$2"\n')
     nvcc.chmod(0o755)
+    (nvcc.parent / "g++").symlink_to(nvcc)
     return dict(NVCC=str(nvcc), MOE_BUILD_DIR=str(tmp_path / "made"))
 
 
@@ -52,6 +53,24 @@ assert os.path.exists(build.build()) and build.up_to_date()
 """
     python(code, "-I", "-S", **compiler)
     assert "libmoe_gb300.so" in os.listdir(tmp_path / "made") and not [f for f in os.listdir(tmp_path / "made") if f.startswith("_tensors")]
+
+
+def test_an_extension_module_of_another_torch_is_not_up_to_date(compiler, tmp_path):
+    (tmp_path / "torch" / "lib").mkdir(parents=True)
+    for f in ("__init__.py", "lib/libc10_cuda.so"):
+        (tmp_path / "torch" / f).touch()
+    code = f"import sys\nsys.path.insert(0, {str(tmp_path)!r})\n" + LOAD + """
+assert build.up_to_date() == (sys.argv[1:] == ["built"])
+build.build()
+assert build.up_to_date() and os.path.exists(build.TENSORS)
+print(build.TENSORS)
+"""
+    def made(version, *args):
+        (tmp_path / "torch" / "version.py").write_text(f"__version__ = '{version}'\n")
+        return python(code.replace("sys.argv[1:]", repr(list(args))), "-I", "-S", PATH=f"{tmp_path / 'bin'}:{os.environ['PATH']}", **compiler)
+
+    first, second = made("9.1.0+cu999"), made("9.2.0")
+    assert first != second and made("9.1.0+cu999", "built") == first
 
 
 def test_calls_without_the_extension_module_are_checked_by_the_package(bare_library):
