@@ -689,7 +689,8 @@ int moe_rope(const moe_rope_t* rope, void* stream);
  *     indices of the pairs that turn `high` times (rounded down, 0 at least) and
  *     `low` times (rounded up, rotary_dim - 1 at most: the last pair may be in the
  *     middle of the ramp)
- *   turns[i] = f_i / (2 pi) * 2^64, rounded, modulo 2^64.
+ *   turns[i] = f_i / (2 pi) * 2^64, rounded, modulo 2^64 (computed with twice a
+ *   double's bits: the last unit is right while f_i stays below 2^20 radians)
  * base > 1; factor, trained > 0; 0 < low < high (not looked at by LINEAR).
  * Writes turns[rotary_dim / 2], host memory.
  */

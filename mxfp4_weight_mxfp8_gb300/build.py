@@ -27,7 +27,7 @@ LIBRARY = os.environ.get("MOE_LIBRARY", os.path.join(BUILD, "libmoe_gb300.so"))
 DEFINES = os.environ.get("MOE_NVCC_DEFINES", "").split()
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-ffp-contract=off", "-I", os.path.join(ROOT, "include")]
 
 
 def _torch_folder():

@@ -2,6 +2,7 @@
 #include <cmath>
 
 #include "decode.h"
+#include "twice.h"
 
 namespace {
 
@@ -79,6 +80,26 @@ const char* attend_args(moe::AttendArgs* a, const moe_kv_cache_t* cache, const m
   return nullptr;
 }
 
+// x modulo 1 in units of 2^-64, rounded, modulo 2^64.
+uint64_t fraction_of(moe::Twice x) {
+  if (!std::isfinite(x.hi)) return 0;
+  const auto whole = [&] {  // of x, which keeps the rest, 0 .. 1
+    double n = std::floor(x.hi);
+    x = moe::quick_sum(x.hi - n, x.lo);
+    if (x.hi < 0.0) {
+      n -= 1.0;
+      x = x + 1.0;
+    }
+    return n;
+  };
+  whole();
+  x = moe::times_two_to(x, 32);
+  const uint64_t upper = static_cast<uint64_t>(whole());
+  x = moe::times_two_to(x, 32);
+  const uint64_t lower = static_cast<uint64_t>(whole());
+  return (upper << 32) + lower + (x.hi >= 0.5 ? 1 : 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,25 +149,23 @@ int moe_rope_turns(int rotary_dim, double base, int scaling, double factor, doub
   if (scaling != MOE_ROPE_LINEAR && scaling != MOE_ROPE_BANDS && scaling != MOE_ROPE_RAMP) return refuse("scaling");
   if (scaling != MOE_ROPE_LINEAR && (!(trained > 0.0) || !std::isfinite(trained) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
     return refuse("trained, low or high out of range");
-  const double tau = 6.283185307179586476925;
   // The pair that turns n times over the trained length: trained * base^(-2i / rotary_dim) = tau n.
-  const auto index = [&](double n) { return rotary_dim * std::log(trained / (tau * n)) / (2.0 * std::log(base)); };
+  const auto index = [&](double n) { return rotary_dim * std::log(trained / (moe::kTau.hi * n)) / (2.0 * std::log(base)); };
   double from = 0.0, to = 1.0;
   if (scaling == MOE_ROPE_RAMP) {
     from = std::fmax(std::floor(index(high)), 0.0);
     to = std::fmin(std::ceil(index(low)), rotary_dim - 1.0);
     if (to <= from) to = from + 0.001;  // a step
   }
+  // From here on with twice a double's bits: a table of 64 is read at positions up to 2^31.
+  const moe::Twice rate = moe::log_of(base) / moe::Twice(rotary_dim);
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rotary_dim), keep = 0.0;
-    if (scaling == MOE_ROPE_BANDS) keep = (trained * f / tau - low) / (high - low);
-    if (scaling == MOE_ROPE_RAMP) keep = 1.0 - (i - from) / (to - from);
-    keep = std::fmin(std::fmax(keep, 0.0), 1.0);
-    f = f * keep + f / factor * (1.0 - keep);
-    double whole;
-    const double turn = std::modf(f / tau, &whole);
-    turns[i] = turn >= 0.5 ? 0 - static_cast<uint64_t>(std::nearbyint(std::ldexp(1.0 - turn, 64)))
-                           : static_cast<uint64_t>(std::nearbyint(std::ldexp(turn, 64)));
+    moe::Twice f = i ? moe::exp_of(rate * (-2.0 * i)) : 1.0, keep = 0.0;
+    if (scaling == MOE_ROPE_BANDS) keep = (f / moe::kTau * trained - low) / (moe::Twice(high) - low);
+    if (scaling == MOE_ROPE_RAMP) keep = moe::Twice(1.0) - moe::Twice(i - from) / (moe::Twice(to) - from);
+    keep = keep.hi > 1.0 ? 1.0 : keep.hi > 0.0 ? keep : 0.0;
+    f = f * keep + f / factor * (moe::Twice(1.0) - keep);
+    turns[i] = fraction_of(f / moe::kTau);
   }
   return MOE_OK;
 }

@@ -1,8 +1,9 @@
 // Rotary positions of queries and keys (moe_rope in include/moe.h).
 //
 // The angle of a pair is position * turns, a whole number of 2^-64 turns: the
-// product modulo 2^64 drops whole turns exactly, and its upper half is the angle
-// to 2^-32 of a turn, whatever the position. A CTA takes a token's heads, so the
+// product modulo 2^64 drops whole turns exactly, and its upper half is that angle
+// to 2^-32 of a turn, whatever the position; the table's own rounding, 2^-65, is
+// 2^-34 of a turn at position 2^31. A CTA takes a token's heads, so the
 // sines are computed once for all of them; every element is read and written once
 // and the bytes bound it: 12592 tokens of 72 heads of 128, half of each turned,
 // 464 MB, take 75 us, 6.2 TB/s, 92 % of a copy's rate (sines for each head anew made
