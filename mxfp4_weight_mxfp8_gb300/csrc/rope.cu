@@ -6,8 +6,8 @@
 // 2^-34 of a turn at position 2^31. A CTA takes a token's heads, so the
 // sines are computed once for all of them; every element is read and written once
 // and the bytes bound it: 12592 tokens of 72 heads of 128, half of each turned,
-// 464 MB, take 75 us, 6.2 TB/s, 92 % of a copy's rate (sines for each head anew made
-// it 83). A decode step's 64 tokens are their launch, 2.7 us, heads shared out so that
+// 464 MB, take 71 us, 6.5 TB/s, 97 % of a copy's rate (sines for each head anew made
+// it 9 more). A decode step's 64 tokens are their launch, 2.7 us, heads shared out so that
 // the GPU is full.
 #include "decode.h"
 
@@ -44,13 +44,14 @@ __device__ __forceinline__ float first_of(float a, float b, float sin, float cos
 __device__ __forceinline__ float second_of(float a, float b, float sin, float cos) { return __fmaf_rn(b, cos, __fmul_rn(a, sin)); }
 
 // A head's row is a number of units of two 16-byte words each: rotated ones (8 pairs), then copied ones, where the output is
-// another tensor. `slots` lanes, a power of two, share the units of a head, so a warp takes whole rows; the heads of a token
+// another tensor: 32 at most. `slots` lanes, a power of two, have one each, so a warp takes whole rows; the heads of a token
 // go by in turn, `heads_per` of them to a CTA's y.
+static_assert(MOE_ROPE_MAX_DIM <= 32 * 16, "a lane for every unit of a head");
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const moe_rope_t a, int slots, int heads_per, int units) {
   __shared__ __align__(16) float s_sin[MOE_ROPE_MAX_DIM / 2], s_cos[MOE_ROPE_MAX_DIM / 2];
   const int pairs = a.rotary_dim / 2, rotated = pairs / 8, all_heads = a.q_heads + a.k_heads;
-  const int slot = threadIdx.x & (slots - 1), groups = kRopeThreads / slots, first = blockIdx.y * heads_per;
+  const int u = threadIdx.x & (slots - 1), groups = kRopeThreads / slots, first = blockIdx.y * heads_per;
   const int last = min(first + heads_per, all_heads), t = blockIdx.x;
   const Rows q{static_cast<const uint16_t*>(a.q) + t * a.q_token_stride, static_cast<uint16_t*>(a.q_out) + t * a.q_out_token_stride,
                0, a.q_head_stride, 0, a.q_out_head_stride};
@@ -58,69 +59,63 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const moe_rope_t a, 
                0, a.k_head_stride, 0, a.k_out_head_stride};
   const auto from_of = [&](int h) { return h >= a.q_heads ? k.from + (h - a.q_heads) * k.head : q.from + h * q.head; };
   const auto to_of = [&](int h) { return h >= a.q_heads ? k.to + (h - a.q_heads) * k.to_head : q.to + h * q.to_head; };
-  const int rounds = (units + slots - 1) / slots;
-  for (int round = 0; round < rounds; ++round) {
-    const int u = slot + round * slots;
-    const bool turned = u < rotated;
-    const int at0 = !turned ? a.rotary_dim + (u - rotated) * 16 : kInterleaved ? u * 16 : u * 8;
-    const int at1 = !turned || kInterleaved ? at0 + 8 : at0 + pairs;
-    const bool has0 = u < units, has1 = has0 && at1 < a.head_dim;  // (a copied unit may be one word)
-    // Two heads' elements are on their way while the sines are computed; then always the next two.
-    int h = first + threadIdx.x / slots;
-    uint4 x[2], y[2];
-    const auto load = [&](int from) {
+  const bool turned = u < rotated;
+  const int at0 = !turned ? a.rotary_dim + (u - rotated) * 16 : kInterleaved ? u * 16 : u * 8;
+  const int at1 = !turned || kInterleaved ? at0 + 8 : at0 + pairs;
+  const bool has0 = u < units, has1 = has0 && at1 < a.head_dim;  // (a copied unit may be one word)
+  // Two heads' elements are on their way while the sines are computed; then always the next two.
+  int h = first + threadIdx.x / slots;
+  uint4 x[2], y[2];
+  const auto load = [&](int from) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (from + e * groups < last) {
-          const uint16_t* p = from_of(from + e * groups);
-          if (has0) x[e] = *reinterpret_cast<const uint4*>(p + at0);
-          if (has1) y[e] = *reinterpret_cast<const uint4*>(p + at1);
-        }
-    };
-    load(h);
-    if (round == 0) {
-      const int position = a.positions[t];
-      for (int i = threadIdx.x; i < pairs; i += kRopeThreads) sin_cos(a.turns[i], position, a.amplitude, s_sin[i], s_cos[i]);
-      __syncthreads();
-    }
-    float sin[8], cos[8];
-    if (turned) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        *reinterpret_cast<float4*>(sin + j) = *reinterpret_cast<const float4*>(s_sin + u * 8 + j);
-        *reinterpret_cast<float4*>(cos + j) = *reinterpret_cast<const float4*>(s_cos + u * 8 + j);
+    for (int e = 0; e < 2; ++e)
+      if (from + e * groups < last) {
+        const uint16_t* p = from_of(from + e * groups);
+        if (has0) x[e] = *reinterpret_cast<const uint4*>(p + at0);
+        if (has1) y[e] = *reinterpret_cast<const uint4*>(p + at1);
       }
+  };
+  load(h);
+  const int position = a.positions[t];
+  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) sin_cos(a.turns[i], position, a.amplitude, s_sin[i], s_cos[i]);
+  __syncthreads();
+  float sin[8], cos[8];
+  if (turned) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<float4*>(sin + j) = *reinterpret_cast<const float4*>(s_sin + u * 8 + j);
+      *reinterpret_cast<float4*>(cos + j) = *reinterpret_cast<const float4*>(s_cos + u * 8 + j);
     }
-    for (; h < last; h += 2 * groups) {
+  }
+  for (; h < last; h += 2 * groups) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (h + e * groups >= last) continue;
-        uint4 xo = x[e], yo = y[e];
-        if (turned) {
-          const uint32_t xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
-          uint32_t p[4], r[4];
+    for (int e = 0; e < 2; ++e) {
+      if (h + e * groups >= last) continue;
+      uint4 xo = x[e], yo = y[e];
+      if (turned) {
+        const uint32_t xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+        uint32_t p[4], r[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kInterleaved) {
-              const float a0 = low(xs[j]), b0 = high(xs[j]), a1 = low(ys[j]), b1 = high(ys[j]);
-              p[j] = pack(first_of(a0, b0, sin[j], cos[j]), second_of(a0, b0, sin[j], cos[j]));
-              r[j] = pack(first_of(a1, b1, sin[4 + j], cos[4 + j]), second_of(a1, b1, sin[4 + j], cos[4 + j]));
-            } else {
-              const float a0 = low(xs[j]), a1 = high(xs[j]), b0 = low(ys[j]), b1 = high(ys[j]);
-              p[j] = pack(first_of(a0, b0, sin[2 * j], cos[2 * j]), first_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
-              r[j] = pack(second_of(a0, b0, sin[2 * j], cos[2 * j]), second_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
-            }
+        for (int j = 0; j < 4; ++j) {
+          if (kInterleaved) {
+            const float a0 = low(xs[j]), b0 = high(xs[j]), a1 = low(ys[j]), b1 = high(ys[j]);
+            p[j] = pack(first_of(a0, b0, sin[j], cos[j]), second_of(a0, b0, sin[j], cos[j]));
+            r[j] = pack(first_of(a1, b1, sin[4 + j], cos[4 + j]), second_of(a1, b1, sin[4 + j], cos[4 + j]));
+          } else {
+            const float a0 = low(xs[j]), a1 = high(xs[j]), b0 = low(ys[j]), b1 = high(ys[j]);
+            p[j] = pack(first_of(a0, b0, sin[2 * j], cos[2 * j]), first_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
+            r[j] = pack(second_of(a0, b0, sin[2 * j], cos[2 * j]), second_of(a1, b1, sin[2 * j + 1], cos[2 * j + 1]));
           }
-          xo = make_uint4(p[0], p[1], p[2], p[3]);
-          yo = make_uint4(r[0], r[1], r[2], r[3]);
         }
-        uint16_t* to = to_of(h + e * groups);
-        if (!turned && to == from_of(h + e * groups)) continue;  // in place: as it is
-        if (has0) *reinterpret_cast<uint4*>(to + at0) = xo;
-        if (has1) *reinterpret_cast<uint4*>(to + at1) = yo;
+        xo = make_uint4(p[0], p[1], p[2], p[3]);
+        yo = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      load(h + 2 * groups);
+      uint16_t* to = to_of(h + e * groups);
+      if (!turned && to == from_of(h + e * groups)) continue;  // in place: as it is
+      if (has0) *reinterpret_cast<uint4*>(to + at0) = xo;
+      if (has1) *reinterpret_cast<uint4*>(to + at1) = yo;
     }
+    load(h + 2 * groups);
   }
 }
 
@@ -271,7 +266,7 @@ cudaError_t launch_rope(const moe_rope_t& a, cudaStream_t stream) {
   const bool copies = a.q != a.q_out || (a.k_heads && a.k != a.k_out);
   const int units = a.rotary_dim / 16 + (copies ? (a.head_dim - a.rotary_dim + 15) / 16 : 0);
   int slots = 1;
-  while (slots < units && slots < 32) slots *= 2;
+  while (slots < units) slots *= 2;
   const int groups = kRopeThreads / slots, n = parts(groups), per = (heads + n - 1) / n;
   const dim3 grid(a.tokens, (heads + per - 1) / per);
   if (a.interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, slots, per, units);
