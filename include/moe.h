@@ -148,8 +148,8 @@ int moe_group(moe_handle h, const int32_t* topk_ids, int batch, void* stream);
  * handle's call on the same stream starts early: its prep grid writes this
  * handle's tables without waiting for the previous launch, and its experts
  * kernel streams weights while the previous call still runs, holding its
- * output rows until that call has ended. Every launch of this library lets
- * the next one start only after its own wait for the launch before it; a
+ * output rows until that call has ended. Every call's last launch lets the
+ * next one start only after its own wait for the launch before it; a
  * caller's kernel launched between two calls with programmatic stream
  * serialization must likewise wait (griddepcontrol.wait) before it ends.
  * Errors: MOE_ERR_ARG (nulls, misalignment, batch range), MOE_ERR_CUDA.
@@ -382,8 +382,8 @@ int moe_small_batch_build(int experts, int hidden, int inter, int batch, int gri
 /* ------------------------------------------------------------------------
  * The decode step around the layer: routing, and attention over a paged
  * 8-bit cache. These calls need no handle: every buffer is the caller's, and
- * each call is asynchronous on `stream`, an ordinary launch that starts when
- * the work before it on the stream has ended. They allocate nothing and may
+ * each call is asynchronous on `stream` and starts its work when the work
+ * before it on the stream has ended. They allocate nothing and may
  * be captured into a CUDA graph (lengths, tables and slots are read on the
  * device). Refusals are found before the launch (MOE_ERR_ARG, with
  * moe_last_error_detail); zero tokens is no work and MOE_OK.
@@ -822,7 +822,10 @@ int moe_kv_reclaim(const moe_kv_reclaim_t* reclaim, void* stream);
  *                work (128 tokens of a cache head for 8 query rows of a request);
  *                0: the library's own number, below which two launches take
  *                longer than one; 1: whatever it saves. From 2 on (and for 0)
- *                a group counts only if it saves a quarter of its prefix's work
+ *                a group counts only if it saves a quarter of its prefix's work.
+ *                What the call's sizes cannot save is not asked for; where the
+ *                lengths, on the device, save too little, the call takes some 5 us
+ *                longer than moe_kv_attend
  * Both tensors are device memory. Shared are the whole pages that every query of the group
  * sees: prefix_len is held to the group's shortest cached context. Requests
  * without queries take no part (their rows may hold anything), a prefix that one

@@ -34,7 +34,7 @@ def _torch_folder():
     """The folder of the installed torch (found, not imported), None without one or with one for CPUs only."""
     spec = importlib.util.find_spec("torch")
     folder = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
-    return folder if folder and os.path.exists(os.path.join(folder, "lib", "libc10_cuda.so")) else None
+    return folder if folder and all(os.path.exists(os.path.join(folder, f)) for f in ("version.py", "lib/libc10_cuda.so")) else None
 
 
 def _tensors_path():

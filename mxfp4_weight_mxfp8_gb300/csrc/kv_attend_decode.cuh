@@ -30,7 +30,7 @@
 // copy's rate, with the schedulers issuing in 57 % of the cycles: the widening's
 // instructions (the loop without them takes 93 us). Two requests of 100 to 131
 // thousand tokens take 53 us for 244 MB: the same, with longer joins. One request
-// of 777 tokens takes 10.3 us, all latency. With several rows a request and a
+// of 777 tokens takes 10.5 us, all latency. With several rows a request and a
 // window (40 requests, up to 24 rows, 1024 tokens of 64: 42 us for 35 MB) an
 // item's start and end bound it, twice as long as a tile.
 #pragma once

@@ -8,8 +8,8 @@
 // launches in between, is 2 us quicker up to some 2000 entries, and three times
 // slower at 16 thousand: not kept). Copy: bytes.
 //
-// Latency bounds the tables: a fork of 1000 requests with its copies takes 7.9 us, a
-// free list from 1000 requests 6.2 us, against 2.5 for any launch. The bytes bound a
+// Latency bounds the tables: a fork of 1000 requests with its copies takes 7.7 us, a
+// free list from 1000 requests 6.4 us, against 2.5 for any launch. The bytes bound a
 // pool's compaction: 64 requests, 198 MB moved, 41 us in all, 34 of them the copy's.
 #include "decode.h"
 #include "ptx.cuh"

@@ -6,8 +6,8 @@
 // 2^-34 of a turn at position 2^31. A CTA takes a token's heads, so the
 // sines are computed once for all of them; every element is read and written once
 // and the bytes bound it: 12592 tokens of 72 heads of 128, half of each turned,
-// 464 MB, take 71 us, 6.5 TB/s, 97 % of a copy's rate (sines for each head anew made
-// it 9 more). A decode step's 64 tokens are their launch, 2.7 us, heads shared out so that
+// 464 MB, take 71 us, 6.5 TB/s, 96 % of a copy's rate (sines for each head anew made
+// it 9 more). A decode step's 64 tokens are their launch, 2.6 us, heads shared out so that
 // the GPU is full.
 #include "decode.h"
 

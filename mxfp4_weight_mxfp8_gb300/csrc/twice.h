@@ -10,7 +10,7 @@ namespace moe {
 
 struct Twice {
   double hi, lo;
-  Twice(double hi = 0.0, double lo = 0.0) : hi(hi), lo(lo) {}
+  constexpr Twice(double hi = 0.0, double lo = 0.0) : hi(hi), lo(lo) {}
 };
 
 // |a| >= |b|, or a is 0.
@@ -50,8 +50,8 @@ inline Twice operator/(Twice a, Twice b) {
 
 inline Twice times_two_to(Twice a, int n) { return {std::ldexp(a.hi, n), std::ldexp(a.lo, n)}; }
 
-const Twice kLogOfTwo(0.693147180559945309417232, 2.31904681384629955842e-17);
-const Twice kTau(6.28318530717958647692529, 2.44929359829470635445e-16);
+constexpr Twice kLogOfTwo(0.693147180559945309417232, 2.31904681384629955842e-17);
+constexpr Twice kTau(6.28318530717958647692529, 2.44929359829470635445e-16);
 
 // e^x = 2^n (e^r)^64, r = (x - n log 2) / 64 up to 0.0055: eleven terms of its series leave 2^-119.
 inline Twice exp_of(Twice x) {
