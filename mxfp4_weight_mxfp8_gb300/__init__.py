@@ -567,7 +567,9 @@ def moe_kv_attend(cache, q, block_table, query_start, seq_lens, out, workspace, 
 
 
 def moe_kv_shared_bytes(tokens: int, q_heads: int, head_dim: int) -> int:
-    """Bytes of moe_kv_attend_shared's scratch."""
+    """Bytes of moe_kv_attend_shared's scratch; 0 for arguments that the call refuses."""
+    if not 0 <= min(tokens, q_heads, head_dim) <= max(tokens, q_heads, head_dim) < 1 << 31:  # (ctypes would take them modulo 2^32)
+        return 0
     return _lib.moe_kv_shared_bytes(tokens, q_heads, head_dim)
 
 
@@ -692,6 +694,8 @@ def moe_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_L
     """The table of moe_rope: int64 [rotary_dim / 2], angles of one position in units of 2^-64 turns; see include/moe.h."""
     import torch
 
+    if not 0 <= min(rotary_dim, scaling) <= max(rotary_dim, scaling) < 1 << 31:  # (ctypes would take them modulo 2^32)
+        _refuse("moe_rope_turns", "rotary_dim or scaling out of range")
     turns = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
     _check(_lib.moe_rope_turns(rotary_dim, base, scaling, factor, trained, low, high, turns.data_ptr()), "moe_rope_turns")
     return turns if device is None else turns.to(device)
