@@ -588,8 +588,8 @@ def moe_kv_attend_shared(cache, q, block_table, query_start, seq_lens, group_sta
     groups, room = prefix_lens.shape[0], scratch.shape
     if len(room) != 1 or room[0] < MOE_KV_SHARED_HEADER + 4 * tokens * heads * (dim + 1):
         _refuse(call, f"scratch must be {moe_kv_shared_bytes(tokens, heads, dim)} bytes of uint8")
-    prefixes = _PREFIXES.pack(_dense(call, "group_start", group_start, _i32t, (groups + 1,), device),
-                              _dense(call, "prefix_lens", prefix_lens, _i32t, (groups,), device), groups, least_tiles)
+    prefixes = _packed_args(call, _PREFIXES, _dense(call, "group_start", group_start, _i32t, (groups + 1,), device),
+                            _dense(call, "prefix_lens", prefix_lens, _i32t, (groups,), device), groups, least_tiles)
     return _check(_attend_shared(block, batch, prefixes, *rows, heads, dim ** -0.5 if scale is None else scale,
                                  _dense(call, "out", out, _bf16t, q.shape, device),
                                  None if lse is None else _dense(call, "lse", lse, _f32t, (tokens, heads), device),
@@ -629,6 +629,14 @@ _PREFIXES = struct.Struct("PP2i")
 _RECLAIM = struct.Struct("PqPPPPqPP4i")
 
 
+def _packed_args(call: str, block: struct.Struct, *values):
+    """The C entry's argument block; refuses numbers that it has no room for."""
+    try:
+        return block.pack(*values)
+    except (struct.error, OverflowError) as e:
+        _refuse(call, f"a number out of range ({e})")
+
+
 def _matrix(call: str, name: str, t, rows: int, columns: int, device: int):
     """(address, row stride) of a [rows, columns] tensor with unit stride along its rows."""
     if t.get_device() == device and t.dim() == 2:
@@ -652,8 +660,8 @@ def _norm_block(call: str, x, weight, out, eps, residual, residual_out, codes, s
     if out is not None and out.dtype is not x.dtype:
         _refuse(call, "out must be of x's type")
     none = (0, hidden)
-    return _NORM.pack(
-        *_matrix(call, "x", x, tokens, hidden, device),
+    return _packed_args(
+        call, _NORM, *_matrix(call, "x", x, tokens, hidden, device),
         *(none if residual is None else _matrix(call, "residual", residual, tokens, hidden, device)),
         *(none if residual_out is None else _matrix(call, "residual_out", residual_out, tokens, hidden, device)),
         _dense(call, "weight", weight, weight.dtype, (hidden,), device),
@@ -736,9 +744,9 @@ def moe_rope(positions, turns, q, k=None, q_out=None, k_out=None, interleaved: b
     elif k_out is not None:
         _refuse(call, "k_out without k")
     pairs = turns.shape[0] if turns.dim() == 1 else 0
-    block = _ROPE.pack(_dense(call, "positions", positions, _i32t, (tokens,), device),
-                       _dense(call, "turns", turns, _i64t, (pairs,), device), *q_in, *q_to[:3], *k_in, *k_to[:3], tokens, heads,
-                       k_heads, dim, 2 * pairs, 1 if interleaved else 0, amplitude)
+    block = _packed_args(call, _ROPE, _dense(call, "positions", positions, _i32t, (tokens,), device),
+                         _dense(call, "turns", turns, _i64t, (pairs,), device), *q_in, *q_to[:3], *k_in, *k_to[:3], tokens, heads,
+                         k_heads, dim, 2 * pairs, 1 if interleaved else 0, amplitude)
     return _check(_rope(block, stream), call)
 
 
@@ -762,13 +770,13 @@ def moe_kv_fork(parents, block_table, seq_lens, page_tokens: int, free_pages, fr
     out, out_stride, out_width = _table(call, out_table, requests, device)
     if out_width != width:
         _refuse(call, "out_table must be as wide as block_table")
-    block = _FORK.pack(_dense(call, "parents", parents, _i32t, (requests,), device), table, table_stride,
-                       _dense(call, "seq_lens", seq_lens, _i32t, (rows,), device),
-                       _dense(call, "free_pages", free_pages, _i32t, (free,), device),
-                       _dense(call, "free_head", free_head, _i32t, (1,), device), out, out_stride,
-                       _dense(call, "out_lens", out_lens, _i32t, (requests,), device),
-                       _dense(call, "moves", moves, _i32t, (requests, 3), device),
-                       _dense(call, "counts", counts, _i32t, (4,), device), rows, requests, page_tokens, width, free)
+    block = _packed_args(call, _FORK, _dense(call, "parents", parents, _i32t, (requests,), device), table, table_stride,
+                         _dense(call, "seq_lens", seq_lens, _i32t, (rows,), device),
+                         _dense(call, "free_pages", free_pages, _i32t, (free,), device),
+                         _dense(call, "free_head", free_head, _i32t, (1,), device), out, out_stride,
+                         _dense(call, "out_lens", out_lens, _i32t, (requests,), device),
+                         _dense(call, "moves", moves, _i32t, (requests, 3), device),
+                         _dense(call, "counts", counts, _i32t, (4,), device), rows, requests, page_tokens, width, free)
     return _check(_fork(block, stream), call)
 
 
@@ -790,7 +798,7 @@ def moe_kv_reclaim(block_table, seq_lens, page_tokens: int, free_pages, counts, 
     room = workspace.shape
     if len(room) != 1 or room[0] < moe_kv_reclaim_bytes(pages):
         _refuse(call, f"workspace must be {moe_kv_reclaim_bytes(pages)} bytes of uint8")
-    block = _RECLAIM.pack(table, table_stride, _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device),
+    block = _packed_args(call, _RECLAIM, table, table_stride, _dense(call, "seq_lens", seq_lens, _i32t, (requests,), device),
                           _dense(call, "free_pages", free_pages, _i32t, (pages,), device),
                           _dense(call, "counts", counts, _i32t, (4,), device), out, out_stride,
                           0 if moves is None else _moves(call, moves, max(1, pages // 2), device),
@@ -867,6 +875,8 @@ class KvCache:
                       return_lse: bool = False, scratch=None, least_tiles: int = 0, stream=None):
         import torch
 
+        if q.dim() != 3:
+            _refuse("moe_kv_attend_shared", "q must be [tokens, q_heads, head_dim]")
         with _allocating_on(stream):
             if out is None:
                 out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
